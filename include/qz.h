@@ -79,7 +79,9 @@ int qz_get_overlap(void);
 
 /* The library's device error word, a bit set: 1 if a kernel gave up a
  * bounded wait (its output is then incomplete); 2 if qz_embed_int8 met a
- * token outside its table (that row was written as zeros).  0 if neither
+ * token outside its table (that row was written as zeros); 4 if a page, a
+ * position or an adapter index lay outside its table (qz_rope_append,
+ * qz_attention_paged, qz_lora; each says what it did then).  0 if none
  * happened since the last clear.  Synchronous (reads device memory);
  * clear = 1 resets it.  Not for use during stream capture. */
 qz_status qz_device_error(int *code, int clear);
@@ -396,6 +398,142 @@ qz_status qz_pager_destroy(qz_pager *p);
  * The pager then drains its copy stream and acquire returns QZ_ERR_IO.
  * layer = -1 clears the injection.  Touches no GPU state. */
 qz_status qz_pager_inject_copy_failure(qz_pager *p, int layer);
+
+/* ======================================================================
+ * Layer glue for serving  [the pages name a decoder LLM but define no step
+ * between its products; these are the usual definitions of such a layer]
+ *
+ * Sizes here: T tokens (rows) of a step, packed sequence after sequence.
+ * ====================================================================== */
+
+/* Residual addition and root-mean-square normalisation of T rows:
+ *   h[t][j] = x[t][j] + residual[t][j]   (h = x when residual is NULL)
+ *   y[t][j] = fp16( h[t][j] * rsqrt(mean_j h[t][j]^2 + eps) * (w_bias + weight[j]) )
+ * h is held in fp32 (the norm is that of the unrounded sum) and rounded once
+ * when stored to sum [T][lds] (NULL: not stored).  weight: fp16 [K]; w_bias is
+ * 0, or 1 for models that store w - 1.  sum may be x or residual and y may be x
+ * (same pointer and stride: in place).  T >= 0 (0 enqueues nothing), 1 <= K <=
+ * 57344, eps >= 0.  2-byte alignment and any stride >= K suffice; rows whose
+ * every array is 16-byte aligned with K and strides multiples of 8 are read
+ * and written 16 bytes at a time. */
+qz_status qz_rmsnorm(const qz_half *x, int64_t ldx, const qz_half *residual, int64_t ldr,
+                     const qz_half *weight, float w_bias, float eps, int64_t T, int64_t K,
+                     qz_half *y, int64_t ldy, qz_half *sum, int64_t lds, qz_stream s);
+
+/* The same with the normalised rows in INT8, one fp32 scale per row, by the
+ * rule of qz_quantize_int8 applied to the unrounded y:
+ *   scale[t] = max_j |y[t][j]| / 127;  q = clamp(rint(y / scale), -127, 127);
+ * a row of zeros gives scale 0 and codes 0.  q [T][ldq], ldq >= K (columns
+ * K.. are not written), scale [T]. */
+qz_status qz_rmsnorm_int8(const qz_half *x, int64_t ldx, const qz_half *residual, int64_t ldr,
+                          const qz_half *weight, float w_bias, float eps, int64_t T, int64_t K,
+                          int8_t *q, int64_t ldq, float *scale, qz_half *sum, int64_t lds,
+                          qz_stream s);
+
+/* A paged key/value cache: a pool of n_pages pages of page_size tokens.  The
+ * row of token slot t of page p and KV head h starts at k + p * k_page +
+ * h * k_head + t * k_token (strides in halves; v likewise) and holds head_dim
+ * contiguous fp16 values.  page_size: 8, 16, 32, 64, 128 or 256.  head_dim:
+ * 64, 128 or 256.  k and v 16-byte aligned, strides multiples of 8. */
+typedef struct {
+  qz_half *k, *v;
+  int64_t n_pages, page_size, n_kv_heads, head_dim;
+  int64_t k_page, k_head, k_token;
+  int64_t v_page, v_head, v_token;
+} qz_kv_cache;
+
+/* The sequences of a step (device arrays, read when the call runs).  Sequence
+ * i brings the new tokens cu_q[i] .. cu_q[i+1]-1 of the n_tokens packed rows
+ * (cu_q non-decreasing, within 0..n_tokens; rows outside every sequence are
+ * neither read nor written) and holds kv_len[i] tokens, the new ones
+ * last: its new token j has position kv_len[i] - (cu_q[i+1] - cu_q[i]) + j.
+ * Token position p lies in slot p % page_size of page
+ * page_table[i * ld_table + p / page_size]. */
+typedef struct {
+  int64_t n_seqs, n_tokens;
+  const int32_t *cu_q;       /* [n_seqs + 1] */
+  const int32_t *kv_len;     /* [n_seqs] */
+  const int32_t *page_table; /* [n_seqs][ld_table] */
+  int64_t ld_table;          /* pages a sequence may have; entries past its last page are not read */
+} qz_seq_batch;
+
+/* Rotary position embedding of new queries and keys, and storage of the keys
+ * and values into the cache.  With half = head_dim / 2 and row
+ * (c_0..c_{half-1}, s_0..s_{half-1}) = rope[position]:
+ *   x'[j] = x[j] c_j - x[j + half] s_j,  x'[j + half] = x[j + half] c_j + x[j] s_j,
+ * computed in fp32 and rounded once.  q, q_out: [n_tokens][n_heads][head_dim]
+ * with strides q_token, q_head (q_out may be q); k, v likewise with
+ * n_kv_heads.  rope: fp32 [rope_len][head_dim], or NULL to store the keys as
+ * they are (q_out may then be NULL; otherwise q is copied).  q may be NULL with
+ * q_out to store keys and values only.  A new token whose position is negative,
+ * has no page, or lies beyond rope (its page outside the pool included) is not
+ * stored, its q_out row is zeros, and bit 4 of the device error word is set
+ * (a negative position, of a sequence that holds fewer tokens than are new,
+ * sets no bit).  Two sequences must not share a page that both write.
+ * Pointers 16-byte aligned, strides multiples of 8. */
+qz_status qz_rope_append(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                         const qz_half *k, int64_t k_token, int64_t k_head, const qz_half *v,
+                         int64_t v_token, int64_t v_head, const float *rope, int64_t rope_len,
+                         const qz_kv_cache *cache, const qz_seq_batch *seqs, qz_half *q_out,
+                         int64_t qo_token, int64_t qo_head, qz_stream s);
+
+/* Attention of the new tokens over the paged cache (which already holds their
+ * keys and values).  For query head g, KV head h = g / (n_heads / n_kv_heads)
+ * and a new token at position p of its sequence:
+ *   x_j = scale * q . k_j;  if softcap > 0: x_j = softcap * tanh(x_j / softcap);
+ *   out = sum_j e^{x_j} v_j / sum_j e^{x_j}  over j <= p, j < kv_len and, if
+ *   window > 0, j > p - window.
+ * One new token per sequence is a decode step; kv_len = number of new tokens
+ * is a whole prompt.  A query that sees no key (kv_len 0, or fewer tokens held
+ * than new) gives zeros.  Slots that no query of a call sees (past kv_len,
+ * before every window, free pages) may hold anything, NaN included; the
+ * others must be finite.  A page outside the pool, or beyond ld_table, reads as
+ * zeros (keys and values) and sets bit 4 of the device error word.
+ * Logits, softmax sums and outputs are held in fp32; the weights e^{x_j - m} are
+ * rounded to fp16 where they enter the tensor cores.  scale: finite.
+ * q, out: [n_tokens][n_heads][head_dim] with strides q_token, q_head, o_token,
+ * o_head; 16-byte aligned, strides multiples of 8.
+ * workspace: qz_attention_workspace_bytes bytes of device memory, 16-byte
+ * aligned, zeroed before its first use and left ready by every call that
+ * completes (zero it again after device error 1); calls that can be in flight
+ * at the same time need different ones.  Results repeat bit for bit. */
+qz_status qz_attention_paged(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                             const qz_kv_cache *cache, const qz_seq_batch *seqs, float scale,
+                             float softcap, int64_t window, qz_half *out, int64_t o_token,
+                             int64_t o_head, void *workspace, size_t workspace_bytes,
+                             qz_stream s);
+
+/* Workspace of qz_attention_paged for up to n_seqs sequences with up to
+ * n_tokens new tokens in all; 0 for invalid sizes.  Host only. */
+size_t qz_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t n_heads,
+                                    int64_t n_kv_heads, int64_t head_dim);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   out[t][i] = fp16( y[t][i] + scale[a] * sum_{r < rank[a]} B_a[i][r] * u_r ),
+ *   u_r = sum_j A_a[r][j] x[t][j],  a = index[t];
+ * a row with index -1 has no adapter (out = y).  y: the projection's output
+ * [T][ldy] (qz_gemm_* of the same x), out [T][ldo] (may be y).  A_a = a +
+ * a * a_adapter, rows a_row apart; B_a = b + a * b_adapter, rows b_row
+ * apart (halves).  rank NULL: all R.  1 <= R <= 128, ranks are clamped to 0..R.
+ * Sums are fp32; u is kept in fp32 between the two products.  An index outside
+ * -1..n_adapters-1 counts as -1 and sets bit 4 of the device error word.
+ * Rows with the same index cost one read of their adapter when they are
+ * neighbours.  2-byte alignment suffices; 16-byte aligned operands with K, R
+ * and strides multiples of 8 run fastest.  K, N <= 2^20.
+ * workspace: qz_lora_workspace_bytes(T, K, R) bytes, 16-byte aligned (any
+ * contents). */
+typedef struct {
+  const qz_half *a, *b;
+  const float *scale;  /* [n_adapters] */
+  const int32_t *rank; /* [n_adapters] or NULL */
+  int64_t n_adapters, R, K, N;
+  int64_t a_adapter, a_row, b_adapter, b_row;
+} qz_lora_adapters;
+
+qz_status qz_lora(const qz_lora_adapters *ad, const int32_t *index, int64_t T,
+                  const qz_half *x, int64_t ldx, const qz_half *y, int64_t ldy, qz_half *out,
+                  int64_t ldo, void *workspace, size_t workspace_bytes, qz_stream s);
+size_t qz_lora_workspace_bytes(int64_t T, int64_t K, int64_t R);
 
 #ifdef __cplusplus
 }

@@ -7,7 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_int, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqz.so")
@@ -38,6 +38,27 @@ class Int4oWeight(ctypes.Structure):
                 ("ld_out", c_int64), ("ld_q4", c_int64),
                 ("perm", c_void_p), ("w_out", c_void_p), ("q4", c_void_p),
                 ("scale", c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p),
+                ("n_pages", c_int64), ("page_size", c_int64), ("n_kv_heads", c_int64),
+                ("head_dim", c_int64),
+                ("k_page", c_int64), ("k_head", c_int64), ("k_token", c_int64),
+                ("v_page", c_int64), ("v_head", c_int64), ("v_token", c_int64)]
+
+
+class SeqBatchArg(ctypes.Structure):
+    _fields_ = [("n_seqs", c_int64), ("n_tokens", c_int64),
+                ("cu_q", c_void_p), ("kv_len", c_void_p), ("page_table", c_void_p),
+                ("ld_table", c_int64)]
+
+
+class LoraArg(ctypes.Structure):
+    _fields_ = [("a", c_void_p), ("b", c_void_p), ("scale", c_void_p), ("rank", c_void_p),
+                ("n_adapters", c_int64), ("R", c_int64), ("K", c_int64), ("N", c_int64),
+                ("a_adapter", c_int64), ("a_row", c_int64),
+                ("b_adapter", c_int64), ("b_row", c_int64)]
 
 
 _S = c_int  # qz_status
@@ -86,6 +107,21 @@ _SIGS = {
     "qz_gemv_int4_outlier_sequence": (_S, [POINTER(Int4oWeight), POINTER(c_int), c_int,
                                            POINTER(c_void_p), POINTER(c_void_p), c_void_p,
                                            c_void_p]),
+    "qz_rmsnorm": (_S, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_float,
+                        c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "qz_rmsnorm_int8": (_S, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_float,
+                             c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
+                             c_void_p]),
+    "qz_rope_append": (_S, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_int64,
+                            c_void_p, c_int64, c_int64, c_void_p, c_int64, POINTER(KvCache),
+                            POINTER(SeqBatchArg), c_void_p, c_int64, c_int64, c_void_p]),
+    "qz_attention_paged": (_S, [c_void_p, c_int64, c_int64, c_int64, POINTER(KvCache),
+                                POINTER(SeqBatchArg), c_float, c_float, c_int64, c_void_p,
+                                c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
+    "qz_attention_workspace_bytes": (c_size_t, [c_int64] * 5),
+    "qz_lora": (_S, [POINTER(LoraArg), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                     c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+    "qz_lora_workspace_bytes": (c_size_t, [c_int64] * 3),
     "qz_pager_create": (_S, [POINTER(c_void_p), POINTER(c_size_t), c_int, c_void_p, c_void_p,
                              c_size_t, c_void_p, c_void_p, POINTER(c_void_p)]),
     "qz_pager_acquire": (_S, [c_void_p, c_int, POINTER(c_void_p)]),

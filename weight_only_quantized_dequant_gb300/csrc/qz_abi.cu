@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "qz_internal.cuh"
+#include "seq_batch.cuh"
 
 namespace qz {
 
@@ -244,6 +245,61 @@ qz_status device_view_t(T *&ptr) {
   return QZ_OK;
 }
 
+// Rows of 16-byte vectors that are `strides` halves apart.
+qz_status check_rows16(const void *p, int64_t s0, int64_t s1) {
+  if (!p || s0 < 0 || s1 < 0) return QZ_ERR_INVALID_ARG;
+  if (!aligned16(p) || s0 % 8 || s1 % 8) return QZ_ERR_ALIGNMENT;
+  return QZ_OK;
+}
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 24;  // grid and index limits of the layer kernels
+constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
+
+qz_status paged_view(const qz_kv_cache *c, PagedView *v) {
+  if (!c || !c->k || !c->v || c->n_pages < 1 || c->n_kv_heads < 1) return QZ_ERR_INVALID_ARG;
+  if (c->head_dim < 1 || c->page_size < 1) return QZ_ERR_INVALID_ARG;
+  for (const int64_t s : {c->k_page, c->k_head, c->k_token, c->v_page, c->v_head, c->v_token}) {
+    if (s < 0) return QZ_ERR_INVALID_ARG;
+    if (s % 8) return QZ_ERR_ALIGNMENT;
+  }
+  if (!aligned16(c->k) || !aligned16(c->v)) return QZ_ERR_ALIGNMENT;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QZ_ERR_UNSUPPORTED;
+  const int64_t ps = c->page_size;
+  if (ps < 8 || ps > 256 || (ps & (ps - 1))) return QZ_ERR_UNSUPPORTED;
+  if (c->n_pages > INT32_MAX || c->n_kv_heads > 4096) return QZ_ERR_UNSUPPORTED;
+  *v = {reinterpret_cast<__half *>(c->k), reinterpret_cast<__half *>(c->v), (int)c->n_pages,
+        (int)ps, __builtin_ctz((unsigned)ps), (int)c->n_kv_heads, (int)c->head_dim, c->k_page,
+        c->k_head, c->k_token, c->v_page, c->v_head, c->v_token};
+  return QZ_OK;
+}
+
+qz_status seq_view(const qz_seq_batch *b, SeqView *v) {
+  if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->ld_table < 0) return QZ_ERR_INVALID_ARG;
+  if (b->n_tokens > 0 && b->n_seqs > 0) {
+    if (!b->cu_q || !b->kv_len || !b->page_table) return QZ_ERR_INVALID_ARG;
+    if (((uintptr_t)b->cu_q | (uintptr_t)b->kv_len | (uintptr_t)b->page_table) & 3u)
+      return QZ_ERR_ALIGNMENT;
+  }
+  if (b->n_seqs > kMaxSeqs || b->n_tokens > kMaxTokens || b->ld_table > INT32_MAX)
+    return QZ_ERR_UNSUPPORTED;
+  *v = {(int)b->n_seqs, b->n_tokens, b->cu_q, b->kv_len, b->page_table, b->ld_table};
+  return QZ_OK;
+}
+
+// Shared checks of the two norms; rows need only the alignment of fp16.
+qz_status check_norm(const qz_half *x, int64_t ldx, const qz_half *r, int64_t ldr,
+                     const qz_half *w, float bias, float eps, int64_t T, int64_t K,
+                     const qz_half *sum, int64_t lds) {
+  if (T < 0 || K < 1 || !(eps >= 0.0f) || bias != bias) return QZ_ERR_INVALID_ARG;
+  if (K > kMaxGemvK || T > kMaxTokens) return QZ_ERR_UNSUPPORTED;
+  if (T == 0) return QZ_OK;
+  QZ_TRY(check_vec(x, T, K, ldx));
+  QZ_TRY(check_vec(w, 1, K, 0));
+  if (r) QZ_TRY(check_vec(r, T, K, ldr));
+  if (sum) QZ_TRY(check_vec(sum, T, K, lds));
+  return QZ_OK;
+}
+
 // Batch-1 grouped product with the weights read in place (zero-copy).
 qz_status mapped_common(bool int4, GemvParams &p, const qz_half *x, qz_half *const *ys, int n,
                         cudaStream_t s) {
@@ -297,7 +353,11 @@ qz_status qz_device_error(int *code, int clear) {
   QZ_TRY(read_gemv_error(&b, clear));
   QZ_TRY(read_embed_error(&c, clear));
   QZ_TRY(read_mv_error(&d, clear));
-  *code = a | b | c | d;
+  int e = 0, f = 0, g = 0;
+  QZ_TRY(read_rope_error(&e, clear));
+  QZ_TRY(read_attn_error(&f, clear));
+  QZ_TRY(read_lora_error(&g, clear));
+  *code = a | b | c | d | e | f | g;
   return QZ_OK;
 }
 
@@ -559,6 +619,130 @@ qz_status qz_gemv_int4_outlier_sequence(const qz_int4o_weight *ws, const int *co
         return (w.K == w0.K && w.n_out == w0.n_out && w.perm == w0.perm) ? QZ_OK
                                                                           : QZ_ERR_INVALID_ARG;
       });
+}
+
+// ------------------------------------------------------------ layer glue --
+qz_status qz_rmsnorm(const qz_half *x, int64_t ldx, const qz_half *residual, int64_t ldr,
+                     const qz_half *weight, float w_bias, float eps, int64_t T, int64_t K,
+                     qz_half *y, int64_t ldy, qz_half *sum, int64_t lds, qz_stream s) {
+  QZ_TRY(check_norm(x, ldx, residual, ldr, weight, w_bias, eps, T, K, sum, lds));
+  if (T == 0) return QZ_OK;
+  QZ_TRY(check_vec(y, T, K, ldy));
+  return launch_rmsnorm(reinterpret_cast<const __half *>(x), ldx,
+                        reinterpret_cast<const __half *>(residual), ldr,
+                        reinterpret_cast<const __half *>(weight), w_bias, eps, T, K,
+                        reinterpret_cast<__half *>(y), ldy, nullptr, 0, nullptr,
+                        reinterpret_cast<__half *>(sum), lds, (cudaStream_t)s);
+}
+
+qz_status qz_rmsnorm_int8(const qz_half *x, int64_t ldx, const qz_half *residual, int64_t ldr,
+                          const qz_half *weight, float w_bias, float eps, int64_t T, int64_t K,
+                          int8_t *q, int64_t ldq, float *scale, qz_half *sum, int64_t lds,
+                          qz_stream s) {
+  QZ_TRY(check_norm(x, ldx, residual, ldr, weight, w_bias, eps, T, K, sum, lds));
+  if (T == 0) return QZ_OK;
+  if (!q || !scale || (T > 1 && ldq < K)) return QZ_ERR_INVALID_ARG;
+  if ((uintptr_t)scale & 3u) return QZ_ERR_ALIGNMENT;
+  return launch_rmsnorm(reinterpret_cast<const __half *>(x), ldx,
+                        reinterpret_cast<const __half *>(residual), ldr,
+                        reinterpret_cast<const __half *>(weight), w_bias, eps, T, K, nullptr, 0, q,
+                        ldq, scale, reinterpret_cast<__half *>(sum), lds, (cudaStream_t)s);
+}
+
+qz_status qz_rope_append(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                         const qz_half *k, int64_t k_token, int64_t k_head, const qz_half *v,
+                         int64_t v_token, int64_t v_head, const float *rope, int64_t rope_len,
+                         const qz_kv_cache *cache, const qz_seq_batch *seqs, qz_half *q_out,
+                         int64_t qo_token, int64_t qo_head, qz_stream s) {
+  PagedView c;
+  SeqView b;
+  QZ_TRY(paged_view(cache, &c));
+  QZ_TRY(seq_view(seqs, &b));
+  if (rope && rope_len < 0) return QZ_ERR_INVALID_ARG;
+  if (rope && !aligned16(rope)) return QZ_ERR_ALIGNMENT;
+  if (q_out && !q) return QZ_ERR_INVALID_ARG;
+  if (rope && q && !q_out) return QZ_ERR_INVALID_ARG;
+  if (q_out && (n_heads < 1 || n_heads > 65536)) return QZ_ERR_INVALID_ARG;
+  if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
+  QZ_TRY(check_rows16(k, k_token, k_head));
+  QZ_TRY(check_rows16(v, v_token, v_head));
+  if (q_out) {
+    QZ_TRY(check_rows16(q, q_token, q_head));
+    QZ_TRY(check_rows16(q_out, qo_token, qo_head));
+  }
+  return launch_rope_append(
+      reinterpret_cast<const __half *>(q), n_heads, q_token, q_head,
+      reinterpret_cast<const __half *>(k), k_token, k_head, reinterpret_cast<const __half *>(v),
+      v_token, v_head, rope, rope_len, c, b, reinterpret_cast<__half *>(q_out), qo_token, qo_head,
+      (cudaStream_t)s);
+}
+
+size_t qz_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t n_heads,
+                                    int64_t n_kv_heads, int64_t head_dim) {
+  if (n_tokens < 0 || n_seqs < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads ||
+      n_tokens > kMaxTokens || n_seqs > kMaxSeqs)
+    return 0;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  return attention_workspace_bytes(n_tokens, n_seqs, n_heads, n_kv_heads, head_dim);
+}
+
+qz_status qz_attention_paged(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                             const qz_kv_cache *cache, const qz_seq_batch *seqs, float scale,
+                             float softcap, int64_t window, qz_half *out, int64_t o_token,
+                             int64_t o_head, void *workspace, size_t workspace_bytes,
+                             qz_stream s) {
+  PagedView c;
+  SeqView b;
+  QZ_TRY(paged_view(cache, &c));
+  QZ_TRY(seq_view(seqs, &b));
+  if (n_heads < 1 || n_heads % c.hkv || window < 0 || !(softcap >= 0.0f) ||
+      !(scale - scale == 0.0f) || !(softcap - softcap == 0.0f))
+    return QZ_ERR_INVALID_ARG;
+  if (n_heads > 65536) return QZ_ERR_UNSUPPORTED;
+  if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
+  QZ_TRY(check_rows16(q, q_token, q_head));
+  QZ_TRY(check_rows16(out, o_token, o_head));
+  if (!workspace ||
+      workspace_bytes < attention_workspace_bytes(b.n_tokens, b.n_seqs, n_heads, c.hkv, c.D))
+    return QZ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return QZ_ERR_ALIGNMENT;
+  return launch_attention(reinterpret_cast<const __half *>(q), n_heads, q_token, q_head, c, b,
+                          scale, softcap, window, reinterpret_cast<__half *>(out), o_token, o_head,
+                          workspace, (cudaStream_t)s);
+}
+
+size_t qz_lora_workspace_bytes(int64_t T, int64_t K, int64_t R) {
+  if (T < 0 || T > kMaxTokens || K < 1 || K > ((int64_t)1 << 20) || R < 1 || R > 128) return 0;
+  return lora_workspace_bytes(T, K, R);
+}
+
+qz_status qz_lora(const qz_lora_adapters *ad, const int32_t *index, int64_t T, const qz_half *x,
+                  int64_t ldx, const qz_half *y, int64_t ldy, qz_half *out, int64_t ldo,
+                  void *workspace, size_t workspace_bytes, qz_stream s) {
+  if (!ad || T < 0 || ad->n_adapters < 0 || ad->R < 1 || ad->K < 1 || ad->N < 1)
+    return QZ_ERR_INVALID_ARG;
+  if (ad->R > 128 || ad->K > ((int64_t)1 << 20) || ad->N > ((int64_t)1 << 20) || T > kMaxTokens ||
+      ad->n_adapters > INT32_MAX)
+    return QZ_ERR_UNSUPPORTED;
+  if (T == 0) return QZ_OK;
+  if (ad->n_adapters > 0) {
+    if (!ad->a || !ad->b || !ad->scale || ad->a_row < ad->K || ad->b_row < ad->R ||
+        ad->a_adapter < 0 || ad->b_adapter < 0)
+      return QZ_ERR_INVALID_ARG;
+    if (((uintptr_t)ad->a | (uintptr_t)ad->b) & 1u) return QZ_ERR_ALIGNMENT;
+    if (((uintptr_t)ad->scale | (uintptr_t)ad->rank) & 3u) return QZ_ERR_ALIGNMENT;
+  }
+  if (!index) return QZ_ERR_INVALID_ARG;
+  if ((uintptr_t)index & 3u) return QZ_ERR_ALIGNMENT;
+  QZ_TRY(check_vec(x, T, ad->K, ldx));
+  QZ_TRY(check_vec(y, T, ad->N, ldy));
+  QZ_TRY(check_vec(out, T, ad->N, ldo));
+  if (!workspace || workspace_bytes < lora_workspace_bytes(T, ad->K, ad->R))
+    return QZ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return QZ_ERR_ALIGNMENT;
+  return launch_lora(*ad, index, T, reinterpret_cast<const __half *>(x), T > 1 ? ldx : 0,
+                     reinterpret_cast<const __half *>(y), T > 1 ? ldy : 0,
+                     reinterpret_cast<__half *>(out), T > 1 ? ldo : 0, workspace, (cudaStream_t)s);
 }
 
 }  // extern "C"

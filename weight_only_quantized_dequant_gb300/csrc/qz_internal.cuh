@@ -109,6 +109,47 @@ qz_status launch_embed_int8(const int8_t *q, int64_t ldq, const float *scale, in
                             const int32_t *tokens, int64_t B, __half *out, int64_t ldo,
                             cudaStream_t s);
 
+// Reads (and clears) a translation unit's device error word.
+template <typename Word>
+inline qz_status read_error_word(Word &word, int *code, int clear) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, word, sizeof(int));
+  if (e != cudaSuccess) return cuda_status(e);
+  if (clear && v) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(word, &zero, sizeof(int));
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  *code = v;
+  return QZ_OK;
+}
+
+// ------------------------------------------------------------ layer glue ---
+struct PagedView;  // seq_batch.cuh
+struct SeqView;
+qz_status launch_rmsnorm(const __half *x, int64_t ldx, const __half *r, int64_t ldr,
+                         const __half *w, float bias, float eps, int64_t T, int64_t K, __half *y,
+                         int64_t ldy, int8_t *q, int64_t ldq, float *scale, __half *sum,
+                         int64_t lds, cudaStream_t s);
+qz_status launch_rope_append(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
+                             const __half *k, int64_t k_token, int64_t k_head, const __half *v,
+                             int64_t v_token, int64_t v_head, const float *rope, int64_t rope_len,
+                             const PagedView &c, const SeqView &sv, __half *qo, int64_t qo_token,
+                             int64_t qo_head, cudaStream_t s);
+size_t attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t hq, int64_t hkv,
+                                 int64_t D);
+qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
+                           const PagedView &c, const SeqView &sv, float scale, float softcap,
+                           int64_t window, __half *out, int64_t o_token, int64_t o_head,
+                           void *workspace, cudaStream_t s);
+size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t R);
+qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t T, const __half *x,
+                      int64_t ldx, const __half *y, int64_t ldy, __half *out, int64_t ldo,
+                      void *workspace, cudaStream_t s);
+qz_status read_rope_error(int *code, int clear);
+qz_status read_attn_error(int *code, int clear);
+qz_status read_lora_error(int *code, int clear);
+
 // ------------------------------------------------------------ quantizers ---
 qz_status launch_quantize_int8(const __half *W, int64_t N, int64_t K,
                                int64_t ldw, int8_t *q, int64_t ldq,
