@@ -493,10 +493,13 @@ qz_status qz_rope_append(const qz_half *q, int64_t n_heads, int64_t q_token, int
  * rounded to fp16 where they enter the tensor cores.  scale: finite.
  * q, out: [n_tokens][n_heads][head_dim] with strides q_token, q_head, o_token,
  * o_head; 16-byte aligned, strides multiples of 8.
+ * n_tokens * n_heads < 2^31.
  * workspace: qz_attention_workspace_bytes bytes of device memory, 16-byte
- * aligned, zeroed before its first use and left ready by every call that
- * completes (zero it again after device error 1); calls that can be in flight
- * at the same time need different ones.  Results repeat bit for bit. */
+ * aligned, the first QZ_ATTENTION_SYNC_BYTES of them zeroed before its first
+ * use and left zero by every call that completes (zero them again after device
+ * error 1); calls that can be in flight at the same time need different ones.
+ * Results repeat bit for bit. */
+#define QZ_ATTENTION_SYNC_BYTES 8192
 qz_status qz_attention_paged(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
                              const qz_kv_cache *cache, const qz_seq_batch *seqs, float scale,
                              float softcap, int64_t window, qz_half *out, int64_t o_token,

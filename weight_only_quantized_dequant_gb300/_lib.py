@@ -16,6 +16,7 @@ STATUS = {0: "QZ_OK", 1: "QZ_ERR_INVALID_ARG", 2: "QZ_ERR_ALIGNMENT",
           3: "QZ_ERR_UNSUPPORTED", 4: "QZ_ERR_CUDA", 5: "QZ_ERR_IO", 6: "QZ_ERR_DATA"}
 QZ_MAX_BATCH = 64
 QZ_MAX_GROUP = 4
+QZ_ATTENTION_SYNC_BYTES = 8192
 
 
 class QzError(RuntimeError):

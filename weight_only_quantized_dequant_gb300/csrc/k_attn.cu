@@ -1,8 +1,35 @@
-// Attention of a step's new tokens over the paged cache.
+// Attention of a step's new tokens over the paged cache, on the 5th-generation
+// tensor cores.
 //
-// One warp per (token, query head): every lane holds D / 32 of the query, a
-// key's logit is one warp-wide sum, and the softmax runs with a running
-// maximum and sum (one pass over the keys).
+// For one KV head the queries of a sequence are packed row r = token * G +
+// head-in-group (G = heads / KV heads), so that a decode step still multiplies
+// a matrix and every row of a tile shares its keys:
+//   S = Q K^T,  P = e^{x - m},  O += P V,  out = O / l,
+// with the running maximum m and sum l of every row (one pass over the keys).
+//
+//  * Tiles of 128 rows (a "stage") by blocks of 128 keys.  S (fp32) and O (fp32)
+//    lie in tensor memory; P overwrites S as fp16 and is the next product's A
+//    operand there.  K and V blocks arrive by TMA, page by page, with the
+//    128-byte swizzle the MMA reads; V is the N-major B operand as it lies.
+//  * Two layouts.  NQ = 2: a tile has 256 rows, each of two warpgroups owns 128
+//    of them (one row a thread), and one's softmax runs under the other's MMAs.
+//    NQ = 1: 128 rows, S double-buffered over the key blocks; the two
+//    warpgroups take 64 key columns of every row each and exchange row maxima
+//    through shared memory.  NQ = 1 serves head size 256 (whose O fills half of
+//    tensor memory) and calls whose sequences bring at most 128 rows (decode,
+//    HBM-bound: the padded MMA rows cost nothing there).
+//  * m moves only when it would grow by more than 2^8 (weights then stay below
+//    256, within fp16): O is rescaled a few times per row, not per block.
+//  * Work units are (tile, key block); every CTA (one per SM) takes an even,
+//    contiguous range of all units, found from the lengths on the device, so
+//    ragged batches and single long contexts fill the GPU alike.  A tile cut
+//    between CTAs leaves fp32 partials in the workspace; the last warp to
+//    arrive for its 32 rows merges them in CTA order (results repeat).
+#include <cuda.h>
+
+#include <cstring>
+#include <mutex>
+
 #include "seq_batch.cuh"
 
 namespace qz {
@@ -10,88 +37,957 @@ namespace {
 
 __device__ int g_attn_error = 0;
 
-constexpr int kWarps = 4;
+constexpr int kN = 128;                // keys per block
+constexpr int kSoftmaxWarps = 8;       // two warpgroups
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kMaxCtas = 160;          // grid cap (partial slots in the workspace)
+constexpr int kHead = 4096;            // barriers and exchange rows at the start of shared memory
+constexpr int kMaxStages = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
+constexpr float kLag = 8.0f;           // log2 of how far a weight may exceed 1
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMinUnits = 2;           // key blocks per CTA at least
+
+template <int D, int NQ>
+struct Cfg {
+  static constexpr int kM = 128 * NQ;                  // rows of a tile
+  static constexpr int kStage = kN * D * 2;            // bytes of a K or V block
+  static constexpr int kQ = kM * D * 2;
+  static constexpr int kNS = D == 256 ? 2 : D == 64 ? 8 : NQ == 2 ? 4 : 5;
+  static constexpr int kSmem = kHead + kQ + kNS * kStage + 1024;
+  static constexpr int kNC = NQ == 2 ? 128 : 64;       // key columns per softmax thread
+  static constexpr int kDC = NQ == 2 ? D : D / 2;      // output columns per softmax thread
+  static constexpr int kPart = 32 * (kDC + 2);         // floats of one warp's partial
+};
 
 struct AttnParams {
+  CUtensorMap kmap, vmap;  // [page][head][slot][D], box 64 x min(page, 128) rows
   const __half *q;
   __half *out;
   int64_t q_token, q_head, o_token, o_head;
-  int hq;
-  float scale, softcap;
-  int64_t window;
-  PagedView c;
+  int G;                // query heads per KV head
+  int hkv, n_pages, page_size, page_shift;
+  float c;              // logit units to log2: |scale| log2(e), or log2(e) with a cap
+  float cap, cap_in;    // softcap, and |scale| / softcap * 2 log2(e)
+  uint32_t keep, flip;  // queries are read as (bits & keep) ^ flip: signs turned when scale < 0,
+                        // zeros when scale = 0 (c stays positive: masked logits are -inf)
+  int window;           // 0: none
   SeqView s;
+  unsigned *cnt;        // [kMaxCtas][8] arrivals per cut tile (by its first CTA) and warp
+  float *part;          // [kMaxCtas][2][8] partials
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) attn_warp_kernel(const AttnParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = blockIdx.x;
-  const int g = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int seq = seq_of_token(p.s, t);
-  if (seq < 0 || g >= p.hq) return;
-  const int64_t kv = __ldg(p.s.kv_len + seq);
-  const int64_t pos = kv - __ldg(p.s.cu_q + seq + 1) + t;
-  const int h = g / (p.hq / p.c.hkv);
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __half2float(p.q[t * p.q_token + g * p.q_head + lane + 32 * e]) * p.scale;
-    o[e] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  const int64_t lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
-  for (int64_t j = lo; j <= pos && j < kv; ++j) {
-    const int64_t pi = j >> p.c.page_shift;
-    const int page = pi < p.s.ld_table ? __ldg(p.s.table + seq * p.s.ld_table + pi) : -1;
-    const bool ok = page >= 0 && page < p.c.n_pages;
-    if (!ok && lane == 0) atomicOr(&g_attn_error, 4);
-    const int64_t slot = j & (p.c.page_size - 1);
-    float x = 0.0f, v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float k = ok ? __half2float(p.c.k[page * p.c.k_page + h * p.c.k_head +
-                                              slot * p.c.k_token + lane + 32 * e])
-                         : 0.0f;
-      v[e] = ok ? __half2float(p.c.v[page * p.c.v_page + h * p.c.v_head + slot * p.c.v_token +
-                                     lane + 32 * e])
-                : 0.0f;
-      x = fmaf(q[e], k, x);
+// ------------------------------------------------------------ PTX pieces --
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ unsigned long long gtimer() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Wait for the phase of the given parity; false (and error 1) if it does not
+// complete within kWaitNs or another wait of the CTA gave up.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, int *abort_flag) {
+  const unsigned long long t0 = gtimer();
+  for (;;) {
+    if (mbar_try(bar, parity)) return true;
+    if (*(volatile int *)abort_flag) return false;
+    if (gtimer() - t0 > kWaitNs) {
+      atomicOr(&g_attn_error, 1);
+      *(volatile int *)abort_flag = 1;
+      return false;
     }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    if (p.softcap > 0.0f) x = p.softcap * tanhf(x / p.softcap);
-    const float mn = fmaxf(m, x), c = expf(m - mn), w = expf(x - mn);
-    l = l * c + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + w * v[e];
-    m = mn;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int *abort_flag) {
+  const bool ok = mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+// D (tensor memory) (+)= A (shared) B (shared).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// D (tensor memory) (+)= A (tensor memory) B (shared).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// 32 consecutive 32-bit columns of this thread's lane, without waiting.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f2h(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Shared-memory operand of 128-byte-swizzled rows of 64 fp16 (8-row groups
+// 1024 bytes apart); mn: bytes between 64-column groups of an N-major operand.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t mn) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(mn >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, A = B = f16, D = f32; A K-major, B K-major or N-major.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_n_major) {
+  return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+// --------------------------------------------------------------- schedule --
+// A sequence, and its row tiles per KV head.
+struct Seq {
+  int i, tok0, q, kv;  // index, first token, new tokens, tokens held
+  int rows, nt;        // q * G, row tiles
+};
+
+template <int kM>
+__device__ __forceinline__ Seq load_seq(const AttnParams &p, int i) {
+  Seq s;
+  s.i = i;
+  const int T = (int)p.s.n_tokens;
+  const int a = max(__ldg(p.s.cu_q + i), 0), b = min(__ldg(p.s.cu_q + i + 1), T);
+  s.tok0 = a;
+  s.q = max(b - a, 0);
+  s.kv = max(__ldg(p.s.kv_len + i), 0);
+  s.rows = s.q * p.G;
+  s.nt = (s.rows + kM - 1) / kM;
+  return s;
+}
+
+// Keys [lo, hi) that any row of row tile rt sees, and the blocks that hold them.
+struct Range {
+  int lo, hi, b0, nb;
+};
+template <int kM>
+__device__ __forceinline__ Range tile_range(const AttnParams &p, const Seq &s, int rt) {
+  Range r;
+  const int first = s.kv - s.q;  // position of the first new token
+  const int last = min((rt + 1) * kM, s.rows) - 1;
+  r.hi = max(first + last / p.G + 1, 0);
+  r.lo = 0;
+  if (p.window > 0) r.lo = max(first + rt * kM / p.G - p.window + 1, 0);
+  r.b0 = r.lo / kN;
+  r.nb = r.hi > r.lo ? (r.hi + kN - 1) / kN - r.b0 : 0;
+  return r;
+}
+
+// Units (key blocks, at least one a tile) of one KV head of a sequence.
+template <int kM>
+__device__ __forceinline__ int64_t head_units(const AttnParams &p, const Seq &s) {
+  int64_t n = 0;
+  for (int rt = 0; rt < s.nt; ++rt) n += max(tile_range<kM>(p, s, rt).nb, 1);
+  return n;
+}
+
+// What one CTA does of one tile.
+struct Seg {
+  Seq s;
+  int head, rt, rows;    // KV head, row tile, its rows
+  Range r;
+  int b0, b1;            // its key blocks [b0, b1); none if the tile sees no key
+  bool whole;
+  int slot;              // partial slot if cut
+  int64_t first;         // the tile's first unit
+  int units;
+};
+
+// Walks a CTA's unit range tile by tile; every warp keeps its own.
+template <int kM>
+struct Walker {
+  int64_t u, u_end, u_begin, first;  // next unit, range, first unit of the current tile
+  Seq s;
+  int head, rt;
+  __device__ __forceinline__ bool next(const AttnParams &p, Seg &g) {
+    if (u >= u_end) return false;
+    while (true) {  // tiles of sequences without new tokens do not exist
+      if (rt < s.nt) break;
+      rt = 0;
+      if (s.nt == 0 || ++head == p.hkv) {
+        head = 0;
+        s = load_seq<kM>(p, s.i + 1);
+      }
+    }
+    g.s = s;
+    g.head = head;
+    g.rt = rt;
+    g.rows = min(s.rows - rt * kM, kM);
+    g.r = tile_range<kM>(p, s, rt);
+    g.units = max(g.r.nb, 1);
+    g.first = first;
+    const int a = (int)(u - first);
+    const int b = (int)min(u_end - first, (int64_t)g.units);
+    g.b0 = g.r.b0 + a;
+    g.b1 = g.r.nb == 0 ? g.b0 : g.r.b0 + b;
+    g.whole = a == 0 && b == g.units;
+    g.slot = u == u_begin ? 0 : 1;
+    u = first + b;
+    if (b == g.units) {
+      first += g.units;
+      ++rt;
+    }
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- kernel --
+template <int D, int NQ, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<D, NQ>;
+  constexpr int kM = C::kM, NS = C::kNS, NC = C::kNC, DC = C::kDC;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(base);
+  uint64_t *kv_full = bars, *kv_empty = bars + kMaxStages;
+  uint64_t *s_full = kv_empty + kMaxStages, *p_full = s_full + 2, *o_done = p_full + 2;
+  uint64_t *q_full = o_done + 2, *xbar = q_full + 1;  // xbar: one per 32-row quarter
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xbar + 4);
+  int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+  int64_t *scan = reinterpret_cast<int64_t *>(base + 512);   // [12] warp sums, then the start
+  float *xch = reinterpret_cast<float *>(base + 1024);       // [2][8 warps][32]
+  uint8_t *q_sm = base + kHead, *kv_sm = q_sm + C::kQ;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&kv_full[i]), 1);
+      mbar_init(smem_u32(&kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), NQ == 2 ? 4 : 8);
+      mbar_init(smem_u32(&o_done[i]), 1);
+    }
+    mbar_init(smem_u32(q_full), kSoftmaxWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&xbar[i]), 2);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+
+  // Units of all sequences, then the sequence that holds this CTA's first one:
+  // kThreads sequences at a time, one a thread.
+  int64_t mine = 0, total = 0;
+  for (int i = tid; i < p.s.n_seqs; i += kThreads)
+    mine += (int64_t)p.hkv * head_units<kM>(p, load_seq<kM>(p, i));
+  {
+    int64_t v = mine;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.out[t * p.o_token + g * p.o_head + lane + 32 * e] = __float2half_rn(o[e] * inv);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) scan[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) total += scan[w];
+  }
+  int ctas = (int)min((int64_t)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
+  if ((int)blockIdx.x >= ctas) return;
+  Walker<kM> start;
+  start.u_begin = start.u = total * blockIdx.x / ctas;
+  start.u_end = total * (blockIdx.x + 1) / ctas;
+  {
+    int64_t before = 0;
+    for (int i0 = 0; i0 < p.s.n_seqs; i0 += kThreads) {
+      const int i = i0 + tid;
+      const int64_t n =
+          i >= p.s.n_seqs ? 0
+          : p.s.n_seqs <= kThreads ? mine : (int64_t)p.hkv * head_units<kM>(p, load_seq<kM>(p, i));
+      int64_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      int64_t off = before, sum = before;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) off += scan[w];
+        sum += scan[w];
+      }
+      if (n > 0 && start.u >= off + incl - n && start.u < off + incl) {
+        scan[10] = i;
+        scan[11] = off + incl - n;
+      }
+      before = sum;
+      if (before > start.u) break;
+    }
+    __syncthreads();
+    start.s = load_seq<kM>(p, (int)scan[10]);
+    start.first = scan[11];
+    const int64_t per = head_units<kM>(p, start.s);
+    start.head = (int)((start.u - start.first) / per);
+    start.first += start.head * per;
+    start.rt = 0;
+    for (;;) {
+      const int n = max(tile_range<kM>(p, start.s, start.rt).nb, 1);
+      if (start.u < start.first + n) break;
+      start.first += n;
+      ++start.rt;
+    }
+  }
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;  // S of stage or buffer i at 128 i, O at 256 (+ D for stage 1)
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------ softmax --
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int my_row = (NQ == 2 ? wg * 128 : 0) + quarter * 32 + lane;  // of the tile
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const int col0 = NQ == 2 ? 0 : wg * NC;    // first key column of this thread
+    const int out0 = NQ == 2 ? 0 : wg * DC;    // first output column
+    const uint32_t o_tm = tmem + lane_base + 256 + (NQ == 2 ? wg * D : out0);
+    uint32_t blocks = 0;   // key blocks so far (NQ = 2: of this stage)
+    uint32_t ends = 0;     // segments finished (NQ = 2: of this stage)
+    uint32_t swaps = 0;    // exchanges with the other warpgroup
+    uint32_t segs = 0;     // segments with keys so far
+    bool ok = true;
+    // The other warpgroup's value of this row (NQ = 1).
+    auto exchange = [&](float v, float *other) -> bool {
+      float *x = xch + (swaps & 1) * 256;
+      x[warp * 32 + lane] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&xbar[quarter]));
+      if (!mbar_wait(smem_u32(&xbar[quarter]), swaps & 1, abort_flag)) return false;
+      *other = x[(warp ^ 4) * 32 + lane];
+      ++swaps;
+      return true;
+    };
+    Walker<kM> w = start;
+    Seg g;
+    while (ok && w.next(p, g)) {
+      const int warp_row = my_row - lane;
+      const int live_rows = min(max(g.rows - warp_row, 0), 32);  // of this warp
+      const int row = g.rt * kM + my_row;                        // of the sequence
+      const int first = g.s.kv - g.s.q;
+      // rows past the tile's end repeat its last row's limits
+      const int pos = first + min(row, g.rt * kM + g.rows - 1) / p.G;
+      const int hi = pos + 1, lo = p.window > 0 ? pos - p.window + 1 : 0;
+      float m = -INFINITY, l = 0.0f;
+      const int nb = g.b1 - g.b0;
+      const bool active = nb > 0 && (NQ == 1 || wg == 0 || g.rows > 128);
+      if (nb > 0) {
+        // ---- queries into shared memory, swizzled like a TMA tile
+        constexpr int CPR = D / 8;  // 16-byte chunks per row
+        constexpr int RPP = 32 / CPR > 0 ? 32 / CPR : 1;
+        if (active) {
+          // a warp fills rows [qrow0, qrow0 + QR) of the tile
+          constexpr int QR = NQ == 2 ? 32 : 16;
+          const int qrow0 = NQ == 2 ? warp * 32 : warp * 16;
+#pragma unroll 4
+          for (int k = 0; k < QR / RPP; ++k) {
+            const int r = qrow0 + k * RPP + lane / CPR, c = lane % CPR;
+            const int rr = g.rt * kM + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < g.rows) {
+              const int tok = rr / p.G, hd = g.head * p.G + rr - tok * p.G;
+              v = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(g.s.tok0 + tok) * p.q_token +
+                                                        hd * p.q_head) + c);
+              v.x = (v.x & p.keep) ^ p.flip;
+              v.y = (v.y & p.keep) ^ p.flip;
+              v.z = (v.z & p.keep) ^ p.flip;
+              v.w = (v.w & p.keep) ^ p.flip;
+            }
+            *reinterpret_cast<uint4 *>(q_sm + (r >> 7) * (128 * D * 2) + (c >> 3) * 16384 +
+                                       (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(q_full));
+        // a warpgroup without rows must not arrive for the next tile before this one's
+        if (!active && !(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
+        ++segs;
+      }
+      for (int b = g.b0; active && b < g.b1; ++b, ++blocks) {
+        const int buf = NQ == 2 ? wg : (int)(blocks & 1);
+        const uint32_t ph = NQ == 2 ? blocks & 1 : (blocks >> 1) & 1;
+        if (!(ok = mbar_wait(smem_u32(&s_full[buf]), ph, abort_flag))) break;
+        if (live_rows == 0) {  // nothing of this warp is stored
+          if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+          continue;
+        }
+        fence_after();
+        const uint32_t s_tm = tmem + lane_base + 128 * buf;
+        float s[NC];
+#pragma unroll
+        for (int k = 0; k < NC / 32; ++k)
+          tmem_ld32(s_tm + col0 + 32 * k, reinterpret_cast<uint32_t *>(s) + 32 * k);
+        tmem_ld_wait();
+        if (CAP) {
+#pragma unroll
+          for (int k = 0; k < NC; ++k)  // cap tanh(t), tanh(t) = 1 - 2 / (1 + e^2t)
+            s[k] = p.cap * (1.0f - 2.0f * rcp(1.0f + ex2(s[k] * p.cap_in)));
+        }
+        const int k_hi = hi - b * kN - col0, k_lo = lo - b * kN - col0;
+        if (__any_sync(0xffffffffu, k_hi < NC || k_lo > 0)) {
+#pragma unroll
+          for (int k = 0; k < NC; ++k)
+            if (k >= k_hi || k < k_lo) s[k] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int k = 4; k < NC; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+        float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (NQ == 1) {
+          float other;
+          if (!(ok = exchange(mb, &other))) break;
+          mb = fmaxf(mb, other);
+        }
+        // move the maximum where it lags too far, and rescale what was summed
+        const bool move = (mb - m) * p.c > kLag || (m == -INFINITY && mb > -INFINITY);
+        if (__any_sync(0xffffffffu, move)) {
+          const float mn = move ? mb : m;
+          const float f = m == -INFINITY ? (move ? 0.0f : 1.0f) : ex2((m - mn) * p.c);
+          m = mn;
+          l *= f;
+          if (b > g.b0) {
+            // NQ = 2: this stage's earlier products precede the S just read
+            if (NQ == 1 &&
+                !(ok = mbar_wait(smem_u32(&o_done[0]), (blocks - 1) & 1, abort_flag)))
+              break;
+            fence_after();
+#pragma unroll 1
+            for (int k = 0; k < DC; k += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_tm + k, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_tm + k, o);
+            }
+          }
+        }
+        const float mc = m == -INFINITY ? 0.0f : m * p.c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < NC / 64; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float a = ex2(fmaf(s[64 * h + 2 * k], p.c, -mc));
+            const float e = ex2(fmaf(s[64 * h + 2 * k + 1], p.c, -mc));
+            sum[(2 * k) & 3] += a;
+            sum[(2 * k + 1) & 3] += e;
+            pk[k] = f2h(a, e);
+          }
+          tmem_st32(s_tm + col0 / 2 + 32 * h, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+      }
+      if (!ok) break;
+      // ---- the tile's rows, or this CTA's part of them
+      if (active) {
+        const uint32_t ph = NQ == 2 ? ends & 1 : (blocks - 1) & 1;
+        // NQ = 1: the last S only proves the product two blocks back complete,
+        // and a wait tells phases apart by parity alone
+        if (NQ == 1 && nb > 1 && !(ok = mbar_wait(smem_u32(&o_done[0]), ph ^ 1, abort_flag))) break;
+        if (!(ok = mbar_wait(smem_u32(&o_done[NQ == 2 ? wg : 0]), ph, abort_flag))) break;
+        ++ends;
+        fence_after();
+        if (NQ == 1 && live_rows > 0) {
+          float other;
+          if (!(ok = exchange(l, &other))) break;
+          l = wg == 0 ? l + other : other + l;
+        }
+      }
+      if (live_rows == 0) continue;
+      const int tok = row / p.G, hd = g.head * p.G + row - tok * p.G;
+      if (g.whole) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(g.s.tok0 + tok) * p.o_token +
+                                               (int64_t)hd * p.o_head + out0);
+#pragma unroll 1
+        for (int k = 0; k < DC; k += 32) {
+          uint32_t o[32];
+          if (active) {
+            tmem_ld32(o_tm + k, o);
+            tmem_ld_wait();
+          }
+          if (lane < live_rows) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                v[i] = active ? f2h(__uint_as_float(o[8 * e + 2 * i]) * inv,
+                                    __uint_as_float(o[8 * e + 2 * i + 1]) * inv)
+                              : 0u;
+              dst[k / 8 + e] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+        continue;
+      }
+      // ---- cut between CTAs: leave the partial, merge if last
+      auto part_of = [&](int cta, int slot) {
+        return p.part + (int64_t)((cta * 2 + slot) * kSoftmaxWarps + warp) * C::kPart;
+      };
+      float *mine_part = part_of(blockIdx.x, g.slot);
+      mine_part[lane] = l > 0.0f ? (m == -INFINITY ? 0.0f : m * p.c) : -INFINITY;
+      mine_part[32 + lane] = l;
+#pragma unroll 1
+      for (int k = 0; k < DC; k += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_tm + k, o);
+        tmem_ld_wait();
+        if (lane < live_rows) {
+          uint4 *dst = reinterpret_cast<uint4 *>(mine_part + 64 + lane * DC + k);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / total); };
+      const int c_lo = owner(g.first), c_hi = owner(g.first + g.units - 1);
+      __threadfence();
+      __syncwarp();
+      unsigned arrived = 0;
+      if (lane == 0) arrived = atomicAdd(&p.cnt[c_lo * kSoftmaxWarps + warp], 1u);
+      arrived = __shfl_sync(0xffffffffu, arrived, 0);
+      if ((int)arrived != c_hi - c_lo) continue;
+      __threadfence();
+      auto part_at = [&](int c) {
+        return part_of(c, total * c / ctas >= g.first ? 0 : 1);
+      };
+      float M = -INFINITY, L = 0.0f;
+      for (int c = c_lo; c <= c_hi; ++c) M = fmaxf(M, __ldcg(part_at(c) + lane));
+      const float Mz = M == -INFINITY ? 0.0f : M;
+      for (int c = c_lo; c <= c_hi; ++c) {
+        const float *pp = part_at(c);
+        L += __ldcg(pp + 32 + lane) * ex2(__ldcg(pp + lane) - Mz);
+      }
+      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      // lanes share the rows' float4 columns
+      constexpr int F4 = DC / 4;
+      const int items = live_rows * F4;
+      for (int i0 = 0; i0 < items; i0 += 128) {
+        float4 acc[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = c_lo; c <= c_hi; ++c) {
+          const float *pp = part_at(c);
+          const float wgt = ex2(__ldcg(pp + lane) - Mz);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int it = i0 + e * 32 + lane;
+            const float f = __shfl_sync(0xffffffffu, wgt, min(it / F4, 31));
+            if (it < items) {
+              const float4 v = __ldcg(reinterpret_cast<const float4 *>(pp + 64) + it);
+              acc[e].x = fmaf(v.x, f, acc[e].x);
+              acc[e].y = fmaf(v.y, f, acc[e].y);
+              acc[e].z = fmaf(v.z, f, acc[e].z);
+              acc[e].w = fmaf(v.w, f, acc[e].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int it = i0 + e * 32 + lane;
+          const float f = __shfl_sync(0xffffffffu, inv, min(it / F4, 31));
+          if (it < items) {
+            const int rr = g.rt * kM + warp_row + it / F4;
+            const int tk = rr / p.G, h2 = g.head * p.G + rr - tk * p.G;
+            *reinterpret_cast<uint2 *>(p.out + (int64_t)(g.s.tok0 + tk) * p.o_token +
+                                       (int64_t)h2 * p.o_head + out0 + it % F4 * 4) =
+                make_uint2(f2h(acc[e].x * f, acc[e].y * f), f2h(acc[e].z * f, acc[e].w * f));
+          }
+        }
+      }
+      if (lane == 0) p.cnt[c_lo * kSoftmaxWarps + warp] = 0;
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- MMA --
+    constexpr uint32_t id_qk = idesc(128, kN, false), id_pv = idesc(128, D, true);
+    uint32_t ring = 0, blocks = 0, segs = 0, n_stage[2] = {0, 0};
+    bool ok = true;
+    auto slot_addr = [&](uint32_t r) { return smem_u32(kv_sm) + (r % NS) * C::kStage; };
+    auto wait_slot = [&](uint32_t r) {
+      return mbar_wait(smem_u32(&kv_full[r % NS]), (r / NS) & 1, abort_flag);
+    };
+    auto release = [&](uint32_t r) { mma_commit(smem_u32(&kv_empty[r % NS])); };
+    auto qk = [&](int stage, int buf, uint32_t r) {  // lane 0
+      const uint64_t a = sdesc(smem_u32(q_sm) + stage * (128 * D * 2), 16);
+      const uint64_t b = sdesc(slot_addr(r), 16);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {  // 32 bytes of a row, 16 KB per 64 columns
+        const uint32_t o = (k & 3) * 2 + (k >> 2) * 1024;
+        mma_ss(tmem + 128 * buf, a + o, b + o, id_qk, k > 0);
+      }
+      mma_commit(smem_u32(&s_full[buf]));
+    };
+    auto pv = [&](int buf, uint32_t o_col, uint32_t r, bool acc) {  // lane 0
+      const uint64_t b = sdesc(slot_addr(r), 16384);
+#pragma unroll
+      for (int k = 0; k < kN / 16; ++k)  // 16 rows of 128 bytes
+        mma_ts(tmem + o_col, tmem + 128 * buf + 8 * k, b + k * 128, id_pv, acc || k > 0);
+    };
+    // Rows of a V block that no query of the tile sees may hold anything, and
+    // a zero weight times NaN is NaN: they become zeros.
+    auto clean = [&](uint32_t r, int b, const Range &t) {
+      const int lo = t.lo - b * kN, hi = t.hi - b * kN;
+      if (lo <= 0 && hi >= kN) return;
+      uint8_t *v = kv_sm + (r % NS) * C::kStage;
+      for (int i = lane; i < kN * D / 8; i += 32) {  // 16-byte chunks; 8 per row and 64 columns
+        const int row = (i >> 3) & (kN - 1);
+        if (row < lo || row >= hi) reinterpret_cast<uint4 *>(v)[i] = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+      __syncwarp();
+    };
+    Walker<kM> w = start;
+    Seg g;
+    while (ok && w.next(p, g)) {
+      const int nb = g.b1 - g.b0;
+      if (nb == 0) continue;
+      if (!(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
+      ++segs;
+      fence_after();
+      if (NQ == 1) {
+        for (int j = 0; j <= nb; ++j) {
+          if (j < nb) {
+            if (!(ok = wait_slot(ring))) break;
+            if (lane == 0) {
+              qk(0, (blocks + j) & 1, ring);
+              release(ring);
+            }
+            ++ring;
+          }
+          if (j > 0) {
+            const uint32_t c = blocks + j - 1;
+            if (!(ok = wait_slot(ring))) break;
+            clean(ring, g.b0 + j - 1, g.r);
+            if (!(ok = mbar_wait(smem_u32(&p_full[c & 1]), (c >> 1) & 1, abort_flag))) break;
+            fence_after();
+            if (lane == 0) {
+              pv(c & 1, 256, ring, j > 1);
+              release(ring);
+              mma_commit(smem_u32(&o_done[0]));
+            }
+            ++ring;
+          }
+          __syncwarp();
+        }
+        blocks += nb;
+      } else {
+        const int stages = g.rows > 128 ? 2 : 1;
+        if (!(ok = wait_slot(ring))) break;
+        if (lane == 0) {
+          for (int t = 0; t < stages; ++t) qk(t, t, ring);
+          release(ring);
+        }
+        ++ring;
+        for (int j = 0; j < nb; ++j) {
+          const uint32_t v = ring, kn = ring + 1;
+          const bool more = j + 1 < nb;
+          if (!(ok = wait_slot(v))) break;
+          clean(v, g.b0 + j, g.r);
+          for (int t = 0; t < stages; ++t) {
+            if (!(ok = mbar_wait(smem_u32(&p_full[t]), n_stage[t] & 1, abort_flag))) break;
+            ++n_stage[t];
+            fence_after();
+            if (lane == 0) {
+              pv(t, 256 + t * D, v, j > 0);
+              if (t == stages - 1) release(v);
+              if (!more) mma_commit(smem_u32(&o_done[t]));
+            }
+            if (more) {
+              if (t == 0 && !(ok = wait_slot(kn))) break;
+              if (lane == 0) {
+                qk(t, t, kn);
+                if (t == stages - 1) release(kn);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          ring += more ? 2 : 1;
+        }
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- load --
+    uint32_t ring = 0;
+    bool ok = true;
+    const int ppb = p.page_size >= kN ? 1 : kN >> p.page_shift;  // pages per block
+    const int box_rows = min(p.page_size, kN);
+    // Lane i's page of block b (-1: none of its slots is needed).
+    auto page_of = [&](const Seg &g, int b) -> int {
+      const int key = b * kN + lane * box_rows;
+      if (lane >= ppb || key >= g.r.hi || key + box_rows <= g.r.lo) return -1;
+      const int64_t pi = key >> p.page_shift;
+      const int page = pi < p.s.ld_table ? __ldg(p.s.table + (int64_t)g.s.i * p.s.ld_table + pi)
+                                         : -1;
+      if (page < 0 || page >= p.n_pages) {
+        atomicOr(&g_attn_error, 4);
+        return INT32_MAX;  // outside the map: the copy fills zeros
+      }
+      return page;
+    };
+    auto issue = [&](const CUtensorMap *map, const Seg &g, int b, int page) -> bool {
+      const int slot = ring % NS;
+      if (ring >= NS &&
+          !mbar_wait(smem_u32(&kv_empty[slot]), (ring / NS - 1) & 1, abort_flag))
+        return false;
+      const uint32_t bar = smem_u32(&kv_full[slot]);
+      const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0)
+        asm volatile(
+            "{\n\t.reg .b64 t;\n\t"
+            "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(bar),
+            "r"((uint32_t)(__popc(live) * box_rows * D * 2))
+            : "memory");
+      __syncwarp();
+      if (page >= 0) {
+        const int at = p.page_size > kN ? (b * kN) & (p.page_size - 1) : 0;
+        const uint32_t dst = smem_u32(kv_sm) + slot * C::kStage + lane * box_rows * 128;
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d)
+          asm volatile(
+              "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+              "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + d * 16384),
+              "l"(reinterpret_cast<uint64_t>(map)), "r"(d * 64), "r"(at), "r"(g.head), "r"(page),
+              "r"(bar)
+              : "memory");
+      }
+      __syncwarp();
+      ++ring;
+      return true;
+    };
+    Walker<kM> w = start;
+    Seg g;
+    while (ok && w.next(p, g)) {
+      const int nb = g.b1 - g.b0;
+      int page = nb > 0 ? page_of(g, g.b0) : -1, prev = -1;
+      for (int j = 0; ok && j < nb; ++j) {
+        const int b = g.b0 + j;
+        const int ahead = j + 1 < nb ? page_of(g, b + 1) : -1;
+        ok = issue(&p.kmap, g, b, page);
+        if (NQ == 1) {  // K0, K1, V0, K2, V1, ..., the order in which they are used
+          if (ok && j > 0) ok = issue(&p.vmap, g, b - 1, prev);
+          if (ok && j == nb - 1) ok = issue(&p.vmap, g, b, page);
+        } else if (ok) {
+          ok = issue(&p.vmap, g, b, page);
+        }
+        prev = page;
+        page = ahead;
+      }
+    }
+    if (!ok) {  // let the copies in flight land before the CTA's memory goes
+      const uint32_t n = ring < NS ? ring : NS;
+      for (uint32_t r = ring - n; r < ring; ++r) {
+        const unsigned long long t0 = gtimer();
+        while (!mbar_try(smem_u32(&kv_full[r % NS]), (r / NS) & 1))
+          if (gtimer() - t0 > kWaitNs) break;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point.
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// The pool as [page][head][slot][64-column group of D], boxes of one page's
+// (at most 128) slots by 64 columns.
+qz_status pool_map(CUtensorMap *map, const __half *base, const PagedView &c, int64_t token,
+                   int64_t head, int64_t page) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return QZ_ERR_CUDA;
+  // a dimension of one element has no stride of its own
+  if (c.hkv == 1) head = token;
+  if (c.n_pages == 1) page = token;
+  const cuuint64_t dim[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.hkv,
+                             (cuuint64_t)c.n_pages};
+  const cuuint64_t stride[3] = {(cuuint64_t)token * 2, (cuuint64_t)head * 2, (cuuint64_t)page * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(c.page_size < kN ? c.page_size : kN), 1, 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<__half *>(base), dim, stride, box,
+         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? QZ_OK : QZ_ERR_UNSUPPORTED;
+}
+
+template <int D, int NQ, bool CAP>
+qz_status launch(const AttnParams &p, int sms, cudaStream_t s) {
+  using C = Cfg<D, NQ>;
+  const cudaError_t e = cudaFuncSetAttribute(
+      attn_kernel<D, NQ, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return cuda_status(e);
+  attn_kernel<D, NQ, CAP><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, C::kSmem, s>>>(p);
+  return launch_status();
+}
+
+template <int D, int NQ>
+qz_status launch_cap(const AttnParams &p, int sms, cudaStream_t s) {
+  return p.cap > 0.0f ? launch<D, NQ, true>(p, sms, s) : launch<D, NQ, false>(p, sms, s);
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 16; }
+size_t attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t D) {
+  const int64_t part = 32 * ((D == 256 ? 128 : D) + 2);  // the larger of the two layouts
+  return QZ_ATTENTION_SYNC_BYTES + (size_t)kMaxCtas * 2 * kSoftmaxWarps * part * sizeof(float);
+}
+static_assert(kMaxCtas * kSoftmaxWarps * sizeof(unsigned) <= QZ_ATTENTION_SYNC_BYTES, "counters");
 
 qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
                            const PagedView &c, const SeqView &sv, float scale, float softcap,
-                           int64_t window, __half *out, int64_t o_token, int64_t o_head, void *,
-                           cudaStream_t s) {
-  const AttnParams p = {q,     out,     q_token, q_head, o_token, o_head, (int)hq,
-                        scale, softcap, window,  c,      sv};
-  const dim3 grid((unsigned)sv.n_tokens, (unsigned)((hq + kWarps - 1) / kWarps));
-  if (c.D == 64)
-    attn_warp_kernel<64><<<grid, 32 * kWarps, 0, s>>>(p);
-  else if (c.D == 128)
-    attn_warp_kernel<128><<<grid, 32 * kWarps, 0, s>>>(p);
-  else
-    attn_warp_kernel<256><<<grid, 32 * kWarps, 0, s>>>(p);
-  return launch_status();
+                           int64_t window, __half *out, int64_t o_token, int64_t o_head,
+                           void *workspace, cudaStream_t s) {
+  DeviceInfo di;
+  qz_status st = device_info(&di);
+  if (st != QZ_OK) return st;
+  AttnParams p;
+  memset(&p, 0, sizeof(p));
+  st = pool_map(&p.kmap, c.k, c, c.k_token, c.k_head, c.k_page);
+  if (st == QZ_OK) st = pool_map(&p.vmap, c.v, c, c.v_token, c.v_head, c.v_page);
+  if (st != QZ_OK) return st;
+  p.q = q;
+  p.out = out;
+  p.q_token = q_token;
+  p.q_head = q_head;
+  p.o_token = o_token;
+  p.o_head = o_head;
+  p.G = (int)(hq / c.hkv);
+  p.hkv = c.hkv;
+  p.n_pages = c.n_pages;
+  p.page_size = c.page_size;
+  p.page_shift = c.page_shift;
+  const float mag = scale == 0.0f ? 1.0f : fabsf(scale);
+  p.keep = scale == 0.0f ? 0u : ~0u;
+  p.flip = scale < 0.0f ? 0x80008000u : 0u;
+  p.c = (softcap > 0.0f ? 1.0f : mag) * kLog2e;
+  p.cap = softcap;
+  p.cap_in = softcap > 0.0f ? mag / softcap * 2.0f * kLog2e : 0.0f;
+  p.window = window > INT32_MAX ? 0 : (int)window;
+  p.s = sv;
+  p.cnt = static_cast<unsigned *>(workspace);
+  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + QZ_ATTENTION_SYNC_BYTES);
+  // Two stages of rows pay once a sequence fills the second one.
+  const bool two = sv.n_tokens * p.G > (int64_t)128 * sv.n_seqs;
+  if (c.D == 256) return launch_cap<256, 1>(p, di.sms, s);
+  if (c.D == 128) return two ? launch_cap<128, 2>(p, di.sms, s) : launch_cap<128, 1>(p, di.sms, s);
+  return two ? launch_cap<64, 2>(p, di.sms, s) : launch_cap<64, 1>(p, di.sms, s);
 }
 
 qz_status read_attn_error(int *code, int clear) {

@@ -698,7 +698,7 @@ qz_status qz_attention_paged(const qz_half *q, int64_t n_heads, int64_t q_token,
   if (n_heads < 1 || n_heads % c.hkv || window < 0 || !(softcap >= 0.0f) ||
       !(scale - scale == 0.0f) || !(softcap - softcap == 0.0f))
     return QZ_ERR_INVALID_ARG;
-  if (n_heads > 65536) return QZ_ERR_UNSUPPORTED;
+  if (n_heads > 65536 || b.n_tokens * n_heads > INT32_MAX) return QZ_ERR_UNSUPPORTED;
   if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
   QZ_TRY(check_rows16(q, q_token, q_head));
   QZ_TRY(check_rows16(out, o_token, o_head));

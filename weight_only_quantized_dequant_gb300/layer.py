@@ -32,13 +32,6 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _zeros(nbytes: int, device, stream) -> torch.Tensor:
-    if stream is None:
-        return torch.zeros((nbytes,), dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.zeros((nbytes,), dtype=torch.uint8, device=device)
-
-
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -247,12 +240,16 @@ def rope_table(positions: int, head_dim: int, theta: float = 10000.0,
 
 def attention_workspace(n_tokens: int, n_seqs: int, n_heads: int, n_kv_heads: int,
                         head_dim: int, device="cuda", stream=None) -> torch.Tensor:
-    """A ready (zeroed) workspace for attention_paged calls of up to that many
-    tokens and sequences; calls that may overlap on the GPU need one each."""
+    """A ready workspace (its counters zeroed) for attention_paged calls of up
+    to that many tokens and sequences; calls that may overlap on the GPU need
+    one each."""
     nbytes = int(_lib.load().qz_attention_workspace_bytes(n_tokens, n_seqs, n_heads, n_kv_heads,
                                                           head_dim))
     _need(nbytes > 0, "attention_workspace: invalid sizes")
-    return _zeros(nbytes, device, stream)
+    ws = _empty((nbytes,), torch.uint8, device, stream)
+    with torch.cuda.stream(stream):
+        ws[:_lib.QZ_ATTENTION_SYNC_BYTES].zero_()
+    return ws
 
 
 def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: float | None = None,
@@ -262,7 +259,7 @@ def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: floa
     already holds their keys and values (``rope_append``).  scale defaults to
     D^-0.5; softcap > 0 caps logits as softcap * tanh(x / softcap); window > 0
     limits every query to its last `window` keys.  workspace: from
-    ``attention_workspace`` (allocated and zeroed here if None)."""
+    ``attention_workspace`` (made here if None)."""
     T, D = q.shape[0], cache.head_dim
     _heads(q, "q", T, None, D)
     if q.shape[1] < 1 or q.shape[1] % cache.n_kv_heads:
