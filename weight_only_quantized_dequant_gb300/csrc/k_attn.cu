@@ -40,7 +40,9 @@ __device__ int g_attn_error = 0;
 constexpr int kN = 128;                // keys per block
 constexpr int kSoftmaxWarps = 8;       // two warpgroups
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;          // the third warpgroup: MMA, loads, two spare warps
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
+static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "register split");
 constexpr int kMaxCtas = 160;          // grid cap (partial slots in the workspace)
 constexpr int kHead = 4096;            // barriers and exchange rows at the start of shared memory
 constexpr int kMaxStages = 8;
@@ -101,7 +103,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 // Wait for the phase of the given parity; false (and error 1) if it does not
 // complete within kWaitNs or another wait of the CTA gave up.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, int *abort_flag) {
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, int *abort_flag) {
   const unsigned long long t0 = gtimer();
   for (;;) {
     if (mbar_try(bar, parity)) return true;
@@ -139,6 +141,14 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // D (tensor memory) (+)= A (shared) B (shared).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -186,6 +196,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
       "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -198,6 +217,28 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations per instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ uint32_t f2h(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -269,39 +310,37 @@ struct Seg {
   int b0, b1;            // its key blocks [b0, b1); none if the tile sees no key
   bool whole;
   int slot;              // partial slot if cut
-  int64_t first;         // the tile's first unit
+  int first;             // the tile's first unit, relative to the CTA's
   int units;
 };
 
-// Walks a CTA's unit range tile by tile; every warp keeps its own.
+// Walks a CTA's unit range tile by tile; every warp keeps its own.  Units are
+// counted from the CTA's first.
 template <int kM>
 struct Walker {
-  int64_t u, u_end, u_begin, first;  // next unit, range, first unit of the current tile
-  Seq s;
-  int head, rt;
+  int u, u_end, first;  // next unit, end, first unit of the current tile
+  int seq, head, rt;
   __device__ __forceinline__ bool next(const AttnParams &p, Seg &g) {
     if (u >= u_end) return false;
-    while (true) {  // tiles of sequences without new tokens do not exist
-      if (rt < s.nt) break;
+    g.s = load_seq<kM>(p, seq);
+    while (rt >= g.s.nt) {  // sequences without new tokens have no tiles
       rt = 0;
-      if (s.nt == 0 || ++head == p.hkv) {
+      if (g.s.nt == 0 || ++head == p.hkv) {
         head = 0;
-        s = load_seq<kM>(p, s.i + 1);
+        g.s = load_seq<kM>(p, ++seq);
       }
     }
-    g.s = s;
     g.head = head;
     g.rt = rt;
-    g.rows = min(s.rows - rt * kM, kM);
-    g.r = tile_range<kM>(p, s, rt);
+    g.rows = min(g.s.rows - rt * kM, kM);
+    g.r = tile_range<kM>(p, g.s, rt);
     g.units = max(g.r.nb, 1);
     g.first = first;
-    const int a = (int)(u - first);
-    const int b = (int)min(u_end - first, (int64_t)g.units);
+    const int a = u - first, b = min(u_end - first, g.units);
     g.b0 = g.r.b0 + a;
     g.b1 = g.r.nb == 0 ? g.b0 : g.r.b0 + b;
     g.whole = a == 0 && b == g.units;
-    g.slot = u == u_begin ? 0 : 1;
+    g.slot = u == 0 ? 0 : 1;
     u = first + b;
     if (b == g.units) {
       first += g.units;
@@ -363,9 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   int ctas = (int)min((int64_t)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
   if ((int)blockIdx.x >= ctas) return;
+  const int64_t u_begin = total * blockIdx.x / ctas;
   Walker<kM> start;
-  start.u_begin = start.u = total * blockIdx.x / ctas;
-  start.u_end = total * (blockIdx.x + 1) / ctas;
+  start.u = 0;
+  start.u_end = (int)(total * (blockIdx.x + 1) / ctas - u_begin);
   {
     int64_t before = 0;
     for (int i0 = 0; i0 < p.s.n_seqs; i0 += kThreads) {
@@ -387,25 +427,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w < warp) off += scan[w];
         sum += scan[w];
       }
-      if (n > 0 && start.u >= off + incl - n && start.u < off + incl) {
-        scan[10] = i;
-        scan[11] = off + incl - n;
+      if (n > 0 && u_begin >= off + incl - n && u_begin < off + incl) {
+        scan[12] = i;
+        scan[13] = off + incl - n;
       }
       before = sum;
-      if (before > start.u) break;
+      if (before > u_begin) break;
     }
     __syncthreads();
-    start.s = load_seq<kM>(p, (int)scan[10]);
-    start.first = scan[11];
-    const int64_t per = head_units<kM>(p, start.s);
-    start.head = (int)((start.u - start.first) / per);
-    start.first += start.head * per;
+    start.seq = (int)scan[12];
+    const Seq q = load_seq<kM>(p, start.seq);
+    int64_t first = scan[13];
+    const int64_t per = head_units<kM>(p, q);
+    start.head = (int)((u_begin - first) / per);
+    first += start.head * per;
     start.rt = 0;
     for (;;) {
-      const int n = max(tile_range<kM>(p, start.s, start.rt).nb, 1);
-      if (start.u < start.first + n) break;
-      start.first += n;
+      const int n = max(tile_range<kM>(p, q, start.rt).nb, 1);
+      if (u_begin < first + n) break;
+      first += n;
       ++start.rt;
+    }
+    start.first = (int)(first - u_begin);
+    if (tid == 0) {
+      scan[14] = u_begin;
+      scan[15] = total;
     }
   }
 
@@ -423,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int wg = warp >> 2, quarter = warp & 3;
     const int my_row = (NQ == 2 ? wg * 128 : 0) + quarter * 32 + lane;  // of the tile
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -519,7 +566,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int k = 4; k < NC; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+        for (int k = 4; k < NC - 4; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[NC - 4 + e]);
         float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (NQ == 1) {
           float other;
@@ -551,21 +602,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float mc = m == -INFINITY ? 0.0f : m * p.c;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float2 c2 = make_float2(p.c, p.c), mc2 = make_float2(-mc, -mc);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int h = 0; h < NC / 64; ++h) {
-          uint32_t pk[32];
+        for (int h = 0; h < NC / 32; ++h) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float a = ex2(fmaf(s[64 * h + 2 * k], p.c, -mc));
-            const float e = ex2(fmaf(s[64 * h + 2 * k + 1], p.c, -mc));
-            sum[(2 * k) & 3] += a;
-            sum[(2 * k + 1) & 3] += e;
-            pk[k] = f2h(a, e);
+          for (int k = 0; k < 16; ++k) {
+            float2 e = fma2(make_float2(s[32 * h + 2 * k], s[32 * h + 2 * k + 1]), c2, mc2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[k & 1] = add2(sum[k & 1], e);
+            pk[k] = f2h(e.x, e.y);
           }
-          tmem_st32(s_tm + col0 / 2 + 32 * h, pk);
+          tmem_st16(s_tm + col0 / 2 + 16 * h, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_wait();
         fence_before();
         __syncwarp();
@@ -634,8 +686,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
-      auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / total); };
-      const int c_lo = owner(g.first), c_hi = owner(g.first + g.units - 1);
+      const int64_t all = scan[15], first_unit = scan[14] + g.first;
+      auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / all); };
+      const int c_lo = owner(first_unit), c_hi = owner(first_unit + g.units - 1);
       __threadfence();
       __syncwarp();
       unsigned arrived = 0;
@@ -644,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((int)arrived != c_hi - c_lo) continue;
       __threadfence();
       auto part_at = [&](int c) {
-        return part_of(c, total * c / ctas >= g.first ? 0 : 1);
+        return part_of(c, all * c / ctas >= first_unit ? 0 : 1);
       };
       float M = -INFINITY, L = 0.0f;
       for (int c = c_lo; c <= c_hi; ++c) M = fmaxf(M, __ldcg(part_at(c) + lane));
@@ -694,6 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA --
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     constexpr uint32_t id_qk = idesc(128, kN, false), id_pv = idesc(128, D, true);
     uint32_t ring = 0, blocks = 0, segs = 0, n_stage[2] = {0, 0};
     bool ok = true;
@@ -702,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return mbar_wait(smem_u32(&kv_full[r % NS]), (r / NS) & 1, abort_flag);
     };
     auto release = [&](uint32_t r) { mma_commit(smem_u32(&kv_empty[r % NS])); };
-    auto qk = [&](int stage, int buf, uint32_t r) {  // lane 0
+    auto qk = [&](int stage, int buf, uint32_t r) {  // one lane
       const uint64_t a = sdesc(smem_u32(q_sm) + stage * (128 * D * 2), 16);
       const uint64_t b = sdesc(slot_addr(r), 16);
 #pragma unroll
@@ -712,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(smem_u32(&s_full[buf]));
     };
-    auto pv = [&](int buf, uint32_t o_col, uint32_t r, bool acc) {  // lane 0
+    auto pv = [&](int buf, uint32_t o_col, uint32_t r, bool acc) {  // one lane
       const uint64_t b = sdesc(slot_addr(r), 16384);
 #pragma unroll
       for (int k = 0; k < kN / 16; ++k)  // 16 rows of 128 bytes
@@ -743,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j <= nb; ++j) {
           if (j < nb) {
             if (!(ok = wait_slot(ring))) break;
-            if (lane == 0) {
+            if (elect_one()) {
               qk(0, (blocks + j) & 1, ring);
               release(ring);
             }
@@ -755,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             clean(ring, g.b0 + j - 1, g.r);
             if (!(ok = mbar_wait(smem_u32(&p_full[c & 1]), (c >> 1) & 1, abort_flag))) break;
             fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
               pv(c & 1, 256, ring, j > 1);
               release(ring);
               mma_commit(smem_u32(&o_done[0]));
@@ -768,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int stages = g.rows > 128 ? 2 : 1;
         if (!(ok = wait_slot(ring))) break;
-        if (lane == 0) {
+        if (elect_one()) {
           for (int t = 0; t < stages; ++t) qk(t, t, ring);
           release(ring);
         }
@@ -782,14 +836,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = mbar_wait(smem_u32(&p_full[t]), n_stage[t] & 1, abort_flag))) break;
             ++n_stage[t];
             fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
               pv(t, 256 + t * D, v, j > 0);
               if (t == stages - 1) release(v);
               if (!more) mma_commit(smem_u32(&o_done[t]));
             }
             if (more) {
               if (t == 0 && !(ok = wait_slot(kn))) break;
-              if (lane == 0) {
+              if (elect_one()) {
                 qk(t, t, kn);
                 if (t == stages - 1) release(kn);
               }
@@ -801,8 +855,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp != kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   } else {
     // --------------------------------------------------------------- load --
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     uint32_t ring = 0;
     bool ok = true;
     const int ppb = p.page_size >= kN ? 1 : kN >> p.page_shift;  // pages per block
