@@ -150,22 +150,51 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
-// D (tensor memory) (+)= A (shared) B (shared).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+// Four steps of 16 along K: D (tensor memory) (+)= A (shared) B (shared), both
+// K-major in 64-column groups, so a step is 32 bytes (2 in descriptor units).
+// Descriptors come as their low words (the address field cannot carry: shared
+// memory lies below 256 KB) and a common high word: the issuing thread's few
+// instructions per product are what a product of this size leaves time for.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                        uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
+      "setp.ne.b32 p0, %5, 0;\n\tsetp.eq.b32 p1, %5, %5;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p0;\n\t"
+      "add.u32 u, %1, 2;\n\tadd.u32 v, %2, 2;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p1;\n\t"
+      "add.u32 u, %1, 4;\n\tadd.u32 v, %2, 4;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p1;\n\t"
+      "add.u32 u, %1, 6;\n\tadd.u32 v, %2, 6;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p1;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
-// D (tensor memory) (+)= A (tensor memory) B (shared).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+// Eight steps of 16 keys: D (tensor memory) (+)= A (tensor memory, 8 columns a
+// step) B (shared, N-major: 16 rows of 128 bytes a step).
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                        uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
+      "setp.ne.b32 p0, %5, 0;\n\tsetp.eq.b32 p1, %5, %5;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p0;\n\t"
+      "add.u32 u, %1, 8;\n\tadd.u32 v, %2, 128;\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
+      "add.u32 u, %1, 16;\n\tadd.u32 v, %2, 256;\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
+      "add.u32 u, %1, 24;\n\tadd.u32 v, %2, 384;\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
+      "add.u32 u, %1, 32;\n\tadd.u32 v, %2, 512;\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
+      "add.u32 u, %1, 40;\n\tadd.u32 v, %2, 640;\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
+      "add.u32 u, %1, 48;\n\tadd.u32 v, %2, 768;\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
+      "add.u32 u, %1, 56;\n\tadd.u32 v, %2, 896;\n\tmov.b64 y, {v, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
 // 32 consecutive 32-bit columns of this thread's lane, without waiting.
@@ -245,11 +274,14 @@ __device__ __forceinline__ uint32_t f2h(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 // Shared-memory operand of 128-byte-swizzled rows of 64 fp16 (8-row groups
-// 1024 bytes apart); mn: bytes between 64-column groups of an N-major operand.
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t mn) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(mn >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// 1024 bytes apart): low word of its descriptor; mn: bytes between 64-column
+// groups of an N-major operand (unused when K-major).
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t addr, uint32_t mn) {
+  return addr >> 4 | (mn >> 4) << 16;
 }
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;  // stride, version, 128-byte swizzle
+// A value that every lane holds, as one the compiler knows to be uniform.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 // kind::f16, A = B = f16, D = f32; A K-major, B K-major or N-major.
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_n_major) {
   return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
@@ -755,22 +787,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_slot = [&](uint32_t r) {
       return mbar_wait(smem_u32(&kv_full[r % NS]), (r / NS) & 1, abort_flag);
     };
-    auto release = [&](uint32_t r) { mma_commit(smem_u32(&kv_empty[r % NS])); };
-    auto qk = [&](int stage, int buf, uint32_t r) {  // one lane
-      const uint64_t a = sdesc(smem_u32(q_sm) + stage * (128 * D * 2), 16);
-      const uint64_t b = sdesc(slot_addr(r), 16);
+    const uint32_t tm = uniform(tmem), q_lo = uniform(sdesc_lo(smem_u32(q_sm), 16));
+    // (whole warp) S = Q K^T of a stage into S buffer buf; O (+)= P V
+    auto qk = [&](int stage, int buf, uint32_t r, bool free_slot) {
+      const uint32_t b = uniform(sdesc_lo(slot_addr(r), 16));
+      const uint32_t a = q_lo + stage * (128 * D * 2 / 16), d = tm + uniform(128 * buf);
+      const uint32_t done = uniform(smem_u32(&s_full[buf]));
+      const uint32_t empty = uniform(smem_u32(&kv_empty[r % NS]));
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {  // 32 bytes of a row, 16 KB per 64 columns
-        const uint32_t o = (k & 3) * 2 + (k >> 2) * 1024;
-        mma_ss(tmem + 128 * buf, a + o, b + o, id_qk, k > 0);
+        for (int k = 0; k < D / 64; ++k)  // 64 columns: 16 KB
+          mma4_ss(d, a + k * 1024, b + k * 1024, kDescHi, id_qk, k > 0);
+        mma_commit(done);
+        if (free_slot) mma_commit(empty);
       }
-      mma_commit(smem_u32(&s_full[buf]));
     };
-    auto pv = [&](int buf, uint32_t o_col, uint32_t r, bool acc) {  // one lane
-      const uint64_t b = sdesc(slot_addr(r), 16384);
-#pragma unroll
-      for (int k = 0; k < kN / 16; ++k)  // 16 rows of 128 bytes
-        mma_ts(tmem + o_col, tmem + 128 * buf + 8 * k, b + k * 128, id_pv, acc || k > 0);
+    auto pv = [&](int buf, uint32_t o_col, uint32_t r, bool acc, bool free_slot, uint64_t *done) {
+      const uint32_t b = uniform(sdesc_lo(slot_addr(r), 16384));
+      const uint32_t a = tm + uniform(128 * buf), d = tm + uniform(o_col);
+      const uint32_t empty = uniform(smem_u32(&kv_empty[r % NS]));
+      const uint32_t bar = done ? uniform(smem_u32(done)) : 0;
+      if (elect_one()) {
+        mma8_ts(d, a, b, kDescHi, id_pv, acc);
+        if (free_slot) mma_commit(empty);
+        if (bar) mma_commit(bar);
+      }
     };
     // Rows of a V block that no query of the tile sees may hold anything, and
     // a zero weight times NaN is NaN: they become zeros.
@@ -797,10 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j <= nb; ++j) {
           if (j < nb) {
             if (!(ok = wait_slot(ring))) break;
-            if (elect_one()) {
-              qk(0, (blocks + j) & 1, ring);
-              release(ring);
-            }
+            qk(0, (blocks + j) & 1, ring, true);
             ++ring;
           }
           if (j > 0) {
@@ -809,11 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             clean(ring, g.b0 + j - 1, g.r);
             if (!(ok = mbar_wait(smem_u32(&p_full[c & 1]), (c >> 1) & 1, abort_flag))) break;
             fence_after();
-            if (elect_one()) {
-              pv(c & 1, 256, ring, j > 1);
-              release(ring);
-              mma_commit(smem_u32(&o_done[0]));
-            }
+            pv(c & 1, 256, ring, j > 1, true, &o_done[0]);
             ++ring;
           }
           __syncwarp();
@@ -822,10 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int stages = g.rows > 128 ? 2 : 1;
         if (!(ok = wait_slot(ring))) break;
-        if (elect_one()) {
-          for (int t = 0; t < stages; ++t) qk(t, t, ring);
-          release(ring);
-        }
+        for (int t = 0; t < stages; ++t) qk(t, t, ring, t == stages - 1);
         ++ring;
         for (int j = 0; j < nb; ++j) {
           const uint32_t v = ring, kn = ring + 1;
@@ -836,17 +867,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = mbar_wait(smem_u32(&p_full[t]), n_stage[t] & 1, abort_flag))) break;
             ++n_stage[t];
             fence_after();
-            if (elect_one()) {
-              pv(t, 256 + t * D, v, j > 0);
-              if (t == stages - 1) release(v);
-              if (!more) mma_commit(smem_u32(&o_done[t]));
-            }
+            pv(t, 256 + t * D, v, j > 0, t == stages - 1, more ? nullptr : &o_done[t]);
             if (more) {
               if (t == 0 && !(ok = wait_slot(kn))) break;
-              if (elect_one()) {
-                qk(t, t, kn);
-                if (t == stages - 1) release(kn);
-              }
+              qk(t, t, kn, t == stages - 1);
             }
             __syncwarp();
           }
