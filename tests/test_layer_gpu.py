@@ -355,6 +355,16 @@ def test_attention_long_context_split():
     check_attention([17, 2], [30000, 9000], 8, 2, 128, 16, seed=16)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_many_tiles_of_several_blocks(D):
+    """Every SM walks through several tiles of a few key blocks each."""
+    check_attention([1] * 160, [257 + (i * 29) % 300 for i in range(160)], 8, 8, D, 16, seed=50)
+    check_attention([i % 5 for i in range(120)], [300 + (i * 31) % 400 for i in range(120)], 24, 8,
+                    D, 64, window=290, seed=51)
+    lens = [130 + (i * 41) % 300 for i in range(24)]
+    check_attention(lens, [n + (i % 3) * 200 for i, n in enumerate(lens)], 16, 8, D, 32, seed=52)
+
+
 def test_attention_many_sequences():
     n = 700
     check_attention([1 + (i % 3 == 0) for i in range(n)], [1 + (i * 37) % 90 for i in range(n)], 4,

@@ -44,7 +44,9 @@ constexpr int kThreads = 384;          // the third warpgroup: MMA, loads, two s
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
 static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "register split");
 constexpr int kMaxCtas = 160;          // grid cap (partial slots in the workspace)
-constexpr int kHead = 4096;            // barriers and exchange rows at the start of shared memory
+constexpr int kBars = 4096;             // barriers and exchange rows at the start of shared memory
+constexpr int kOutBytes = 32 * 64;     // per softmax warp: 32 rows x 32 outputs on their way out
+constexpr int kHead = kBars + 8 * kOutBytes;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
@@ -171,9 +173,9 @@ __device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint
       "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
-// Eight steps of 16 keys: D (tensor memory) (+)= A (tensor memory, 8 columns a
+// Four steps of 16 keys: D (tensor memory) (+)= A (tensor memory, 8 columns a
 // step) B (shared, N-major: 16 rows of 128 bytes a step).
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
                                         uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p0, p1;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
@@ -185,14 +187,6 @@ __device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint32_t b, uint
       "add.u32 u, %1, 16;\n\tadd.u32 v, %2, 256;\n\tmov.b64 y, {v, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
       "add.u32 u, %1, 24;\n\tadd.u32 v, %2, 384;\n\tmov.b64 y, {v, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
-      "add.u32 u, %1, 32;\n\tadd.u32 v, %2, 512;\n\tmov.b64 y, {v, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
-      "add.u32 u, %1, 40;\n\tadd.u32 v, %2, 640;\n\tmov.b64 y, {v, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
-      "add.u32 u, %1, 48;\n\tadd.u32 v, %2, 768;\n\tmov.b64 y, {v, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t"
-      "add.u32 u, %1, 56;\n\tadd.u32 v, %2, 896;\n\tmov.b64 y, {v, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p1;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
@@ -394,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(base);
   uint64_t *kv_full = bars, *kv_empty = bars + kMaxStages;
   uint64_t *s_full = kv_empty + kMaxStages, *p_full = s_full + 2, *o_done = p_full + 2;
-  uint64_t *q_full = o_done + 2, *xbar = q_full + 1;  // xbar: one per 32-row quarter
+  uint64_t *p_half = o_done + 2;  // NQ = 2: the first 64 keys' weights
+  uint64_t *q_full = p_half + 2, *xbar = q_full + 1;  // xbar: one per 32-row quarter
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xbar + 4);
   int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
   int64_t *scan = reinterpret_cast<int64_t *>(base + 512);   // [12] warp sums, then the start
@@ -412,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&p_full[i]), NQ == 2 ? 4 : 8);
       mbar_init(smem_u32(&o_done[i]), 1);
+      mbar_init(smem_u32(&p_half[i]), 4);
     }
     mbar_init(smem_u32(q_full), kSoftmaxWarps);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&xbar[i]), 2);
@@ -524,7 +520,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++swaps;
       return true;
     };
+    // This warp's rows of a tile's queries, into shared memory as a TMA copy
+    // with the 128-byte swizzle would lay them; rows past the tile are zeros.
+    constexpr int CPR = D / 8, RPP = 32 / CPR;        // 16-byte chunks a row, rows per pass
+    constexpr int QR = NQ == 2 ? 32 : 16;             // rows per warp
+    auto q_chunk = [&](int k, int &r, int &c) {       // pass k: tile row and chunk of this lane
+      r = warp * QR + k * RPP + lane / CPR;
+      c = lane % CPR;
+      return smem_u32(q_sm) + (r >> 7) * (128 * D * 2) + (c >> 3) * 16384 + (r & 127) * 128 +
+             (((c & 7) ^ (r & 7)) << 4);
+    };
+    auto load_q = [&](const Seg &t) {
+#pragma unroll 4
+      for (int k = 0; k < QR / RPP; ++k) {
+        int r, c;
+        const uint32_t dst = q_chunk(k, r, c);
+        const int rr = t.rt * kM + min(r, t.rows - 1), tok = rr / p.G;
+        const __half *src = p.q + (int64_t)(t.s.tok0 + tok) * p.q_token +
+                            (int64_t)(t.head * p.G + rr - tok * p.G) * p.q_head + c * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                     "r"(r < t.rows ? 16 : 0)
+                     : "memory");
+      }
+    };
+    // The copies have landed: turn signs where asked, and tell the MMA warp.
+    auto publish_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (p.flip != 0 || p.keep != ~0u) {
+        for (int k = 0; k < QR / RPP; ++k) {
+          int r, c;
+          const uint32_t at = q_chunk(k, r, c);
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(at));
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at),
+                       "r"((v[0] & p.keep) ^ p.flip), "r"((v[1] & p.keep) ^ p.flip),
+                       "r"((v[2] & p.keep) ^ p.flip), "r"((v[3] & p.keep) ^ p.flip)
+                       : "memory");
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(q_full));
+    };
     Walker<kM> w = start;
+    // Queries of the next tile with keys after the walker's place, if any.
+    auto load_next_q = [&]() {
+      Walker<kM> ahead = w;
+      Seg t;
+      while (ahead.next(p, t))
+        if (t.b1 > t.b0) {
+          load_q(t);
+          return true;
+        }
+      return false;
+    };
+    // Four 16-byte pieces of this lane's row, out through shared memory so that
+    // a store covers 64 contiguous bytes of 8 rows: dst[i] is where piece
+    // lane % 4 of row 8 i + lane / 4 goes (null: nowhere).
+    const uint32_t stage_sm = smem_u32(base) + kBars + warp * kOutBytes;
+    auto store_rows = [&](const uint32_t (&v)[16], char *const (&dst)[4], int offset) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                         stage_sm + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
+                     "r"(v[4 * c]), "r"(v[4 * c + 1]), "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
+                     : "memory");
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        uint4 o;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                     : "r"(stage_sm + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)));
+        if (dst[i]) *reinterpret_cast<uint4 *>(dst[i] + offset) = o;
+      }
+      __syncwarp();
+    };
+    if (load_next_q()) publish_q();
     Seg g;
     while (ok && w.next(p, g)) {
       const int warp_row = my_row - lane;
@@ -538,44 +613,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nb = g.b1 - g.b0;
       const bool active = nb > 0 && (NQ == 1 || wg == 0 || g.rows > 128);
       if (nb > 0) {
-        // ---- queries into shared memory, swizzled like a TMA tile
-        constexpr int CPR = D / 8;  // 16-byte chunks per row
-        constexpr int RPP = 32 / CPR > 0 ? 32 / CPR : 1;
-        if (active) {
-          // a warp fills rows [qrow0, qrow0 + QR) of the tile
-          constexpr int QR = NQ == 2 ? 32 : 16;
-          const int qrow0 = NQ == 2 ? warp * 32 : warp * 16;
-#pragma unroll 4
-          for (int k = 0; k < QR / RPP; ++k) {
-            const int r = qrow0 + k * RPP + lane / CPR, c = lane % CPR;
-            const int rr = g.rt * kM + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < g.rows) {
-              const int tok = rr / p.G, hd = g.head * p.G + rr - tok * p.G;
-              v = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(g.s.tok0 + tok) * p.q_token +
-                                                        hd * p.q_head) + c);
-              v.x = (v.x & p.keep) ^ p.flip;
-              v.y = (v.y & p.keep) ^ p.flip;
-              v.z = (v.z & p.keep) ^ p.flip;
-              v.w = (v.w & p.keep) ^ p.flip;
-            }
-            *reinterpret_cast<uint4 *>(q_sm + (r >> 7) * (128 * D * 2) + (c >> 3) * 16384 +
-                                       (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-          }
-          fence_async_smem();
+        if (!active) {  // this warpgroup has no rows here: it must not run ahead of the other
+          if (!(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
+          if (load_next_q()) publish_q();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(q_full));
-        // a warpgroup without rows must not arrive for the next tile before this one's
-        if (!active && !(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
         ++segs;
       }
+      // whole blocks of this range need no mask in this warp
+      const int see_lo = __reduce_max_sync(0xffffffffu, lo), see_hi = __reduce_min_sync(0xffffffffu, hi);
+      // NQ = 1: the previous block's product is complete.  Every live warp sees
+      // each of them before it lets the next one start: a wait tells a
+      // barrier's phases apart by parity alone.
+      auto last_product = [&](int b) {
+        return b == g.b0 || mbar_wait(smem_u32(&o_done[0]), (blocks - 1) & 1, abort_flag);
+      };
       for (int b = g.b0; active && b < g.b1; ++b, ++blocks) {
         const int buf = NQ == 2 ? wg : (int)(blocks & 1);
         const uint32_t ph = NQ == 2 ? blocks & 1 : (blocks >> 1) & 1;
         if (!(ok = mbar_wait(smem_u32(&s_full[buf]), ph, abort_flag))) break;
+        // the tile's last S is done with its queries
+        const bool next_q = b == g.b1 - 1 && load_next_q();
         if (live_rows == 0) {  // nothing of this warp is stored
-          if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+          if (lane == 0) {
+            if (NQ == 2) mbar_arrive(smem_u32(&p_half[buf]));
+            mbar_arrive(smem_u32(&p_full[buf]));
+          }
+          if (next_q) publish_q();
           continue;
         }
         fence_after();
@@ -591,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s[k] = p.cap * (1.0f - 2.0f * rcp(1.0f + ex2(s[k] * p.cap_in)));
         }
         const int k_hi = hi - b * kN - col0, k_lo = lo - b * kN - col0;
-        if (__any_sync(0xffffffffu, k_hi < NC || k_lo > 0)) {
+        if (b * kN + col0 < see_lo || b * kN + col0 + NC > see_hi) {
 #pragma unroll
           for (int k = 0; k < NC; ++k)
             if (k >= k_hi || k < k_lo) s[k] = -INFINITY;
@@ -618,9 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= f;
           if (b > g.b0) {
             // NQ = 2: this stage's earlier products precede the S just read
-            if (NQ == 1 &&
-                !(ok = mbar_wait(smem_u32(&o_done[0]), (blocks - 1) & 1, abort_flag)))
-              break;
+            if (NQ == 1 && !(ok = last_product(b))) break;
             fence_after();
 #pragma unroll 1
             for (int k = 0; k < DC; k += 32) {
@@ -648,54 +709,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[k] = f2h(e.x, e.y);
           }
           tmem_st16(s_tm + col0 / 2 + 16 * h, pk);
+          if (NQ == 2 && h == 1) {  // the product starts on these
+            tmem_st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_half[buf]));
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if (NQ == 1 && !(ok = last_product(b))) break;
         tmem_st_wait();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+        if (next_q) publish_q();
       }
       if (!ok) break;
       // ---- the tile's rows, or this CTA's part of them
-      if (active) {
+      if (active && live_rows > 0) {
         const uint32_t ph = NQ == 2 ? ends & 1 : (blocks - 1) & 1;
-        // NQ = 1: the last S only proves the product two blocks back complete,
-        // and a wait tells phases apart by parity alone
-        if (NQ == 1 && nb > 1 && !(ok = mbar_wait(smem_u32(&o_done[0]), ph ^ 1, abort_flag))) break;
         if (!(ok = mbar_wait(smem_u32(&o_done[NQ == 2 ? wg : 0]), ph, abort_flag))) break;
-        ++ends;
         fence_after();
-        if (NQ == 1 && live_rows > 0) {
+        if (NQ == 1) {
           float other;
           if (!(ok = exchange(l, &other))) break;
           l = wg == 0 ? l + other : other + l;
         }
       }
+      if (active) ++ends;
       if (live_rows == 0) continue;
-      const int tok = row / p.G, hd = g.head * p.G + row - tok * p.G;
       if (g.whole) {
+        const int tok = row / p.G;
+        const int64_t at = (int64_t)(g.s.tok0 + tok) * p.o_token +
+                           (int64_t)(g.head * p.G + row - tok * p.G) * p.o_head + out0;
+        char *dst[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2);
+          const int64_t o = __shfl_sync(0xffffffffu, at, r);
+          dst[i] = r < live_rows ? reinterpret_cast<char *>(p.out + o) + (lane & 3) * 16 : nullptr;
+        }
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(g.s.tok0 + tok) * p.o_token +
-                                               (int64_t)hd * p.o_head + out0);
 #pragma unroll 1
         for (int k = 0; k < DC; k += 32) {
-          uint32_t o[32];
+          uint32_t o[32], v[16];
           if (active) {
             tmem_ld32(o_tm + k, o);
             tmem_ld_wait();
           }
-          if (lane < live_rows) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t v[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                v[i] = active ? f2h(__uint_as_float(o[8 * e + 2 * i]) * inv,
-                                    __uint_as_float(o[8 * e + 2 * i + 1]) * inv)
-                              : 0u;
-              dst[k / 8 + e] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-          }
+          for (int e = 0; e < 16; ++e)
+            v[e] = active ? f2h(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
+                          : 0u;
+          store_rows(v, dst, k * 2);
         }
         continue;
       }
@@ -706,16 +772,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       float *mine_part = part_of(blockIdx.x, g.slot);
       mine_part[lane] = l > 0.0f ? (m == -INFINITY ? 0.0f : m * p.c) : -INFINITY;
       mine_part[32 + lane] = l;
+      char *dst[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        dst[i] = r < live_rows
+                     ? reinterpret_cast<char *>(mine_part + 64 + r * DC) + (lane & 3) * 16
+                     : nullptr;
+      }
 #pragma unroll 1
       for (int k = 0; k < DC; k += 32) {
         uint32_t o[32];
         tmem_ld32(o_tm + k, o);
         tmem_ld_wait();
-        if (lane < live_rows) {
-          uint4 *dst = reinterpret_cast<uint4 *>(mine_part + 64 + lane * DC + k);
+        uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = o[16 * h + e];
+          store_rows(v, dst, (k + 16 * h) * 4);
         }
       }
       const int64_t all = scan[15], first_unit = scan[14] + g.first;
@@ -788,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return mbar_wait(smem_u32(&kv_full[r % NS]), (r / NS) & 1, abort_flag);
     };
     const uint32_t tm = uniform(tmem), q_lo = uniform(sdesc_lo(smem_u32(q_sm), 16));
-    // (whole warp) S = Q K^T of a stage into S buffer buf; O (+)= P V
+    // (whole warp) S = Q K^T of a stage into S buffer buf
     auto qk = [&](int stage, int buf, uint32_t r, bool free_slot) {
       const uint32_t b = uniform(sdesc_lo(slot_addr(r), 16));
       const uint32_t a = q_lo + stage * (128 * D * 2 / 16), d = tm + uniform(128 * buf);
@@ -802,13 +877,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (free_slot) mma_commit(empty);
       }
     };
-    auto pv = [&](int buf, uint32_t o_col, uint32_t r, bool acc, bool free_slot, uint64_t *done) {
-      const uint32_t b = uniform(sdesc_lo(slot_addr(r), 16384));
-      const uint32_t a = tm + uniform(128 * buf), d = tm + uniform(o_col);
+    // (whole warp) O (+)= P V: keys 64 half.. of S buffer buf
+    auto pv = [&](int buf, int half, uint32_t o_col, uint32_t r, bool acc, bool free_slot,
+                  uint64_t *done) {
+      const uint32_t b = uniform(sdesc_lo(slot_addr(r), 16384) + half * 512);
+      const uint32_t a = tm + uniform(128 * buf + 32 * half), d = tm + uniform(o_col);
       const uint32_t empty = uniform(smem_u32(&kv_empty[r % NS]));
       const uint32_t bar = done ? uniform(smem_u32(done)) : 0;
       if (elect_one()) {
-        mma8_ts(d, a, b, kDescHi, id_pv, acc);
+        mma4_ts(d, a, b, kDescHi, id_pv, acc || half);
         if (free_slot) mma_commit(empty);
         if (bar) mma_commit(bar);
       }
@@ -847,7 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             clean(ring, g.b0 + j - 1, g.r);
             if (!(ok = mbar_wait(smem_u32(&p_full[c & 1]), (c >> 1) & 1, abort_flag))) break;
             fence_after();
-            pv(c & 1, 256, ring, j > 1, true, &o_done[0]);
+            pv(c & 1, 0, 256, ring, j > 1, false, nullptr);
+            pv(c & 1, 1, 256, ring, true, true, &o_done[0]);
             ++ring;
           }
           __syncwarp();
@@ -864,10 +942,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_slot(v))) break;
           clean(v, g.b0 + j, g.r);
           for (int t = 0; t < stages; ++t) {
-            if (!(ok = mbar_wait(smem_u32(&p_full[t]), n_stage[t] & 1, abort_flag))) break;
-            ++n_stage[t];
+            if (!(ok = mbar_wait(smem_u32(&p_half[t]), n_stage[t] & 1, abort_flag))) break;
             fence_after();
-            pv(t, 256 + t * D, v, j > 0, t == stages - 1, more ? nullptr : &o_done[t]);
+            pv(t, 0, 256 + t * D, v, j > 0, false, nullptr);
+            if (!(ok = mbar_wait(smem_u32(&p_full[t]), n_stage[t] & 1, abort_flag))) break;
+            fence_after();
+            ++n_stage[t];
+            pv(t, 1, 256 + t * D, v, true, t == stages - 1, more ? nullptr : &o_done[t]);
             if (more) {
               if (t == 0 && !(ok = wait_slot(kn))) break;
               qk(t, t, kn, t == stages - 1);
