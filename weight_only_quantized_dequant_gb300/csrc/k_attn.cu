@@ -52,7 +52,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr float kLag = 8.0f;           // log2 of how far a weight may exceed 1
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMinUnits = 2;           // key blocks per CTA at least
+constexpr int kMinUnits = 3;           // units per CTA at least
+constexpr int kTileUnits = 1;          // a tile's fixed time, in key blocks
+constexpr int kSegs = 4;               // tiles announced ahead
 
 template <int D, int NQ>
 struct Cfg {
@@ -72,6 +74,7 @@ struct AttnParams {
   __half *out;
   int64_t q_token, q_head, o_token, o_head;
   int G;                // query heads per KV head
+  float inv_g;          // 1 / G
   int hkv, n_pages, page_size, page_shift;
   float c;              // logit units to log2: |scale| log2(e), or log2(e) with a cap
   float cap, cap_in;    // softcap, and |scale| / softcap * 2 log2(e)
@@ -320,59 +323,95 @@ __device__ __forceinline__ Range tile_range(const AttnParams &p, const Seq &s, i
   return r;
 }
 
-// Units (key blocks, at least one a tile) of one KV head of a sequence.
+// Units of a tile: its key blocks (one if it sees no key), and before them the
+// time that a tile costs whatever its length, in blocks.
+template <int kM>
+__device__ __forceinline__ int tile_units(const Range &r) {
+  return kTileUnits + max(r.nb, 1);
+}
+
+// Units of one KV head of a sequence.
 template <int kM>
 __device__ __forceinline__ int64_t head_units(const AttnParams &p, const Seq &s) {
   int64_t n = 0;
-  for (int rt = 0; rt < s.nt; ++rt) n += max(tile_range<kM>(p, s, rt).nb, 1);
+  for (int rt = 0; rt < s.nt; ++rt) n += tile_units<kM>(tile_range<kM>(p, s, rt));
   return n;
 }
 
-// What one CTA does of one tile.
-struct Seg {
-  Seq s;
-  int head, rt, rows;    // KV head, row tile, its rows
-  Range r;
-  int b0, b1;            // its key blocks [b0, b1); none if the tile sees no key
-  bool whole;
-  int slot;              // partial slot if cut
-  int first;             // the tile's first unit, relative to the CTA's
-  int units;
+// What one CTA does of one tile, as the load warp tells the others.
+struct __align__(16) Seg {
+  int rows;            // rows of the tile (0: the CTA has no more tiles)
+  int b0, b1;          // its key blocks [b0, b1) of this CTA; none if the tile sees no key
+  int head;            // KV head
+  int tok, rem, pos;   // token of row 0, row 0's place among that token's heads, its position
+  int lo, hi;          // keys [lo, hi) that any row sees
+  int slot;            // -1: all of the tile; else the CTA's partial slot
+  int c_lo, parts;     // cut tile: first CTA, and how many share it
+  int first_slot;      // cut tile: the first CTA's partial slot (the others': 0)
+  int seq;             // sequence
+  int pad[2];
 };
+static_assert(sizeof(Seg) == 64, "four 16-byte reads");
 
-// Walks a CTA's unit range tile by tile; every warp keeps its own.  Units are
-// counted from the CTA's first.
+// Walks a CTA's unit range tile by tile (load warp only).  Units are counted
+// from the CTA's first.
 template <int kM>
 struct Walker {
   int u, u_end, first;  // next unit, end, first unit of the current tile
   int seq, head, rt;
-  __device__ __forceinline__ bool next(const AttnParams &p, Seg &g) {
-    if (u >= u_end) return false;
-    g.s = load_seq<kM>(p, seq);
-    while (rt >= g.s.nt) {  // sequences without new tokens have no tiles
-      rt = 0;
-      if (g.s.nt == 0 || ++head == p.hkv) {
-        head = 0;
-        g.s = load_seq<kM>(p, ++seq);
+  int64_t u_begin, total;
+  int ctas;
+  __device__ __forceinline__ int owner(int64_t unit) const {
+    return (int)(((unit + 1) * ctas - 1) / total);
+  }
+  __device__ __forceinline__ Seg next(const AttnParams &p) {
+    Seg g;
+    g.rows = 0;
+    while (u < u_end) {
+      Seq s = load_seq<kM>(p, seq);
+      while (rt >= s.nt) {  // sequences without new tokens have no tiles
+        rt = 0;
+        if (s.nt == 0 || ++head == p.hkv) {
+          head = 0;
+          s = load_seq<kM>(p, ++seq);
+        }
       }
+      const Range r = tile_range<kM>(p, s, rt);
+      const int units = tile_units<kM>(r), tile_first = first;
+      const int a = max(u - first - kTileUnits, 0);                 // of its blocks
+      const int b = min(u_end - first, units) - kTileUnits;
+      g.slot = u == 0 ? 0 : 1;
+      g.head = head;
+      g.seq = seq;
+      const int row0 = rt * kM;
+      const bool done = u_end - first >= units;
+      u = first + min(u_end - first, units);
+      if (done) {
+        first += units;
+        ++rt;
+      }
+      if (b <= a) continue;  // only the fixed part of the tile's time falls to this CTA
+      const int i0 = row0 / p.G;
+      g.rows = min(s.rows - row0, kM);
+      g.tok = s.tok0 + i0;
+      g.rem = row0 - i0 * p.G;
+      g.pos = s.kv - s.q + i0;
+      g.lo = r.lo;
+      g.hi = r.hi;
+      g.b0 = r.b0 + a;
+      g.b1 = r.nb == 0 ? g.b0 : r.b0 + b;
+      g.c_lo = g.parts = g.first_slot = 0;
+      if (a == 0 && done) {
+        g.slot = -1;
+      } else {
+        g.c_lo = owner(u_begin + tile_first + kTileUnits);
+        g.parts = owner(u_begin + tile_first + units - 1) - g.c_lo + 1;
+        if (g.parts == 1) g.slot = -1;
+        g.first_slot = total * g.c_lo / ctas >= u_begin + tile_first ? 0 : 1;
+      }
+      break;
     }
-    g.head = head;
-    g.rt = rt;
-    g.rows = min(g.s.rows - rt * kM, kM);
-    g.r = tile_range<kM>(p, g.s, rt);
-    g.units = max(g.r.nb, 1);
-    g.first = first;
-    const int a = u - first, b = min(u_end - first, g.units);
-    g.b0 = g.r.b0 + a;
-    g.b1 = g.r.nb == 0 ? g.b0 : g.r.b0 + b;
-    g.whole = a == 0 && b == g.units;
-    g.slot = u == 0 ? 0 : 1;
-    u = first + b;
-    if (b == g.units) {
-      first += g.units;
-      ++rt;
-    }
-    return true;
+    return g;
   }
 };
 
@@ -390,9 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *s_full = kv_empty + kMaxStages, *p_full = s_full + 2, *o_done = p_full + 2;
   uint64_t *p_half = o_done + 2;  // NQ = 2: the first 64 keys' weights
   uint64_t *q_full = p_half + 2, *xbar = q_full + 1;  // xbar: one per 32-row quarter
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xbar + 4);
+  uint64_t *seg_full = xbar + 4, *seg_empty = seg_full + kSegs;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(seg_empty + kSegs);
   int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
   int64_t *scan = reinterpret_cast<int64_t *>(base + 512);   // [12] warp sums, then the start
+  Seg *seg_sm = reinterpret_cast<Seg *>(base + 768);         // [kSegs]
   float *xch = reinterpret_cast<float *>(base + 1024);       // [2][8 warps][32]
   uint8_t *q_sm = base + kHead, *kv_sm = q_sm + C::kQ;
 
@@ -411,6 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(q_full), kSoftmaxWarps);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&xbar[i]), 2);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(smem_u32(&seg_full[i]), 1);
+      mbar_init(smem_u32(&seg_empty[i]), kSoftmaxWarps + 1);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -432,6 +477,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if ((int)blockIdx.x >= ctas) return;
   const int64_t u_begin = total * blockIdx.x / ctas;
   Walker<kM> start;
+  start.u_begin = u_begin;
+  start.total = total;
+  start.ctas = ctas;
   start.u = 0;
   start.u_end = (int)(total * (blockIdx.x + 1) / ctas - u_begin);
   {
@@ -471,16 +519,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     first += start.head * per;
     start.rt = 0;
     for (;;) {
-      const int n = max(tile_range<kM>(p, q, start.rt).nb, 1);
+      const int n = tile_units<kM>(tile_range<kM>(p, q, start.rt));
       if (u_begin < first + n) break;
       first += n;
       ++start.rt;
     }
     start.first = (int)(first - u_begin);
-    if (tid == 0) {
-      scan[14] = u_begin;
-      scan[15] = total;
-    }
   }
 
   if (warp == 0) {
@@ -494,6 +538,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;  // S of stage or buffer i at 128 i, O at 256 (+ D for stage 1)
+
+  // The n-th announced tile (softmax and MMA warps).
+  auto read_seg = [&](uint32_t n, Seg &g) {
+    if (!mbar_wait(smem_u32(&seg_full[n % kSegs]), (n / kSegs) & 1, abort_flag)) return false;
+    const uint4 *src = reinterpret_cast<const uint4 *>(&seg_sm[n % kSegs]);
+    uint4 *dst = reinterpret_cast<uint4 *>(&g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = src[i];
+    return true;
+  };
+  auto free_seg = [&](uint32_t n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n % kSegs]));
+  };
 
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax --
@@ -520,6 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++swaps;
       return true;
     };
+    // n / G for n < G + 256: (n + 1/2) / G stays further from every whole number
+    // than fp32 rounding can move it.
+    auto row_token = [&](int n) { return (int)(((float)n + 0.5f) * p.inv_g); };
     // This warp's rows of a tile's queries, into shared memory as a TMA copy
     // with the 128-byte swizzle would lay them; rows past the tile are zeros.
     constexpr int CPR = D / 8, RPP = 32 / CPR;        // 16-byte chunks a row, rows per pass
@@ -535,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < QR / RPP; ++k) {
         int r, c;
         const uint32_t dst = q_chunk(k, r, c);
-        const int rr = t.rt * kM + min(r, t.rows - 1), tok = rr / p.G;
-        const __half *src = p.q + (int64_t)(t.s.tok0 + tok) * p.q_token +
-                            (int64_t)(t.head * p.G + rr - tok * p.G) * p.q_head + c * 8;
+        const int n = t.rem + min(r, t.rows - 1), i = row_token(n);
+        const __half *src = p.q + (int64_t)(t.tok + i) * p.q_token +
+                            (int64_t)(t.head * p.G + n - i * p.G) * p.q_head + c * 8;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                      "r"(r < t.rows ? 16 : 0)
                      : "memory");
@@ -564,17 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(q_full));
     };
-    Walker<kM> w = start;
-    // Queries of the next tile with keys after the walker's place, if any.
-    auto load_next_q = [&]() {
-      Walker<kM> ahead = w;
+    uint32_t n_seg = 0;    // tiles read so far
+    // Queries of tile n, if it has keys.
+    auto load_next_q = [&](uint32_t n) {
       Seg t;
-      while (ahead.next(p, t))
-        if (t.b1 > t.b0) {
-          load_q(t);
-          return true;
-        }
-      return false;
+      if (!read_seg(n, t) || t.rows == 0 || t.b1 <= t.b0) return false;
+      load_q(t);
+      return true;
     };
     // Four 16-byte pieces of this lane's row, out through shared memory so that
     // a store covers 64 contiguous bytes of 8 rows: dst[i] is where piece
@@ -599,26 +656,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    if (load_next_q()) publish_q();
-    Seg g;
-    while (ok && w.next(p, g)) {
+    if (load_next_q(0)) publish_q();
+    while (ok) {
+      Seg g;
+      if (!(ok = read_seg(n_seg, g))) break;
+      free_seg(n_seg++);
+      if (g.rows == 0) break;
       const int warp_row = my_row - lane;
       const int live_rows = min(max(g.rows - warp_row, 0), 32);  // of this warp
-      const int row = g.rt * kM + my_row;                        // of the sequence
-      const int first = g.s.kv - g.s.q;
       // rows past the tile's end repeat its last row's limits
-      const int pos = first + min(row, g.rt * kM + g.rows - 1) / p.G;
+      const int pos = g.pos + row_token(g.rem + min(my_row, g.rows - 1));
       const int hi = pos + 1, lo = p.window > 0 ? pos - p.window + 1 : 0;
       float m = -INFINITY, l = 0.0f;
       const int nb = g.b1 - g.b0;
       const bool active = nb > 0 && (NQ == 1 || wg == 0 || g.rows > 128);
-      if (nb > 0) {
-        if (!active) {  // this warpgroup has no rows here: it must not run ahead of the other
-          if (!(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
-          if (load_next_q()) publish_q();
-        }
-        ++segs;
+      if (!active) {
+        // a warpgroup without rows here must not run ahead of the other
+        if (nb > 0 && !(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
+        if (load_next_q(n_seg)) publish_q();
       }
+      if (nb > 0) ++segs;
       // whole blocks of this range need no mask in this warp
       const int see_lo = __reduce_max_sync(0xffffffffu, lo), see_hi = __reduce_min_sync(0xffffffffu, hi);
       // NQ = 1: the previous block's product is complete.  Every live warp sees
@@ -632,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ph = NQ == 2 ? blocks & 1 : (blocks >> 1) & 1;
         if (!(ok = mbar_wait(smem_u32(&s_full[buf]), ph, abort_flag))) break;
         // the tile's last S is done with its queries
-        const bool next_q = b == g.b1 - 1 && load_next_q();
+        const bool next_q = b == g.b1 - 1 && load_next_q(n_seg);
         if (live_rows == 0) {  // nothing of this warp is stored
           if (lane == 0) {
             if (NQ == 2) mbar_arrive(smem_u32(&p_half[buf]));
@@ -738,16 +795,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (active) ++ends;
       if (live_rows == 0) continue;
-      if (g.whole) {
-        const int tok = row / p.G;
-        const int64_t at = (int64_t)(g.s.tok0 + tok) * p.o_token +
-                           (int64_t)(g.head * p.G + row - tok * p.G) * p.o_head + out0;
+      // where a row's outputs go
+      auto out_at = [&](int r) {
+        const int n = g.rem + r, i = row_token(n);
+        return (int64_t)(g.tok + i) * p.o_token + (int64_t)(g.head * p.G + n - i * p.G) * p.o_head +
+               out0;
+      };
+      if (g.slot < 0) {
         char *dst[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + (lane >> 2);
-          const int64_t o = __shfl_sync(0xffffffffu, at, r);
-          dst[i] = r < live_rows ? reinterpret_cast<char *>(p.out + o) + (lane & 3) * 16 : nullptr;
+          dst[i] = r < live_rows
+                       ? reinterpret_cast<char *>(p.out + out_at(warp_row + r)) + (lane & 3) * 16
+                       : nullptr;
         }
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
@@ -793,64 +854,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_rows(v, dst, (k + 16 * h) * 4);
         }
       }
-      const int64_t all = scan[15], first_unit = scan[14] + g.first;
-      auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / all); };
-      const int c_lo = owner(first_unit), c_hi = owner(first_unit + g.units - 1);
       __threadfence();
       __syncwarp();
       unsigned arrived = 0;
-      if (lane == 0) arrived = atomicAdd(&p.cnt[c_lo * kSoftmaxWarps + warp], 1u);
+      if (lane == 0) arrived = atomicAdd(&p.cnt[g.c_lo * kSoftmaxWarps + warp], 1u);
       arrived = __shfl_sync(0xffffffffu, arrived, 0);
-      if ((int)arrived != c_hi - c_lo) continue;
+      if ((int)arrived != g.parts - 1) continue;
       __threadfence();
-      auto part_at = [&](int c) {
-        return part_of(c, all * c / ctas >= first_unit ? 0 : 1);
-      };
+      auto part_at = [&](int k) { return part_of(g.c_lo + k, k == 0 ? g.first_slot : 0); };
       float M = -INFINITY, L = 0.0f;
-      for (int c = c_lo; c <= c_hi; ++c) M = fmaxf(M, __ldcg(part_at(c) + lane));
+#pragma unroll 4
+      for (int k = 0; k < g.parts; ++k) M = fmaxf(M, __ldcg(part_at(k) + lane));
       const float Mz = M == -INFINITY ? 0.0f : M;
-      for (int c = c_lo; c <= c_hi; ++c) {
-        const float *pp = part_at(c);
+#pragma unroll 4
+      for (int k = 0; k < g.parts; ++k) {
+        const float *pp = part_at(k);
         L += __ldcg(pp + 32 + lane) * ex2(__ldcg(pp + lane) - Mz);
       }
       const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-      // lanes share the rows' float4 columns
-      constexpr int F4 = DC / 4;
+      // lanes share the rows' float4 columns, 4 each, 4 partials in flight
+      constexpr int F4 = DC / 4, E = 4, U = 4;
       const int items = live_rows * F4;
-      for (int i0 = 0; i0 < items; i0 += 128) {
-        float4 acc[4];
+      for (int i0 = 0; i0 < items; i0 += 32 * E) {
+        float4 acc[E];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int c = c_lo; c <= c_hi; ++c) {
-          const float *pp = part_at(c);
-          const float wgt = ex2(__ldcg(pp + lane) - Mz);
+        for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k0 = 0; k0 < g.parts; k0 += U) {
+          float4 v[U][E];
+          float wgt[U];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int it = i0 + e * 32 + lane;
-            const float f = __shfl_sync(0xffffffffu, wgt, min(it / F4, 31));
-            if (it < items) {
-              const float4 v = __ldcg(reinterpret_cast<const float4 *>(pp + 64) + it);
-              acc[e].x = fmaf(v.x, f, acc[e].x);
-              acc[e].y = fmaf(v.y, f, acc[e].y);
-              acc[e].z = fmaf(v.z, f, acc[e].z);
-              acc[e].w = fmaf(v.w, f, acc[e].w);
-            }
+          for (int k = 0; k < U; ++k) {
+            const float *pp = part_at(min(k0 + k, g.parts - 1));
+            wgt[k] = k0 + k < g.parts ? ex2(__ldcg(pp + lane) - Mz) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              v[k][e] = __ldcg(reinterpret_cast<const float4 *>(pp + 64) +
+                               min(i0 + e * 32 + lane, items - 1));
           }
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float f =
+                  __shfl_sync(0xffffffffu, wgt[k], min((i0 + e * 32 + lane) / F4, 31));
+              acc[e].x = fmaf(v[k][e].x, f, acc[e].x);
+              acc[e].y = fmaf(v[k][e].y, f, acc[e].y);
+              acc[e].z = fmaf(v[k][e].z, f, acc[e].z);
+              acc[e].w = fmaf(v[k][e].w, f, acc[e].w);
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < E; ++e) {
           const int it = i0 + e * 32 + lane;
           const float f = __shfl_sync(0xffffffffu, inv, min(it / F4, 31));
-          if (it < items) {
-            const int rr = g.rt * kM + warp_row + it / F4;
-            const int tk = rr / p.G, h2 = g.head * p.G + rr - tk * p.G;
-            *reinterpret_cast<uint2 *>(p.out + (int64_t)(g.s.tok0 + tk) * p.o_token +
-                                       (int64_t)h2 * p.o_head + out0 + it % F4 * 4) =
+          if (it < items)
+            *reinterpret_cast<uint2 *>(p.out + out_at(warp_row + it / F4) + it % F4 * 4) =
                 make_uint2(f2h(acc[e].x * f, acc[e].y * f), f2h(acc[e].z * f, acc[e].w * f));
-          }
         }
       }
-      if (lane == 0) p.cnt[c_lo * kSoftmaxWarps + warp] = 0;
+      if (lane == 0) p.cnt[g.c_lo * kSoftmaxWarps + warp] = 0;
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA --
@@ -892,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Rows of a V block that no query of the tile sees may hold anything, and
     // a zero weight times NaN is NaN: they become zeros.
-    auto clean = [&](uint32_t r, int b, const Range &t) {
+    auto clean = [&](uint32_t r, int b, const Seg &t) {
       const int lo = t.lo - b * kN, hi = t.hi - b * kN;
       if (lo <= 0 && hi >= kN) return;
       uint8_t *v = kv_sm + (r % NS) * C::kStage;
@@ -903,9 +965,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_smem();
       __syncwarp();
     };
-    Walker<kM> w = start;
-    Seg g;
-    while (ok && w.next(p, g)) {
+    uint32_t n_seg = 0;
+    while (ok) {
+      Seg g;
+      if (!(ok = read_seg(n_seg, g))) break;
+      free_seg(n_seg++);
+      if (g.rows == 0) break;
       const int nb = g.b1 - g.b0;
       if (nb == 0) continue;
       if (!(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
@@ -921,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > 0) {
             const uint32_t c = blocks + j - 1;
             if (!(ok = wait_slot(ring))) break;
-            clean(ring, g.b0 + j - 1, g.r);
+            clean(ring, g.b0 + j - 1, g);
             if (!(ok = mbar_wait(smem_u32(&p_full[c & 1]), (c >> 1) & 1, abort_flag))) break;
             fence_after();
             pv(c & 1, 0, 256, ring, j > 1, false, nullptr);
@@ -940,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t v = ring, kn = ring + 1;
           const bool more = j + 1 < nb;
           if (!(ok = wait_slot(v))) break;
-          clean(v, g.b0 + j, g.r);
+          clean(v, g.b0 + j, g);
           for (int t = 0; t < stages; ++t) {
             if (!(ok = mbar_wait(smem_u32(&p_half[t]), n_stage[t] & 1, abort_flag))) break;
             fence_after();
@@ -972,9 +1037,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Lane i's page of block b (-1: none of its slots is needed).
     auto page_of = [&](const Seg &g, int b) -> int {
       const int key = b * kN + lane * box_rows;
-      if (lane >= ppb || key >= g.r.hi || key + box_rows <= g.r.lo) return -1;
+      if (lane >= ppb || key >= g.hi || key + box_rows <= g.lo) return -1;
       const int64_t pi = key >> p.page_shift;
-      const int page = pi < p.s.ld_table ? __ldg(p.s.table + (int64_t)g.s.i * p.s.ld_table + pi)
+      const int page = pi < p.s.ld_table ? __ldg(p.s.table + (int64_t)g.seq * p.s.ld_table + pi)
                                          : -1;
       if (page < 0 || page >= p.n_pages) {
         atomicOr(&g_attn_error, 4);
@@ -1013,8 +1078,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     Walker<kM> w = start;
-    Seg g;
-    while (ok && w.next(p, g)) {
+    // Tiles are announced one ahead of their loads, so that the softmax warps
+    // find the next one's queries to fetch.
+    uint32_t n_seg = 0;
+    auto announce = [&](const Seg &g) -> bool {
+      const uint32_t at = n_seg % kSegs;
+      if (n_seg >= kSegs &&
+          !mbar_wait(smem_u32(&seg_empty[at]), (n_seg / kSegs - 1) & 1, abort_flag))
+        return false;
+      if (lane == 0) {
+        seg_sm[at] = g;
+        mbar_arrive(smem_u32(&seg_full[at]));
+      }
+      __syncwarp();
+      ++n_seg;
+      return true;
+    };
+    Seg next = w.next(p);
+    ok = announce(next);
+    while (ok && next.rows > 0) {
+      const Seg g = next;
+      next = w.next(p);
+      if (!(ok = announce(next))) break;
       const int nb = g.b1 - g.b0;
       int page = nb > 0 ? page_of(g, g.b0) : -1, prev = -1;
       for (int j = 0; ok && j < nb; ++j) {
@@ -1131,6 +1216,7 @@ qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t
   p.o_token = o_token;
   p.o_head = o_head;
   p.G = (int)(hq / c.hkv);
+  p.inv_g = 1.0f / (float)p.G;
   p.hkv = c.hkv;
   p.n_pages = c.n_pages;
   p.page_size = c.page_size;
