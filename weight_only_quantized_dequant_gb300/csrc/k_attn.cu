@@ -39,8 +39,8 @@ __device__ int g_attn_error = 0;
 
 constexpr int kN = 128;                // keys per block
 constexpr int kSoftmaxWarps = 8;       // two warpgroups
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 384;          // the third warpgroup: MMA, loads, two spare warps
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10;  // and 11: queries
+constexpr int kThreads = 384;          // the third warpgroup: MMA, key and value loads, query loads (2)
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
 static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "register split");
 constexpr int kMaxCtas = 160;          // grid cap (partial slots in the workspace)
@@ -75,6 +75,7 @@ struct AttnParams {
   int64_t q_token, q_head, o_token, o_head;
   int G;                // query heads per KV head
   float inv_g;          // 1 / G
+  uint64_t magic_g;     // ceil(2^64 / G), 0 for G = 1
   int hkv, n_pages, page_size, page_shift;
   float c;              // logit units to log2: |scale| log2(e), or log2(e) with a cap
   float cap, cap_in;    // softcap, and |scale| / softcap * 2 log2(e)
@@ -286,6 +287,17 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_n_major) {
 }
 
 // --------------------------------------------------------------- schedule --
+// n / G for 0 <= n < 2^31, G <= 2^16: the excess of ceil(2^64 / G) over 2^64 / G
+// adds less than n / 2^64 < 1 / G.
+__device__ __forceinline__ int div_g(const AttnParams &p, int n) {
+  return p.magic_g ? (int)__umul64hi((uint64_t)(uint32_t)n, p.magic_g) : n;
+}
+// Non-negative quotient; the 64-bit division costs several times the 32-bit one.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // A sequence, and its row tiles per KV head.
 struct Seq {
   int i, tok0, q, kv;  // index, first token, new tokens, tokens held
@@ -315,9 +327,9 @@ __device__ __forceinline__ Range tile_range(const AttnParams &p, const Seq &s, i
   Range r;
   const int first = s.kv - s.q;  // position of the first new token
   const int last = min((rt + 1) * kM, s.rows) - 1;
-  r.hi = max(first + last / p.G + 1, 0);
+  r.hi = max(first + div_g(p, last) + 1, 0);
   r.lo = 0;
-  if (p.window > 0) r.lo = max(first + rt * kM / p.G - p.window + 1, 0);
+  if (p.window > 0) r.lo = max(first + div_g(p, rt * kM) - p.window + 1, 0);
   r.b0 = r.lo / kN;
   r.nb = r.hi > r.lo ? (r.hi + kN - 1) / kN - r.b0 : 0;
   return r;
@@ -330,11 +342,27 @@ __device__ __forceinline__ int tile_units(const Range &r) {
   return kTileUnits + max(r.nb, 1);
 }
 
-// Units of one KV head of a sequence.
+// Units of one KV head of each lane's sequence (whole warp): long sequences'
+// tiles are counted by all lanes together.
 template <int kM>
 __device__ __forceinline__ int64_t head_units(const AttnParams &p, const Seq &s) {
+  constexpr int kOwn = 4;
+  const int lane = threadIdx.x & 31;
   int64_t n = 0;
-  for (int rt = 0; rt < s.nt; ++rt) n += tile_units<kM>(tile_range<kM>(p, s, rt));
+  for (int rt = 0; rt < min(s.nt, kOwn); ++rt) n += tile_units<kM>(tile_range<kM>(p, s, rt));
+  for (unsigned m = __ballot_sync(0xffffffffu, s.nt > kOwn); m; m &= m - 1) {
+    const int src = __ffs(m) - 1;
+    Seq t;
+    t.q = __shfl_sync(0xffffffffu, s.q, src);
+    t.kv = __shfl_sync(0xffffffffu, s.kv, src);
+    t.rows = __shfl_sync(0xffffffffu, s.rows, src);
+    t.nt = __shfl_sync(0xffffffffu, s.nt, src);
+    int64_t v = 0;
+    for (int rt = kOwn + lane; rt < t.nt; rt += 32) v += tile_units<kM>(tile_range<kM>(p, t, rt));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == src) n += v;
+  }
   return n;
 }
 
@@ -359,11 +387,14 @@ template <int kM>
 struct Walker {
   int u, u_end, first;  // next unit, end, first unit of the current tile
   int seq, head, rt;
-  int64_t u_begin, total;
-  int ctas;
+  int64_t u_begin, each;  // the CTA's first unit; units per CTA, and one more for the first `more`
+  int more;
+  __device__ __forceinline__ int64_t begin_of(int cta) const { return each * cta + min(cta, more); }
   __device__ __forceinline__ int owner(int64_t unit) const {
-    return (int)(((unit + 1) * ctas - 1) / total);
+    const int64_t big = (each + 1) * more;
+    return unit < big ? (int)div64(unit, each + 1) : more + (int)div64(unit - big, each);
   }
+  __device__ __forceinline__ bool start(const AttnParams &p);
   __device__ __forceinline__ Seg next(const AttnParams &p) {
     Seg g;
     g.rows = 0;
@@ -391,7 +422,7 @@ struct Walker {
         ++rt;
       }
       if (b <= a) continue;  // only the fixed part of the tile's time falls to this CTA
-      const int i0 = row0 / p.G;
+      const int i0 = div_g(p, row0);
       g.rows = min(s.rows - row0, kM);
       g.tok = s.tok0 + i0;
       g.rem = row0 - i0 * p.G;
@@ -407,13 +438,99 @@ struct Walker {
         g.c_lo = owner(u_begin + tile_first + kTileUnits);
         g.parts = owner(u_begin + tile_first + units - 1) - g.c_lo + 1;
         if (g.parts == 1) g.slot = -1;
-        g.first_slot = total * g.c_lo / ctas >= u_begin + tile_first ? 0 : 1;
+        g.first_slot = begin_of(g.c_lo) >= u_begin + tile_first ? 0 : 1;
       }
       break;
     }
     return g;
   }
 };
+
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += u;
+  }
+  return v;
+}
+
+// This CTA's range of the units of all sequences, and the tile that holds its
+// first one (whole warp; kPer sequences a lane at a time).  False: no units.
+template <int kM>
+__device__ __forceinline__ bool Walker<kM>::start(const AttnParams &p) {
+  constexpr int kPer = 4;
+  const int lane = threadIdx.x & 31, S = p.s.n_seqs;
+  int64_t h[kPer];  // units per head of this lane's sequences
+  auto count = [&](int i0) {
+    Seq s[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {  // all loads ahead of their uses
+      const int i = i0 + lane * kPer + k;
+      s[k] = load_seq<kM>(p, min(i, S - 1));
+      if (i >= S) s[k].nt = 0;
+    }
+    int64_t n = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) n += h[k] = head_units<kM>(p, s[k]);
+    return warp_scan(n * p.hkv);
+  };
+  int64_t total = 0, incl = 0;
+  for (int i0 = 0; i0 < S; i0 += 32 * kPer) {
+    incl = count(i0);
+    total += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  const int ctas = (int)min((int64_t)gridDim.x, div64(total + kMinUnits - 1, kMinUnits));
+  if ((int)blockIdx.x >= ctas) return false;
+  each = div64(total, ctas);
+  more = (int)(total - each * ctas);
+  u_begin = begin_of(blockIdx.x);
+  u = 0;
+  u_end = (int)(begin_of(blockIdx.x + 1) - u_begin);
+  int64_t before = 0;
+  for (int i0 = 0;; i0 += 32 * kPer) {
+    if (S > 32 * kPer) incl = count(i0);
+    const unsigned m = __ballot_sync(0xffffffffu, before + incl > u_begin);
+    if (m == 0) {
+      before += __shfl_sync(0xffffffffu, incl, 31);
+      continue;
+    }
+    const int src = __ffs(m) - 1;
+    int64_t at = before + incl, hs = 0;
+    int i = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) at -= h[k] * p.hkv;  // units before this lane's sequences
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (hs == 0 && u_begin < at + h[k] * p.hkv) {
+        hs = h[k];
+        i = i0 + lane * kPer + k;
+      } else if (hs == 0) {
+        at += h[k] * p.hkv;
+      }
+    }
+    seq = __shfl_sync(0xffffffffu, i, src);
+    at = __shfl_sync(0xffffffffu, at, src);
+    hs = __shfl_sync(0xffffffffu, hs, src);
+    head = (int)div64(u_begin - at, hs);
+    at += head * hs;
+    const Seq s = load_seq<kM>(p, seq);
+    for (rt = 0;; rt += 32) {
+      const int n = rt + lane < s.nt ? tile_units<kM>(tile_range<kM>(p, s, rt + lane)) : 0;
+      const int64_t in = warp_scan(n);
+      const unsigned t = __ballot_sync(0xffffffffu, at + in > u_begin);
+      if (t == 0) {
+        at += __shfl_sync(0xffffffffu, in, 31);
+        continue;
+      }
+      const int l = __ffs(t) - 1;
+      first = (int)(at + __shfl_sync(0xffffffffu, in - n, l) - u_begin);
+      rt += l;
+      return true;
+    }
+  }
+}
 
 // ---------------------------------------------------------------- kernel --
 template <int D, int NQ, bool CAP>
@@ -429,11 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *s_full = kv_empty + kMaxStages, *p_full = s_full + 2, *o_done = p_full + 2;
   uint64_t *p_half = o_done + 2;  // NQ = 2: the first 64 keys' weights
   uint64_t *q_full = p_half + 2, *xbar = q_full + 1;  // xbar: one per 32-row quarter
-  uint64_t *seg_full = xbar + 4, *seg_empty = seg_full + kSegs;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(seg_empty + kSegs);
+  uint64_t *seg_full = xbar + 4, *seg_empty = seg_full + kSegs, *q_empty = seg_empty + kSegs;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_empty + 1);
   int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
-  int64_t *scan = reinterpret_cast<int64_t *>(base + 512);   // [12] warp sums, then the start
-  Seg *seg_sm = reinterpret_cast<Seg *>(base + 768);         // [kSegs]
+  Seg *seg_sm = reinterpret_cast<Seg *>(base + 512);         // [kSegs]
   float *xch = reinterpret_cast<float *>(base + 1024);       // [2][8 warps][32]
   uint8_t *q_sm = base + kHead, *kv_sm = q_sm + C::kQ;
 
@@ -450,83 +566,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&o_done[i]), 1);
       mbar_init(smem_u32(&p_half[i]), 4);
     }
-    mbar_init(smem_u32(q_full), kSoftmaxWarps);
+    mbar_init(smem_u32(q_full), 2);
+    mbar_init(smem_u32(q_empty), 1);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&xbar[i]), 2);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(smem_u32(&seg_full[i]), 1);
-      mbar_init(smem_u32(&seg_empty[i]), kSoftmaxWarps + 1);
+      mbar_init(smem_u32(&seg_empty[i]), kSoftmaxWarps + 3);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
-  // Units of all sequences, then the sequence that holds this CTA's first one:
-  // kThreads sequences at a time, one a thread.
-  int64_t mine = 0, total = 0;
-  for (int i = tid; i < p.s.n_seqs; i += kThreads)
-    mine += (int64_t)p.hkv * head_units<kM>(p, load_seq<kM>(p, i));
-  {
-    int64_t v = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) scan[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) total += scan[w];
-  }
-  int ctas = (int)min((int64_t)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
-  if ((int)blockIdx.x >= ctas) return;
-  const int64_t u_begin = total * blockIdx.x / ctas;
-  Walker<kM> start;
-  start.u_begin = u_begin;
-  start.total = total;
-  start.ctas = ctas;
-  start.u = 0;
-  start.u_end = (int)(total * (blockIdx.x + 1) / ctas - u_begin);
-  {
-    int64_t before = 0;
-    for (int i0 = 0; i0 < p.s.n_seqs; i0 += kThreads) {
-      const int i = i0 + tid;
-      const int64_t n =
-          i >= p.s.n_seqs ? 0
-          : p.s.n_seqs <= kThreads ? mine : (int64_t)p.hkv * head_units<kM>(p, load_seq<kM>(p, i));
-      int64_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      __syncthreads();
-      if (lane == 31) scan[warp] = incl;
-      __syncthreads();
-      int64_t off = before, sum = before;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) off += scan[w];
-        sum += scan[w];
-      }
-      if (n > 0 && u_begin >= off + incl - n && u_begin < off + incl) {
-        scan[12] = i;
-        scan[13] = off + incl - n;
-      }
-      before = sum;
-      if (before > u_begin) break;
-    }
-    __syncthreads();
-    start.seq = (int)scan[12];
-    const Seq q = load_seq<kM>(p, start.seq);
-    int64_t first = scan[13];
-    const int64_t per = head_units<kM>(p, q);
-    start.head = (int)((u_begin - first) / per);
-    first += start.head * per;
-    start.rt = 0;
-    for (;;) {
-      const int n = tile_units<kM>(tile_range<kM>(p, q, start.rt));
-      if (u_begin < first + n) break;
-      first += n;
-      ++start.rt;
-    }
-    start.first = (int)(first - u_begin);
-  }
-
+  Walker<kM> w;
+  w.u = w.u_end = 0;
+  if (warp == kLoadWarp) w.start(p);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -539,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = *tmem_slot;  // S of stage or buffer i at 128 i, O at 256 (+ D for stage 1)
 
-  // The n-th announced tile (softmax and MMA warps).
+  // The n-th announced tile (every warp but the one that announces).
   auto read_seg = [&](uint32_t n, Seg &g) {
     if (!mbar_wait(smem_u32(&seg_full[n % kSegs]), (n / kSegs) & 1, abort_flag)) return false;
     const uint4 *src = reinterpret_cast<const uint4 *>(&seg_sm[n % kSegs]);
@@ -553,6 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n % kSegs]));
   };
 
+  // n / G for n < G + 256: (n + 1/2) / G stays further from every whole number
+  // than fp32 rounding can move it.
+  auto row_token = [&](int n) { return (int)(((float)n + 0.5f) * p.inv_g); };
+
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -565,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t blocks = 0;   // key blocks so far (NQ = 2: of this stage)
     uint32_t ends = 0;     // segments finished (NQ = 2: of this stage)
     uint32_t swaps = 0;    // exchanges with the other warpgroup
-    uint32_t segs = 0;     // segments with keys so far
     bool ok = true;
     // The other warpgroup's value of this row (NQ = 1).
     auto exchange = [&](float v, float *other) -> bool {
@@ -578,61 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++swaps;
       return true;
     };
-    // n / G for n < G + 256: (n + 1/2) / G stays further from every whole number
-    // than fp32 rounding can move it.
-    auto row_token = [&](int n) { return (int)(((float)n + 0.5f) * p.inv_g); };
-    // This warp's rows of a tile's queries, into shared memory as a TMA copy
-    // with the 128-byte swizzle would lay them; rows past the tile are zeros.
-    constexpr int CPR = D / 8, RPP = 32 / CPR;        // 16-byte chunks a row, rows per pass
-    constexpr int QR = NQ == 2 ? 32 : 16;             // rows per warp
-    auto q_chunk = [&](int k, int &r, int &c) {       // pass k: tile row and chunk of this lane
-      r = warp * QR + k * RPP + lane / CPR;
-      c = lane % CPR;
-      return smem_u32(q_sm) + (r >> 7) * (128 * D * 2) + (c >> 3) * 16384 + (r & 127) * 128 +
-             (((c & 7) ^ (r & 7)) << 4);
-    };
-    auto load_q = [&](const Seg &t) {
-#pragma unroll 4
-      for (int k = 0; k < QR / RPP; ++k) {
-        int r, c;
-        const uint32_t dst = q_chunk(k, r, c);
-        const int n = t.rem + min(r, t.rows - 1), i = row_token(n);
-        const __half *src = p.q + (int64_t)(t.tok + i) * p.q_token +
-                            (int64_t)(t.head * p.G + n - i * p.G) * p.q_head + c * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                     "r"(r < t.rows ? 16 : 0)
-                     : "memory");
-      }
-    };
-    // The copies have landed: turn signs where asked, and tell the MMA warp.
-    auto publish_q = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (p.flip != 0 || p.keep != ~0u) {
-        for (int k = 0; k < QR / RPP; ++k) {
-          int r, c;
-          const uint32_t at = q_chunk(k, r, c);
-          uint32_t v[4];
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                       : "r"(at));
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at),
-                       "r"((v[0] & p.keep) ^ p.flip), "r"((v[1] & p.keep) ^ p.flip),
-                       "r"((v[2] & p.keep) ^ p.flip), "r"((v[3] & p.keep) ^ p.flip)
-                       : "memory");
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(q_full));
-    };
     uint32_t n_seg = 0;    // tiles read so far
-    // Queries of tile n, if it has keys.
-    auto load_next_q = [&](uint32_t n) {
-      Seg t;
-      if (!read_seg(n, t) || t.rows == 0 || t.b1 <= t.b0) return false;
-      load_q(t);
-      return true;
-    };
     // Four 16-byte pieces of this lane's row, out through shared memory so that
     // a store covers 64 contiguous bytes of 8 rows: dst[i] is where piece
     // lane % 4 of row 8 i + lane / 4 goes (null: nowhere).
@@ -656,7 +658,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    if (load_next_q(0)) publish_q();
     while (ok) {
       Seg g;
       if (!(ok = read_seg(n_seg, g))) break;
@@ -670,12 +671,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.0f;
       const int nb = g.b1 - g.b0;
       const bool active = nb > 0 && (NQ == 1 || wg == 0 || g.rows > 128);
-      if (!active) {
-        // a warpgroup without rows here must not run ahead of the other
-        if (nb > 0 && !(ok = mbar_wait(smem_u32(q_full), segs & 1, abort_flag))) break;
-        if (load_next_q(n_seg)) publish_q();
-      }
-      if (nb > 0) ++segs;
       // whole blocks of this range need no mask in this warp
       const int see_lo = __reduce_max_sync(0xffffffffu, lo), see_hi = __reduce_min_sync(0xffffffffu, hi);
       // NQ = 1: the previous block's product is complete.  Every live warp sees
@@ -688,14 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = NQ == 2 ? wg : (int)(blocks & 1);
         const uint32_t ph = NQ == 2 ? blocks & 1 : (blocks >> 1) & 1;
         if (!(ok = mbar_wait(smem_u32(&s_full[buf]), ph, abort_flag))) break;
-        // the tile's last S is done with its queries
-        const bool next_q = b == g.b1 - 1 && load_next_q(n_seg);
         if (live_rows == 0) {  // nothing of this warp is stored
           if (lane == 0) {
             if (NQ == 2) mbar_arrive(smem_u32(&p_half[buf]));
             mbar_arrive(smem_u32(&p_full[buf]));
           }
-          if (next_q) publish_q();
           continue;
         }
         fence_after();
@@ -710,11 +702,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < NC; ++k)  // cap tanh(t), tanh(t) = 1 - 2 / (1 + e^2t)
             s[k] = p.cap * (1.0f - 2.0f * rcp(1.0f + ex2(s[k] * p.cap_in)));
         }
-        const int k_hi = hi - b * kN - col0, k_lo = lo - b * kN - col0;
-        if (b * kN + col0 < see_lo || b * kN + col0 + NC > see_hi) {
+        // keys [k_lo, k_hi) of this row; a block that no bound cuts needs neither
+        if (b * kN + col0 + NC > see_hi) {
+          const int k_hi = hi - b * kN - col0;
 #pragma unroll
-          for (int k = 0; k < NC; ++k)
-            if (k >= k_hi || k < k_lo) s[k] = -INFINITY;
+          for (int k = 0; k < NC; ++k) s[k] = k < k_hi ? s[k] : -INFINITY;
+        }
+        if (b * kN + col0 < see_lo) {
+          const int k_lo = lo - b * kN - col0;
+#pragma unroll
+          for (int k = 0; k < NC; ++k) s[k] = k >= k_lo ? s[k] : -INFINITY;
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -779,7 +776,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
-        if (next_q) publish_q();
       }
       if (!ok) break;
       // ---- the tile's rows, or this CTA's part of them
@@ -863,14 +859,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       auto part_at = [&](int k) { return part_of(g.c_lo + k, k == 0 ? g.first_slot : 0); };
       float M = -INFINITY, L = 0.0f;
-#pragma unroll 4
-      for (int k = 0; k < g.parts; ++k) M = fmaxf(M, __ldcg(part_at(k) + lane));
-      const float Mz = M == -INFINITY ? 0.0f : M;
-#pragma unroll 4
-      for (int k = 0; k < g.parts; ++k) {
-        const float *pp = part_at(k);
-        L += __ldcg(pp + 32 + lane) * ex2(__ldcg(pp + lane) - Mz);
+      for (int k0 = 0; k0 < g.parts; k0 += 8) {
+        float mk[8], lk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float *pp = part_at(min(k0 + k, g.parts - 1));
+          mk[k] = k0 + k < g.parts ? __ldcg(pp + lane) : -INFINITY;
+          lk[k] = __ldcg(pp + 32 + lane);
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mn = fmaxf(mn, mk[k]);
+        const float z = mn == -INFINITY ? 0.0f : mn;
+        L *= ex2(M - z);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) L = fmaf(lk[k], ex2(mk[k] - z), L);
+        M = mn;
       }
+      const float Mz = M == -INFINITY ? 0.0f : M;
       const float inv = L > 0.0f ? 1.0f / L : 0.0f;
       // lanes share the rows' float4 columns, 4 each, 4 partials in flight
       constexpr int F4 = DC / 4, E = 4, U = 4;
@@ -926,10 +932,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const uint32_t tm = uniform(tmem), q_lo = uniform(sdesc_lo(smem_u32(q_sm), 16));
     // (whole warp) S = Q K^T of a stage into S buffer buf
-    auto qk = [&](int stage, int buf, uint32_t r, bool free_slot) {
+    auto qk = [&](int stage, int buf, uint32_t r, bool free_slot, bool free_q) {
       const uint32_t b = uniform(sdesc_lo(slot_addr(r), 16));
       const uint32_t a = q_lo + stage * (128 * D * 2 / 16), d = tm + uniform(128 * buf);
-      const uint32_t done = uniform(smem_u32(&s_full[buf]));
+      const uint32_t done = uniform(smem_u32(&s_full[buf])), qe = uniform(smem_u32(q_empty));
       const uint32_t empty = uniform(smem_u32(&kv_empty[r % NS]));
       if (elect_one()) {
 #pragma unroll
@@ -937,6 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma4_ss(d, a + k * 1024, b + k * 1024, kDescHi, id_qk, k > 0);
         mma_commit(done);
         if (free_slot) mma_commit(empty);
+        if (free_q) mma_commit(qe);
       }
     };
     // (whole warp) O (+)= P V: keys 64 half.. of S buffer buf
@@ -980,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j <= nb; ++j) {
           if (j < nb) {
             if (!(ok = wait_slot(ring))) break;
-            qk(0, (blocks + j) & 1, ring, true);
+            qk(0, (blocks + j) & 1, ring, true, j == nb - 1);
             ++ring;
           }
           if (j > 0) {
@@ -999,7 +1006,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int stages = g.rows > 128 ? 2 : 1;
         if (!(ok = wait_slot(ring))) break;
-        for (int t = 0; t < stages; ++t) qk(t, t, ring, t == stages - 1);
+        for (int t = 0; t < stages; ++t)
+          qk(t, t, ring, t == stages - 1, nb == 1 && t == stages - 1);
         ++ring;
         for (int j = 0; j < nb; ++j) {
           const uint32_t v = ring, kn = ring + 1;
@@ -1016,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pv(t, 1, 256 + t * D, v, true, t == stages - 1, more ? nullptr : &o_done[t]);
             if (more) {
               if (t == 0 && !(ok = wait_slot(kn))) break;
-              qk(t, t, kn, t == stages - 1);
+              qk(t, t, kn, t == stages - 1, j + 2 == nb && t == stages - 1);
             }
             __syncwarp();
           }
@@ -1025,8 +1033,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp != kLoadWarp) {
+  } else if (warp >= kQWarp) {
+    // ------------------------------------------------------------ queries --
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // A tile's queries, laid in shared memory as a TMA copy with the 128-byte
+    // swizzle would (rows of a group of heads are no box); rows past the tile are
+    // zeros.  Each warp takes half of the rows.
+    constexpr int CPR = D / 8, RPP = 32 / CPR;  // 16-byte chunks a row, rows per pass
+    constexpr int PASSES = kM / 2 / RPP;
+    const int c = lane % CPR;
+    auto tile_row = [&](int k) { return (warp - kQWarp) * (kM / 2) + k * RPP + lane / CPR; };
+    auto place = [&](int r) {
+      return smem_u32(q_sm) + (r >> 7) * (128 * D * 2) + (c >> 3) * 16384 + (r & 127) * 128 +
+             (((c & 7) ^ (r & 7)) << 4);
+    };
+    auto source = [&](const Seg &g, int r) {
+      const int n = g.rem + min(r, g.rows - 1), i = row_token(n);
+      return p.q + (int64_t)(g.tok + i) * p.q_token + (int64_t)(g.head * p.G + n - i * p.G) * p.q_head +
+             c * 8;
+    };
+    uint32_t n_seg = 0, segs = 0;
+    for (;;) {
+      Seg g;
+      if (!read_seg(n_seg, g)) break;
+      free_seg(n_seg++);
+      if (g.rows == 0) break;
+      if (g.b1 <= g.b0) continue;
+      // while the tile before still reads its own, bring these as far as L2
+      if (c % 8 == 0)
+        for (int k = 0; k < PASSES; ++k) {
+          const int r = tile_row(k);
+          if (r < g.rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(source(g, r)));
+        }
+      __syncwarp();
+      if (segs > 0 && !mbar_wait(smem_u32(q_empty), (segs - 1) & 1, abort_flag)) break;
+#pragma unroll 8
+      for (int k = 0; k < PASSES; ++k) {
+        const int r = tile_row(k);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(r)),
+                     "l"(source(g, r)), "r"(r < g.rows ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (p.flip != 0 || p.keep != ~0u) {  // a negative or zero scale
+        for (int k = 0; k < PASSES; ++k) {
+          const uint32_t at = place(tile_row(k));
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(at));
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at),
+                       "r"((v[0] & p.keep) ^ p.flip), "r"((v[1] & p.keep) ^ p.flip),
+                       "r"((v[2] & p.keep) ^ p.flip), "r"((v[3] & p.keep) ^ p.flip)
+                       : "memory");
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(q_full));
+      ++segs;
+    }
   } else {
     // --------------------------------------------------------------- load --
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -1077,9 +1143,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ring;
       return true;
     };
-    Walker<kM> w = start;
-    // Tiles are announced one ahead of their loads, so that the softmax warps
-    // find the next one's queries to fetch.
+    // Tiles are announced one ahead of their loads, so that the next one's
+    // queries are fetched meanwhile.
     uint32_t n_seg = 0;
     auto announce = [&](const Seg &g) -> bool {
       const uint32_t at = n_seg % kSegs;
@@ -1098,10 +1163,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = announce(next);
     while (ok && next.rows > 0) {
       const Seg g = next;
-      next = w.next(p);
-      if (!(ok = announce(next))) break;
       const int nb = g.b1 - g.b0;
       int page = nb > 0 ? page_of(g, g.b0) : -1, prev = -1;
+      next = w.next(p);
+      if (!(ok = announce(next))) break;
       for (int j = 0; ok && j < nb; ++j) {
         const int b = g.b0 + j;
         const int ahead = j + 1 < nb ? page_of(g, b + 1) : -1;
@@ -1217,6 +1282,7 @@ qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t
   p.o_head = o_head;
   p.G = (int)(hq / c.hkv);
   p.inv_g = 1.0f / (float)p.G;
+  p.magic_g = p.G > 1 ? ~(uint64_t)0 / (uint64_t)p.G + 1 : 0;
   p.hkv = c.hkv;
   p.n_pages = c.n_pages;
   p.page_size = c.page_size;
