@@ -151,12 +151,16 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+def fail(name: str, st: int) -> None:
+    """Raise the QzError of a qz_* call that returned the status st != 0."""
+    raise QzError(name, st, load().qz_last_cuda_error() if st == 4 else 0)
+
+
 def call(name: str, *args) -> None:
     """Call a qz_* function that returns a status; raise QzError on failure."""
-    lib = load()
-    st = getattr(lib, name)(*args)
+    st = getattr(load(), name)(*args)
     if st != 0:
-        raise QzError(name, st, lib.qz_last_cuda_error() if st == 4 else 0)
+        fail(name, st)
 
 
 def status(name: str, *args) -> int:

@@ -394,6 +394,7 @@ struct Walker {
     const int64_t big = (each + 1) * more;
     return unit < big ? (int)div64(unit, each + 1) : more + (int)div64(unit - big, each);
   }
+  template <int kPer>
   __device__ __forceinline__ bool start(const AttnParams &p);
   __device__ __forceinline__ Seg next(const AttnParams &p) {
     Seg g;
@@ -459,8 +460,8 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {
 // This CTA's range of the units of all sequences, and the tile that holds its
 // first one (whole warp; kPer sequences a lane at a time).  False: no units.
 template <int kM>
+template <int kPer>
 __device__ __forceinline__ bool Walker<kM>::start(const AttnParams &p) {
-  constexpr int kPer = 4;
   const int lane = threadIdx.x & 31, S = p.s.n_seqs;
   int64_t h[kPer];  // units per head of this lane's sequences
   auto count = [&](int i0) {
@@ -579,7 +580,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Walker<kM> w;
   w.u = w.u_end = 0;
-  if (warp == kLoadWarp) w.start(p);
+  if (warp == kLoadWarp) {  // one load's latency either way, few instructions for small batches
+    if (p.s.n_seqs <= 32)
+      w.template start<1>(p);
+    else
+      w.template start<8>(p);
+  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -878,43 +884,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float Mz = M == -INFINITY ? 0.0f : M;
       const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-      // lanes share the rows' float4 columns, 4 each, 4 partials in flight
+      // lanes share the rows' float4 columns, 4 each; 4 partials in flight
       constexpr int F4 = DC / 4, E = 4, U = 4;
       const int items = live_rows * F4;
+      const int64_t row_at = out_at(warp_row + lane);
       for (int i0 = 0; i0 < items; i0 += 32 * E) {
         float4 acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int k0 = 0; k0 < g.parts; k0 += U) {
           float4 v[U][E];
-          float wgt[U];
+          float mk[U];
 #pragma unroll
           for (int k = 0; k < U; ++k) {
+            const bool on = k0 + k < g.parts;
             const float *pp = part_at(min(k0 + k, g.parts - 1));
-            wgt[k] = k0 + k < g.parts ? ex2(__ldcg(pp + lane) - Mz) : 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              v[k][e] = __ldcg(reinterpret_cast<const float4 *>(pp + 64) +
-                               min(i0 + e * 32 + lane, items - 1));
-          }
-#pragma unroll
-          for (int k = 0; k < U; ++k)
+            mk[k] = on ? __ldcg(pp + lane) : -INFINITY;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-              const float f =
-                  __shfl_sync(0xffffffffu, wgt[k], min((i0 + e * 32 + lane) / F4, 31));
+              const int it = i0 + e * 32 + lane;
+              v[k][e] = on && it < items ? __ldcg(reinterpret_cast<const float4 *>(pp + 64) + it)
+                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const float wgt = ex2(mk[k] - Mz);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float f = __shfl_sync(0xffffffffu, wgt, min((i0 + e * 32 + lane) / F4, 31));
               acc[e].x = fmaf(v[k][e].x, f, acc[e].x);
               acc[e].y = fmaf(v[k][e].y, f, acc[e].y);
               acc[e].z = fmaf(v[k][e].z, f, acc[e].z);
               acc[e].w = fmaf(v[k][e].w, f, acc[e].w);
             }
+          }
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const int it = i0 + e * 32 + lane;
-          const float f = __shfl_sync(0xffffffffu, inv, min(it / F4, 31));
+          const int it = i0 + e * 32 + lane, row = min(it / F4, 31);
+          const float f = __shfl_sync(0xffffffffu, inv, row);
+          const int64_t at = __shfl_sync(0xffffffffu, row_at, row);
           if (it < items)
-            *reinterpret_cast<uint2 *>(p.out + out_at(warp_row + it / F4) + it % F4 * 4) =
+            *reinterpret_cast<uint2 *>(p.out + at + it % F4 * 4) =
                 make_uint2(f2h(acc[e].x * f, acc[e].y * f), f2h(acc[e].z * f, acc[e].w * f));
         }
       }
@@ -1047,10 +1059,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       return smem_u32(q_sm) + (r >> 7) * (128 * D * 2) + (c >> 3) * 16384 + (r & 127) * 128 +
              (((c & 7) ^ (r & 7)) << 4);
     };
-    auto source = [&](const Seg &g, int r) {
-      const int n = g.rem + min(r, g.rows - 1), i = row_token(n);
-      return p.q + (int64_t)(g.tok + i) * p.q_token + (int64_t)(g.head * p.G + n - i * p.G) * p.q_head +
-             c * 8;
+    // Visits this lane's chunk of its rows in order: f(row, source).
+    auto each_row = [&](const Seg &g, auto f) {
+      const int r0 = tile_row(0), n = g.rem + r0, i = row_token(n);
+      int head = n - i * p.G;
+      const __half *src = p.q + (int64_t)(g.tok + i) * p.q_token +
+                          (int64_t)(g.head * p.G + head) * p.q_head + c * 8;
+      const int64_t step = RPP * p.q_head, wrap = p.q_token - p.G * p.q_head;
+#pragma unroll 4
+      for (int k = 0; k < PASSES; ++k) {
+        f(r0 + k * RPP, src);
+        src += step;
+        for (head += RPP; head >= p.G; head -= p.G) src += wrap;
+      }
     };
     uint32_t n_seg = 0, segs = 0;
     for (;;) {
@@ -1059,21 +1080,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       free_seg(n_seg++);
       if (g.rows == 0) break;
       if (g.b1 <= g.b0) continue;
-      // while the tile before still reads its own, bring these as far as L2
-      if (c % 8 == 0)
-        for (int k = 0; k < PASSES; ++k) {
-          const int r = tile_row(k);
-          if (r < g.rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(source(g, r)));
-        }
-      __syncwarp();
-      if (segs > 0 && !mbar_wait(smem_u32(q_empty), (segs - 1) & 1, abort_flag)) break;
-#pragma unroll 8
-      for (int k = 0; k < PASSES; ++k) {
-        const int r = tile_row(k);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(r)),
-                     "l"(source(g, r)), "r"(r < g.rows ? 16 : 0)
-                     : "memory");
+      if (segs > 0) {
+        // while the tile before still reads its own, bring these as far as L2
+        if (c % 8 == 0)
+          each_row(g, [&](int r, const __half *src) {
+            if (r < g.rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+          });
+        __syncwarp();
+        if (!mbar_wait(smem_u32(q_empty), (segs - 1) & 1, abort_flag)) break;
       }
+      each_row(g, [&](int r, const __half *src) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(r)),
+                     "l"(r < g.rows ? src : p.q), "r"(r < g.rows ? 16 : 0)
+                     : "memory");
+      });
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (p.flip != 0 || p.keep != ~0u) {  // a negative or zero scale
         for (int k = 0; k < PASSES; ++k) {
@@ -1100,18 +1120,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const int ppb = p.page_size >= kN ? 1 : kN >> p.page_shift;  // pages per block
     const int box_rows = min(p.page_size, kN);
-    // Lane i's page of block b (-1: none of its slots is needed).
+    // Page ids, 32 entries of the table at a time and one batch ahead, an entry a
+    // lane (-1: none of its slots is needed).
+    int batch = 0, ids = -1, ids_ahead = -1;  // first entry of ids; ids; the next 32
+    auto fetch = [&](const Seg &g, int first) -> int {
+      const int pi = first + lane;
+      const int64_t key = (int64_t)pi << p.page_shift;
+      if (key >= g.hi || key + p.page_size <= g.lo) return -1;
+      const int id = pi < p.s.ld_table ? __ldg(p.s.table + (int64_t)g.seq * p.s.ld_table + pi) : -2;
+      return id == -1 ? -2 : id;
+    };
+    // Lane i's page of block b; outside the pool: an id outside the map, so that
+    // the copy fills zeros.
     auto page_of = [&](const Seg &g, int b) -> int {
-      const int key = b * kN + lane * box_rows;
-      if (lane >= ppb || key >= g.hi || key + box_rows <= g.lo) return -1;
-      const int64_t pi = key >> p.page_shift;
-      const int page = pi < p.s.ld_table ? __ldg(p.s.table + (int64_t)g.seq * p.s.ld_table + pi)
-                                         : -1;
-      if (page < 0 || page >= p.n_pages) {
-        atomicOr(&g_attn_error, 4);
-        return INT32_MAX;  // outside the map: the copy fills zeros
+      const int pi = (int)(((int64_t)b * kN + lane * box_rows) >> p.page_shift);
+      if (__shfl_sync(0xffffffffu, pi, ppb - 1) >= batch + 32) {
+        batch += 32;
+        ids = ids_ahead;
+        ids_ahead = fetch(g, batch + 32);
       }
-      return page;
+      const int id = __shfl_sync(0xffffffffu, ids, pi - batch);
+      if (lane >= ppb || id == -1) return -1;
+      if (id < 0 || id >= p.n_pages) {
+        atomicOr(&g_attn_error, 4);
+        return INT32_MAX;
+      }
+      return id;
     };
     auto issue = [&](const CUtensorMap *map, const Seg &g, int b, int page) -> bool {
       const int slot = ring % NS;
@@ -1143,8 +1177,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ring;
       return true;
     };
-    // Tiles are announced one ahead of their loads, so that the next one's
-    // queries are fetched meanwhile.
+    // The next tile is announced before a tile's loads, so that its queries come
+    // to L2 early, but for the CTA's first tile, whose own loads come first.
     uint32_t n_seg = 0;
     auto announce = [&](const Seg &g) -> bool {
       const uint32_t at = n_seg % kSegs;
@@ -1164,21 +1198,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && next.rows > 0) {
       const Seg g = next;
       const int nb = g.b1 - g.b0;
-      int page = nb > 0 ? page_of(g, g.b0) : -1, prev = -1;
-      next = w.next(p);
-      if (!(ok = announce(next))) break;
-      for (int j = 0; ok && j < nb; ++j) {
+      if (nb > 0) {
+        batch = (int)(((int64_t)g.b0 * kN) >> p.page_shift);
+        ids = fetch(g, batch);
+        ids_ahead = fetch(g, batch + 32);
+      }
+      int prev = -1;
+      if (n_seg > 1) ok = announce(next = w.next(p));
+      for (int j = 0; ok && j < max(nb, 1); ++j) {
         const int b = g.b0 + j;
-        const int ahead = j + 1 < nb ? page_of(g, b + 1) : -1;
-        ok = issue(&p.kmap, g, b, page);
-        if (NQ == 1) {  // K0, K1, V0, K2, V1, ..., the order in which they are used
-          if (ok && j > 0) ok = issue(&p.vmap, g, b - 1, prev);
-          if (ok && j == nb - 1) ok = issue(&p.vmap, g, b, page);
-        } else if (ok) {
-          ok = issue(&p.vmap, g, b, page);
+        if (nb > 0) {
+          const int page = page_of(g, b);
+          ok = issue(&p.kmap, g, b, page);
+          if (NQ == 1) {  // K0, K1, V0, K2, V1, ..., the order in which they are used
+            if (ok && j > 0) ok = issue(&p.vmap, g, b - 1, prev);
+            if (ok && j == nb - 1) ok = issue(&p.vmap, g, b, page);
+          } else if (ok) {
+            ok = issue(&p.vmap, g, b, page);
+          }
+          prev = page;
         }
-        prev = page;
-        page = ahead;
+        if (ok && j == 0 && n_seg == 1) ok = announce(next = w.next(p));
       }
     }
     if (!ok) {  // let the copies in flight land before the CTA's memory goes

@@ -15,8 +15,12 @@ import torch
 
 from . import _lib
 
-_F16 = torch.float16
+_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() costs 10x as much
+
+# A decode step makes hundreds of these calls and the kernels of small batches
+# take a few microseconds, so the checks below are few attribute reads each and
+# the library is called without another layer.
 
 
 def _stream_of(t: torch.Tensor, stream) -> int:
@@ -32,47 +36,45 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type, allocated as by _empty."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _rows(t: torch.Tensor, what: str, shape=None, dtype=_F16) -> torch.Tensor:
-    """A CUDA matrix whose rows are contiguous."""
+def _cuda_or_raise(t) -> None:
     if not t.is_cuda:
         raise ValueError("libqz works on CUDA tensors only (no CPU fallback)")
-    if t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a 2-D {dtype} tensor with contiguous rows is needed")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
-    return t
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride; that of one row (which torch may report as anything) is its length."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t: torch.Tensor, what: str, shape, dtype=_F16) -> int:
+    """Row stride of a CUDA matrix with contiguous rows (that of a single row,
+    which torch may report as anything, is its length)."""
+    if t.is_cuda and t.dtype is dtype and t.shape == shape:
+        if t.is_contiguous():
+            return shape[1]
+        if t.stride(1) == 1 or shape[1] <= 1:
+            return t.stride(0) if shape[0] > 1 else shape[1]
+    _cuda_or_raise(t)
+    raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}; a {dtype} "
+                     f"matrix {tuple(shape)} with contiguous rows is needed")
 
 
-def _vec(t: torch.Tensor, what: str, n: int, dtype) -> torch.Tensor:
-    if not t.is_cuda:
-        raise ValueError("libqz works on CUDA tensors only (no CPU fallback)")
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous {dtype} vector of {n} is needed")
-    return t
+def _vec(t: torch.Tensor, what: str, n: int, dtype) -> int:
+    """Address of a contiguous CUDA vector of n."""
+    if t.is_cuda and t.dtype is dtype and t.shape == (n,) and t.is_contiguous():
+        return t.data_ptr()
+    _cuda_or_raise(t)
+    raise ValueError(f"{what}: a contiguous {dtype} vector of {n} is needed")
 
 
 # ------------------------------------------------------------------ norm ---
-def _norm_args(x, weight, residual, residual_out):
-    x = _rows(x, "x")
-    T, K = x.shape
-    _vec(weight, "weight", K, _F16)
-    if residual is not None:
-        _rows(residual, "residual", (T, K))
-    if residual_out is not None:
-        _rows(residual_out, "residual_out", (T, K))
-    return T, K
-
-
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             residual: torch.Tensor | None = None, w_bias: float = 0.0,
             out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
@@ -81,20 +83,26 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     weight) for fp16 rows x [T, K].  h, the next residual, goes to residual_out
     (may be residual or x; allocated if None); without a residual h is x itself
     and is not written."""
-    T, K = _norm_args(x, weight, residual, residual_out)
+    shape = x.shape
+    _need(len(shape) == 2, "x: two dimensions are needed")
+    T, K = shape
+    ldx = _rows(x, "x", shape)
+    w = _vec(weight, "weight", K, _F16)
+    r = ldr = h = ldh = 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", shape)
+        if residual_out is None:
+            residual_out = _like(x, stream)
+    if residual_out is not None:
+        h, ldh = residual_out.data_ptr(), _rows(residual_out, "residual_out", shape)
     if out is None:
-        out = _empty((T, K), _F16, x.device, stream)
-    else:
-        _rows(out, "out", (T, K))
-    h = residual_out
-    if h is None and residual is not None:
-        h = _empty((T, K), _F16, x.device, stream)
-    _lib.call("qz_rmsnorm", x.data_ptr(), _ld(x),
-              None if residual is None else residual.data_ptr(),
-              0 if residual is None else _ld(residual), weight.data_ptr(), w_bias, eps, T, K,
-              out.data_ptr(), _ld(out), None if h is None else h.data_ptr(),
-              0 if h is None else _ld(h), _stream_of(x, stream))
-    return out, (x if h is None else h)
+        out = _like(x, stream)
+    ldy = _rows(out, "out", shape)
+    st = _lib.load().qz_rmsnorm(x.data_ptr(), ldx, r, ldr, w, w_bias, eps, T, K, out.data_ptr(),
+                                ldy, h, ldh, _stream_of(x, stream))
+    if st:
+        _lib.fail("qz_rmsnorm", st)
+    return out, (x if residual_out is None else residual_out)
 
 
 def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -103,24 +111,29 @@ def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
                  residual_out: torch.Tensor | None = None, stream=None):
     """(q, scale, h): the rows of ``rmsnorm`` as int8 codes [T, K] and one fp32
     scale per row (y ~ q * scale, scale = max|y| / 127)."""
-    T, K = _norm_args(x, weight, residual, residual_out)
+    shape = x.shape
+    _need(len(shape) == 2, "x: two dimensions are needed")
+    T, K = shape
+    ldx = _rows(x, "x", shape)
+    w = _vec(weight, "weight", K, _F16)
+    r = ldr = h = ldh = 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", shape)
+        if residual_out is None:
+            residual_out = _like(x, stream)
+    if residual_out is not None:
+        h, ldh = residual_out.data_ptr(), _rows(residual_out, "residual_out", shape)
     if out is None:
-        out = _empty((T, K), torch.int8, x.device, stream)
-    else:
-        _rows(out, "out", (T, K), torch.int8)
+        out = _empty(shape, torch.int8, x.device, stream)
+    ldq = _rows(out, "out", shape, torch.int8)
     if scale is None:
-        scale = _empty((T,), torch.float32, x.device, stream)
-    else:
-        _vec(scale, "scale", T, torch.float32)
-    h = residual_out
-    if h is None and residual is not None:
-        h = _empty((T, K), _F16, x.device, stream)
-    _lib.call("qz_rmsnorm_int8", x.data_ptr(), _ld(x),
-              None if residual is None else residual.data_ptr(),
-              0 if residual is None else _ld(residual), weight.data_ptr(), w_bias, eps, T, K,
-              out.data_ptr(), _ld(out), scale.data_ptr(), None if h is None else h.data_ptr(),
-              0 if h is None else _ld(h), _stream_of(x, stream))
-    return out, scale, (x if h is None else h)
+        scale = _empty((T,), _F32, x.device, stream)
+    s = _vec(scale, "scale", T, _F32)
+    st = _lib.load().qz_rmsnorm_int8(x.data_ptr(), ldx, r, ldr, w, w_bias, eps, T, K,
+                                     out.data_ptr(), ldq, s, h, ldh, _stream_of(x, stream))
+    if st:
+        _lib.fail("qz_rmsnorm_int8", st)
+    return out, scale, (x if residual_out is None else residual_out)
 
 
 # ----------------------------------------------------------- paged cache ---
@@ -143,6 +156,7 @@ class PagedKV:
                                  k.shape[3], k.stride(0), k.stride(1), k.stride(2), v.stride(0),
                                  v.stride(1), v.stride(2))
         self._ref = ctypes.byref(self._arg)
+        self.shape = tuple(k.shape)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
@@ -173,15 +187,13 @@ class SeqBatch:
 
     def __post_init__(self):
         S = self.kv_len.shape[0]
-        _vec(self.cu_q, "cu_q", S + 1, torch.int32)
-        _vec(self.kv_len, "kv_len", S, torch.int32)
-        _rows(self.page_table, "page_table", dtype=torch.int32)
-        _need(self.page_table.shape[0] == S, "page_table: one row per sequence")
-        # a row's stride bounds what may be read of it
-        ld = self.page_table.stride(0) if S > 1 else self.page_table.shape[1]
-        _need(ld >= self.page_table.shape[1], "page_table: rows must not overlap")
-        self.page_table = self.page_table if ld == self.page_table.shape[1] \
-            else self.page_table.contiguous()
+        _vec(self.cu_q, "cu_q", S + 1, _I32)
+        _vec(self.kv_len, "kv_len", S, _I32)
+        _need(self.page_table.dim() == 2 and self.page_table.shape[0] == S,
+              "page_table: one row per sequence")
+        # the row stride is also the number of entries that may be read
+        _need(_rows(self.page_table, "page_table", self.page_table.shape, _I32)
+              == self.page_table.shape[1], "page_table: a contiguous table is needed")
         self._arg = _lib.SeqBatchArg(S, 0, self.cu_q.data_ptr(), self.kv_len.data_ptr(),
                                      self.page_table.data_ptr(), self.page_table.shape[1])
         self._ref = ctypes.byref(self._arg)
@@ -191,14 +203,15 @@ class SeqBatch:
         return self.kv_len.shape[0]
 
 
-def _heads(t: torch.Tensor, what: str, T: int, heads: int | None, D: int) -> torch.Tensor:
-    if not t.is_cuda:
-        raise ValueError("libqz works on CUDA tensors only (no CPU fallback)")
-    if t.dtype != _F16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.stride(2) != 1:
-        raise ValueError(f"{what}: fp16 [{T}, heads, {D}] with contiguous rows is needed")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{what}: {t.shape[1]} heads, expected {heads}")
-    return t
+def _heads(t: torch.Tensor, what: str, T: int, heads: int, D: int):
+    """Token and head strides of a CUDA fp16 [T, heads, D] with contiguous rows."""
+    if t.is_cuda and t.dtype is _F16 and t.shape == (T, heads, D):
+        st, sh, sd = t.stride()
+        if sd == 1:
+            return st, sh
+    _cuda_or_raise(t)
+    raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}; fp16 "
+                     f"{(T, heads, D)} with contiguous rows is needed")
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKV,
@@ -208,24 +221,28 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedK
     keys k [T, kv_heads, D] by their positions, and store keys and values v
     into their slots of the cache.  rope: fp32 [positions, D], cosines then
     sines (``rope_table``), or None for no rotation."""
-    T, D, hkv = q.shape[0], cache.head_dim, cache.n_kv_heads
-    _heads(q, "q", T, None, D)
-    _heads(k, "k", T, hkv, D)
-    _heads(v, "v", T, hkv, D)
-    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 2
-                             or rope.shape[1] != D or not rope.is_contiguous()
-                             or not rope.is_cuda):
-        raise ValueError(f"rope: a contiguous fp32 CUDA tensor [positions, {D}] is needed")
+    _need(q.dim() == 3, "q: three dimensions are needed")
+    T, H, _ = q.shape
+    _, hkv, _, D = cache.shape
+    qt, qh = _heads(q, "q", T, H, D)
+    kt, kh = _heads(k, "k", T, hkv, D)
+    vt, vh = _heads(v, "v", T, hkv, D)
+    rp = n = 0
+    if rope is not None:
+        if not (rope.is_cuda and rope.dtype is _F32 and rope.dim() == 2 and rope.shape[1] == D
+                and rope.is_contiguous()):
+            raise ValueError(f"rope: a contiguous fp32 CUDA tensor [positions, {D}] is needed")
+        rp, n = rope.data_ptr(), rope.shape[0]
     if q_out is None:
-        q_out = _empty(q.shape, _F16, q.device, stream)
+        q_out, ot, oh = _empty((T, H, D), _F16, q.device, stream), H * D, D
     else:
-        _heads(q_out, "q_out", T, q.shape[1], D)
+        ot, oh = _heads(q_out, "q_out", T, H, D)
     seqs._arg.n_tokens = T
-    _lib.call("qz_rope_append", q.data_ptr(), q.shape[1], q.stride(0), q.stride(1),
-              k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-              None if rope is None else rope.data_ptr(), 0 if rope is None else rope.shape[0],
-              cache._ref, seqs._ref, q_out.data_ptr(), q_out.stride(0), q_out.stride(1),
-              _stream_of(q, stream))
+    st = _lib.load().qz_rope_append(q.data_ptr(), H, qt, qh, k.data_ptr(), kt, kh, v.data_ptr(),
+                                    vt, vh, rp, n, cache._ref, seqs._ref, q_out.data_ptr(), ot,
+                                    oh, _stream_of(q, stream))
+    if st:
+        _lib.fail("qz_rope_append", st)
     return q_out
 
 
@@ -260,22 +277,25 @@ def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: floa
     D^-0.5; softcap > 0 caps logits as softcap * tanh(x / softcap); window > 0
     limits every query to its last `window` keys.  workspace: from
     ``attention_workspace`` (made here if None)."""
-    T, D = q.shape[0], cache.head_dim
-    _heads(q, "q", T, None, D)
-    if q.shape[1] < 1 or q.shape[1] % cache.n_kv_heads:
-        raise ValueError(f"q: {q.shape[1]} heads over {cache.n_kv_heads} KV heads")
+    _need(q.dim() == 3, "q: three dimensions are needed")
+    T, H, _ = q.shape
+    _, hkv, _, D = cache.shape
+    qt, qh = _heads(q, "q", T, H, D)
+    if H < 1 or H % hkv:
+        raise ValueError(f"q: {H} heads over {hkv} KV heads")
     if out is None:
-        out = _empty(q.shape, _F16, q.device, stream)
+        out, ot, oh = _empty((T, H, D), _F16, q.device, stream), H * D, D
     else:
-        _heads(out, "out", T, q.shape[1], D)
+        ot, oh = _heads(out, "out", T, H, D)
     if workspace is None:
-        workspace = attention_workspace(T, seqs.n_seqs, q.shape[1], cache.n_kv_heads, D,
-                                        q.device, stream)
+        workspace = attention_workspace(T, seqs.n_seqs, H, hkv, D, q.device, stream)
     seqs._arg.n_tokens = T
-    _lib.call("qz_attention_paged", q.data_ptr(), q.shape[1], q.stride(0), q.stride(1),
-              cache._ref, seqs._ref, D ** -0.5 if scale is None else scale, softcap, window,
-              out.data_ptr(), out.stride(0), out.stride(1), workspace.data_ptr(),
-              workspace.numel(), _stream_of(q, stream))
+    st = _lib.load().qz_attention_paged(q.data_ptr(), H, qt, qh, cache._ref, seqs._ref,
+                                        D ** -0.5 if scale is None else scale, softcap, window,
+                                        out.data_ptr(), ot, oh, workspace.data_ptr(),
+                                        workspace.numel(), _stream_of(q, stream))
+    if st:
+        _lib.fail("qz_attention_paged", st)
     return out
 
 
@@ -299,14 +319,15 @@ class LoraAdapters:
         _need(b.shape[0] == n and b.shape[2] == R, "b: shape does not match a")
         _need((a.stride(2) == 1 or K == 1) and (b.stride(2) == 1 or R == 1),
               "a and b: contiguous rows")
-        _vec(self.scale, "scale", n, torch.float32)
+        _vec(self.scale, "scale", n, _F32)
         if self.rank is not None:
-            _vec(self.rank, "rank", n, torch.int32)
+            _vec(self.rank, "rank", n, _I32)
         self._arg = _lib.LoraArg(a.data_ptr(), b.data_ptr(), self.scale.data_ptr(),
                                  None if self.rank is None else self.rank.data_ptr(), n, R, K,
                                  b.shape[1], a.stride(0), a.stride(1) if R > 1 else K,
                                  b.stride(0), b.stride(1) if b.shape[1] > 1 else R)
         self._ref = ctypes.byref(self._arg)
+        self.sizes = (K, R, b.shape[1])
 
     @property
     def K(self) -> int:
@@ -334,17 +355,19 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters, index: torch.
     """out[t] = y[t] + scale_a * B_a (A_a x[t]) with a = index[t] (int32; -1: no
     adapter).  x [T, K] is the projection's input and y [T, N] its output (out
     may be y)."""
-    T = x.shape[0]
-    _rows(x, "x", (T, adapters.K))
-    _rows(y, "y", (T, adapters.N))
-    _vec(index, "index", T, torch.int32)
+    _need(x.dim() == 2, "x: two dimensions are needed")
+    T, K, R, N = x.shape[0], *adapters.sizes
+    ldx = _rows(x, "x", (T, K))
+    ldy = _rows(y, "y", (T, N))
+    i = _vec(index, "index", T, _I32)
     if out is None:
-        out = _empty((T, adapters.N), _F16, x.device, stream)
-    else:
-        _rows(out, "out", (T, adapters.N))
+        out = _like(y, stream)
+    ldo = _rows(out, "out", (T, N))
     if workspace is None:
-        workspace = lora_workspace(T, adapters.K, adapters.R, x.device, stream)
-    _lib.call("qz_lora", adapters._ref, index.data_ptr(), T, x.data_ptr(), _ld(x), y.data_ptr(),
-              _ld(y), out.data_ptr(), _ld(out), workspace.data_ptr(), workspace.numel(),
-              _stream_of(x, stream))
+        workspace = lora_workspace(T, K, R, x.device, stream)
+    st = _lib.load().qz_lora(adapters._ref, i, T, x.data_ptr(), ldx, y.data_ptr(), ldy,
+                             out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(),
+                             _stream_of(x, stream))
+    if st:
+        _lib.fail("qz_lora", st)
     return out
