@@ -1282,8 +1282,7 @@ qz_status pool_map(CUtensorMap *map, const __half *base, const PagedView &c, int
 template <int D, int NQ, bool CAP>
 qz_status launch(const AttnParams &p, int sms, cudaStream_t s) {
   using C = Cfg<D, NQ>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      attn_kernel<D, NQ, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e = allow_smem<attn_kernel<D, NQ, CAP>>(C::kSmem);
   if (e != cudaSuccess) return cuda_status(e);
   attn_kernel<D, NQ, CAP><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, C::kSmem, s>>>(p);
   return launch_status();

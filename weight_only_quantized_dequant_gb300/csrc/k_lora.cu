@@ -1,18 +1,21 @@
 // Low-rank adapters beside a shared projection: out = y + s_a B_a (A_a x).
 //
 // Two launches over the same rows, on warp-level matrix instructions (rank and
-// run lengths are far below a tcgen05 tile; HBM or launch latency bounds every
-// size, not the products):
+// run lengths are far below a tcgen05 tile):
 //   down: u = A_a x.  A CTA takes a few rows and a slice of K; neighbouring rows
 //     of one adapter (a run) are the 8 columns of m16n8k16 products whose 16
 //     rows are ranks, so one request a run wastes columns, not reads.  Its 8
-//     warps split the slice, add up through shared memory in warp order, and
-//     leave one fp32 partial of u per slice in the workspace.
-//   up: B_a u.  A CTA adds the slices' partials in order, then its warps take 64
-//     outputs each.  u enters as two fp16 parts of its value scaled by a power of
-//     two per row (22 bits and more, any fp32 range); sums stay fp32 and y is
-//     added before the one rounding.  The launch overlaps the first one's tail
-//     and prefetches B meanwhile.
+//     warps split the slice and add up through shared memory, the slices of a
+//     row are a cluster and add up through distributed shared memory, always in
+//     the same order.
+//   up: B_a u.  A CTA keeps its rows' u in shared memory; a warp takes 64 outputs
+//     at a time.  The launch overlaps the first one, and its first B and y are on
+//     their way before u is.
+// Precision of u: its fp32 sum is scaled by a power of two per row (any fp32
+// range) and enters the second product as fp16.  From K = 4096 on that rounding,
+// 2^-12 of u, is within the bound K 2^-24 of the fp32 sums that form u; below, a
+// second fp16 part carries the remainder (22 bits), at the price of twice the
+// products.  Sums stay fp32 and y is added before the one rounding.
 // In both, a thread's 16-byte load holds 8 consecutive k of its fragment row:
 // the two operands use the same order of k, so no shuffle is needed; likewise the
 // rows of B_a are dealt so that a thread ends with 8 consecutive outputs.
@@ -24,32 +27,35 @@ namespace {
 
 __device__ int g_lora_error = 0;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;                   // down
 constexpr int kThreads = 32 * kWarps;
+constexpr int kUpWarps = 4;
 constexpr int kSub = 64;                    // k per warp and step
 constexpr int kSlice = kSub * kWarps;       // k per CTA and step
 constexpr int kMaxRows = 32;                // rows of a CTA (one per lane when runs are found)
-constexpr int kRowRanks = 2048;             // rows x padded rank of a CTA (shared memory)
-constexpr int kMaxSlices = 16;              // partials of u per row
 constexpr int kOut = 64;                    // outputs per warp and step
+constexpr int64_t kOnePart = 4096;          // K from which u enters as one fp16 part
+constexpr int kRowRanks = 2048;             // rows x padded rank of a CTA (shared memory)
+constexpr int kMaxSlices = 8;               // CTAs of a cluster, which split K
 
 struct LoraParams {
   const __half *a, *b, *x, *y;
   __half *out;
   const float *scale;
   const int32_t *rank, *index;
-  int n_adapters, R, Rp, K, N;  // Rp: R rounded up to 16
+  int n_adapters, R, Rp, Rk, K, N;  // Rp, Rk: R rounded up to 16 and 32
   int64_t T, a_adapter, a_row, b_adapter, b_row, ldx, ldy, ldo;
-  float *u;       // [slices][T][Rp]
-  int slices;     // partials per row
+  __half *uh, *ul;  // [T][Rk] u 2^e, and its remainder where two parts are used
+  int two;
+  float *fs;        // [T] scale_a 2^-e
+  int slices;
   int k_slice;    // k per CTA (a multiple of kSlice)
   int rows_down, rows_up;
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -99,104 +105,105 @@ __device__ __forceinline__ int rank_of(const LoraParams &p, int a) {
   return p.rank ? min(max(__ldg(p.rank + a), 0), p.R) : p.R;
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) lora_down_kernel(const LoraParams p) {
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// NT: 8-row column tiles of a CTA (1: at most 8 rows, where latency counts and
+// the registers hold more of K at a time; 4: up to 32 rows).
+template <bool VEC, int NT>
+__global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const LoraParams p) {
   extern __shared__ float part[];  // [kWarps][rows][Rp]
   asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int MT = NT == 1 ? 2 : 1, KU = NT == 1 ? 2 : 1;  // 16-rank tiles, steps of K at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const int64_t t0 = (int64_t)blockIdx.x * p.rows_down;
   const int rows = (int)min((int64_t)p.rows_down, p.T - t0);
   const int k_begin = blockIdx.y * p.k_slice, k_end = min(k_begin + p.k_slice, p.K);
   const Runs runs(p, t0, rows);
+  const uint4 z = make_uint4(0, 0, 0, 0);
   for (int at = 0, end; at < rows; at = end) {
     const int a = runs.run(at, end);
     if (a < 0) continue;
     const int rank = rank_of(p, a);
-    const __half *A = p.a + a * p.a_adapter;
-    for (int m0 = 0; m0 < rank; m0 += 16) {
-      float c[4][4];
+    const __half *A = p.a + a * p.a_adapter + g * p.a_row;
+    const __half *X = p.x + (t0 + at + g) * p.ldx;
+    for (int m0 = 0; m0 < rank; m0 += 16 * MT) {
+      float c[MT][NT][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
-      const int r0 = m0 + g, r1 = m0 + g + 8;
-      for (int k0 = k_begin + warp * kSub; k0 < k_end; k0 += kSlice) {
-        uint4 av[2][2], xv[2][4];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = k0 + 32 * h + 8 * tig;
-          const uint4 z = make_uint4(0, 0, 0, 0);
-          av[h][0] = r0 < rank ? load8<VEC>(A + r0 * p.a_row, k, k_end) : z;
-          av[h][1] = r1 < rank ? load8<VEC>(A + r1 * p.a_row, k, k_end) : z;
+          for (int i = 0; i < 4; ++i) c[m][n][i] = 0.0f;
+      for (int k0 = k_begin + warp * kSub; k0 < k_end; k0 += KU * kSlice) {
+        uint4 av[KU][2][MT][2], xv[KU][2][NT];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const int t = at + 8 * n + g;
-            xv[h][n] = t < end ? load8<VEC>(p.x + (t0 + t) * p.ldx, k, k_end) : z;
+        for (int u = 0; u < KU; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = k0 + u * kSlice + 32 * h + 8 * tig;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int r = m0 + 16 * m + 8 * i;
+                av[u][h][m][i] = r + g < rank ? load8<VEC>(A + r * p.a_row, k, k_end) : z;
+              }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              xv[u][h][n] = at + 8 * n + g < end ? load8<VEC>(X + 8 * n * p.ldx, k, k_end) : z;
           }
-        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int u = 0; u < KU; ++u)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            if (at + 8 * n >= end) break;
-            mma16816(c[n], av[h][0].x, av[h][1].x, av[h][0].y, av[h][1].y, xv[h][n].x, xv[h][n].y);
-            mma16816(c[n], av[h][0].z, av[h][1].z, av[h][0].w, av[h][1].w, xv[h][n].z, xv[h][n].w);
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (n > 0 && at + 8 * n >= end) break;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                const uint4 a0 = av[u][h][m][0], a1 = av[u][h][m][1], b = xv[u][h][n];
+                mma16816(c[m][n], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+                mma16816(c[m][n], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+              }
+            }
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = at + 8 * n + 2 * tig + (i & 1);
-          if (t < end) part[(warp * rows + t) * p.Rp + (i & 2 ? r1 : r0)] = c[n][i];
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = at + 8 * n + 2 * tig + (i & 1), r = m0 + 16 * m + g + (i & 2 ? 8 : 0);
+            if (t < end && r < rank) part[(warp * rows + t) * p.Rp + r] = c[m][n][i];
+          }
     }
   }
   __syncthreads();
-  // rows without an adapter and ranks past an adapter's own are never read again
-  float *u = p.u + ((int64_t)blockIdx.y * p.T + t0) * p.Rp;
+  // ranks past an adapter's own, and rows without one, are never written or read
   for (int i = threadIdx.x; i < rows * p.Rp; i += kThreads) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += part[w * rows * p.Rp + i];
-    u[i] = v;
+    part[i] = v;  // this thread alone reads and writes element i
   }
-}
-
-__device__ __forceinline__ uint32_t pack2(__half a, __half b) {
-  return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
-}
-
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const LoraParams p) {
-  // Per row of Rk ranks (R rounded up to 32, a pad against bank conflicts): u
-  // in two fp16 parts; then the factor that undoes the scaling.
-  extern __shared__ __align__(16) uint8_t sm[];
-  const int Rk = (p.R + 31) / 32 * 32, pitch = Rk + 8;
-  __half *uh = reinterpret_cast<__half *>(sm);
-  __half *ul = uh + p.rows_up * pitch;
-  float *fs = reinterpret_cast<float *>(ul + p.rows_up * pitch);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const int64_t t0 = (int64_t)blockIdx.x * p.rows_up;
-  const int rows = (int)min((int64_t)p.rows_up, p.T - t0);
-  const Runs runs(p, t0, rows);
-  const int i_step = gridDim.y * kWarps * kOut;
-  const int i_first = (blockIdx.y * kWarps + warp) * kOut;
-
-  {  // B of the first run and y of its row, ahead of the wait for u
-    int end;
-    const int a = runs.run(0, end);
-    if (a >= 0 && i_first < p.N) {
-      const char *b = reinterpret_cast<const char *>(p.b + a * p.b_adapter +
-                                                     (int64_t)i_first * p.b_row);
-      const int64_t bytes = (int64_t)(min(kOut, p.N - i_first) - 1) * p.b_row * 2 + p.R * 2;
-      for (int64_t o = lane * 128; o < bytes; o += 32 * 128)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(b + o));
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.slices > 1) cluster_sync();
+  else __syncthreads();
   // One warp a row: sum of the slices, largest magnitude, two fp16 parts.
-  for (int t = warp; t < rows; t += kWarps) {
+  const uint32_t sums = (uint32_t)__cvta_generic_to_shared(part);
+  for (int t = blockIdx.y + p.slices * warp; t < rows; t += p.slices * kWarps) {
     const int a = __shfl_sync(0xffffffffu, runs.adapter, t);
     if (a < 0) continue;
     const int rank = rank_of(p, a);
@@ -206,101 +213,179 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const LoraParams p
       const int r = lane + 32 * q;
       v[q] = 0.0f;
       if (r < rank) {
-        const float *u = p.u + (t0 + t) * p.Rp + r;
-        for (int s = 0; s < p.slices; ++s) v[q] += __ldcg(u + (int64_t)s * p.T * p.Rp);
+#pragma unroll
+        for (int s = 0; s < kMaxSlices; ++s)
+          if (s < p.slices) v[q] += ld_cluster(sums + (t * p.Rp + r) * 4, s);
       }
       mx = fmaxf(mx, fabsf(v[q]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     // 2^e brings the largest into [2^9, 2^10); |e| <= 126 keeps both powers normal
-    int e = mx > 0.0f ? 10 - ilogbf(mx) - 1 : 0;
+    int e = mx > 0.0f ? 9 - ilogbf(mx) : 0;
     e = min(max(e, -126), 126);
     const float up = __int_as_float((127 + e) << 23), down = __int_as_float((127 - e) << 23);
-    if (lane == 0) fs[t] = down * __ldg(p.scale + a);
+    if (lane == 0) p.fs[t0 + t] = down * __ldg(p.scale + a);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int r = lane + 32 * q;
-      if (r < Rk) {
+      if (r < p.Rk) {
         const float w = v[q] * up;
         const __half h = __float2half_rn(w);
-        uh[t * pitch + r] = h;
-        ul[t * pitch + r] = __float2half_rn(w - __half2float(h));
+        p.uh[(t0 + t) * p.Rk + r] = h;
+        if (p.two) p.ul[(t0 + t) * p.Rk + r] = __float2half_rn(w - __half2float(h));
       }
     }
   }
-  __syncthreads();
+  if (p.slices > 1) cluster_sync();  // the others may still read this CTA's sums
+}
 
-  for (int i0 = i_first; i0 < p.N; i0 += i_step) {
-    const int i = i0 + g * 8;  // this thread's 8 outputs
+__device__ __forceinline__ uint4 ld_cg16(const __half *p) {
+  return __ldcg(reinterpret_cast<const uint4 *>(p));
+}
+
+// RC: 32-rank groups of B_a that a thread holds at a time; NN: 8-row column
+// tiles at a time; TWO: u comes in two parts.
+template <bool VEC, int RC, int NN, bool TWO>
+__global__ void __launch_bounds__(32 * kUpWarps, RC * NN == 1 ? 6 : RC * NN == 2 ? 4 : 3)
+    lora_up_kernel(const LoraParams p) {
+  // [rows][pitch], once or twice: the parts of u, rows padded against bank conflicts
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int pitch = p.Rk + 8;
+  float *fs = reinterpret_cast<float *>(sm);
+  __half *uh = reinterpret_cast<__half *>(sm + kMaxRows * sizeof(float));
+  __half *ul = uh + p.rows_up * pitch;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const int64_t t0 = (int64_t)blockIdx.x * p.rows_up;
+  const int rows = (int)min((int64_t)p.rows_up, p.T - t0);
+  const Runs runs(p, t0, rows);
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  bool ready = false;  // u is in shared memory
+  for (int i0 = (blockIdx.y * kUpWarps + warp) * kOut; !ready || i0 < p.N;
+       i0 += gridDim.y * kUpWarps * kOut) {
+    const int i = i0 + g * 8;               // this thread's 8 outputs
+    const bool all = VEC && i + 8 <= p.N;   // all of them exist
     for (int at = 0, end; at < rows; at = end) {
       const int a = runs.run(at, end);
       const int rank = a < 0 ? 0 : rank_of(p, a);
-      const __half *B = p.b + (a < 0 ? 0 : a) * p.b_adapter;
-      for (int n0 = at; n0 < end; n0 += 16) {  // 2 x 8 rows at a time
-        uint4 yv[2][2];
+      const __half *B = p.b + (a < 0 ? 0 : a) * p.b_adapter + (int64_t)i * p.b_row + 8 * tig;
+      uint4 bv[RC][4][2];
+      auto load_b = [&](int r0) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int q = 0; q < RC; ++q) {
+          const int r = r0 + 32 * q;
+          const __half *row = B + r;
+          if (all && r + 8 * tig + 8 <= rank) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j, row += p.b_row)
+              bv[q][j >> 1][j & 1] = __ldg(reinterpret_cast<const uint4 *>(row));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j, row += p.b_row)
+              bv[q][j >> 1][j & 1] = i + j < p.N ? load8<VEC>(row, 0, rank - r - 8 * tig) : z;
+          }
+        }
+      };
+      // rows 2 tig + {0, 1} of a column tile
+      const __half *Y = p.y + (t0 + at + 2 * tig) * p.ldy + i;
+      auto load_y = [&](int n0, uint4 (&yv)[NN][2]) {
+        const __half *row = Y + (n0 - at) * p.ldy;
+#pragma unroll
+        for (int n = 0; n < NN; ++n, row += 8 * p.ldy)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int t = n0 + 8 * n + 2 * tig + k;
-            yv[n][k] = t < end ? load8<VEC>(p.y + (t0 + t) * p.ldy, i, p.N) : make_uint4(0, 0, 0, 0);
+            const __half *src = row + k * p.ldy;
+            const bool on = n0 + 8 * n + 2 * tig + k < end;
+            if (all)
+              yv[n][k] = on ? __ldg(reinterpret_cast<const uint4 *>(src)) : z;
+            else
+              yv[n][k] = on ? load8<VEC>(src, 0, p.N - i) : z;
           }
-        float c[2][4][4];
+      };
+      uint4 yv[NN][2];
+      load_y(at, yv);
+      if (rank > 0) load_b(0);
+      if (!ready) {  // u comes from the launch before
+        ready = true;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int per = p.Rk / 8;  // 16-byte pieces a row
+        for (int e = threadIdx.x; e < rows * per; e += 32 * kUpWarps) {
+          const int t = e / per, c = (e - t * per) * 8;
+          const int64_t src = (t0 + t) * p.Rk + c;
+          *reinterpret_cast<uint4 *>(uh + t * pitch + c) = ld_cg16(p.uh + src);
+          if (TWO) *reinterpret_cast<uint4 *>(ul + t * pitch + c) = ld_cg16(p.ul + src);
+        }
+        if (threadIdx.x < rows) fs[threadIdx.x] = __ldcg(p.fs + t0 + threadIdx.x);
+        __syncthreads();
+      }
+      for (int n0 = at; n0 < end; n0 += 8 * NN) {
+        float c[NN][4][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NN; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) c[n][j][q] = 0.0f;
-        for (int r0 = 0; r0 < rank; r0 += 32) {
-          const int r = r0 + 8 * tig;
-          uint4 bv[4][2];
+        for (int r0 = 0; r0 < rank; r0 += 32 * RC) {
+          if (rank > 32 * RC && (r0 > 0 || n0 > at)) load_b(r0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int q = 0; q < RC; ++q) {
+            if (r0 + 32 * q >= rank) break;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              bv[j][k] = i + 2 * j + k < p.N
-                             ? load8<VEC>(B + (int64_t)(i + 2 * j + k) * p.b_row, r, rank)
-                             : make_uint4(0, 0, 0, 0);
+            for (int n = 0; n < NN; ++n) {
+              if (n > 0 && n0 + 8 * n >= end) break;
+              // columns past the run repeat its last row and are not stored
+              const int u = min(n0 + 8 * n + g, end - 1) * pitch + r0 + 32 * q + 8 * tig;
+              const uint4 hv = *reinterpret_cast<const uint4 *>(uh + u);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            if (n0 + 8 * n >= end) break;
-            const int t = min(n0 + 8 * n + g, rows - 1);  // columns past the run are not stored
-            const uint4 hv = *reinterpret_cast<const uint4 *>(uh + t * pitch + r);
-            const uint4 lv = *reinterpret_cast<const uint4 *>(ul + t * pitch + r);
+              for (int j = 0; j < 4; ++j) {
+                const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
+                mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, hv.x, hv.y);
+                mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, hv.z, hv.w);
+              }
+              if (TWO) {
+                const uint4 lv = *reinterpret_cast<const uint4 *>(ul + u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma16816(c[n][j], bv[j][0].x, bv[j][1].x, bv[j][0].y, bv[j][1].y, hv.x, hv.y);
-              mma16816(c[n][j], bv[j][0].z, bv[j][1].z, bv[j][0].w, bv[j][1].w, hv.z, hv.w);
-              mma16816(c[n][j], bv[j][0].x, bv[j][1].x, bv[j][0].y, bv[j][1].y, lv.x, lv.y);
-              mma16816(c[n][j], bv[j][0].z, bv[j][1].z, bv[j][0].w, bv[j][1].w, lv.z, lv.w);
+                for (int j = 0; j < 4; ++j) {
+                  const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
+                  mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, lv.x, lv.y);
+                  mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, lv.z, lv.w);
+                }
+              }
             }
           }
         }
+        uint4 o[NN][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NN; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int t = n0 + 8 * n + 2 * tig + k;
-            if (t >= end || i >= p.N) continue;
-            uint4 o = yv[n][k];
+            o[n][k] = yv[n][k];
             if (a >= 0) {
-              const float f = fs[t];
-              uint32_t w[4] = {o.x, o.y, o.z, o.w};
+              const float f = fs[min(n0 + 8 * n + 2 * tig + k, rows - 1)];
+              uint32_t w[4] = {o[n][k].x, o[n][k].y, o[n][k].z, o[n][k].w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const float2 yy = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                w[j] = pack2(__float2half_rn(fmaf(f, c[n][j][k], yy.x)),
-                             __float2half_rn(fmaf(f, c[n][j][2 + k], yy.y)));
+                const __half2 h = __floats2half2_rn(fmaf(f, c[n][j][k], yy.x),
+                                                    fmaf(f, c[n][j][2 + k], yy.y));
+                w[j] = *reinterpret_cast<const uint32_t *>(&h);
               }
-              o = make_uint4(w[0], w[1], w[2], w[3]);
+              o[n][k] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            __half *dst = p.out + (t0 + t) * p.ldo + i;
-            if (VEC && i + 8 <= p.N) {
-              *reinterpret_cast<uint4 *>(dst) = o;
+          }
+        if (n0 + 8 * NN < end) load_y(n0 + 8 * NN, yv);
+        __half *row = p.out + (t0 + n0 + 2 * tig) * p.ldo + i;
+#pragma unroll
+        for (int n = 0; n < NN; ++n, row += 8 * p.ldo)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (n0 + 8 * n + 2 * tig + k >= end) continue;
+            __half *dst = row + k * p.ldo;
+            if (all) {
+              *reinterpret_cast<uint4 *>(dst) = o[n][k];
             } else {
-              const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+              const uint32_t w[4] = {o[n][k].x, o[n][k].y, o[n][k].z, o[n][k].w};
               for (int q = 0; q < 8 && i + q < p.N; ++q)
                 dst[q] = __ushort_as_half((unsigned short)(w[q >> 1] >> (16 * (q & 1))));
             }
@@ -318,14 +403,51 @@ int pow2_at_least(int64_t v, int hi) {
   return r;
 }
 
-int padded_rank(int64_t R) { return (int)((R + 15) / 16 * 16); }
+template <bool VEC, int NT>
+cudaError_t launch_down(const LoraParams &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3((unsigned)((p.T + p.rows_down - 1) / p.rows_down), (unsigned)p.slices);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)kWarps * p.rows_down * p.Rp * sizeof(float);
+  cfg.stream = s;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.y = (unsigned)p.slices;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = allow_smem<lora_down_kernel<VEC, NT>>(cfg.dynamicSmemBytes);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, lora_down_kernel<VEC, NT>, p);
+}
+
+template <bool VEC, int RC, int NN, bool TWO>
+cudaError_t launch_up(const LoraParams &p, int ctas_n, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3((unsigned)((p.T + p.rows_up - 1) / p.rows_up), (unsigned)ctas_n);
+  cfg.blockDim = dim3(32 * kUpWarps);
+  cfg.dynamicSmemBytes = kMaxRows * sizeof(float) +
+                         (size_t)p.rows_up * (TWO ? 2 : 1) * (p.Rk + 8) * sizeof(__half);
+  cfg.stream = s;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lora_up_kernel<VEC, RC, NN, TWO>, p);
+}
+
+template <bool VEC, int RC, int NN>
+cudaError_t launch_up(const LoraParams &p, int ctas_n, cudaStream_t s) {
+  return p.two ? launch_up<VEC, RC, NN, true>(p, ctas_n, s)
+               : launch_up<VEC, RC, NN, false>(p, ctas_n, s);
+}
 
 }  // namespace
 
-size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t R) {
-  const int64_t slices = (K + kSlice - 1) / kSlice;
-  return (size_t)((slices < kMaxSlices ? slices : kMaxSlices) * (T > 0 ? T : 1) * padded_rank(R)) *
-         sizeof(float);
+size_t lora_workspace_bytes(int64_t T, int64_t, int64_t R) {
+  const int64_t Rk = (R + 31) / 32 * 32, rows = T > 0 ? T : 1;
+  return (size_t)(rows * Rk) * 2 * sizeof(__half) + (size_t)rows * sizeof(float);
 }
 
 qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t T, const __half *x,
@@ -345,7 +467,8 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.index = index;
   p.n_adapters = (int)ad.n_adapters;
   p.R = (int)ad.R;
-  p.Rp = padded_rank(ad.R);
+  p.Rp = (int)((ad.R + 15) / 16 * 16);
+  p.Rk = (int)((ad.R + 31) / 32 * 32);
   p.K = (int)ad.K;
   p.N = (int)ad.N;
   p.T = T;
@@ -356,7 +479,9 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.ldx = ldx;
   p.ldy = ldy;
   p.ldo = ldo;
-  p.u = static_cast<float *>(workspace);
+  p.uh = static_cast<__half *>(workspace);
+  p.ul = p.uh + T * p.Rk;
+  p.fs = reinterpret_cast<float *>(p.ul + T * p.Rk);
   // Slices of K: as many as there are steps of kSlice, at most kMaxSlices.
   const int64_t steps = (ad.K + kSlice - 1) / kSlice;
   p.slices = (int)(steps < kMaxSlices ? steps : kMaxSlices);
@@ -368,34 +493,31 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   const int64_t want = (int64_t)di.sms * 4;
   const int cap = kRowRanks / p.Rp < kMaxRows ? kRowRanks / p.Rp : kMaxRows;
   p.rows_down = pow2_at_least((T * p.slices + want - 1) / want, cap);
-  const int64_t chunks = (ad.N + kOut * kWarps - 1) / (kOut * kWarps);
-  p.rows_up = pow2_at_least((T * chunks + want - 1) / want, kMaxRows);
+  const int64_t per = kOut * kUpWarps, chunks = (ad.N + per - 1) / per;
+  p.rows_up = pow2_at_least((T * chunks + 2 * want - 1) / (2 * want), kMaxRows);
+  // CTAs along N: as many as fill the GPU beside those along the rows, so that a
+  // CTA that has its rows' u goes on to further outputs.
+  const int64_t fill = p.rows_up <= 8 ? 2 * want : want;
+  const int64_t tiles = (T + p.rows_up - 1) / p.rows_up, fit = (fill + tiles - 1) / tiles;
+  const int n = (int)(chunks < fit ? chunks : fit);
+  p.two = ad.K < kOnePart;
   const bool va = rows16(p.a, p.a_row) && p.a_adapter % 8 == 0 && rows16(x, ldx) && p.K % 8 == 0;
   const bool vb = rows16(p.b, p.b_row) && p.b_adapter % 8 == 0 && rows16(y, ldy) && rows16(out, ldo);
 
-  const int down_sm = kWarps * p.rows_down * p.Rp * (int)sizeof(float);
-  auto down = va ? lora_down_kernel<true> : lora_down_kernel<false>;
-  cudaError_t e = cudaSuccess;
-  if (down_sm > 48 * 1024)
-    e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, down_sm);
+  cudaError_t e;
+  if (p.rows_down <= 8)
+    e = va ? launch_down<true, 1>(p, s) : launch_down<false, 1>(p, s);
+  else
+    e = va ? launch_down<true, 4>(p, s) : launch_down<false, 4>(p, s);
   if (e != cudaSuccess) return cuda_status(e);
-  const dim3 gd((unsigned)((T + p.rows_down - 1) / p.rows_down), (unsigned)p.slices);
-  down<<<gd, kThreads, down_sm, s>>>(p);
-  qz_status launched = launch_status();
-  if (launched != QZ_OK) return launched;
-
-  const int pitch = (p.R + 31) / 32 * 32 + 8;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((T + p.rows_up - 1) / p.rows_up), (unsigned)chunks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)p.rows_up * (2 * pitch * sizeof(__half) + sizeof(float));
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, vb ? lora_up_kernel<true> : lora_up_kernel<false>, p));
+  // B_a of up to 64 ranks stays in registers for a run's rows
+  if (p.rows_up <= 8)
+    e = p.R <= 32 ? (vb ? launch_up<true, 1, 1>(p, n, s) : launch_up<false, 1, 1>(p, n, s))
+                  : (vb ? launch_up<true, 2, 1>(p, n, s) : launch_up<false, 2, 1>(p, n, s));
+  else
+    e = p.R <= 32 ? (vb ? launch_up<true, 1, 2>(p, n, s) : launch_up<false, 1, 2>(p, n, s))
+                  : (vb ? launch_up<true, 2, 2>(p, n, s) : launch_up<false, 2, 2>(p, n, s));
+  return cuda_status(e);
 }
 
 qz_status read_lora_error(int *code, int clear) {

@@ -195,12 +195,9 @@ bool fits16(const void *p, int64_t ld) { return ((uintptr_t)p & 15u) == 0 && ld 
 
 template <bool INT8>
 qz_status launch_row(const NormParams &p, cudaStream_t s) {
-  const int bytes = (int)(p.K * sizeof(float));
-  if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_row_kernel<INT8>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
+  const size_t bytes = (size_t)p.K * sizeof(float);
+  const cudaError_t e = allow_smem<norm_row_kernel<INT8>>(bytes);
+  if (e != cudaSuccess) return cuda_status(e);
   norm_row_kernel<INT8><<<(unsigned)p.T, kRowThreads, bytes, s>>>(p);
   return launch_status();
 }

@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/qz.h"
@@ -108,6 +109,23 @@ qz_status read_embed_error(int *code, int clear);
 qz_status launch_embed_int8(const int8_t *q, int64_t ldq, const float *scale, int64_t V, int64_t K,
                             const int32_t *tokens, int64_t B, __half *out, int64_t ldo,
                             cudaStream_t s);
+
+// Lets kernel Kern use `bytes` of dynamic shared memory on the current device;
+// the attribute call (about a microsecond) is made only when the size grows.
+template <auto Kern>
+inline cudaError_t allow_smem(size_t bytes) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> allowed[kMaxDev];
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDev;
+  if (known && allowed[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && known) allowed[dev].store((int)bytes, std::memory_order_relaxed);
+  return e;
+}
 
 // Reads (and clears) a translation unit's device error word.
 template <typename Word>
