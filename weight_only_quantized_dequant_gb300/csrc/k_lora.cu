@@ -244,10 +244,15 @@ __device__ __forceinline__ uint4 ld_cg16(const __half *p) {
   return __ldcg(reinterpret_cast<const uint4 *>(p));
 }
 
+// CTAs per SM that the registers of a variant allow.
+__host__ __device__ constexpr int up_ctas(int rc, int nn) {
+  return rc * nn == 1 ? 6 : rc * nn == 2 ? 4 : 3;
+}
+
 // RC: 32-rank groups of B_a that a thread holds at a time; NN: 8-row column
 // tiles at a time; TWO: u comes in two parts.
 template <bool VEC, int RC, int NN, bool TWO>
-__global__ void __launch_bounds__(32 * kUpWarps, RC * NN == 1 ? 6 : RC * NN == 2 ? 4 : 3)
+__global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
     lora_up_kernel(const LoraParams p) {
   // [rows][pitch], once or twice: the parts of u, rows padded against bank conflicts
   extern __shared__ __align__(16) uint8_t sm[];
@@ -495,10 +500,12 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.rows_down = pow2_at_least((T * p.slices + want - 1) / want, cap);
   const int64_t per = kOut * kUpWarps, chunks = (ad.N + per - 1) / per;
   p.rows_up = pow2_at_least((T * chunks + 2 * want - 1) / (2 * want), kMaxRows);
-  // CTAs along N: as many as fill the GPU beside those along the rows, so that a
-  // CTA that has its rows' u goes on to further outputs.
-  const int64_t fill = p.rows_up <= 8 ? 2 * want : want;
-  const int64_t tiles = (T + p.rows_up - 1) / p.rows_up, fit = (fill + tiles - 1) / tiles;
+  // CTAs along N: as many as the GPU holds at once beside those along the rows
+  // (a CTA that has its rows' u goes on to further outputs; a second wave of
+  // CTAs would cost as much as the first).
+  const int64_t tiles = (T + p.rows_up - 1) / p.rows_up;
+  const int64_t slots = (int64_t)di.sms * up_ctas(p.R <= 32 ? 1 : 2, p.rows_up <= 8 ? 1 : 2);
+  const int64_t fit = slots / tiles > 1 ? slots / tiles : 1;
   const int n = (int)(chunks < fit ? chunks : fit);
   p.two = ad.K < kOnePart;
   const bool va = rows16(p.a, p.a_row) && p.a_adapter % 8 == 0 && rows16(x, ldx) && p.K % 8 == 0;
