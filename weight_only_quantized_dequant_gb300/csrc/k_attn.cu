@@ -1065,12 +1065,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       int head = n - i * p.G;
       const __half *src = p.q + (int64_t)(g.tok + i) * p.q_token +
                           (int64_t)(g.head * p.G + head) * p.q_head + c * 8;
-      const int64_t step = RPP * p.q_head, wrap = p.q_token - p.G * p.q_head;
-#pragma unroll 4
+      const int toks = row_token(RPP), heads = RPP - toks * p.G;  // RPP rows further on
+      const int64_t wrap = p.q_token - p.G * p.q_head;
+      const int64_t step = toks * p.q_token + heads * p.q_head;
+#pragma unroll 8
       for (int k = 0; k < PASSES; ++k) {
         f(r0 + k * RPP, src);
         src += step;
-        for (head += RPP; head >= p.G; head -= p.G) src += wrap;
+        head += heads;
+        if (head >= p.G) {
+          head -= p.G;
+          src += wrap;
+        }
       }
     };
     uint32_t n_seg = 0, segs = 0;
