@@ -70,6 +70,8 @@ struct Cfg {
 
 struct AttnParams {
   CUtensorMap kmap, vmap;  // [page][head][slot][D], box 64 x min(page, 128) rows
+  CUtensorMap qmap;        // [token][head][D], box 64 x G heads x tokens of half a tile
+  int q_boxes;             // queries come by qmap
   const __half *q;
   __half *out;
   int64_t q_token, q_head, o_token, o_head;
@@ -1048,9 +1050,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kQWarp) {
     // ------------------------------------------------------------ queries --
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    // A tile's queries, laid in shared memory as a TMA copy with the 128-byte
-    // swizzle would (rows of a group of heads are no box); rows past the tile are
-    // zeros.  Each warp takes half of the rows.
+    // A tile's queries, half of the rows a warp.  Where a group of heads divides
+    // them they are a box of the query tensor; else (and for a negative or zero
+    // scale, which the copy cannot apply) they are laid row by row as TMA with the
+    // 128-byte swizzle would, rows past the tile as zeros.
     constexpr int CPR = D / 8, RPP = 32 / CPR;  // 16-byte chunks a row, rows per pass
     constexpr int PASSES = kM / 2 / RPP;
     const int c = lane % CPR;
@@ -1086,6 +1089,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       free_seg(n_seg++);
       if (g.rows == 0) break;
       if (g.b1 <= g.b0) continue;
+      if (p.q_boxes) {
+        // Rows past the tile are whatever follows (or zeros past the last token):
+        // they are computed and not stored.
+        const int half = warp - kQWarp, tok = g.tok + half * (kM / 2) / p.G;
+        if (segs > 0) {
+          if (lane == 0)
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+              asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
+                               reinterpret_cast<uint64_t>(&p.qmap)),
+                           "r"(d * 64), "r"(g.head * p.G), "r"(tok)
+                           : "memory");
+          __syncwarp();
+          if (!mbar_wait(smem_u32(q_empty), (segs - 1) & 1, abort_flag)) break;
+        }
+        if (lane == 0) {
+          asm volatile(
+              "{\n\t.reg .b64 t;\n\t"
+              "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(smem_u32(q_full)),
+              "r"((uint32_t)(kM / 2 * D * 2))
+              : "memory");
+          const uint32_t dst = smem_u32(q_sm) + (NQ == 2 ? half * (128 * D * 2) : half * 64 * 128);
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst + d * 16384),
+                "l"(reinterpret_cast<uint64_t>(&p.qmap)), "r"(d * 64), "r"(g.head * p.G), "r"(tok),
+                "r"(smem_u32(q_full))
+                : "memory");
+        }
+        __syncwarp();
+        ++segs;
+        continue;
+      }
       if (segs > 0) {
         // while the tile before still reads its own, bring these as far as L2
         if (c % 8 == 0)
@@ -1264,6 +1302,24 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
+// The queries as [token][head][64-column group of D]; false: not such a box.
+bool query_map(CUtensorMap *map, const __half *q, int64_t T, int64_t H, int D, int64_t token,
+               int64_t head, int G, int rows) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn || G > rows || rows % G) return false;
+  // a dimension of one element has no stride of its own
+  if (H == 1) head = D;
+  if (T == 1) token = H * D;
+  const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t stride[2] = {(cuuint64_t)head * 2, (cuuint64_t)token * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(rows / G)};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(q), dim, stride, box,
+            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The pool as [page][head][slot][64-column group of D], boxes of one page's
 // (at most 128) slots by 64 columns.
 qz_status pool_map(CUtensorMap *map, const __half *base, const PagedView &c, int64_t token,
@@ -1343,7 +1399,9 @@ qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t
   p.cnt = static_cast<unsigned *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + QZ_ATTENTION_SYNC_BYTES);
   // Two stages of rows pay once a sequence fills the second one.
-  const bool two = sv.n_tokens * p.G > (int64_t)128 * sv.n_seqs;
+  const bool two = c.D < 256 && sv.n_tokens * p.G > (int64_t)128 * sv.n_seqs;
+  p.q_boxes = scale > 0.0f && query_map(&p.qmap, q, sv.n_tokens, hq, c.D, q_token, q_head, p.G,
+                                        two ? 128 : 64);
   if (c.D == 256) return launch_cap<256, 1>(p, di.sms, s);
   if (c.D == 128) return two ? launch_cap<128, 2>(p, di.sms, s) : launch_cap<128, 1>(p, di.sms, s);
   return two ? launch_cap<64, 2>(p, di.sms, s) : launch_cap<64, 1>(p, di.sms, s);
