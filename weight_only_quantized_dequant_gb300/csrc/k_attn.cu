@@ -787,9 +787,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the tile's rows, or this CTA's part of them
-      if (active && live_rows > 0) {
+      if (live_rows == 0) {
+        if (active) ++ends;
+        continue;
+      }
+      auto out_at = [&](int r) {  // where a row's outputs go
+        const int n = g.rem + r, i = row_token(n);
+        return (int64_t)(g.tok + i) * p.o_token + (int64_t)(g.head * p.G + n - i * p.G) * p.o_head +
+               out0;
+      };
+      auto part_of = [&](int cta, int slot) {
+        return p.part + (int64_t)((cta * 2 + slot) * kSoftmaxWarps + warp) * C::kPart;
+      };
+      float *mine_part = part_of(blockIdx.x, g.slot);
+      char *dst[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        dst[i] = g.slot < 0 ? reinterpret_cast<char *>(p.out + out_at(warp_row + r))
+                            : reinterpret_cast<char *>(mine_part + 64 + r * DC);
+        dst[i] = r < live_rows ? dst[i] + (lane & 3) * 16 : nullptr;
+      }
+      if (active) {
         const uint32_t ph = NQ == 2 ? ends & 1 : (blocks - 1) & 1;
         if (!(ok = mbar_wait(smem_u32(&o_done[NQ == 2 ? wg : 0]), ph, abort_flag))) break;
+        ++ends;
         fence_after();
         if (NQ == 1) {
           float other;
@@ -797,23 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = wg == 0 ? l + other : other + l;
         }
       }
-      if (active) ++ends;
-      if (live_rows == 0) continue;
-      // where a row's outputs go
-      auto out_at = [&](int r) {
-        const int n = g.rem + r, i = row_token(n);
-        return (int64_t)(g.tok + i) * p.o_token + (int64_t)(g.head * p.G + n - i * p.G) * p.o_head +
-               out0;
-      };
       if (g.slot < 0) {
-        char *dst[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + (lane >> 2);
-          dst[i] = r < live_rows
-                       ? reinterpret_cast<char *>(p.out + out_at(warp_row + r)) + (lane & 3) * 16
-                       : nullptr;
-        }
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int k = 0; k < DC; k += 32) {
@@ -831,20 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // ---- cut between CTAs: leave the partial, merge if last
-      auto part_of = [&](int cta, int slot) {
-        return p.part + (int64_t)((cta * 2 + slot) * kSoftmaxWarps + warp) * C::kPart;
-      };
-      float *mine_part = part_of(blockIdx.x, g.slot);
       mine_part[lane] = l > 0.0f ? (m == -INFINITY ? 0.0f : m * p.c) : -INFINITY;
       mine_part[32 + lane] = l;
-      char *dst[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        dst[i] = r < live_rows
-                     ? reinterpret_cast<char *>(mine_part + 64 + r * DC) + (lane & 3) * 16
-                     : nullptr;
-      }
 #pragma unroll 1
       for (int k = 0; k < DC; k += 32) {
         uint32_t o[32];
