@@ -39,7 +39,9 @@ __device__ int g_attn_error = 0;
 
 constexpr int kN = 128;                // keys per block
 constexpr int kSoftmaxWarps = 8;       // two warpgroups
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10;  // and 11: queries
+// With few rows only softmax warps 0 and 4 have any, both on the SM's first
+// scheduler: the MMA and load warps sit on others.
+constexpr int kQWarp = 8, kMmaWarp = 10, kLoadWarp = 11;  // 8 and 9: queries
 constexpr int kThreads = 384;          // the third warpgroup: MMA, key and value loads, query loads (2)
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
 static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "register split");
@@ -1041,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp >= kQWarp) {
+  } else if (warp < kQWarp + 2) {
     // ------------------------------------------------------------ queries --
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // A tile's queries, half of the rows a warp.  Where a group of heads divides
