@@ -55,6 +55,7 @@ constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr float kLag = 8.0f;           // log2 of how far a weight may exceed 1
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMinUnits = 3;           // units per CTA at least
+constexpr float kMergeUnits = 0.2f;    // time to merge one partial, in key blocks
 constexpr int kTileUnits = 1;          // a tile's fixed time, in key blocks
 constexpr int kSegs = 4;               // tiles announced ahead
 
@@ -468,6 +469,7 @@ template <int kPer>
 __device__ __forceinline__ bool Walker<kM>::start(const AttnParams &p) {
   const int lane = threadIdx.x & 31, S = p.s.n_seqs;
   int64_t h[kPer];  // units per head of this lane's sequences
+  int64_t tiles = 0;  // of this lane's sequences
   auto count = [&](int i0) {
     Seq s[kPer];
 #pragma unroll
@@ -478,7 +480,10 @@ __device__ __forceinline__ bool Walker<kM>::start(const AttnParams &p) {
     }
     int64_t n = 0;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) n += h[k] = head_units<kM>(p, s[k]);
+    for (int k = 0; k < kPer; ++k) {
+      n += h[k] = head_units<kM>(p, s[k]);
+      tiles += s[k].nt;
+    }
     return warp_scan(n * p.hkv);
   };
   int64_t total = 0, incl = 0;
@@ -486,7 +491,12 @@ __device__ __forceinline__ bool Walker<kM>::start(const AttnParams &p) {
     incl = count(i0);
     total += __shfl_sync(0xffffffffu, incl, 31);
   }
-  const int ctas = (int)min((int64_t)gridDim.x, div64(total + kMinUnits - 1, kMinUnits));
+  // A tile cut in n leaves n partials for one CTA to merge, about kMergeUnits of
+  // a block's time each, so a tile of U units is best cut in sqrt(U / kMergeUnits).
+  tiles = __shfl_sync(0xffffffffu, warp_scan(tiles), 31) * p.hkv;
+  const float cuts = (float)tiles * sqrtf((float)total / ((float)tiles * kMergeUnits));
+  const int ctas = (int)min(min((int64_t)gridDim.x, div64(total + kMinUnits - 1, kMinUnits)),
+                            (int64_t)ceilf(fmaxf(cuts, 1.0f)));
   if ((int)blockIdx.x >= ctas) return false;
   each = div64(total, ctas);
   more = (int)(total - each * ctas);
