@@ -323,6 +323,12 @@ def test_attention_rows_that_see_nothing():
     assert bool(out[4:7].any()) and bool(out[7 + 130].any())
 
 
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31, 2**40])
+def test_attention_window_longer_than_any_cache(window):
+    # with tokens before the cache's first position, whose window starts below 32 bits
+    check_attention([5, 140, 1], [3, 10, 300], 4, 2, 128, 16, window=window, seed=9)
+
+
 def test_attention_rows_outside_sequences():
     check_attention([1, 3], [50, 60], 4, 2, 64, 16, seed=10, before=3)
 
