@@ -492,7 +492,7 @@ qz_status qz_rope_append(const qz_half *q, int64_t n_heads, int64_t q_token, int
  * Logits, softmax sums and outputs are held in fp32; the weights e^{x_j - m} are
  * rounded to fp16 where they enter the tensor cores.  scale: finite.
  * q, out: [n_tokens][n_heads][head_dim] with strides q_token, q_head, o_token,
- * o_head; 16-byte aligned, strides multiples of 8.
+ * o_head; 16-byte aligned, strides multiples of 8; out must not overlap q.
  * n_tokens * n_heads < 2^31.
  * workspace: qz_attention_workspace_bytes bytes of device memory, 16-byte
  * aligned, the first QZ_ATTENTION_SYNC_BYTES of them zeroed before its first
@@ -526,7 +526,7 @@ size_t qz_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t n_
  * neighbours.  2-byte alignment suffices; 16-byte aligned operands with K, R
  * and strides multiples of 8 run fastest.  K, N <= 2^20.
  * workspace: qz_lora_workspace_bytes(T, K, R) bytes, 16-byte aligned (any
- * contents). */
+ * contents); calls that can be in flight at the same time need different ones. */
 typedef struct {
   const qz_half *a, *b;
   const float *scale;  /* [n_adapters] */

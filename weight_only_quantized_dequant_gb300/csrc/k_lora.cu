@@ -20,6 +20,13 @@
 // the two operands use the same order of k, so no shuffle is needed; likewise the
 // rows of B_a are dealt so that a thread ends with 8 consecutive outputs.
 // Operands without 16-byte rows take the same path with 2-byte loads.
+//
+// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10-11 us, of
+// which down 5, up 3 after it; the chain index, adapter, products, cluster, u,
+// products is latency.  1500 rows of 8 adapters of ranks up to 64, 4096 x 11008:
+// 52 us, down 19 in a wave and a quarter of CTAs (one takes 11), up the rest: each
+// step of 64 outputs waits for its own loads (a product is 8 clocks of a
+// scheduler, so the matrix instructions are a tenth of the time).
 #include "qz_internal.cuh"
 
 namespace qz {

@@ -6,6 +6,10 @@
 // One pass over memory: a row's h stays on chip (registers, fp32) between the
 // sum of squares, the maximum and the store, so the traffic is the floor's
 // (x, r in; y or q, h out) and HBM bounds long calls, launch latency short ones.
+// The threads of a row are the fewest that hold it in kMaxVec 16-byte vectors each,
+// all loaded before the first use.  Measured (GB300): 2048 x 8192 with residual
+// 21.7 us, 6.2 TB/s (93% of a plain copy's rate); 16 x 8192 2.6 us; 1021 x 3584
+// to INT8 rows 7.7 us.
 #include "qz_internal.cuh"
 
 namespace qz {
