@@ -21,12 +21,13 @@
 // rows of B_a are dealt so that a thread ends with 8 consecutive outputs.
 // Operands without 16-byte rows take the same path with 2-byte loads.
 //
-// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10-11 us, of
+// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10 us, of
 // which down 5, up 3 after it; the chain index, adapter, products, cluster, u,
 // products is latency.  1500 rows of 8 adapters of ranks up to 64, 4096 x 11008:
-// 52 us, down 19 in a wave and a quarter of CTAs (one takes 11), up the rest: each
-// step of 64 outputs waits for its own loads (a product is 8 clocks of a
-// scheduler, so the matrix instructions are a tenth of the time).
+// 48 us, down 19 in a wave and a quarter of CTAs (one takes 11), up the rest: each
+// step of 64 outputs waits for its own loads (3.7 us a step, half of it loads; a
+// product is 8 clocks of a scheduler, so the matrix instructions are a tenth of
+// the time), twice in the few row tiles that two runs share.
 #include "qz_internal.cuh"
 
 namespace qz {
@@ -66,6 +67,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The first product of a sum.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Elements [at, at + 8) of a row with n elements; zeros past its end.
@@ -251,6 +261,18 @@ __device__ __forceinline__ uint4 ld_cg16(const __half *p) {
   return __ldcg(reinterpret_cast<const uint4 *>(p));
 }
 
+// y + f c of a row's 8 outputs (row k of the products' two), rounded once.
+__device__ __forceinline__ uint4 add_rows(uint4 y, float f, const float (&c)[4][4], int k) {
+  uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 yy = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+    const __half2 h = __floats2half2_rn(fmaf(f, c[j][k], yy.x), fmaf(f, c[j][2 + k], yy.y));
+    w[j] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // CTAs per SM that the registers of a variant allow.
 __host__ __device__ constexpr int up_ctas(int rc, int nn) {
   return rc * nn == 1 ? 6 : rc * nn == 2 ? 4 : 3;
@@ -276,7 +298,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
   for (int i0 = (blockIdx.y * kUpWarps + warp) * kOut; !ready || i0 < p.N;
        i0 += gridDim.y * kUpWarps * kOut) {
     const int i = i0 + g * 8;               // this thread's 8 outputs
-    const bool all = VEC && i + 8 <= p.N;   // all of them exist
+    const bool all = VEC && i0 + kOut <= p.N;  // all of the warp's exist
     for (int at = 0, end; at < rows; at = end) {
       const int a = runs.run(at, end);
       const int rank = a < 0 ? 0 : rank_of(p, a);
@@ -287,10 +309,11 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
         for (int q = 0; q < RC; ++q) {
           const int r = r0 + 32 * q;
           const __half *row = B + r;
-          if (all && r + 8 * tig + 8 <= rank) {
+          if (all && (rank & 7) == 0) {
+            const bool on = r + 8 * tig < rank;
 #pragma unroll
             for (int j = 0; j < 8; ++j, row += p.b_row)
-              bv[q][j >> 1][j & 1] = __ldg(reinterpret_cast<const uint4 *>(row));
+              bv[q][j >> 1][j & 1] = on ? __ldg(reinterpret_cast<const uint4 *>(row)) : z;
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j, row += p.b_row)
@@ -302,6 +325,14 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
       const __half *Y = p.y + (t0 + at + 2 * tig) * p.ldy + i;
       auto load_y = [&](int n0, uint4 (&yv)[NN][2]) {
         const __half *row = Y + (n0 - at) * p.ldy;
+        if (all && n0 + 8 * NN <= end) {
+#pragma unroll
+          for (int n = 0; n < NN; ++n, row += 8 * p.ldy) {
+            yv[n][0] = __ldg(reinterpret_cast<const uint4 *>(row));
+            yv[n][1] = __ldg(reinterpret_cast<const uint4 *>(row + p.ldy));
+          }
+          return;
+        }
 #pragma unroll
         for (int n = 0; n < NN; ++n, row += 8 * p.ldy)
 #pragma unroll
@@ -330,7 +361,53 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
         if (threadIdx.x < rows) fs[threadIdx.x] = __ldcg(p.fs + t0 + threadIdx.x);
         __syncthreads();
       }
-      for (int n0 = at; n0 < end; n0 += 8 * NN) {
+      // Whole tiles of rows and outputs, whose ranks are in registers: no bounds.
+      int n0 = at;
+      if (all && rank > 0 && rank <= 32 * RC) {
+        const __half *u = uh + (at + g) * pitch + 8 * tig;
+        const float *f = fs + at + 2 * tig;
+        __half *row = p.out + (t0 + at + 2 * tig) * p.ldo + i;
+        for (; n0 + 8 * NN <= end; n0 += 8 * NN, u += 8 * NN * pitch, f += 8 * NN) {
+          float c[NN][4][4];
+#pragma unroll
+          for (int q = 0; q < RC; ++q) {
+            if (q > 0 && 32 * q >= rank) break;
+#pragma unroll
+            for (int n = 0; n < NN; ++n) {
+              const uint4 hv = *reinterpret_cast<const uint4 *>(u + 8 * n * pitch + 32 * q);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
+                if (q == 0) mma16816_first(c[n][j], b0.x, b1.x, b0.y, b1.y, hv.x, hv.y);
+                else mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, hv.x, hv.y);
+                mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, hv.z, hv.w);
+              }
+              if (TWO) {
+                const uint4 lv = *reinterpret_cast<const uint4 *>(u + 8 * n * pitch + 32 * q +
+                                                                  p.rows_up * pitch);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
+                  mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, lv.x, lv.y);
+                  mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, lv.z, lv.w);
+                }
+              }
+            }
+          }
+          uint4 o[NN][2];
+#pragma unroll
+          for (int n = 0; n < NN; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) o[n][k] = add_rows(yv[n][k], f[8 * n + k], c[n], k);
+          if (n0 + 8 * NN < end) load_y(n0 + 8 * NN, yv);
+#pragma unroll
+          for (int n = 0; n < NN; ++n, row += 8 * p.ldo) {
+            *reinterpret_cast<uint4 *>(row) = o[n][0];
+            *reinterpret_cast<uint4 *>(row + p.ldo) = o[n][1];
+          }
+        }
+      }
+      for (; n0 < end; n0 += 8 * NN) {
         float c[NN][4][4];
 #pragma unroll
         for (int n = 0; n < NN; ++n)
@@ -373,18 +450,8 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             o[n][k] = yv[n][k];
-            if (a >= 0) {
-              const float f = fs[min(n0 + 8 * n + 2 * tig + k, rows - 1)];
-              uint32_t w[4] = {o[n][k].x, o[n][k].y, o[n][k].z, o[n][k].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 yy = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                const __half2 h = __floats2half2_rn(fmaf(f, c[n][j][k], yy.x),
-                                                    fmaf(f, c[n][j][2 + k], yy.y));
-                w[j] = *reinterpret_cast<const uint32_t *>(&h);
-              }
-              o[n][k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            if (a >= 0)
+              o[n][k] = add_rows(yv[n][k], fs[min(n0 + 8 * n + 2 * tig + k, rows - 1)], c[n], k);
           }
         if (n0 + 8 * NN < end) load_y(n0 + 8 * NN, yv);
         __half *row = p.out + (t0 + n0 + 2 * tig) * p.ldo + i;
