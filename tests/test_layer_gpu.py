@@ -526,6 +526,30 @@ def test_rope_append(D, hq, hkv, page, nhd):
     assert torch.equal(p.cache.k[p.rows[4][128 // page], :, 128 % page], k[last])
 
 
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (9, 3), (32, 8)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rope_append_long_steps(D, hq, hkv):
+    # more blocks than the GPU holds at once: several heads a thread
+    qs, kvs, page = [2500, 0, 333], [2500, 7, 400], 64
+    p = Paged(qs, kvs, hkv, page, D, 36)
+    g = gen(37)
+    q, k, v = randn(g, p.T, hq, D), randn(g, p.T, hkv, D), randn(g, p.T, hkv, D)
+    rope = qz().rope_table(2500, D)
+    out = qz().rope_append(q, k, v, p.cache, p.seqs, rope)
+    for i, (n, L) in enumerate(zip(qs, kvs)):
+        if n == 0:
+            continue
+        rows = slice(p.cu[i], p.cu[i] + n)
+        pos = torch.arange(L - n, L, device=DEV)
+        pages, slots = i32(p.rows[i])[pos // page].long(), pos % page
+        want, mag = rotate_ref(q[rows], rope, pos)
+        within(out[rows], want, U16 * want.abs() + 3 * U32 * mag + S16)
+        want, mag = rotate_ref(k[rows], rope, pos)
+        within(p.cache.k[pages, :, slots], want, U16 * want.abs() + 3 * U32 * mag + S16)
+        assert torch.equal(p.cache.v[pages, :, slots], v[rows])
+    assert qz().device_error() == 0
+
+
 def test_rope_append_many_sequences():
     n, D = 1500, 64
     p = Paged([i % 3 for i in range(n)], [2 + i % 20 for i in range(n)], 1, 8, D, 32)
