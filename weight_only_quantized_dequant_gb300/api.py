@@ -48,7 +48,9 @@ def get_overlap() -> bool:
 
 
 def device_error(clear: bool = True) -> int:
-    """The library's device error word (1 = a kernel gave up a bounded wait)."""
+    """The library's device error word (bit 1: a kernel gave up a bounded wait;
+    bit 2: a token outside the vocabulary; bit 4: a page, position or adapter
+    index outside its table)."""
     v = ctypes.c_int()
     _lib.call("qz_device_error", ctypes.byref(v), 1 if clear else 0)
     return v.value
