@@ -522,8 +522,8 @@ size_t qz_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t n_
  * row's largest value from K = 4096 on (2^-12, within K 2^-24), and held to 22
  * bits below.  An index outside
  * -1..n_adapters-1 counts as -1 and sets bit 4 of the device error word.
- * Rows with the same index cost one read of their adapter when they are
- * neighbours.  2-byte alignment suffices; 16-byte aligned operands with K, R
+ * Rows with the same index share reads of their adapter, in calls of fewer than
+ * 128 rows when they are neighbours.  2-byte alignment suffices; 16-byte aligned operands with K, R
  * and strides multiples of 8 run fastest.  K, N <= 2^20.
  * workspace: qz_lora_workspace_bytes(T, K, R) bytes, 16-byte aligned (any
  * contents); calls that can be in flight at the same time need different ones. */

@@ -636,6 +636,31 @@ def test_lora_sizes(K, N, R):
     check_lora(19, K, N, R, 4, runs(19, 3, 4))
 
 
+@pytest.mark.parametrize("T", [127, 128, 129, 500, 2100, 4500])
+def test_lora_rows_in_any_order(T):
+    # rows of an adapter far apart, over several sorted segments; more adapters
+    # than bins of the sort; every row the same one
+    g = torch.Generator().manual_seed(T)
+    mixed = torch.randint(-1, 9, (T,), generator=g).tolist()
+    check_lora(T, 128, 136, 24, 9, mixed, rank=[24, 0, 3, 8, 16, 24, 99, 1, 17])
+    wide = [-1 if i % 7 == 6 else i * 523 % 1500 for i in range(T)]
+    check_lora(T, 64, 72, 8, 1500, wide)
+    check_lora(T, 64, 72, 8, 2, [1] * T)
+    check_lora(T, 64, 72, 8, 2, [-1] * T)
+
+
+def test_lora_indices_outside_the_pool_in_any_order():
+    g = gen(46)
+    T = 300
+    x, y = randn(g, T, 64), randn(g, T, 64)
+    ad = qz().LoraAdapters(randn(g, 3, 8, 64), randn(g, 3, 64, 8), torch.ones(3, device=DEV))
+    idx = [(t % 7) - 2 for t in range(T)]  # -2 .. 4
+    out = qz().lora(x, y, ad, i32(idx))
+    assert qz().device_error() == 4
+    for t, a in enumerate(idx):
+        assert torch.equal(out[t], y[t]) == (a < 0 or a > 2)
+
+
 def test_lora_mixed_ranks():
     check_lora(60, 1024, 512, 64, 6, runs(60, 2, 6), rank=[64, 32, 0, 1, 17, 99])
     check_lora(300, 1024, 512, 32, 3, runs(300, 70, 3), rank=[32, 8, 24])

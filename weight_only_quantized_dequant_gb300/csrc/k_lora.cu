@@ -21,13 +21,17 @@
 // rows of B_a are dealt so that a thread ends with 8 consecutive outputs.
 // Operands without 16-byte rows take the same path with 2-byte loads.
 //
-// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10 us, of
+// From kOrderRows rows on, the rows are sorted by adapter first (a third launch, which the
+// others overlap), so that an adapter is read for up to 32 of its rows at once however they come.
+//
+// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10.5 us, of
 // which down 5, up 3 after it; the chain index, adapter, products, cluster, u,
-// products is latency.  1500 rows of 8 adapters of ranks up to 64, 4096 x 11008:
-// 48 us, down 19 in a wave and a quarter of CTAs (one takes 11), up the rest: each
-// step of 64 outputs waits for its own loads (3.7 us a step, half of it loads; a
-// product is 8 clocks of a scheduler, so the matrix instructions are a tenth of
-// the time), twice in the few row tiles that two runs share.
+// products is latency.  1500 rows of 8 adapters of ranks up to 64 in runs of 300,
+// 4096 x 11008: 50 us, 2 of them the sort, down 19 in a wave and a quarter of CTAs
+// (one takes 11), up the rest: each step of 64 outputs waits for its own loads (3.7
+// us a step, half of it loads; a product is 8 clocks of a scheduler, so the matrix
+// instructions are a tenth of the time), twice in the few row tiles that two runs
+// share.  1500 rows of 48 adapters of rank 16 in turn: 48 us (265 unsorted).
 #include "qz_internal.cuh"
 
 namespace qz {
@@ -44,6 +48,13 @@ constexpr int kMaxRows = 32;                // rows of a CTA (one per lane when 
 constexpr int kOut = 64;                    // outputs per warp and step
 constexpr int64_t kOnePart = 4096;          // K from which u enters as one fp16 part
 constexpr int kRowRanks = 2048;             // rows x padded rank of a CTA (shared memory)
+// Rows from which they are sorted first.  1500 rows of 48 adapters in turn, rank
+// 16, 4096 x 11008: 265 -> 48.5 us; 128 of 16, rank 64: 48 -> 29; 64 of 4, rank 16,
+// 4096 x 4096: 13.8 -> 16.7.  Rows that come grouped
+// pay 2 us for it (1500 in runs of 300: 48.7 -> 50.5).
+constexpr int64_t kOrderRows = 128;
+constexpr int kBins = 1024;                 // of the sort by adapter
+constexpr int kSegment = 2048;              // rows sorted together
 constexpr int kMaxSlices = 8;               // CTAs of a cluster, which split K
 
 struct LoraParams {
@@ -55,6 +66,7 @@ struct LoraParams {
   int64_t T, a_adapter, a_row, b_adapter, b_row, ldx, ldy, ldo;
   __half *uh, *ul;  // [T][Rk] u 2^e, and its remainder where two parts are used
   int two;
+  int2 *order;      // [T] (row, index) sorted by adapter, or null: rows as they come
   float *fs;        // [T] scale_a 2^-e
   int slices;
   int k_slice;    // k per CTA (a multiple of kSlice)
@@ -99,12 +111,23 @@ __device__ __forceinline__ uint4 load8(const __half *row, int at, int n) {
 // Runs of equal adapters among rows [t0, t0 + n), n <= 32; every warp holds
 // the same: lane i the adapter of row i, and the mask of rows that start a run.
 struct Runs {
+  int64_t row;      // of x, y and out, for this lane's place
   int adapter;      // of this lane's row
   unsigned starts;  // run starts, and one bit at n (if n < 32)
   int n;
   __device__ __forceinline__ Runs(const LoraParams &p, int64_t t0, int rows) : n(rows) {
     const int lane = threadIdx.x & 31;
-    const int raw = lane < n ? __ldg(p.index + t0 + lane) : -1;
+    int raw = -1;
+    row = t0 + lane;
+    if (lane < n) {
+      if (p.order) {
+        const int2 v = __ldcg(p.order + t0 + lane);
+        row = v.x;
+        raw = v.y;
+      } else {
+        raw = __ldg(p.index + t0 + lane);
+      }
+    }
     adapter = raw >= 0 && raw < p.n_adapters ? raw : -1;
     if (adapter != raw && raw != -1) atomicOr(&g_lora_error, 4);
     const int prev = __shfl_up_sync(0xffffffffu, adapter, 1);
@@ -116,7 +139,65 @@ struct Runs {
     end = later ? __ffs(later) - 1 : n;
     return __shfl_sync(0xffffffffu, adapter, at);
   }
+  // The row at place t (a place past the end: that of the last).
+  __device__ __forceinline__ int64_t row_at(int t) const {
+    return __shfl_sync(0xffffffffu, (int)row, min(t, n - 1));
+  }
 };
+
+// Rows of a segment sorted by adapter, so that the CTAs below read an adapter
+// once for many of them however the rows come (a counting sort; adapters that
+// share a bin only make more runs).  The order within a bin is that in which
+// warps arrive: no row's sums depend on it.
+__global__ void __launch_bounds__(1024) lora_order_kernel(const LoraParams p) {
+  __shared__ int count[kBins];
+  __shared__ int warp_sum[32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  count[tid] = 0;
+  __syncthreads();
+  int raw[kSegment / 1024], bin[kSegment / 1024], at[kSegment / 1024];
+  const int64_t t0 = (int64_t)blockIdx.x * kSegment + tid;
+#pragma unroll
+  for (int i = 0; i < kSegment / 1024; ++i)
+    raw[i] = t0 + i * 1024 < p.T ? __ldg(p.index + t0 + i * 1024) : -1;
+#pragma unroll
+  for (int i = 0; i < kSegment / 1024; ++i) {
+    const bool on = t0 + i * 1024 < p.T;
+    bin[i] = !on ? kBins : raw[i] >= 0 && raw[i] < p.n_adapters ? (raw[i] + 1) & (kBins - 1) : 0;
+    const unsigned same = __match_any_sync(0xffffffffu, bin[i]);
+    const int first = __ffs(same) - 1;
+    at[i] = on && lane == first ? atomicAdd(count + bin[i], __popc(same)) : 0;
+    at[i] = __shfl_sync(0xffffffffu, at[i], first) + __popc(same & ((1u << lane) - 1));
+  }
+  __syncthreads();
+  const int own = count[tid];
+  int sum = own;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    int v = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    warp_sum[lane] = v;
+  }
+  __syncthreads();
+  count[tid] = sum - own + (warp > 0 ? warp_sum[warp - 1] : 0);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSegment / 1024; ++i)
+    if (t0 + i * 1024 < p.T)
+      p.order[(int64_t)blockIdx.x * kSegment + count[bin[i]] + at[i]] =
+          make_int2((int)(t0 + i * 1024), raw[i]);
+}
 
 __device__ __forceinline__ int rank_of(const LoraParams &p, int a) {
   return p.rank ? min(max(__ldg(p.rank + a), 0), p.R) : p.R;
@@ -142,7 +223,9 @@ __device__ __forceinline__ void cluster_sync() {
 template <bool VEC, int NT>
 __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const LoraParams p) {
   extern __shared__ float part[];  // [kWarps][rows][Rp]
-  asm volatile("griddepcontrol.launch_dependents;");
+  // The up product starts once every CTA is past this: the order is then complete.
+  if (p.order) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int MT = NT == 1 ? 2 : 1, KU = NT == 1 ? 2 : 1;  // 16-rank tiles, steps of K at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const int64_t t0 = (int64_t)blockIdx.x * p.rows_down;
@@ -155,7 +238,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const LoraParams
     if (a < 0) continue;
     const int rank = rank_of(p, a);
     const __half *A = p.a + a * p.a_adapter + g * p.a_row;
-    const __half *X = p.x + (t0 + at + g) * p.ldx;
+    const __half *X[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) X[n] = p.x + runs.row_at(at + 8 * n + g) * p.ldx;
     for (int m0 = 0; m0 < rank; m0 += 16 * MT) {
       float c[MT][NT][4];
 #pragma unroll
@@ -180,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const LoraParams
               }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              xv[u][h][n] = at + 8 * n + g < end ? load8<VEC>(X + 8 * n * p.ldx, k, k_end) : z;
+              xv[u][h][n] = at + 8 * n + g < end ? load8<VEC>(X[n], k, k_end) : z;
           }
 #pragma unroll
         for (int u = 0; u < KU; ++u)
@@ -286,13 +371,19 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
   // [rows][pitch], once or twice: the parts of u, rows padded against bank conflicts
   extern __shared__ __align__(16) uint8_t sm[];
   const int pitch = p.Rk + 8;
-  float *fs = reinterpret_cast<float *>(sm);
-  __half *uh = reinterpret_cast<__half *>(sm + kMaxRows * sizeof(float));
+  int64_t *y_at = reinterpret_cast<int64_t *>(sm), *out_at = y_at + kMaxRows;  // rows' offsets
+  float *fs = reinterpret_cast<float *>(out_at + kMaxRows);
+  __half *uh = reinterpret_cast<__half *>(fs + kMaxRows);
   __half *ul = uh + p.rows_up * pitch;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const int64_t t0 = (int64_t)blockIdx.x * p.rows_up;
   const int rows = (int)min((int64_t)p.rows_up, p.T - t0);
   const Runs runs(p, t0, rows);
+  if (threadIdx.x < rows) {
+    y_at[threadIdx.x] = runs.row * p.ldy;
+    out_at[threadIdx.x] = runs.row * p.ldo;
+  }
+  __syncthreads();
   const uint4 z = make_uint4(0, 0, 0, 0);
   bool ready = false;  // u is in shared memory
   for (int i0 = (blockIdx.y * kUpWarps + warp) * kOut; !ready || i0 < p.N;
@@ -322,27 +413,18 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
         }
       };
       // rows 2 tig + {0, 1} of a column tile
-      const __half *Y = p.y + (t0 + at + 2 * tig) * p.ldy + i;
       auto load_y = [&](int n0, uint4 (&yv)[NN][2]) {
-        const __half *row = Y + (n0 - at) * p.ldy;
-        if (all && n0 + 8 * NN <= end) {
 #pragma unroll
-          for (int n = 0; n < NN; ++n, row += 8 * p.ldy) {
-            yv[n][0] = __ldg(reinterpret_cast<const uint4 *>(row));
-            yv[n][1] = __ldg(reinterpret_cast<const uint4 *>(row + p.ldy));
-          }
-          return;
-        }
-#pragma unroll
-        for (int n = 0; n < NN; ++n, row += 8 * p.ldy)
+        for (int n = 0; n < NN; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const __half *src = row + k * p.ldy;
-            const bool on = n0 + 8 * n + 2 * tig + k < end;
-            if (all)
-              yv[n][k] = on ? __ldg(reinterpret_cast<const uint4 *>(src)) : z;
-            else
-              yv[n][k] = on ? load8<VEC>(src, 0, p.N - i) : z;
+            const int t = n0 + 8 * n + 2 * tig + k;
+            yv[n][k] = z;
+            if (t < end) {
+              const __half *src = p.y + y_at[t] + i;
+              yv[n][k] = all ? __ldg(reinterpret_cast<const uint4 *>(src))
+                             : load8<VEC>(src, 0, p.N - i);
+            }
           }
       };
       uint4 yv[NN][2];
@@ -366,7 +448,6 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
       if (all && rank > 0 && rank <= 32 * RC) {
         const __half *u = uh + (at + g) * pitch + 8 * tig;
         const float *f = fs + at + 2 * tig;
-        __half *row = p.out + (t0 + at + 2 * tig) * p.ldo + i;
         for (; n0 + 8 * NN <= end; n0 += 8 * NN, u += 8 * NN * pitch, f += 8 * NN) {
           float c[NN][4][4];
 #pragma unroll
@@ -401,10 +482,10 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
             for (int k = 0; k < 2; ++k) o[n][k] = add_rows(yv[n][k], f[8 * n + k], c[n], k);
           if (n0 + 8 * NN < end) load_y(n0 + 8 * NN, yv);
 #pragma unroll
-          for (int n = 0; n < NN; ++n, row += 8 * p.ldo) {
-            *reinterpret_cast<uint4 *>(row) = o[n][0];
-            *reinterpret_cast<uint4 *>(row + p.ldo) = o[n][1];
-          }
+          for (int n = 0; n < NN; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<uint4 *>(p.out + out_at[n0 + 8 * n + 2 * tig + k] + i) = o[n][k];
         }
       }
       for (; n0 < end; n0 += 8 * NN) {
@@ -454,13 +535,13 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
               o[n][k] = add_rows(yv[n][k], fs[min(n0 + 8 * n + 2 * tig + k, rows - 1)], c[n], k);
           }
         if (n0 + 8 * NN < end) load_y(n0 + 8 * NN, yv);
-        __half *row = p.out + (t0 + n0 + 2 * tig) * p.ldo + i;
 #pragma unroll
-        for (int n = 0; n < NN; ++n, row += 8 * p.ldo)
+        for (int n = 0; n < NN; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if (n0 + 8 * n + 2 * tig + k >= end) continue;
-            __half *dst = row + k * p.ldo;
+            const int t = n0 + 8 * n + 2 * tig + k;
+            if (t >= end) continue;
+            __half *dst = p.out + out_at[t] + i;
             if (all) {
               *reinterpret_cast<uint4 *>(dst) = o[n][k];
             } else {
@@ -485,17 +566,19 @@ int pow2_at_least(int64_t v, int hi) {
 template <bool VEC, int NT>
 cudaError_t launch_down(const LoraParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3((unsigned)((p.T + p.rows_down - 1) / p.rows_down), (unsigned)p.slices);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)kWarps * p.rows_down * p.Rp * sizeof(float);
   cfg.stream = s;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 1;
-  attr.val.clusterDim.y = (unsigned)p.slices;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = (unsigned)p.slices;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.order ? 2 : 1;  // it waits itself for the rows' order
   const cudaError_t e = allow_smem<lora_down_kernel<VEC, NT>>(cfg.dynamicSmemBytes);
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, lora_down_kernel<VEC, NT>, p);
 }
@@ -506,7 +589,7 @@ cudaError_t launch_up(const LoraParams &p, int ctas_n, cudaStream_t s) {
   cudaLaunchAttribute attr;
   cfg.gridDim = dim3((unsigned)((p.T + p.rows_up - 1) / p.rows_up), (unsigned)ctas_n);
   cfg.blockDim = dim3(32 * kUpWarps);
-  cfg.dynamicSmemBytes = kMaxRows * sizeof(float) +
+  cfg.dynamicSmemBytes = kMaxRows * (2 * sizeof(int64_t) + sizeof(float)) +
                          (size_t)p.rows_up * (TWO ? 2 : 1) * (p.Rk + 8) * sizeof(__half);
   cfg.stream = s;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -526,7 +609,7 @@ cudaError_t launch_up(const LoraParams &p, int ctas_n, cudaStream_t s) {
 
 size_t lora_workspace_bytes(int64_t T, int64_t, int64_t R) {
   const int64_t Rk = (R + 31) / 32 * 32, rows = T > 0 ? T : 1;
-  return (size_t)(rows * Rk) * 2 * sizeof(__half) + (size_t)rows * sizeof(float);
+  return (size_t)(rows * Rk) * 2 * sizeof(__half) + (size_t)rows * (sizeof(int2) + sizeof(float));
 }
 
 qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t T, const __half *x,
@@ -560,16 +643,22 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.ldo = ldo;
   p.uh = static_cast<__half *>(workspace);
   p.ul = p.uh + T * p.Rk;
-  p.fs = reinterpret_cast<float *>(p.ul + T * p.Rk);
+  p.order = reinterpret_cast<int2 *>(p.ul + T * p.Rk);
+  p.fs = reinterpret_cast<float *>(p.order + T);
+  if (T < kOrderRows || ad.n_adapters < 2) p.order = nullptr;
   // Slices of K: as many as there are steps of kSlice, at most kMaxSlices.
   const int64_t steps = (ad.K + kSlice - 1) / kSlice;
   p.slices = (int)(steps < kMaxSlices ? steps : kMaxSlices);
   p.k_slice = (int)((steps + p.slices - 1) / p.slices) * kSlice;
   p.slices = (int)((ad.K + p.k_slice - 1) / p.k_slice);
-  // Rows per CTA: one while that still leaves few CTAs per SM (a decode step's
-  // adapters are read by the whole GPU at once), more as calls grow, so that a
-  // run's adapter is read by fewer CTAs.
-  const int64_t want = (int64_t)di.sms * 4;
+  // Rows per CTA: one while the GPU holds all of the down product's CTAs at once
+  // (2 per SM; a decode step's adapters are read by the whole GPU together), more
+  // as calls grow, so that a run's adapter is read by fewer CTAs; the up product
+  // likewise at 4 per SM.  64 rows of 16 adapters in turn, 4096 x 4096: 12.4 us,
+  // with one row a CTA 14.2; 256 of 16: 13.7, with half as many rows a CTA 20.2.
+  // Twice as many help grouped rows and cost scattered ones (256 rows of as many
+  // adapters: 35.7 -> 39.8 in the down product, 48.5 in the up product).
+  const int64_t want = (int64_t)di.sms * 2;
   const int cap = kRowRanks / p.Rp < kMaxRows ? kRowRanks / p.Rp : kMaxRows;
   p.rows_down = pow2_at_least((T * p.slices + want - 1) / want, cap);
   const int64_t per = kOut * kUpWarps, chunks = (ad.N + per - 1) / per;
@@ -586,6 +675,10 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   const bool vb = rows16(p.b, p.b_row) && p.b_adapter % 8 == 0 && rows16(y, ldy) && rows16(out, ldo);
 
   cudaError_t e;
+  if (p.order) {
+    lora_order_kernel<<<(unsigned)((T + kSegment - 1) / kSegment), 1024, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
+  }
   if (p.rows_down <= 8)
     e = va ? launch_down<true, 1>(p, s) : launch_down<false, 1>(p, s);
   else
