@@ -719,6 +719,26 @@ def test_lora_own_stream():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("T", [20, 260])
+def test_lora_in_a_graph(T):
+    # captured once, replayed with other rows and indices
+    g = gen(47)
+    ad = qz().LoraAdapters(randn(g, 5, 16, 192), randn(g, 5, 320, 16), torch.ones(5, device=DEV))
+    x, y, idx = randn(g, T, 192), randn(g, T, 320), i32(runs(T, 3, 5))
+    out, ws = torch.empty_like(y), qz().lora_workspace(T, 192, 16)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        qz().lora(x, y, ad, idx, out=out, workspace=ws)
+    for k in range(3):
+        x.copy_(randn(g, T, 192))
+        idx.copy_(i32([(t * (k + 2)) % 6 - 1 for t in range(T)]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, qz().lora(x, y, ad, idx))
+
+
 def test_lora_refusals():
     g = gen(45)
     x, y = randn(g, 4, 64), randn(g, 4, 32)

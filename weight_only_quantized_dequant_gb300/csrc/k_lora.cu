@@ -27,7 +27,7 @@
 // Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10.5 us, of
 // which down 5, up 3 after it; the chain index, adapter, products, cluster, u,
 // products is latency.  1500 rows of 8 adapters of ranks up to 64 in runs of 300,
-// 4096 x 11008: 50 us, 2 of them the sort, down 19 in a wave and a quarter of CTAs
+// 4096 x 11008: 48.5 us, 2 of them the sort, down 19 in a wave and a quarter of CTAs
 // (one takes 11), up the rest: each step of 64 outputs waits for its own loads (3.7
 // us a step, half of it loads; a product is 8 clocks of a scheduler, so the matrix
 // instructions are a tenth of the time), twice in the few row tiles that two runs
@@ -390,6 +390,10 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
        i0 += gridDim.y * kUpWarps * kOut) {
     const int i = i0 + g * 8;               // this thread's 8 outputs
     const bool all = VEC && i0 + kOut <= p.N;  // all of the warp's exist
+    // y of the next step on its way to the L2 (calls of more rows 50.0 -> 48.5 us;
+    // few rows have few steps, and 32 of them took 10.7 -> 11.1)
+    if (const int next = i0 + gridDim.y * kUpWarps * kOut; NN == 2 && next < p.N && lane < rows)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.y + y_at[lane] + next));
     for (int at = 0, end; at < rows; at = end) {
       const int a = runs.run(at, end);
       const int rank = a < 0 ? 0 : rank_of(p, a);
