@@ -29,7 +29,7 @@
 //
 // Measured (GB300).  32 single tokens over contexts up to 16384, 64 heads, 8 KV
 // heads of 128: 208 us, 6.56 TB/s of keys and values, the rate of a plain copy.
-// Four packed prompts up to 4096, 32 heads: 335-350 us, 975-1020 TFLOP/s; four
+// Four packed prompts up to 4096, 32 heads: 317-340 us, 1005-1077 TFLOP/s; four
 // chunks of 64 tokens over 24000, 64 heads on 8: 112 us, 921 TFLOP/s.  A block of
 // a 256-row tile takes about 3200 SM clocks: 2048 are the MMAs (64 each), the
 // rest is the chain of one stage (softmax 1550, its two products 1024 + 500 to
@@ -66,12 +66,18 @@ constexpr uint32_t kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr float kLag = 8.0f;           // log2 of how far a weight may exceed 1
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMinUnits = 3;           // units per CTA at least
+// Units per CTA at least.  One token over 199 keys takes 11.3 us with 1, 10.2 with 3
+// and 13.6 with 6; over 1000 keys 13.2, 15.0 and 19.5.
+constexpr int kMinUnits = 3;
 // Time to merge one partial, in key blocks: 8 rows over 30000 keys of one KV head
 // take 52 us when all SMs share the tile, 38 with this, 33 with 0.5, which costs
 // one token over 4096 keys 15.3 -> 17.7 us.
 constexpr float kMergeUnits = 0.2f;
-constexpr int kTileUnits = 1;          // a tile's fixed time, in key blocks
+// A tile's fixed time, in key blocks.  256 rows: four prompts of up to 4096 take 343
+// us with none, 326 with 1, 317 with 2; 128 rows: one token over 199 keys takes 15.1
+// us with none, 10.2 with 1, 11.0 with 2.
+template <int kM>
+constexpr int kTileUnits = kM / 128;
 constexpr int kSegs = 4;               // tiles announced ahead
 
 template <int D, int NQ>
@@ -364,7 +370,7 @@ __device__ __forceinline__ Range tile_range(const AttnParams &p, const Seq &s, i
 // time that a tile costs whatever its length, in blocks.
 template <int kM>
 __device__ __forceinline__ int tile_units(const Range &r) {
-  return kTileUnits + max(r.nb, 1);
+  return kTileUnits<kM> + max(r.nb, 1);
 }
 
 // Units of one KV head of each lane's sequence (whole warp): long sequences'
@@ -435,8 +441,8 @@ struct Walker {
       }
       const Range r = tile_range<kM>(p, s, rt);
       const int units = tile_units<kM>(r), tile_first = first;
-      const int a = max(u - first - kTileUnits, 0);                 // of its blocks
-      const int b = min(u_end - first, units) - kTileUnits;
+      const int a = max(u - first - kTileUnits<kM>, 0);                 // of its blocks
+      const int b = min(u_end - first, units) - kTileUnits<kM>;
       g.slot = u == 0 ? 0 : 1;
       g.head = head;
       g.seq = seq;
@@ -461,7 +467,7 @@ struct Walker {
       if (a == 0 && done) {
         g.slot = -1;
       } else {
-        g.c_lo = owner(u_begin + tile_first + kTileUnits);
+        g.c_lo = owner(u_begin + tile_first + kTileUnits<kM>);
         g.parts = owner(u_begin + tile_first + units - 1) - g.c_lo + 1;
         if (g.parts == 1) g.slot = -1;
         g.first_slot = begin_of(g.c_lo) >= u_begin + tile_first ? 0 : 1;
@@ -1424,7 +1430,12 @@ qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t
   p.s = sv;
   p.cnt = static_cast<unsigned *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + QZ_ATTENTION_SYNC_BYTES);
-  // Two stages of rows pay once a sequence fills the second one.
+  // Two stages of rows pay once a sequence fills the second one: 4 x 64 tokens
+  // over 24000 keys, 64 heads on 8, take 111 us with two and 144 with one, four
+  // prompts of up to 4096 326 and 381; 8 x 16 tokens over 4000 36.2 with one, 39.7
+  // with two, 64 single tokens, 32 heads, 97 and 125.  Short prompts, whose tiles
+  // are few, would gain with one (6 of up to 300: 26.8 -> 24.8), but the lengths
+  // held are known on the device only.
   const bool two = c.D < 256 && sv.n_tokens * p.G > (int64_t)128 * sv.n_seqs;
   p.q_boxes = scale > 0.0f && query_map(&p.qmap, q, sv.n_tokens, hq, c.D, q_token, q_head, p.G,
                                         two ? 128 : 64);
