@@ -1,6 +1,6 @@
 // Low-rank adapters beside a shared projection: out = y + s_a B_a (A_a x).
 //
-// Two launches over the same rows, on warp-level matrix instructions (rank and
+// Two products over the same rows, on warp-level matrix instructions (rank and
 // run lengths are far below a tcgen05 tile):
 //   down: u = A_a x.  A CTA takes a few rows and a slice of K; neighbouring rows
 //     of one adapter (a run) are the 8 columns of m16n8k16 products whose 16
@@ -27,8 +27,8 @@
 // Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10.5 us, of
 // which down 5, up 3 after it; the chain index, adapter, products, cluster, u,
 // products is latency.  1500 rows of 8 adapters of ranks up to 64 in runs of 300,
-// 4096 x 11008: 48.5 us, 2 of them the sort, down 19 in a wave and a quarter of CTAs
-// (one takes 11), up the rest: each step of 64 outputs waits for its own loads (3.7
+// 4096 x 11008: 48.5 us, 2 of them the sort, down 19 (one
+// wave of CTAs with fewer slices takes as long), up the rest: each step of 64 outputs waits for its own loads (3.7
 // us a step, half of it loads; a product is 8 clocks of a scheduler, so the matrix
 // instructions are a tenth of the time), twice in the few row tiles that two runs
 // share.  1500 rows of 48 adapters of rank 16 in turn: 48 us (265 unsorted).
