@@ -104,20 +104,28 @@ class PageTable:
 
     def step(self, new: dict, device="cuda") -> layer.SeqBatch:
         """The SeqBatch of a step that brings new[i] tokens to sequence i (in the
-        order of the dict); pages are taken from the pool as needed."""
-        cu, lens, rows = [0], [], []
+        order of the dict); pages are taken from the pool as needed.  A step that
+        does not fit raises and changes nothing, so that it can be tried again once
+        other sequences have given pages back."""
+        cu, lens, pages, at = [0], {}, {}, len(self.free)
         for i, n in new.items():
-            pages = self.pages.setdefault(i, [])
-            self.lens[i] = self.lens.get(i, 0) + n
-            while len(pages) * self.page_size < self.lens[i]:
-                if not self.free or len(pages) == self.max_pages:
-                    raise RuntimeError(f"no page for sequence {i}")
-                pages.append(self.free.pop())
+            if n < 0:
+                raise ValueError(f"sequence {i}: {n} new tokens")
+            lens[i] = self.lens.get(i, 0) + n
+            held = self.pages.get(i, [])
+            more = max(0, -(-lens[i] // self.page_size) - len(held))
+            if more > at or len(held) + more > self.max_pages:
+                raise RuntimeError(f"no page for sequence {i}")
+            pages[i] = held + self.free[at - more:at][::-1]
+            at -= more
             cu.append(cu[-1] + n)
-            lens.append(self.lens[i])
-            rows.append(pages + [0] * (self.max_pages - len(pages)))
-        return layer.SeqBatch(*(torch.tensor(t, dtype=torch.int32, device=device)
-                                for t in (cu, lens, rows)))
+        rows = [p + [0] * (self.max_pages - len(p)) for p in pages.values()]
+        batch = layer.SeqBatch(*(torch.tensor(t, dtype=torch.int32, device=device)
+                                 for t in (cu, list(lens.values()), rows)))
+        del self.free[at:]
+        self.pages.update(pages)
+        self.lens.update(lens)
+        return batch
 
     def release(self, i) -> None:
         """Give a finished sequence's pages back."""
