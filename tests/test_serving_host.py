@@ -74,3 +74,14 @@ def test_pages_are_handed_out_in_order(table):
     t.release(1)
     t.release("never seen")
     assert 1 not in t.lens and whole(t, 6)
+
+
+@pytest.mark.parametrize("index,want", [(None, []), ("rows", ["q", "v"])])
+def test_a_step_without_an_index_has_no_adapters(monkeypatch, index, want):
+    calls = []
+    monkeypatch.setattr(layer, "lora", lambda x, y, ad, i, out: calls.append((ad, i, out is y)))
+    lay = object.__new__(serving.ServedLayer)
+    lay.adapters = {"q": "q", "v": "v"}
+    lay.products = lambda names, x: [n + x for n in names]
+    assert lay._linear(("q", "k", "v"), "x", index) == ["qx", "kx", "vx"]
+    assert calls == [(n, index, True) for n in want]

@@ -64,7 +64,7 @@ class ServedLayer:
     def _linear(self, names, x, index):
         ys = self.products(names, x)
         for n, y in zip(names, ys):
-            if n in self.adapters:
+            if n in self.adapters and index is not None:
                 layer.lora(x, y, self.adapters[n], index, out=y)
         return ys
 
@@ -72,7 +72,8 @@ class ServedLayer:
                  index: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
         """(output [T, hidden], residual): x is the previous layer's output (the
         embeddings in the first one, with residual None), index the adapter of
-        every row (int32, -1: none), workspace from layer.attention_workspace."""
+        every row (int32, -1: none; None: no row has one), workspace from
+        layer.attention_workspace."""
         T, D, hkv = x.shape[0], self.cache.head_dim, self.cache.n_kv_heads
         y, residual = layer.rmsnorm(x, self.norms[0], self.eps, residual=residual,
                                     w_bias=self.w_bias, residual_out=residual)
