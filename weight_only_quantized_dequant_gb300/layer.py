@@ -43,6 +43,13 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
     return _empty(t.shape, t.dtype, t.device, stream)
 
 
+# Handles hold the addresses of their tensors for the kernels, made once, so their
+# fields are frozen; a handle with another tensor is dataclasses.replace(handle, ...).
+def _set(handle, **values) -> None:
+    for name, v in values.items():
+        object.__setattr__(handle, name, v)
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -137,7 +144,7 @@ def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
 
 # ----------------------------------------------------------- paged cache ---
-@dataclass
+@dataclass(frozen=True)
 class PagedKV:
     """A paged key/value cache: k and v fp16 [n_pages, n_kv_heads, page_size,
     head_dim] with any strides that are multiples of 8 (a pool laid out
@@ -152,11 +159,10 @@ class PagedKV:
         _need(k.dtype == _F16 and v.dtype == _F16 and k.dim() == 4 and k.shape == v.shape,
               "k and v: fp16 [n_pages, n_kv_heads, page_size, head_dim]")
         _need(k.stride(3) == 1 and v.stride(3) == 1, "k and v: contiguous head_dim")
-        self._arg = _lib.KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], k.shape[1],
-                                 k.shape[3], k.stride(0), k.stride(1), k.stride(2), v.stride(0),
-                                 v.stride(1), v.stride(2))
-        self._ref = ctypes.byref(self._arg)
-        self.shape = tuple(k.shape)
+        arg = _lib.KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], k.shape[1],
+                           k.shape[3], k.stride(0), k.stride(1), k.stride(2), v.stride(0),
+                           v.stride(1), v.stride(2))
+        _set(self, _arg=arg, _ref=ctypes.byref(arg), shape=tuple(k.shape))
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
@@ -174,7 +180,7 @@ class PagedKV:
         return self.k.shape[3]
 
 
-@dataclass
+@dataclass(frozen=True)
 class SeqBatch:
     """The sequences of a step: cu_q int32 [S+1] (rows cu_q[i]..cu_q[i+1]-1 are
     the new tokens of sequence i), kv_len int32 [S] (tokens held, the new ones
@@ -194,9 +200,9 @@ class SeqBatch:
         # the row stride is also the number of entries that may be read
         _need(_rows(self.page_table, "page_table", self.page_table.shape, _I32)
               == self.page_table.shape[1], "page_table: a contiguous table is needed")
-        self._arg = _lib.SeqBatchArg(S, 0, self.cu_q.data_ptr(), self.kv_len.data_ptr(),
-                                     self.page_table.data_ptr(), self.page_table.shape[1])
-        self._ref = ctypes.byref(self._arg)
+        arg = _lib.SeqBatchArg(S, 0, self.cu_q.data_ptr(), self.kv_len.data_ptr(),
+                               self.page_table.data_ptr(), self.page_table.shape[1])
+        _set(self, _arg=arg, _ref=ctypes.byref(arg))
 
     @property
     def n_seqs(self) -> int:
@@ -300,7 +306,7 @@ def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: floa
 
 
 # ------------------------------------------------------------------ LoRA ---
-@dataclass
+@dataclass(frozen=True)
 class LoraAdapters:
     """A pool of low-rank adapters of one projection: a fp16 [n, R, K], b fp16
     [n, N, R], scale fp32 [n], rank int32 [n] (None: every adapter has rank R)."""
@@ -322,12 +328,11 @@ class LoraAdapters:
         _vec(self.scale, "scale", n, _F32)
         if self.rank is not None:
             _vec(self.rank, "rank", n, _I32)
-        self._arg = _lib.LoraArg(a.data_ptr(), b.data_ptr(), self.scale.data_ptr(),
-                                 None if self.rank is None else self.rank.data_ptr(), n, R, K,
-                                 b.shape[1], a.stride(0), a.stride(1) if R > 1 else K,
-                                 b.stride(0), b.stride(1) if b.shape[1] > 1 else R)
-        self._ref = ctypes.byref(self._arg)
-        self.sizes = (K, R, b.shape[1])
+        arg = _lib.LoraArg(a.data_ptr(), b.data_ptr(), self.scale.data_ptr(),
+                           None if self.rank is None else self.rank.data_ptr(), n, R, K,
+                           b.shape[1], a.stride(0), a.stride(1) if R > 1 else K,
+                           b.stride(0), b.stride(1) if b.shape[1] > 1 else R)
+        _set(self, _arg=arg, _ref=ctypes.byref(arg), sizes=(K, R, b.shape[1]))
 
     @property
     def K(self) -> int:
