@@ -92,3 +92,27 @@ def test_a_handle_with_another_tensor_is_a_new_one():
     ad = adapters()
     assert dataclasses.replace(ad, rank=gpu(2, dtype=I32))._arg.rank is not None
     assert ad._arg.rank is None
+
+
+def test_calls_that_share_sequences_keep_their_row_counts(lib):
+    """The library runs without the interpreter's lock, so another thread may call
+    with the same SeqBatch before it has read this call's arguments."""
+    cache, seqs = handles()
+
+    def append(T):
+        q = gpu(T, 4, 64)
+        layer.rope_append(q, gpu(T, 2, 64), gpu(T, 2, 64), cache, seqs, None, q_out=q,
+                          stream=Stream)
+
+    def attend(T):
+        q = gpu(T, 4, 64)
+        layer.attention_paged(q, cache, seqs, out=q, workspace=gpu(1 << 20, dtype=torch.uint8),
+                              stream=Stream)
+
+    lib.before = {"qz_rope_append": lambda: append(3), "qz_attention_paged": lambda: attend(4)}
+    append(5)
+    attend(6)
+    append(2)
+    rows = [a._obj.n_tokens for _, args in lib.calls for a in args
+            if isinstance(getattr(a, "_obj", None), _lib.SeqBatchArg)]
+    assert rows == [3, 5, 4, 6, 2]

@@ -200,13 +200,12 @@ class SeqBatch:
         # the row stride is also the number of entries that may be read
         _need(_rows(self.page_table, "page_table", self.page_table.shape, _I32)
               == self.page_table.shape[1], "page_table: a contiguous table is needed")
-        arg = _lib.SeqBatchArg(S, 0, self.cu_q.data_ptr(), self.kv_len.data_ptr(),
-                               self.page_table.data_ptr(), self.page_table.shape[1])
-        _set(self, _arg=arg, _ref=ctypes.byref(arg))
+        _set(self, _arg=(self.cu_q.data_ptr(), self.kv_len.data_ptr(),
+                         self.page_table.data_ptr(), self.page_table.shape[1]), n_seqs=S)
 
-    @property
-    def n_seqs(self) -> int:
-        return self.kv_len.shape[0]
+    def _ref(self, n_tokens: int):
+        """The library's view for one call: another thread may share the batch."""
+        return ctypes.byref(_lib.SeqBatchArg(self.n_seqs, n_tokens, *self._arg))
 
 
 def _heads(t: torch.Tensor, what: str, T: int, heads: int, D: int):
@@ -243,9 +242,8 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedK
         q_out, ot, oh = _empty((T, H, D), _F16, q.device, stream), H * D, D
     else:
         ot, oh = _heads(q_out, "q_out", T, H, D)
-    seqs._arg.n_tokens = T
     st = _lib.load().qz_rope_append(q.data_ptr(), H, qt, qh, k.data_ptr(), kt, kh, v.data_ptr(),
-                                    vt, vh, rp, n, cache._ref, seqs._ref, q_out.data_ptr(), ot,
+                                    vt, vh, rp, n, cache._ref, seqs._ref(T), q_out.data_ptr(), ot,
                                     oh, _stream_of(q, stream))
     if st:
         _lib.fail("qz_rope_append", st)
@@ -295,8 +293,7 @@ def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: floa
         ot, oh = _heads(out, "out", T, H, D)
     if workspace is None:
         workspace = attention_workspace(T, seqs.n_seqs, H, hkv, D, q.device, stream)
-    seqs._arg.n_tokens = T
-    st = _lib.load().qz_attention_paged(q.data_ptr(), H, qt, qh, cache._ref, seqs._ref,
+    st = _lib.load().qz_attention_paged(q.data_ptr(), H, qt, qh, cache._ref, seqs._ref(T),
                                         D ** -0.5 if scale is None else scale, softcap, window,
                                         out.data_ptr(), ot, oh, workspace.data_ptr(),
                                         workspace.numel(), _stream_of(q, stream))
