@@ -56,6 +56,7 @@ class Library:
 def lib(monkeypatch):
     rec = Library()
     monkeypatch.setattr(_lib, "load", lambda: rec)
+    monkeypatch.setattr(layer, "_current_device", lambda: 0, raising=False)
     return rec
 
 
@@ -116,3 +117,105 @@ def test_calls_that_share_sequences_keep_their_row_counts(lib):
     rows = [a._obj.n_tokens for _, args in lib.calls for a in args
             if isinstance(getattr(a, "_obj", None), _lib.SeqBatchArg)]
     assert rows == [3, 5, 4, 6, 2]
+
+
+# ---------------------------------------------------- devices, workspaces ---
+def norm_args(**kw):
+    return dict(dict(x=gpu(3, 64), weight=gpu(64), residual=gpu(3, 64), out=gpu(3, 64),
+                     residual_out=gpu(3, 64), stream=Stream), **kw)
+
+
+def int8_args(**kw):
+    return norm_args(**dict(dict(out=gpu(3, 64, dtype=torch.int8), scale=gpu(3, dtype=F32)), **kw))
+
+
+def append_args(**kw):
+    cache, seqs = handles()
+    return dict(dict(q=gpu(3, 4, 64), k=gpu(3, 2, 64), v=gpu(3, 2, 64), cache=cache, seqs=seqs,
+                     rope=gpu(9, 64, dtype=F32), q_out=gpu(3, 4, 64), stream=Stream), **kw)
+
+
+def attention_args(**kw):
+    cache, seqs = handles()
+    return dict(dict(q=gpu(3, 4, 64), cache=cache, seqs=seqs, out=gpu(3, 4, 64),
+                     workspace=gpu(64, dtype=torch.uint8), stream=Stream), **kw)
+
+
+def lora_args(**kw):
+    return dict(dict(x=gpu(3, 64), y=gpu(3, 32), adapters=adapters(), index=gpu(3, dtype=I32),
+                     out=gpu(3, 32), workspace=gpu(64, dtype=torch.uint8), stream=Stream), **kw)
+
+
+CALLS = [(layer.rmsnorm, norm_args), (layer.rmsnorm_int8, int8_args),
+         (layer.rope_append, append_args), (layer.attention_paged, attention_args),
+         (layer.lora, lora_args)]
+OPERANDS = [(f, make, n) for f, make in CALLS for n, v in make().items() if isinstance(v, OnGpu)]
+
+
+def moved(t, index):
+    return OnGpu(t.t, index)
+
+
+@pytest.mark.parametrize("f,make", CALLS)
+def test_operands_of_the_current_device_are_taken(lib, f, make):
+    f(**make())
+    assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("f,make,name", OPERANDS)
+def test_operands_of_another_device_are_refused(lib, f, make, name):
+    args = make()
+    with pytest.raises(ValueError):
+        f(**dict(args, **{name: moved(args[name], 1)}))
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("f,make,name", OPERANDS)
+def test_operands_on_the_host_are_refused(lib, f, make, name):
+    args = make()
+    with pytest.raises(ValueError):
+        f(**dict(args, **{name: args[name].t}))
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("f,make", CALLS)
+def test_a_call_beside_the_current_device_is_refused(lib, monkeypatch, f, make):
+    """The library launches on the current device, whatever the operands'."""
+    monkeypatch.setattr(layer, "_current_device", lambda: 1, raising=False)
+    with pytest.raises(ValueError):
+        f(**make())
+    assert not lib.calls
+
+
+def test_handles_of_another_device_are_refused(lib):
+    cache, seqs = handles()
+    other = dataclasses.replace(cache, k=moved(cache.k, 1), v=moved(cache.v, 1))
+    far = dataclasses.replace(seqs, cu_q=moved(seqs.cu_q, 1), kv_len=moved(seqs.kv_len, 1),
+                              page_table=moved(seqs.page_table, 1))
+    for f, make in CALLS[2:4]:
+        for kw in (dict(cache=other), dict(seqs=far)):
+            with pytest.raises(ValueError):
+                f(**make(**kw))
+    ad = adapters()
+    away = layer.LoraAdapters(moved(ad.a, 1), moved(ad.b, 1), moved(ad.scale, 1))
+    with pytest.raises(ValueError):
+        layer.lora(**lora_args(adapters=away))
+    assert not lib.calls
+    # one handle, two devices
+    for h in (cache, seqs, layer.LoraAdapters(ad.a, ad.b, ad.scale, gpu(2, dtype=I32))):
+        for field in dataclasses.fields(h):
+            t = getattr(h, field.name)
+            if isinstance(t, OnGpu):
+                with pytest.raises(ValueError):
+                    dataclasses.replace(h, **{field.name: moved(t, 1)})
+
+
+@pytest.mark.parametrize("f,make", CALLS[3:])
+def test_workspaces(lib, f, make):
+    f(**make(workspace=gpu(100, dtype=F32)))  # any type: its bytes count
+    assert lib.calls[-1][1][-2] == 400
+    for bad in (torch.zeros(64, dtype=torch.uint8), gpu(64, dtype=torch.uint8, index=1),
+                OnGpu(torch.zeros(64, dtype=torch.uint8)[::2])):
+        with pytest.raises(ValueError):
+            f(**make(workspace=bad))
+    assert len(lib.calls) == 1

@@ -4,7 +4,8 @@ of the library (include/qz.h, "Layer glue for serving"): ``rmsnorm`` and
 cache, and ``lora`` for the low-rank adapters beside a shared projection.
 
 Every function takes ``stream`` (default: the current one); outputs and
-workspaces that a call allocates belong to that stream.
+workspaces that a call allocates belong to that stream.  All tensors of a call
+lie on the current device.
 """
 from __future__ import annotations
 
@@ -17,14 +18,15 @@ from . import _lib
 
 _F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() costs 10x as much
+_current_device = torch._C._cuda_getDevice  # any tensor on a GPU has started CUDA by then
 
 # A decode step makes hundreds of these calls and the kernels of small batches
 # take a few microseconds, so the checks below are few attribute reads each and
 # the library is called without another layer.
 
 
-def _stream_of(t: torch.Tensor, stream) -> int:
-    return _raw_stream(t.device.index) if stream is None else stream.cuda_stream
+def _stream_of(dev: int, stream) -> int:
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -60,25 +62,55 @@ def _cuda_or_raise(t) -> None:
         raise ValueError("libqz works on CUDA tensors only (no CPU fallback)")
 
 
-def _rows(t: torch.Tensor, what: str, shape, dtype=_F16) -> int:
-    """Row stride of a CUDA matrix with contiguous rows (that of a single row,
+def _place_or_raise(t, what: str, dev: int) -> None:
+    """Why t does not lie on GPU dev, if so."""
+    _cuda_or_raise(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on GPU {t.get_device()}, but the call runs on GPU {dev}")
+
+
+def _device(t: torch.Tensor, what: str) -> int:
+    """The GPU of a call's first operand: the current one, where the library launches."""
+    _cuda_or_raise(t)
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"{what}: on GPU {dev}, but the current device is GPU "
+                         f"{_current_device()}; torch.cuda.device({dev}) selects it")
+    return dev
+
+
+def _rows(t: torch.Tensor, what: str, dev: int, shape, dtype=_F16) -> int:
+    """Row stride of a matrix with contiguous rows on GPU dev (that of a single row,
     which torch may report as anything, is its length)."""
-    if t.is_cuda and t.dtype is dtype and t.shape == shape:
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape:
         if t.is_contiguous():
             return shape[1]
         if t.stride(1) == 1 or shape[1] <= 1:
             return t.stride(0) if shape[0] > 1 else shape[1]
-    _cuda_or_raise(t)
+    _place_or_raise(t, what, dev)
     raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}; a {dtype} "
                      f"matrix {tuple(shape)} with contiguous rows is needed")
 
 
-def _vec(t: torch.Tensor, what: str, n: int, dtype) -> int:
-    """Address of a contiguous CUDA vector of n."""
-    if t.is_cuda and t.dtype is dtype and t.shape == (n,) and t.is_contiguous():
+def _vec(t: torch.Tensor, what: str, dev: int, n: int, dtype) -> int:
+    """Address of a contiguous vector of n on GPU dev."""
+    if t.get_device() == dev and t.dtype is dtype and t.shape == (n,) and t.is_contiguous():
         return t.data_ptr()
-    _cuda_or_raise(t)
+    _place_or_raise(t, what, dev)
     raise ValueError(f"{what}: a contiguous {dtype} vector of {n} is needed")
+
+
+def _space(t: torch.Tensor, dev: int) -> int:
+    """Bytes of a workspace on GPU dev."""
+    if t.get_device() == dev and t.is_contiguous():
+        return t.numel() * t.element_size()
+    _place_or_raise(t, "workspace", dev)
+    raise ValueError("workspace: a contiguous tensor is needed")
+
+
+def _on(handle, what: str, dev: int) -> None:
+    if handle.device_index != dev:
+        raise ValueError(f"{what}: on GPU {handle.device_index}, but the call runs on GPU {dev}")
 
 
 # ------------------------------------------------------------------ norm ---
@@ -93,20 +125,21 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     shape = x.shape
     _need(len(shape) == 2, "x: two dimensions are needed")
     T, K = shape
-    ldx = _rows(x, "x", shape)
-    w = _vec(weight, "weight", K, _F16)
+    dev = _device(x, "x")
+    ldx = _rows(x, "x", dev, shape)
+    w = _vec(weight, "weight", dev, K, _F16)
     r = ldr = h = ldh = 0
     if residual is not None:
-        r, ldr = residual.data_ptr(), _rows(residual, "residual", shape)
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", dev, shape)
         if residual_out is None:
             residual_out = _like(x, stream)
     if residual_out is not None:
-        h, ldh = residual_out.data_ptr(), _rows(residual_out, "residual_out", shape)
+        h, ldh = residual_out.data_ptr(), _rows(residual_out, "residual_out", dev, shape)
     if out is None:
         out = _like(x, stream)
-    ldy = _rows(out, "out", shape)
+    ldy = _rows(out, "out", dev, shape)
     st = _lib.load().qz_rmsnorm(x.data_ptr(), ldx, r, ldr, w, w_bias, eps, T, K, out.data_ptr(),
-                                ldy, h, ldh, _stream_of(x, stream))
+                                ldy, h, ldh, _stream_of(dev, stream))
     if st:
         _lib.fail("qz_rmsnorm", st)
     return out, (x if residual_out is None else residual_out)
@@ -121,23 +154,24 @@ def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     shape = x.shape
     _need(len(shape) == 2, "x: two dimensions are needed")
     T, K = shape
-    ldx = _rows(x, "x", shape)
-    w = _vec(weight, "weight", K, _F16)
+    dev = _device(x, "x")
+    ldx = _rows(x, "x", dev, shape)
+    w = _vec(weight, "weight", dev, K, _F16)
     r = ldr = h = ldh = 0
     if residual is not None:
-        r, ldr = residual.data_ptr(), _rows(residual, "residual", shape)
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", dev, shape)
         if residual_out is None:
             residual_out = _like(x, stream)
     if residual_out is not None:
-        h, ldh = residual_out.data_ptr(), _rows(residual_out, "residual_out", shape)
+        h, ldh = residual_out.data_ptr(), _rows(residual_out, "residual_out", dev, shape)
     if out is None:
         out = _empty(shape, torch.int8, x.device, stream)
-    ldq = _rows(out, "out", shape, torch.int8)
+    ldq = _rows(out, "out", dev, shape, torch.int8)
     if scale is None:
         scale = _empty((T,), _F32, x.device, stream)
-    s = _vec(scale, "scale", T, _F32)
+    s = _vec(scale, "scale", dev, T, _F32)
     st = _lib.load().qz_rmsnorm_int8(x.data_ptr(), ldx, r, ldr, w, w_bias, eps, T, K,
-                                     out.data_ptr(), ldq, s, h, ldh, _stream_of(x, stream))
+                                     out.data_ptr(), ldq, s, h, ldh, _stream_of(dev, stream))
     if st:
         _lib.fail("qz_rmsnorm_int8", st)
     return out, scale, (x if residual_out is None else residual_out)
@@ -155,14 +189,16 @@ class PagedKV:
 
     def __post_init__(self):
         k, v = self.k, self.v
-        _need(k.is_cuda and v.is_cuda, "libqz works on CUDA tensors only (no CPU fallback)")
+        _cuda_or_raise(k)
+        dev = k.get_device()
+        _place_or_raise(v, "v", dev)
         _need(k.dtype == _F16 and v.dtype == _F16 and k.dim() == 4 and k.shape == v.shape,
               "k and v: fp16 [n_pages, n_kv_heads, page_size, head_dim]")
         _need(k.stride(3) == 1 and v.stride(3) == 1, "k and v: contiguous head_dim")
         arg = _lib.KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], k.shape[1],
                            k.shape[3], k.stride(0), k.stride(1), k.stride(2), v.stride(0),
                            v.stride(1), v.stride(2))
-        _set(self, _arg=arg, _ref=ctypes.byref(arg), shape=tuple(k.shape))
+        _set(self, _arg=arg, _ref=ctypes.byref(arg), shape=tuple(k.shape), device_index=dev)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
@@ -192,29 +228,30 @@ class SeqBatch:
     _arg: object = field(default=None, repr=False, compare=False)
 
     def __post_init__(self):
-        S = self.kv_len.shape[0]
-        _vec(self.cu_q, "cu_q", S + 1, _I32)
-        _vec(self.kv_len, "kv_len", S, _I32)
+        S, dev = self.kv_len.shape[0], self.kv_len.get_device()
+        _vec(self.kv_len, "kv_len", dev, S, _I32)
+        _vec(self.cu_q, "cu_q", dev, S + 1, _I32)
         _need(self.page_table.dim() == 2 and self.page_table.shape[0] == S,
               "page_table: one row per sequence")
         # the row stride is also the number of entries that may be read
-        _need(_rows(self.page_table, "page_table", self.page_table.shape, _I32)
+        _need(_rows(self.page_table, "page_table", dev, self.page_table.shape, _I32)
               == self.page_table.shape[1], "page_table: a contiguous table is needed")
         _set(self, _arg=(self.cu_q.data_ptr(), self.kv_len.data_ptr(),
-                         self.page_table.data_ptr(), self.page_table.shape[1]), n_seqs=S)
+                         self.page_table.data_ptr(), self.page_table.shape[1]),
+             n_seqs=S, device_index=dev)
 
     def _ref(self, n_tokens: int):
         """The library's view for one call: another thread may share the batch."""
         return ctypes.byref(_lib.SeqBatchArg(self.n_seqs, n_tokens, *self._arg))
 
 
-def _heads(t: torch.Tensor, what: str, T: int, heads: int, D: int):
-    """Token and head strides of a CUDA fp16 [T, heads, D] with contiguous rows."""
-    if t.is_cuda and t.dtype is _F16 and t.shape == (T, heads, D):
+def _heads(t: torch.Tensor, what: str, dev: int, T: int, heads: int, D: int):
+    """Token and head strides of an fp16 [T, heads, D] with contiguous rows on GPU dev."""
+    if t.get_device() == dev and t.dtype is _F16 and t.shape == (T, heads, D):
         st, sh, sd = t.stride()
         if sd == 1:
             return st, sh
-    _cuda_or_raise(t)
+    _place_or_raise(t, what, dev)
     raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}; fp16 "
                      f"{(T, heads, D)} with contiguous rows is needed")
 
@@ -229,22 +266,26 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedK
     _need(q.dim() == 3, "q: three dimensions are needed")
     T, H, _ = q.shape
     _, hkv, _, D = cache.shape
-    qt, qh = _heads(q, "q", T, H, D)
-    kt, kh = _heads(k, "k", T, hkv, D)
-    vt, vh = _heads(v, "v", T, hkv, D)
+    dev = _device(q, "q")
+    _on(cache, "cache", dev)
+    _on(seqs, "seqs", dev)
+    qt, qh = _heads(q, "q", dev, T, H, D)
+    kt, kh = _heads(k, "k", dev, T, hkv, D)
+    vt, vh = _heads(v, "v", dev, T, hkv, D)
     rp = n = 0
     if rope is not None:
-        if not (rope.is_cuda and rope.dtype is _F32 and rope.dim() == 2 and rope.shape[1] == D
+        _place_or_raise(rope, "rope", dev)
+        if not (rope.dtype is _F32 and rope.dim() == 2 and rope.shape[1] == D
                 and rope.is_contiguous()):
             raise ValueError(f"rope: a contiguous fp32 CUDA tensor [positions, {D}] is needed")
         rp, n = rope.data_ptr(), rope.shape[0]
     if q_out is None:
         q_out, ot, oh = _empty((T, H, D), _F16, q.device, stream), H * D, D
     else:
-        ot, oh = _heads(q_out, "q_out", T, H, D)
+        ot, oh = _heads(q_out, "q_out", dev, T, H, D)
     st = _lib.load().qz_rope_append(q.data_ptr(), H, qt, qh, k.data_ptr(), kt, kh, v.data_ptr(),
                                     vt, vh, rp, n, cache._ref, seqs._ref(T), q_out.data_ptr(), ot,
-                                    oh, _stream_of(q, stream))
+                                    oh, _stream_of(dev, stream))
     if st:
         _lib.fail("qz_rope_append", st)
     return q_out
@@ -284,19 +325,23 @@ def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: floa
     _need(q.dim() == 3, "q: three dimensions are needed")
     T, H, _ = q.shape
     _, hkv, _, D = cache.shape
-    qt, qh = _heads(q, "q", T, H, D)
+    dev = _device(q, "q")
+    _on(cache, "cache", dev)
+    _on(seqs, "seqs", dev)
+    qt, qh = _heads(q, "q", dev, T, H, D)
     if H < 1 or H % hkv:
         raise ValueError(f"q: {H} heads over {hkv} KV heads")
     if out is None:
         out, ot, oh = _empty((T, H, D), _F16, q.device, stream), H * D, D
     else:
-        ot, oh = _heads(out, "out", T, H, D)
+        ot, oh = _heads(out, "out", dev, T, H, D)
     if workspace is None:
         workspace = attention_workspace(T, seqs.n_seqs, H, hkv, D, q.device, stream)
+    nbytes = _space(workspace, dev)
     st = _lib.load().qz_attention_paged(q.data_ptr(), H, qt, qh, cache._ref, seqs._ref(T),
                                         D ** -0.5 if scale is None else scale, softcap, window,
                                         out.data_ptr(), ot, oh, workspace.data_ptr(),
-                                        workspace.numel(), _stream_of(q, stream))
+                                        nbytes, _stream_of(dev, stream))
     if st:
         _lib.fail("qz_attention_paged", st)
     return out
@@ -315,21 +360,23 @@ class LoraAdapters:
 
     def __post_init__(self):
         a, b = self.a, self.b
-        _need(a.is_cuda and b.is_cuda, "libqz works on CUDA tensors only (no CPU fallback)")
+        _cuda_or_raise(a)
+        dev = a.get_device()
+        _place_or_raise(b, "b", dev)
         _need(a.dtype == _F16 and b.dtype == _F16 and a.dim() == 3 and b.dim() == 3,
               "a and b: fp16 [n, R, K] and [n, N, R]")
         n, R, K = a.shape
         _need(b.shape[0] == n and b.shape[2] == R, "b: shape does not match a")
         _need((a.stride(2) == 1 or K == 1) and (b.stride(2) == 1 or R == 1),
               "a and b: contiguous rows")
-        _vec(self.scale, "scale", n, _F32)
+        _vec(self.scale, "scale", dev, n, _F32)
         if self.rank is not None:
-            _vec(self.rank, "rank", n, _I32)
+            _vec(self.rank, "rank", dev, n, _I32)
         arg = _lib.LoraArg(a.data_ptr(), b.data_ptr(), self.scale.data_ptr(),
                            None if self.rank is None else self.rank.data_ptr(), n, R, K,
                            b.shape[1], a.stride(0), a.stride(1) if R > 1 else K,
                            b.stride(0), b.stride(1) if b.shape[1] > 1 else R)
-        _set(self, _arg=arg, _ref=ctypes.byref(arg), sizes=(K, R, b.shape[1]))
+        _set(self, _arg=arg, _ref=ctypes.byref(arg), sizes=(K, R, b.shape[1]), device_index=dev)
 
     @property
     def K(self) -> int:
@@ -359,17 +406,20 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters, index: torch.
     may be y)."""
     _need(x.dim() == 2, "x: two dimensions are needed")
     T, K, R, N = x.shape[0], *adapters.sizes
-    ldx = _rows(x, "x", (T, K))
-    ldy = _rows(y, "y", (T, N))
-    i = _vec(index, "index", T, _I32)
+    dev = _device(x, "x")
+    _on(adapters, "adapters", dev)
+    ldx = _rows(x, "x", dev, (T, K))
+    ldy = _rows(y, "y", dev, (T, N))
+    i = _vec(index, "index", dev, T, _I32)
     if out is None:
         out = _like(y, stream)
-    ldo = _rows(out, "out", (T, N))
+    ldo = _rows(out, "out", dev, (T, N))
     if workspace is None:
         workspace = lora_workspace(T, K, R, x.device, stream)
+    nbytes = _space(workspace, dev)
     st = _lib.load().qz_lora(adapters._ref, i, T, x.data_ptr(), ldx, y.data_ptr(), ldy,
-                             out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(),
-                             _stream_of(x, stream))
+                             out.data_ptr(), ldo, workspace.data_ptr(), nbytes,
+                             _stream_of(dev, stream))
     if st:
         _lib.fail("qz_lora", st)
     return out
