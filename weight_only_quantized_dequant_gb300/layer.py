@@ -69,13 +69,17 @@ def _place_or_raise(t, what: str, dev: int) -> None:
         raise ValueError(f"{what}: on GPU {t.get_device()}, but the call runs on GPU {dev}")
 
 
+def _wrong_device(t, what: str) -> None:
+    _cuda_or_raise(t)
+    raise ValueError(f"{what}: on GPU {t.get_device()}, but the current device is GPU "
+                     f"{_current_device()}; torch.cuda.device selects another")
+
+
 def _device(t: torch.Tensor, what: str) -> int:
     """The GPU of a call's first operand: the current one, where the library launches."""
-    _cuda_or_raise(t)
     dev = t.get_device()
-    if dev != _current_device():
-        raise ValueError(f"{what}: on GPU {dev}, but the current device is GPU "
-                         f"{_current_device()}; torch.cuda.device({dev}) selects it")
+    if dev < 0 or dev != _current_device():
+        _wrong_device(t, what)
     return dev
 
 
@@ -103,14 +107,13 @@ def _vec(t: torch.Tensor, what: str, dev: int, n: int, dtype) -> int:
 def _space(t: torch.Tensor, dev: int) -> int:
     """Bytes of a workspace on GPU dev."""
     if t.get_device() == dev and t.is_contiguous():
-        return t.numel() * t.element_size()
+        return t.nbytes
     _place_or_raise(t, "workspace", dev)
     raise ValueError("workspace: a contiguous tensor is needed")
 
 
-def _on(handle, what: str, dev: int) -> None:
-    if handle.device_index != dev:
-        raise ValueError(f"{what}: on GPU {handle.device_index}, but the call runs on GPU {dev}")
+def _far(handle, what: str, dev: int) -> None:
+    raise ValueError(f"{what}: on GPU {handle.device_index}, but the call runs on GPU {dev}")
 
 
 # ------------------------------------------------------------------ norm ---
@@ -238,11 +241,16 @@ class SeqBatch:
               == self.page_table.shape[1], "page_table: a contiguous table is needed")
         _set(self, _arg=(self.cu_q.data_ptr(), self.kv_len.data_ptr(),
                          self.page_table.data_ptr(), self.page_table.shape[1]),
-             n_seqs=S, device_index=dev)
+             n_seqs=S, device_index=dev, _last=(-1, None))
 
     def _ref(self, n_tokens: int):
-        """The library's view for one call: another thread may share the batch."""
-        return ctypes.byref(_lib.SeqBatchArg(self.n_seqs, n_tokens, *self._arg))
+        """The library's view of a step of n_tokens rows.  Another thread may call with
+        another count, so a view is never changed once it is made."""
+        n, ref = self._last
+        if n != n_tokens:
+            ref = ctypes.byref(_lib.SeqBatchArg(self.n_seqs, n_tokens, *self._arg))
+            _set(self, _last=(n_tokens, ref))
+        return ref
 
 
 def _heads(t: torch.Tensor, what: str, dev: int, T: int, heads: int, D: int):
@@ -267,16 +275,18 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedK
     T, H, _ = q.shape
     _, hkv, _, D = cache.shape
     dev = _device(q, "q")
-    _on(cache, "cache", dev)
-    _on(seqs, "seqs", dev)
+    if cache.device_index != dev:
+        _far(cache, "cache", dev)
+    if seqs.device_index != dev:
+        _far(seqs, "seqs", dev)
     qt, qh = _heads(q, "q", dev, T, H, D)
     kt, kh = _heads(k, "k", dev, T, hkv, D)
     vt, vh = _heads(v, "v", dev, T, hkv, D)
     rp = n = 0
     if rope is not None:
-        _place_or_raise(rope, "rope", dev)
-        if not (rope.dtype is _F32 and rope.dim() == 2 and rope.shape[1] == D
-                and rope.is_contiguous()):
+        if not (rope.get_device() == dev and rope.dtype is _F32 and rope.dim() == 2
+                and rope.shape[1] == D and rope.is_contiguous()):
+            _place_or_raise(rope, "rope", dev)
             raise ValueError(f"rope: a contiguous fp32 CUDA tensor [positions, {D}] is needed")
         rp, n = rope.data_ptr(), rope.shape[0]
     if q_out is None:
@@ -326,8 +336,10 @@ def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: floa
     T, H, _ = q.shape
     _, hkv, _, D = cache.shape
     dev = _device(q, "q")
-    _on(cache, "cache", dev)
-    _on(seqs, "seqs", dev)
+    if cache.device_index != dev:
+        _far(cache, "cache", dev)
+    if seqs.device_index != dev:
+        _far(seqs, "seqs", dev)
     qt, qh = _heads(q, "q", dev, T, H, D)
     if H < 1 or H % hkv:
         raise ValueError(f"q: {H} heads over {hkv} KV heads")
@@ -407,7 +419,8 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters, index: torch.
     _need(x.dim() == 2, "x: two dimensions are needed")
     T, K, R, N = x.shape[0], *adapters.sizes
     dev = _device(x, "x")
-    _on(adapters, "adapters", dev)
+    if adapters.device_index != dev:
+        _far(adapters, "adapters", dev)
     ldx = _rows(x, "x", dev, (T, K))
     ldy = _rows(y, "y", dev, (T, N))
     i = _vec(index, "index", dev, T, _I32)
