@@ -4,10 +4,10 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 
 #include "../../include/qz.h"
+#include "grow_limit.h"
 
 namespace qz {
 
@@ -115,16 +115,15 @@ qz_status launch_embed_int8(const int8_t *q, int64_t ldq, const float *scale, in
 template <auto Kern>
 inline cudaError_t allow_smem(size_t bytes) {
   constexpr int kMaxDev = 64;
-  static std::atomic<int> allowed[kMaxDev];
+  static GrowLimit limit[kMaxDev];
   if (bytes <= 48 * 1024) return cudaSuccess;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < kMaxDev;
-  if (known && allowed[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && known) allowed[dev].store((int)bytes, std::memory_order_relaxed);
-  return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  return (cudaError_t)limit[dev].ensure((int)bytes, [](int v) {
+    return (int)cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+  });
 }
 
 // Reads (and clears) a translation unit's device error word.
