@@ -76,3 +76,42 @@ def test_a_limit_only_grows(tmp_path):
     one, two = run(tmp_path, GROW).splitlines()
     assert one.split() == ["7", "0", "0", "7", "0", "0", "4"]
     assert two.split() == ["64", "100"]  # the naive one allows 64 and counts on 100
+
+
+PLAN = """
+    #include <cstdio>
+    #include "lora_plan.h"
+    int main() {
+      const long Ts[] = {1, 2, 3, 7, 16, 31, 64, 127, 128, 200, 300, 1000, 1500, 4500, 100000},
+                 Ks[] = {1, 64, 512, 513, 1000, 2048, 4096, 4104, 8192, 12000, 1 << 20},
+                 Ns[] = {1, 64, 136, 256, 257, 4096, 11008, 1 << 20};
+      const int all[] = {1, 132, 148, 152, 160};
+      for (int sms : all)
+        for (long T : Ts) for (long K : Ks) for (long N : Ns)
+          for (long R = 1; R <= 128; R += R < 24 ? 1 : 8) {
+            const qz::LoraPlan p = qz::lora_plan(T, K, N, R, sms);
+            std::printf("%d %ld %ld %ld %ld %d %d %d %d %d %d %d\\n", sms, T, K, N, R, p.Rp, p.Rk,
+                        p.slices, p.k_slice, p.rows_down, p.rows_up, p.along_n);
+          }
+    }
+"""
+
+
+def test_adapter_plans_keep_to_what_the_kernels_hold(tmp_path):
+    import numpy as np
+    v = np.loadtxt(run(tmp_path, PLAN).splitlines(), dtype=np.int64).T
+    sms, T, K, N, R, Rp, Rk, slices, k_slice, down, up, along_n = v
+    assert ((Rp - R < 16) & (Rp >= R) & (Rp % 16 == 0)).all()
+    assert ((Rk - R < 32) & (Rk >= R) & (Rk % 32 == 0)).all()
+    # slices: at most a portable cluster, whole steps, none empty, all of K
+    assert ((slices >= 1) & (slices <= 8) & (k_slice % 512 == 0)).all()
+    assert ((slices * k_slice >= K) & ((slices - 1) * k_slice < K)).all()
+    for rows in (down, up):
+        assert ((rows >= 1) & (rows <= 32) & (rows & (rows - 1) == 0)).all()
+    # 8 warps' sums: two CTAs of the down product share an SM's 227 KB (1 KB of it each reserved)
+    smem = 8 * down * Rp * 4
+    assert (2 * (smem + 1024) <= 227 * 1024).all()
+    assert (smem <= 96 * 1024).all()
+    assert ((along_n >= 1) & (along_n <= -(-N // 256))).all()
+    # the sizes that the tests and real calls reach
+    assert set(np.unique(down)) == set(np.unique(up)) == {1, 2, 4, 8, 16, 32}

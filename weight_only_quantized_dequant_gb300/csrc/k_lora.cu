@@ -32,6 +32,7 @@
 // us a step, half of it loads; a product is 8 clocks of a scheduler, so the matrix
 // instructions are a tenth of the time), twice in the few row tiles that two runs
 // share.  1500 rows of 48 adapters of rank 16 in turn: 48 us (265 unsorted).
+#include "lora_plan.h"
 #include "qz_internal.cuh"
 
 namespace qz {
@@ -39,15 +40,10 @@ namespace {
 
 __device__ int g_lora_error = 0;
 
-constexpr int kWarps = 8;                   // down
-constexpr int kThreads = 32 * kWarps;
-constexpr int kUpWarps = 4;
-constexpr int kSub = 64;                    // k per warp and step
-constexpr int kSlice = kSub * kWarps;       // k per CTA and step
-constexpr int kMaxRows = 32;                // rows of a CTA (one per lane when runs are found)
-constexpr int kOut = 64;                    // outputs per warp and step
+constexpr int kWarps = kLoraWarps, kUpWarps = kLoraUpWarps, kSub = kLoraSub, kSlice = kLoraSlice;
+constexpr int kMaxRows = kLoraMaxRows, kOut = kLoraOut, kMaxSlices = kLoraMaxSlices;
+constexpr int kThreads = 32 * kWarps;       // down
 constexpr int64_t kOnePart = 4096;          // K from which u enters as one fp16 part
-constexpr int kRowRanks = 2048;             // rows x padded rank of a CTA (shared memory)
 // Rows from which they are sorted first.  1500 rows of 48 adapters in turn, rank
 // 16, 4096 x 11008: 265 -> 48.5 us; 128 of 16, rank 64: 48 -> 29; 64 of 4, rank 16,
 // 4096 x 4096: 13.8 -> 16.7.  Rows that come grouped
@@ -55,7 +51,6 @@ constexpr int kRowRanks = 2048;             // rows x padded rank of a CTA (shar
 constexpr int64_t kOrderRows = 128;
 constexpr int kBins = 1024;                 // of the sort by adapter
 constexpr int kSegment = 2048;              // rows sorted together
-constexpr int kMaxSlices = 8;               // CTAs of a cluster, which split K
 
 struct LoraParams {
   const __half *a, *b, *x, *y;
@@ -358,15 +353,10 @@ __device__ __forceinline__ uint4 add_rows(uint4 y, float f, const float (&c)[4][
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// CTAs per SM that the registers of a variant allow.
-__host__ __device__ constexpr int up_ctas(int rc, int nn) {
-  return rc * nn == 1 ? 6 : rc * nn == 2 ? 4 : 3;
-}
-
 // RC: 32-rank groups of B_a that a thread holds at a time; NN: 8-row column
 // tiles at a time; TWO: u comes in two parts.
 template <bool VEC, int RC, int NN, bool TWO>
-__global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
+__global__ void __launch_bounds__(32 * kUpWarps, lora_up_ctas(RC, NN))
     lora_up_kernel(const LoraParams p) {
   // [rows][pitch], once or twice: the parts of u, rows padded against bank conflicts
   extern __shared__ __align__(16) uint8_t sm[];
@@ -561,12 +551,6 @@ __global__ void __launch_bounds__(32 * kUpWarps, up_ctas(RC, NN))
 
 bool rows16(const void *p, int64_t ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0; }
 
-int pow2_at_least(int64_t v, int hi) {
-  int r = 1;
-  while (r < v && r < hi) r *= 2;
-  return r;
-}
-
 template <bool VEC, int NT>
 cudaError_t launch_down(const LoraParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -622,6 +606,7 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   DeviceInfo di;
   const qz_status st = device_info(&di);
   if (st != QZ_OK) return st;
+  const LoraPlan plan = lora_plan(T, ad.K, ad.N, ad.R, di.sms);
   LoraParams p;
   p.a = reinterpret_cast<const __half *>(ad.a);
   p.b = reinterpret_cast<const __half *>(ad.b);
@@ -633,8 +618,8 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.index = index;
   p.n_adapters = (int)ad.n_adapters;
   p.R = (int)ad.R;
-  p.Rp = (int)((ad.R + 15) / 16 * 16);
-  p.Rk = (int)((ad.R + 31) / 32 * 32);
+  p.Rp = plan.Rp;
+  p.Rk = plan.Rk;
   p.K = (int)ad.K;
   p.N = (int)ad.N;
   p.T = T;
@@ -650,30 +635,11 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.order = reinterpret_cast<int2 *>(p.ul + T * p.Rk);
   p.fs = reinterpret_cast<float *>(p.order + T);
   if (T < kOrderRows || ad.n_adapters < 2) p.order = nullptr;
-  // Slices of K: as many as there are steps of kSlice, at most kMaxSlices.
-  const int64_t steps = (ad.K + kSlice - 1) / kSlice;
-  p.slices = (int)(steps < kMaxSlices ? steps : kMaxSlices);
-  p.k_slice = (int)((steps + p.slices - 1) / p.slices) * kSlice;
-  p.slices = (int)((ad.K + p.k_slice - 1) / p.k_slice);
-  // Rows per CTA: one while the GPU holds all of the down product's CTAs at once
-  // (2 per SM; a decode step's adapters are read by the whole GPU together), more
-  // as calls grow, so that a run's adapter is read by fewer CTAs; the up product
-  // likewise at 4 per SM.  64 rows of 16 adapters in turn, 4096 x 4096: 12.4 us,
-  // with one row a CTA 14.2; 256 of 16: 13.7, with half as many rows a CTA 20.2.
-  // Twice as many help grouped rows and cost scattered ones (256 rows of as many
-  // adapters: 35.7 -> 39.8 in the down product, 48.5 in the up product).
-  const int64_t want = (int64_t)di.sms * 2;
-  const int cap = kRowRanks / p.Rp < kMaxRows ? kRowRanks / p.Rp : kMaxRows;
-  p.rows_down = pow2_at_least((T * p.slices + want - 1) / want, cap);
-  const int64_t per = kOut * kUpWarps, chunks = (ad.N + per - 1) / per;
-  p.rows_up = pow2_at_least((T * chunks + 2 * want - 1) / (2 * want), kMaxRows);
-  // CTAs along N: as many as the GPU holds at once beside those along the rows
-  // (a CTA that has its rows' u goes on to further outputs; a second wave of
-  // CTAs would cost as much as the first).
-  const int64_t tiles = (T + p.rows_up - 1) / p.rows_up;
-  const int64_t slots = (int64_t)di.sms * up_ctas(p.R <= 32 ? 1 : 2, p.rows_up <= 8 ? 1 : 2);
-  const int64_t fit = slots / tiles > 1 ? slots / tiles : 1;
-  const int n = (int)(chunks < fit ? chunks : fit);
+  p.slices = plan.slices;
+  p.k_slice = plan.k_slice;
+  p.rows_down = plan.rows_down;
+  p.rows_up = plan.rows_up;
+  const int n = plan.along_n;
   p.two = ad.K < kOnePart;
   const bool va = rows16(p.a, p.a_row) && p.a_adapter % 8 == 0 && rows16(x, ldx) && p.K % 8 == 0;
   const bool vb = rows16(p.b, p.b_row) && p.b_adapter % 8 == 0 && rows16(y, ldy) && rows16(out, ldo);
