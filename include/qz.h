@@ -518,13 +518,12 @@ size_t qz_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t n_
  * [T][ldy] (qz_gemm_* of the same x), out [T][ldo] (may be y).  A_a = a +
  * a * a_adapter, rows a_row apart; B_a = b + a * b_adapter, rows b_row
  * apart (halves).  rank NULL: all R.  1 <= R <= 128, ranks are clamped to 0..R.
- * Sums are fp32; between the two products u is rounded to fp16 in units of its
- * row's largest value from K = 4096 on (2^-12, within K 2^-24), and held to 22
- * bits below.  An index outside
+ * Sums are fp32; between the two products u is held to 22 bits of its row's
+ * largest value (two fp16 parts), at every K.  An index outside
  * -1..n_adapters-1 counts as -1 and sets bit 4 of the device error word.
  * Rows with the same index share reads of their adapter, in calls of fewer than
- * 128 rows when they are neighbours.  2-byte alignment suffices; 16-byte aligned operands with K, R
- * and strides multiples of 8 run fastest.  K, N <= 2^20.
+ * 128 rows when they are neighbours.  2-byte alignment suffices; 16-byte aligned
+ * operands with K, R and strides multiples of 8 run fastest.  K, N <= 2^20.
  * workspace: qz_lora_workspace_bytes(T, K, R) bytes, 16-byte aligned (any
  * contents); calls that can be in flight at the same time need different ones. */
 typedef struct {

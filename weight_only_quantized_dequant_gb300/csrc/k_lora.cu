@@ -12,26 +12,27 @@
 //     at a time.  The launch overlaps the first one, and its first B and y are on
 //     their way before u is.
 // Precision of u: its fp32 sum is scaled by a power of two per row (any fp32
-// range) and enters the second product as fp16.  From K = 4096 on that rounding,
-// 2^-12 of u, is within the bound K 2^-24 of the fp32 sums that form u; below, a
-// second fp16 part carries the remainder (22 bits), at the price of twice the
-// products.  Sums stay fp32 and y is added before the one rounding.
+// range) and enters the second product as two fp16 parts, which hold it to 22 bits of
+// the row's largest.  One part would be off by up to 2^-11 of it, as much as out's own
+// rounding at every K; it took 48.4 us where two take 52.8 (1500 rows of ranks up to 64,
+// below), 10.4 for 11.3 (32 rows of rank 16).
 // In both, a thread's 16-byte load holds 8 consecutive k of its fragment row:
 // the two operands use the same order of k, so no shuffle is needed; likewise the
 // rows of B_a are dealt so that a thread ends with 8 consecutive outputs.
 // Operands without 16-byte rows take the same path with 2-byte loads.
 //
-// From kOrderRows rows on, the rows are sorted by adapter first (a third launch, which the
-// others overlap), so that an adapter is read for up to 32 of its rows at once however they come.
+// From kOrderRows rows on, the rows are sorted by adapter first (a third launch, which
+// the others overlap), so that an adapter is read for up to 32 of its rows at once
+// however they come.
 //
-// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 10.5 us, of
-// which down 5, up 3 after it; the chain index, adapter, products, cluster, u,
+// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 11.3 us, of
+// which down 5, up 3.5 after it; the chain index, adapter, products, cluster, u,
 // products is latency.  1500 rows of 8 adapters of ranks up to 64 in runs of 300,
-// 4096 x 11008: 48.5 us, 2 of them the sort, down 19 (one
-// wave of CTAs with fewer slices takes as long), up the rest: each step of 64 outputs waits for its own loads (3.7
-// us a step, half of it loads; a product is 8 clocks of a scheduler, so the matrix
-// instructions are a tenth of the time), twice in the few row tiles that two runs
-// share.  1500 rows of 48 adapters of rank 16 in turn: 48 us (265 unsorted).
+// 4096 x 11008: 52.8 us, 2 of them the sort, down 19 (one wave of CTAs with fewer
+// slices takes as long), up the rest: each step of 64 outputs waits for its own loads
+// (about half of its 4 us; a product is 8 clocks of a scheduler, so the matrix
+// instructions are a fifth of the time), twice in the few row tiles that two runs
+// share.  1500 rows of 48 adapters of rank 16 in turn: 50.3 us.
 #include "lora_plan.h"
 #include "qz_internal.cuh"
 
@@ -43,7 +44,6 @@ __device__ int g_lora_error = 0;
 constexpr int kWarps = kLoraWarps, kUpWarps = kLoraUpWarps, kSub = kLoraSub, kSlice = kLoraSlice;
 constexpr int kMaxRows = kLoraMaxRows, kOut = kLoraOut, kMaxSlices = kLoraMaxSlices;
 constexpr int kThreads = 32 * kWarps;       // down
-constexpr int64_t kOnePart = 4096;          // K from which u enters as one fp16 part
 // Rows from which they are sorted first.  1500 rows of 48 adapters in turn, rank
 // 16, 4096 x 11008: 265 -> 48.5 us; 128 of 16, rank 64: 48 -> 29; 64 of 4, rank 16,
 // 4096 x 4096: 13.8 -> 16.7.  Rows that come grouped
@@ -59,8 +59,7 @@ struct LoraParams {
   const int32_t *rank, *index;
   int n_adapters, R, Rp, Rk, K, N;  // Rp, Rk: R rounded up to 16 and 32
   int64_t T, a_adapter, a_row, b_adapter, b_row, ldx, ldy, ldo;
-  __half *uh, *ul;  // [T][Rk] u 2^e, and its remainder where two parts are used
-  int two;
+  __half *uh, *ul;  // [T][Rk] u 2^e and its remainder
   int2 *order;      // [T] (row, index) sorted by adapter, or null: rows as they come
   float *fs;        // [T] scale_a 2^-e
   int slices;
@@ -330,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const LoraParams
         const float w = v[q] * up;
         const __half h = __float2half_rn(w);
         p.uh[(t0 + t) * p.Rk + r] = h;
-        if (p.two) p.ul[(t0 + t) * p.Rk + r] = __float2half_rn(w - __half2float(h));
+        p.ul[(t0 + t) * p.Rk + r] = __float2half_rn(w - __half2float(h));
       }
     }
   }
@@ -354,11 +353,11 @@ __device__ __forceinline__ uint4 add_rows(uint4 y, float f, const float (&c)[4][
 }
 
 // RC: 32-rank groups of B_a that a thread holds at a time; NN: 8-row column
-// tiles at a time; TWO: u comes in two parts.
-template <bool VEC, int RC, int NN, bool TWO>
+// tiles at a time.
+template <bool VEC, int RC, int NN>
 __global__ void __launch_bounds__(32 * kUpWarps, lora_up_ctas(RC, NN))
     lora_up_kernel(const LoraParams p) {
-  // [rows][pitch], once or twice: the parts of u, rows padded against bank conflicts
+  // [2][rows][pitch]: the parts of u, rows padded against bank conflicts
   extern __shared__ __align__(16) uint8_t sm[];
   const int pitch = p.Rk + 8;
   int64_t *y_at = reinterpret_cast<int64_t *>(sm), *out_at = y_at + kMaxRows;  // rows' offsets
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, lora_up_ctas(RC, NN))
           const int t = e / per, c = (e - t * per) * 8;
           const int64_t src = (t0 + t) * p.Rk + c;
           *reinterpret_cast<uint4 *>(uh + t * pitch + c) = ld_cg16(p.uh + src);
-          if (TWO) *reinterpret_cast<uint4 *>(ul + t * pitch + c) = ld_cg16(p.ul + src);
+          *reinterpret_cast<uint4 *>(ul + t * pitch + c) = ld_cg16(p.ul + src);
         }
         if (threadIdx.x < rows) fs[threadIdx.x] = __ldcg(p.fs + t0 + threadIdx.x);
         __syncthreads();
@@ -457,15 +456,13 @@ __global__ void __launch_bounds__(32 * kUpWarps, lora_up_ctas(RC, NN))
                 else mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, hv.x, hv.y);
                 mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, hv.z, hv.w);
               }
-              if (TWO) {
-                const uint4 lv = *reinterpret_cast<const uint4 *>(u + 8 * n * pitch + 32 * q +
-                                                                  p.rows_up * pitch);
+              const uint4 lv = *reinterpret_cast<const uint4 *>(u + 8 * n * pitch + 32 * q +
+                                                                p.rows_up * pitch);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
-                  mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, lv.x, lv.y);
-                  mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, lv.z, lv.w);
-                }
+              for (int j = 0; j < 4; ++j) {
+                const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
+                mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, lv.x, lv.y);
+                mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, lv.z, lv.w);
               }
             }
           }
@@ -507,14 +504,12 @@ __global__ void __launch_bounds__(32 * kUpWarps, lora_up_ctas(RC, NN))
                 mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, hv.x, hv.y);
                 mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, hv.z, hv.w);
               }
-              if (TWO) {
-                const uint4 lv = *reinterpret_cast<const uint4 *>(ul + u);
+              const uint4 lv = *reinterpret_cast<const uint4 *>(ul + u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
-                  mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, lv.x, lv.y);
-                  mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, lv.z, lv.w);
-                }
+              for (int j = 0; j < 4; ++j) {
+                const uint4 b0 = bv[q][j][0], b1 = bv[q][j][1];
+                mma16816(c[n][j], b0.x, b1.x, b0.y, b1.y, lv.x, lv.y);
+                mma16816(c[n][j], b0.z, b1.z, b0.w, b1.w, lv.z, lv.w);
               }
             }
           }
@@ -571,26 +566,20 @@ cudaError_t launch_down(const LoraParams &p, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, lora_down_kernel<VEC, NT>, p);
 }
 
-template <bool VEC, int RC, int NN, bool TWO>
+template <bool VEC, int RC, int NN>
 cudaError_t launch_up(const LoraParams &p, int ctas_n, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   cfg.gridDim = dim3((unsigned)((p.T + p.rows_up - 1) / p.rows_up), (unsigned)ctas_n);
   cfg.blockDim = dim3(32 * kUpWarps);
   cfg.dynamicSmemBytes = kMaxRows * (2 * sizeof(int64_t) + sizeof(float)) +
-                         (size_t)p.rows_up * (TWO ? 2 : 1) * (p.Rk + 8) * sizeof(__half);
+                         (size_t)p.rows_up * 2 * (p.Rk + 8) * sizeof(__half);
   cfg.stream = s;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_up_kernel<VEC, RC, NN, TWO>, p);
-}
-
-template <bool VEC, int RC, int NN>
-cudaError_t launch_up(const LoraParams &p, int ctas_n, cudaStream_t s) {
-  return p.two ? launch_up<VEC, RC, NN, true>(p, ctas_n, s)
-               : launch_up<VEC, RC, NN, false>(p, ctas_n, s);
+  return cudaLaunchKernelEx(&cfg, lora_up_kernel<VEC, RC, NN>, p);
 }
 
 }  // namespace
@@ -640,7 +629,6 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.rows_down = plan.rows_down;
   p.rows_up = plan.rows_up;
   const int n = plan.along_n;
-  p.two = ad.K < kOnePart;
   const bool va = rows16(p.a, p.a_row) && p.a_adapter % 8 == 0 && rows16(x, ldx) && p.K % 8 == 0;
   const bool vb = rows16(p.b, p.b_row) && p.b_adapter % 8 == 0 && rows16(y, ldy) && rows16(out, ldo);
 
