@@ -423,8 +423,9 @@ qz_status qz_rmsnorm(const qz_half *x, int64_t ldx, const qz_half *residual, int
 /* The same with the normalised rows in INT8, one fp32 scale per row, by the
  * rule of qz_quantize_int8 applied to the unrounded y:
  *   scale[t] = max_j |y[t][j]| / 127;  q = clamp(rint(y / scale), -127, 127);
- * a row of zeros gives scale 0 and codes 0.  q [T][ldq], ldq >= K (columns
- * K.. are not written), scale [T]. */
+ * a row of zeros gives scale 0 and codes 0 (whatever eps), a row with a NaN or an
+ * infinity in x, residual or weight a scale that is not finite and codes 0.
+ * q [T][ldq], ldq >= K (columns K.. are not written), scale [T]. */
 qz_status qz_rmsnorm_int8(const qz_half *x, int64_t ldx, const qz_half *residual, int64_t ldr,
                           const qz_half *weight, float w_bias, float eps, int64_t T, int64_t K,
                           int8_t *q, int64_t ldq, float *scale, qz_half *sum, int64_t lds,

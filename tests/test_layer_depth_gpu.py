@@ -77,3 +77,39 @@ def test_lora_inner_vector_keeps_its_bits(T, R, N, K):
     assert torch.equal(want.to(F16).to(F64), want)
     ad = qz().LoraAdapters(a, b, torch.ones(3, device=DEV))
     assert torch.equal(qz().lora(x, y, ad, index), want.to(F16))
+
+
+# ------------------------------------------------------------------- norm ---
+@pytest.mark.parametrize("K,pad", [(64, 0), (1000, 0), (4096, 0), (4096, 1), (16384, 0),
+                                   (20000, 0)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_rmsnorm_int8_shows_what_is_not_finite(K, pad, bad):
+    """A row with a NaN or an infinity gets a scale that is not finite: rmsnorm's row
+    holds a NaN too.  The other rows are what they are without it."""
+    g = gen(70)
+    x, w = randn(g, 9, K + pad)[:, :K], randn(g, K)
+    q0, s0, _ = qz().rmsnorm_int8(x, w, 1e-5)
+    for at in (0, K // 3, K - 1):
+        y = torch.empty((9, K + pad), dtype=F16, device=DEV)[:, :K].copy_(x)
+        y[4, at] = bad
+        q, s, _ = qz().rmsnorm_int8(y, w, 1e-5)
+        assert not bool(qz().rmsnorm(y, w, 1e-5)[0][4].isfinite().all())
+        assert not bool(s[4].isfinite()) and not q[4].any()
+        keep = torch.arange(9, device=DEV) != 4
+        assert torch.equal(q[keep], q0[keep]) and torch.equal(s[keep], s0[keep])
+    r = torch.zeros_like(x)
+    r[4, 0] = bad  # through the residual
+    assert not bool(qz().rmsnorm_int8(x, w, 1e-5, residual=r)[1][4].isfinite())
+    v = w.clone()
+    v[K // 2] = bad  # through the weight: every row
+    q, s, _ = qz().rmsnorm_int8(x, v, 1e-5)
+    assert not bool(s.isfinite().any()) and not bool(q.any())
+
+
+@pytest.mark.parametrize("K", [64, 1000, 4096, 20000])
+def test_rmsnorm_int8_rows_of_zeros_without_eps(K):
+    x, w = torch.zeros((3, K), dtype=F16, device=DEV), torch.ones((K,), dtype=F16, device=DEV)
+    x[1, K // 2] = 2.0
+    q, s, _ = qz().rmsnorm_int8(x, w, 0.0)
+    assert not bool(s[::2].any()) and not bool(q[::2].any())
+    assert int(q[1, K // 2]) == 127 and bool(s[1] > 0)

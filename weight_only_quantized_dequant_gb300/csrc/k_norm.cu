@@ -39,13 +39,28 @@ __device__ __forceinline__ uint32_t f2h(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// 1 / sqrt(mean + eps); a row of zeros with eps = 0 stays zeros where it becomes codes.
+template <bool INT8>
+__device__ __forceinline__ float inv_rms(float ss, int K, float eps) {
+  const float d = ss / (float)K + eps;
+  return INT8 && d == 0.0f ? 0.0f : rsqrtf(d);
+}
+
+// The larger value, or NaN where either is one: a row with a NaN must not pass for one
+// without (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Sum or maximum over the TPR threads of a row, in a fixed order.
 template <int TPR, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float *part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? fmaxf(v, u) : v + u;
+    v = MAX ? max_nan(v, u) : v + u;
   }
   if (TPR > 32) {
     const int warp = threadIdx.x >> 5;
@@ -53,15 +68,15 @@ __device__ __forceinline__ float row_reduce(float v, float *part) {
     __syncthreads();
     v = part[0];
 #pragma unroll
-    for (int i = 1; i < TPR / 32; ++i) v = MAX ? fmaxf(v, part[i]) : v + part[i];
+    for (int i = 1; i < TPR / 32; ++i) v = MAX ? max_nan(v, part[i]) : v + part[i];
   }
   return v;
 }
 
 // q = clamp(rint(y / s)): the IEEE division of the quantizers, so that codes
-// follow the same rule.
+// follow the same rule; 0 beside a scale of 0, infinity or NaN.
 __device__ __forceinline__ uint32_t code(float y, float s) {
-  const float c = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f) : 0.0f;
+  const float c = s > 0.0f && s < INFINITY ? fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f) : 0.0f;
   return (uint32_t)(int)c & 0xFFu;
 }
 
@@ -114,7 +129,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_vec_kernel(const N
     }
   }
   ss = row_reduce<TPR, false>(ss, part[0]);
-  const float rs = rsqrtf(ss / (float)p.K + p.eps);
+  const float rs = inv_rms<INT8>(ss, (int)p.K, p.eps);
   float mx = 0.0f;
 #pragma unroll
   for (int i = 0; i < kMaxVec; ++i) {
@@ -124,7 +139,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_vec_kernel(const N
       const float2 u = h2f(a[k]);
       h[i][2 * k] *= rs * (p.bias + u.x);
       h[i][2 * k + 1] *= rs * (p.bias + u.y);
-      if (INT8) mx = fmaxf(mx, fmaxf(fabsf(h[i][2 * k]), fabsf(h[i][2 * k + 1])));
+      if (INT8) mx = max_nan(mx, max_nan(fabsf(h[i][2 * k]), fabsf(h[i][2 * k + 1])));
     }
   }
   if (INT8) {
@@ -175,13 +190,13 @@ __global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormParams 
     ss = fmaf(v, v, ss);
   }
   ss = row_reduce<kRowThreads, false>(ss, part[0]);
-  const float rs = rsqrtf(ss / (float)K + p.eps);
+  const float rs = inv_rms<INT8>(ss, K, p.eps);
   float mx = 0.0f;
   for (int j = threadIdx.x; j < K; j += kRowThreads) {
     const float v = row[j] * (rs * (p.bias + __half2float(p.w[j])));
     if (INT8) {
       row[j] = v;
-      mx = fmaxf(mx, fabsf(v));
+      mx = max_nan(mx, fabsf(v));
     } else {
       p.y[t * p.ldy + j] = __float2half_rn(v);
     }

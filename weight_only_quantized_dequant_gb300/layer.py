@@ -153,7 +153,8 @@ def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
                  out: torch.Tensor | None = None, scale: torch.Tensor | None = None,
                  residual_out: torch.Tensor | None = None, stream=None):
     """(q, scale, h): the rows of ``rmsnorm`` as int8 codes [T, K] and one fp32
-    scale per row (y ~ q * scale, scale = max|y| / 127)."""
+    scale per row (y ~ q * scale, scale = max|y| / 127; a row that is not finite
+    gets such a scale)."""
     shape = x.shape
     _need(len(shape) == 2, "x: two dimensions are needed")
     T, K = shape
