@@ -69,3 +69,79 @@ def cancelling_adapters(T, n, R, K, N, device):
     d = (c.gather(1, first) - c.gather(1, (first + 1) % R)) / 16
     out = y.to(F64) + torch.where(index[:, None] >= 0, d.to(F64), 0.0)
     return x, y, a, b, index.to(torch.int32), out
+
+
+# -------------------------------------------------------------- attention ---
+BLOCK = 128  # keys that the kernel takes at a time
+
+# (new tokens, tokens held, heads, KV heads, D, page, window): long contexts, cut
+# between many CTAs, and tiles of many blocks that one CTA walks through
+CONTEXTS = [([1], [40000], 8, 1, 128, 64, 0), ([1, 1, 1], [20001, 7, 12345], 4, 2, 256, 128, 0),
+            ([17, 2], [30000, 9000], 8, 2, 128, 16, 0), ([1, 1], [40000, 33333], 8, 2, 64, 32, 0),
+            ([150, 1], [20000, 40000], 4, 2, 128, 64, 0), ([300], [9999], 4, 1, 64, 128, 0),
+            ([40], [15000], 2, 2, 256, 64, 0), ([1, 60], [40000, 30000], 4, 1, 128, 16, 17000),
+            ([1] * 40, [1500 + 97 * i for i in range(40)], 8, 4, 128, 32, 0)]
+
+
+def signal_inputs(qs, kvs, hq, hkv, D, seed, device):
+    """(queries of all sequences, keys and values of each).  Channel c of the values tells
+    of the key blocks c, c + D, c + 2 D, ...: it is 1 to 2 there and 0 elsewhere, so that one
+    output channel comes from five blocks at most.  The logits rise and fall by 2 from block
+    to block (through channel 0 of the keys) around small random ones."""
+    g = torch.Generator(device=device).manual_seed(seed)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=g, device=device)
+
+    q = randn(sum(qs), hq, D) * 0.4
+    q[..., 0] = D ** 0.5
+    ks, vs = [], []
+    for n in kvs:
+        j = torch.arange(n, device=device)
+        b = j // BLOCK
+        k = randn(n, hkv, D)
+        k[..., 0] = (2.0 * torch.sin(b * 0.7 + 0.1 * (j % BLOCK) / BLOCK))[:, None]
+        v = torch.zeros((n, hkv, D), device=device)
+        h = torch.arange(hkv, device=device)[None, :]
+        v[j[:, None], h, b[:, None] % D] = 1.0 + (j[:, None] * 13 + h) % 8 / 8
+        ks.append(k.to(F16))
+        vs.append(v.to(F16))
+    return q.to(F16), ks, vs
+
+
+def weights(q, k, pos, window, scale):
+    """(e^(x - max) of one head's rows, the largest sum of |q k| a row) in 64 bits."""
+    j = torch.arange(k.shape[0], device=k.device)[None, :]
+    seen = j <= pos[:, None]
+    if window:
+        seen &= j > pos[:, None] - window
+    q, k = q.to(F64), k.to(F64)
+    x = (q @ k.T * scale).masked_fill(~seen, float("-inf"))
+    dot = (q.abs() @ k.abs().T * scale).masked_fill(~seen, 0.0).amax(1)
+    return torch.exp(x - x.amax(1, keepdim=True)), dot
+
+
+def signal_bound(out, w, v, dot, D):
+    """Roundings of out = w v / sum(w), v >= 0: every weight to fp16 (relative, and half of
+    the smallest fp16 beside the largest weight), logits by fp32 sums of D products and
+    their exponential, the output once; sums of positive fp32 terms, a tensor core's with up
+    to 2^-23 for each of a block's 8 steps, block after block (a drift of 2^-12 at 40000)."""
+    rel = 2 * U16 + 2 * (D + 64) * 2.0 ** -24 * (dot[:, None] + 1) + 2.0 ** -12
+    small = (w > 0).to(F64) @ v * (S16 / 2) / w.sum(1, keepdim=True)
+    return rel * out + small + S16
+
+
+def signal_reference(q, ks, vs, qs, kvs, hq, window):
+    """(out, bound) of all rows."""
+    D, G = q.shape[2], hq // ks[0].shape[1]
+    out, tol, t = torch.empty(q.shape, dtype=F64, device=q.device), None, 0
+    tol = torch.empty_like(out)
+    for n, L, k, v in zip(qs, kvs, ks, vs):
+        pos = torch.arange(L - n, L, device=q.device)
+        for h in range(hq):
+            w, dot = weights(q[t:t + n, h], k[:, h // G], pos, window, D ** -0.5)
+            vv = v[:, h // G].to(F64)
+            o = w @ vv / w.sum(1, keepdim=True)
+            out[t:t + n, h], tol[t:t + n, h] = o, signal_bound(o, w, vv, dot, D)
+        t += n
+    return out, tol

@@ -115,3 +115,31 @@ def test_adapter_plans_keep_to_what_the_kernels_hold(tmp_path):
     assert ((along_n >= 1) & (along_n <= -(-N // 256))).all()
     # the sizes that the tests and real calls reach
     assert set(np.unique(down)) == set(np.unique(up)) == {1, 2, 4, 8, 16, 32}
+
+
+def test_adapter_cases_reach_every_variant(tmp_path):
+    """The tests' calls of many rows take the wide forms of both products: more than 8
+    rows a CTA, u in registers whole (R <= 32) or in halves, aligned rows or not."""
+    import layer_cases as C
+    calls = "".join(f"P({sms}, {T}, {K}, {N}, {R});" for sms in (148, 152)
+                    for T, _, _, R, K, N, _, _ in C.ADAPTERS)
+    out = run(tmp_path, """
+        #include <cstdio>
+        #include "lora_plan.h"
+        static void P(int sms, long T, long K, long N, long R) {
+          const qz::LoraPlan p = qz::lora_plan(T, K, N, R, sms);
+          std::printf("%%d %%d %%d\\n", p.rows_down, p.rows_up, p.slices);
+        }
+        int main() { %s }
+    """ % calls)
+    v = [tuple(map(int, line.split())) for line in out.splitlines()]
+    n = len(C.ADAPTERS)
+    for plans in (v[:n], v[n:]):
+        got = [(down > 8, up, slices == 8, R <= 32, K % 8 == 0 and not off,
+                N % 8 == 0 and R % 8 == 0 and not off)
+               for (down, up, slices), (_, _, _, R, K, N, _, off) in zip(plans, C.ADAPTERS)]
+        assert {16, 32} <= {up for _, up, *_ in got}
+        assert {(up > 8, small, vb) for _, up, _, small, _, vb in got} >= {
+            (True, True, True), (True, True, False), (True, False, True), (True, False, False)}
+        assert {(down, va) for down, _, full, _, va, _ in got if full} >= {
+            (True, True), (True, False)}

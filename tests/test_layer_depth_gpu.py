@@ -113,3 +113,35 @@ def test_rmsnorm_int8_rows_of_zeros_without_eps(K):
     q, s, _ = qz().rmsnorm_int8(x, w, 0.0)
     assert not bool(s[::2].any()) and not bool(q[::2].any())
     assert int(q[1, K // 2]) == 127 and bool(s[1] > 0)
+
+
+# -------------------------------------------------------------- attention ---
+def paged(ks, vs, page, D, hkv, nan=True):
+    """A cache of the sequences' keys and values, pages in random order, NaN elsewhere."""
+    need = [-(-k.shape[0] // page) for k in ks]
+    order = torch.randperm(sum(need) + 2, generator=gen(90), device=DEV)
+    kc = torch.full((sum(need) + 2, hkv, page, D), float("nan"), dtype=F16, device=DEV)
+    vc = torch.full_like(kc, float("nan"))
+    table = torch.full((len(ks), max(need) + 1), -7, dtype=torch.int32, device=DEV)
+    at = 0
+    for i, (k, v) in enumerate(zip(ks, vs)):
+        pages = order[at:at + need[i]]
+        at += need[i]
+        table[i, :need[i]] = pages
+        j = torch.arange(k.shape[0], device=DEV)
+        kc[pages[j // page], :, j % page] = k
+        vc[pages[j // page], :, j % page] = v
+    return qz().PagedKV(kc, vc), table
+
+
+def batch(qs, kvs, table):
+    cu = torch.tensor([0] + qs, device=DEV).cumsum(0).to(torch.int32)
+    return qz().SeqBatch(cu, torch.tensor(kvs, dtype=torch.int32, device=DEV), table)
+
+
+@pytest.mark.parametrize("qs,kvs,hq,hkv,D,page,window", C.CONTEXTS)
+def test_attention_takes_every_block_once(qs, kvs, hq, hkv, D, page, window):
+    q, ks, vs = C.signal_inputs(qs, kvs, hq, hkv, D, 91, DEV)
+    cache, table = paged(ks, vs, page, D, hkv)
+    got = qz().attention_paged(q, cache, batch(qs, kvs, table), window=window)
+    within(got, *C.signal_reference(q, ks, vs, qs, kvs, hq, window))
