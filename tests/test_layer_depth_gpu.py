@@ -145,3 +145,29 @@ def test_attention_takes_every_block_once(qs, kvs, hq, hkv, D, page, window):
     cache, table = paged(ks, vs, page, D, hkv)
     got = qz().attention_paged(q, cache, batch(qs, kvs, table), window=window)
     within(got, *C.signal_reference(q, ks, vs, qs, kvs, hq, window))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,window", [(1, 300), (1, 1), (140, 200), (3, 128)])
+def test_attention_at_the_last_position(D, n, window):
+    """2^31 - 1 tokens held: the last slot of the last block lies past them."""
+    L, page, hkv = 2**31 - 1, 256, 1
+    held = 2 * page - 1  # the slots that exist, the last one past the end
+    g = gen(95)
+    kc, vc = randn(g, 3, hkv, page, D), randn(g, 3, hkv, page, D)
+    k, v = kc[[2, 0], 0].reshape(-1, D)[:held], vc[[2, 0], 0].reshape(-1, D)[:held]
+    k, v = k.clone(), v.clone()
+    kc[0, :, -1] = float("nan")
+    vc[0, :, -1] = float("nan")
+    kc[1], vc[1] = float("nan"), float("nan")
+    table = torch.full((1, 2**31 // page), -1, dtype=torch.int32, device=DEV)
+    table[0, -2:] = torch.tensor([2, 0], dtype=torch.int32, device=DEV)
+    q = randn(g, n, 2, D)
+    got = qz().attention_paged(q, qz().PagedKV(kc, vc), batch([n], [L], table), window=window)
+    pos = torch.arange(held - n, held, device=DEV)
+    for h in range(2):
+        w, dot = C.weights(q[:, h], k, pos, window, D ** -0.5)
+        w = w / w.sum(1, keepdim=True)
+        tol = C.U16 * (w @ v.to(F64).abs()) + 4 * (D + 64) * 2.0 ** -24 * (dot[:, None] + 1)
+        want = w @ v.to(F64)
+        within(got[:, h], want, tol + C.U16 * want.abs() + held * C.S16)

@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s[k] = p.cap * (1.0f - 2.0f * rcp(1.0f + ex2(s[k] * p.cap_in)));
         }
         // keys [k_lo, k_hi) of this row; a block that no bound cuts needs neither
-        if (b * kN + col0 + NC > see_hi) {
+        if (see_hi - b * kN < col0 + NC) {  // (the block's end may pass 32 bits)
           const int k_hi = hi - b * kN - col0;
 #pragma unroll
           for (int k = 0; k < NC; ++k) s[k] = k < k_hi ? s[k] : -INFINITY;
