@@ -171,3 +171,26 @@ def test_attention_at_the_last_position(D, n, window):
         tol = C.U16 * (w @ v.to(F64).abs()) + 4 * (D + 64) * 2.0 ** -24 * (dot[:, None] + 1)
         want = w @ v.to(F64)
         within(got[:, h], want, tol + C.U16 * want.abs() + held * C.S16)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 150])
+def test_attention_weights_far_below_the_largest(D, n):
+    """One key stands e^18 above 6000 others: each of them is below half of fp16's smallest
+    value beside it, all of them together are not.  The values are 0 at the one and 1 at the
+    others; enough sequences that one SM walks through the whole context."""
+    L, S, page = 6000, 160, 64
+    k = torch.zeros((L, 1, D), dtype=F16, device=DEV)
+    v = torch.ones_like(k)
+    k[0, :, 0] = 18.0
+    v[0] = 0.0
+    cache, table = paged([k], [v], page, D, 1)
+    seqs = batch([n] * S, [L] * S, table.expand(S, -1).contiguous())  # all hold the same pages
+    q = torch.zeros((n * S, 2, D), dtype=F16, device=DEV)
+    q[..., 0] = 1.0
+    got = qz().attention_paged(q, cache, seqs, scale=1.0)
+    e = torch.exp(torch.tensor(-18.0, dtype=F64, device=DEV))
+    others = torch.arange(L - n, L, device=DEV, dtype=F64).repeat(S)[:, None, None]
+    want = (others * e / (1.0 + others * e)).expand(q.shape)
+    # weights are held to 2^-32 of the largest; exponentials and sums; the rounding of out
+    within(got, want, others * 2.0 ** -32 + want * (2.0 ** -9) + C.S16)

@@ -18,8 +18,10 @@
 //    through shared memory.  NQ = 1 serves head size 256 (whose O fills half of
 //    tensor memory) and calls whose sequences bring at most 128 rows (decode,
 //    HBM-bound: the padded MMA rows cost nothing there).
-//  * m moves only when it would grow by more than 2^8 (weights then stay below
-//    256, within fp16): O is rescaled a few times per row, not per block.
+//  * m moves only when it would grow by more than 2^8: O is rescaled a few times per
+//    row, not per block.  Weights (and with them l and O, whose quotient does not change)
+//    are 2^7 e^{x - m}: below 2^15, within fp16, and down to 2^-32 of the largest in the
+//    product, so that many small ones together are not lost beside it.
 //  * Work units are (tile, key block); every CTA (one per SM) takes an even,
 //    contiguous range of all units, which its load warp finds from the lengths
 //    on the device and announces tile by tile, so ragged batches and single long
@@ -64,7 +66,9 @@ constexpr int kHead = kBars + 8 * kOutBytes;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
-constexpr float kLag = 8.0f;           // log2 of how far a weight may exceed 1
+constexpr float kLag = 8.0f;           // log2 of how far a key may exceed m
+constexpr float kLift = 7.0f;          // log2 of the weight at m
+static_assert(kLag + kLift < 16.0f, "weights are fp16");
 constexpr float kLog2e = 1.4426950408889634f;
 // Units per CTA at least.  One token over 199 keys takes 11.3 us with 1, 10.2 with 3
 // and 13.6 with 6; over 1000 keys 13.2, 15.0 and 19.5.
@@ -794,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float mc = m == -INFINITY ? 0.0f : m * p.c;
+        const float mc = m == -INFINITY ? 0.0f : m * p.c - kLift;
         const float2 c2 = make_float2(p.c, p.c), mc2 = make_float2(-mc, -mc);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
