@@ -492,7 +492,8 @@ qz_status qz_rope_append(const qz_half *q, int64_t n_heads, int64_t q_token, int
  * zeros (keys and values) and sets bit 4 of the device error word.
  * Logits, softmax sums and outputs are held in fp32; the weights e^{x_j - m} are
  * rounded to fp16 where they enter the tensor cores (to 2^-11 of each, or 2^-32 of
- * the largest).  scale: finite.
+ * the largest).  softcap is good to fp32 at any size; up to 64 the capped logit is
+ * off by 2^-22 of the cap and is cheaper.  scale: finite.
  * q, out: [n_tokens][n_heads][head_dim] with strides q_token, q_head, o_token,
  * o_head; 16-byte aligned, strides multiples of 8; out must not overlap q.
  * n_tokens * n_heads < 2^31.

@@ -194,3 +194,47 @@ def test_attention_weights_far_below_the_largest(D, n):
     want = (others * e / (1.0 + others * e)).expand(q.shape)
     # weights are held to 2^-32 of the largest; exponentials and sums; the rounding of out
     within(got, want, others * 2.0 ** -32 + want * (2.0 ** -9) + C.S16)
+
+
+CAPS = [1e-38, 1e-6, 0.5, 50.0, 64.0, 65.0, 1e3, 1e4, 1e6, 1e8, 1e15, 3e38]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap", CAPS)
+def test_attention_caps_of_any_size(cap, D):
+    """Logits of up to several hundred, small ones among them, under caps from far below
+    to far above them."""
+    qs, kvs, hq, hkv = [1, 140, 5], [300, 200, 517], 4, 2
+    g = gen(96)
+    ks, vs = ([randn(g, n, hkv, D) for n in kvs] for _ in range(2))
+    q = randn(g, sum(qs), hq, D, scale=1.0) * torch.logspace(-2, 1.5, hq, device=DEV)[:, None]
+    q = q.to(F16)
+    cache, table = paged(ks, vs, 32, D, hkv)
+    got = qz().attention_paged(q, cache, batch(qs, kvs, table), softcap=cap)
+    t = 0
+    for n, L, k, v in zip(qs, kvs, ks, vs):
+        seen = torch.arange(L, device=DEV)[None, :] <= torch.arange(L - n, L, device=DEV)[:, None]
+        for h in range(hq):
+            qq, kk, vv = q[t:t + n, h].to(F64), k[:, h // 2].to(F64), v[:, h // 2].to(F64)
+            raw = qq @ kk.T * D ** -0.5
+            x = cap * torch.tanh(raw / cap)
+            w = torch.softmax(x.masked_fill(~seen, float("-inf")), 1)
+            want, mag = w @ vv, w @ vv.abs()
+            # a logit: a fp32 sum of D products, the cap's few roundings of it, and for caps
+            # up to 64 those of 1 beside the tanh; then exp; the weights and out to fp16
+            dot = (qq.abs() @ kk.abs().T * D ** -0.5).masked_fill(~seen, 0.0).amax(1, keepdim=True)
+            x_max = x.abs().masked_fill(~seen, 0.0).amax(1, keepdim=True)
+            dx = (D + 8) * 2.0 ** -24 * torch.minimum(dot, 64 * x_max + cap * (cap < 1)) \
+                + 32 * 2.0 ** -24 * (x_max + 1) + (4 * 2.0 ** -22 * cap if cap <= 64 else 0.0)
+            within(got[t:t + n, h], want, 2 * mag * dx + C.U16 * (mag + want.abs()) + 4 * L * C.S16)
+        t += n
+
+
+@pytest.mark.parametrize("cap", CAPS)
+def test_attention_caps_of_logits_of_zero(cap):
+    k, v = (randn(gen(97), 200, 1, 64) for _ in range(2))
+    cache, table = paged([k], [v], 16, 64, 1)
+    q = torch.zeros((1, 1, 64), dtype=F16, device=DEV)
+    got = qz().attention_paged(q, cache, batch([1], [200], table), softcap=cap)
+    want = v.to(F64).mean(0)[None]
+    within(got, want, C.U16 * want.abs() + 2.0 ** -18)

@@ -41,6 +41,8 @@
 // first block), where code and data are read for the first time.
 #include <cuda.h>
 
+#include <cfloat>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -68,6 +70,11 @@ constexpr uint32_t kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr float kLag = 8.0f;           // log2 of how far a key may exceed m
 constexpr float kLift = 7.0f;          // log2 of the weight at m
+// Caps up to here come from 1 - 2 / (1 + e^2t) alone: off by 2^-22 of the cap, 1.5e-5 in a
+// logit, a sixteenth of the weights' rounding.  Four prompts of up to 4096 take 327 us
+// without a cap, 634 with one of these and 948 with the form for any cap; 32 decode tokens
+// over 16384 207, 261 and 353.
+constexpr float kShortCap = 64.0f;
 static_assert(kLag + kLift < 16.0f, "weights are fp16");
 constexpr float kLog2e = 1.4426950408889634f;
 // Units per CTA at least.  One token over 199 keys takes 11.3 us with 1, 10.2 with 3
@@ -109,6 +116,7 @@ struct AttnParams {
   int hkv, n_pages, page_size, page_shift;
   float c;              // logit units to log2: |scale| log2(e), or log2(e) with a cap
   float cap, cap_in;    // softcap, and |scale| / softcap * 2 log2(e)
+  float mag, cap_t;     // |scale|, and |scale| / softcap
   uint32_t keep, flip;  // queries are read as (bits & keep) ^ flip: signs turned when scale < 0,
                         // zeros when scale = 0 (c stays positive: masked logits are -inf)
   int window;           // 0: none
@@ -314,6 +322,29 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_n_major) {
   return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
+}
+
+// c ? a : b, both formed: a branch for each of a thread's 128 logits costs more.
+__device__ __forceinline__ float pick(bool c, float a, float b) {
+  float d;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tselp.f32 %0, %1, %2, p;\n\t}"
+      : "=f"(d)
+      : "f"(a), "f"(b), "r"((uint32_t)c));
+  return d;
+}
+// cap tanh(t) of a product s = q . k, t = s |scale| / cap: tanh(t) = 1 - 2 / (1 + e^2t),
+// which cancels for small t.
+__device__ __forceinline__ float cap_far(const AttnParams &p, float s) {
+  return p.cap * (1.0f - 2.0f * rcp(1.0f + ex2(s * p.cap_in)));
+}
+// The same for any cap: below 1/4 by the series t - t^3/3 + 2t^5/15 - 17t^7/315 + 62t^9/2835,
+// whose next term is below 2^-26 of the first there.
+__device__ __forceinline__ float cap_any(const AttnParams &p, float s) {
+  const float t = s * p.cap_t, u = t * t, x = s * p.mag;
+  float g = fmaf(u, 62.0f / 2835.0f, -17.0f / 315.0f);
+  g = fmaf(u, g, 2.0f / 15.0f);
+  g = fmaf(u, g, -1.0f / 3.0f);
+  return pick(fabsf(t) < 0.25f, fmaf(x * u, g, x), cap_far(p, s));
 }
 
 // --------------------------------------------------------------- schedule --
@@ -578,7 +609,8 @@ __device__ __forceinline__ bool Walker<kM>::start(const AttnParams &p) {
 }
 
 // ---------------------------------------------------------------- kernel --
-template <int D, int NQ, bool CAP>
+// CAP: 0 none, 1 of up to kShortCap, 2 of any size.
+template <int D, int NQ, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ AttnParams p) {
   using C = Cfg<D, NQ>;
@@ -749,8 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         if (CAP) {
 #pragma unroll
-          for (int k = 0; k < NC; ++k)  // cap tanh(t), tanh(t) = 1 - 2 / (1 + e^2t)
-            s[k] = p.cap * (1.0f - 2.0f * rcp(1.0f + ex2(s[k] * p.cap_in)));
+          for (int k = 0; k < NC; ++k) s[k] = CAP == 1 ? cap_far(p, s[k]) : cap_any(p, s[k]);
         }
         // keys [k_lo, k_hi) of this row; a block that no bound cuts needs neither
         if (see_hi - b * kN < col0 + NC) {  // (the block's end may pass 32 bits)
@@ -1377,7 +1408,7 @@ qz_status pool_map(CUtensorMap *map, const __half *base, const PagedView &c, int
   return r == CUDA_SUCCESS ? QZ_OK : QZ_ERR_UNSUPPORTED;
 }
 
-template <int D, int NQ, bool CAP>
+template <int D, int NQ, int CAP>
 qz_status launch(const AttnParams &p, int sms, cudaStream_t s) {
   using C = Cfg<D, NQ>;
   const cudaError_t e = allow_smem<attn_kernel<D, NQ, CAP>>(C::kSmem);
@@ -1388,7 +1419,8 @@ qz_status launch(const AttnParams &p, int sms, cudaStream_t s) {
 
 template <int D, int NQ>
 qz_status launch_cap(const AttnParams &p, int sms, cudaStream_t s) {
-  return p.cap > 0.0f ? launch<D, NQ, true>(p, sms, s) : launch<D, NQ, false>(p, sms, s);
+  if (p.cap == 0.0f) return launch<D, NQ, 0>(p, sms, s);
+  return p.cap <= kShortCap ? launch<D, NQ, 1>(p, sms, s) : launch<D, NQ, 2>(p, sms, s);
 }
 
 }  // namespace
@@ -1429,7 +1461,10 @@ qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t
   p.flip = scale < 0.0f ? 0x80008000u : 0u;
   p.c = (softcap > 0.0f ? 1.0f : mag) * kLog2e;
   p.cap = softcap;
-  p.cap_in = softcap > 0.0f ? mag / softcap * 2.0f * kLog2e : 0.0f;
+  // (finite for the smallest caps: a logit of 0 stays 0, the others reach the cap all the same)
+  p.mag = mag;
+  p.cap_t = softcap > 0.0f ? fminf(mag / softcap, FLT_MAX) : 0.0f;
+  p.cap_in = fminf(p.cap_t * 2.0f * kLog2e, FLT_MAX);
   p.window = window > INT32_MAX ? 0 : (int)window;  // longer than any cache: none
   p.s = sv;
   p.cnt = static_cast<unsigned *>(workspace);
