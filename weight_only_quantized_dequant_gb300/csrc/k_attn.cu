@@ -163,6 +163,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int *ab
   const bool ok = mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
   return __all_sync(0xffffffffu, ok);
 }
+// The same at the end of a CTA that gave up, until `until`: copies and products in flight
+// have to be over before its memory goes.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity,
+                                           unsigned long long until) {
+  while (!mbar_try(bar, parity))
+    if (gtimer() > until) return;
+}
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -624,7 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *p_half = o_done + 2;  // NQ = 2: the first 64 keys' weights
   uint64_t *q_full = p_half + 2, *xbar = q_full + 1;  // xbar: one per 32-row quarter
   uint64_t *seg_full = xbar + 4, *seg_empty = seg_full + kSegs, *q_empty = seg_empty + kSegs;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_empty + 1);
+  uint64_t *drained = q_empty + 1;  // the products of a CTA that gave up
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
   Seg *seg_sm = reinterpret_cast<Seg *>(base + 512);         // [kSegs]
   float *xch = reinterpret_cast<float *>(base + 1024);       // [2][8 warps][32]
@@ -645,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(q_full), 2);
     mbar_init(smem_u32(q_empty), 1);
+    mbar_init(smem_u32(drained), 1);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&xbar[i]), 2);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(smem_u32(&seg_full[i]), 1);
@@ -687,6 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n % kSegs]));
   };
+
+  uint32_t issued = 0;  // copies of a load warp, tiles of a query warp
 
   // n / G for n < G + 256: (n + 1/2) / G stays further from every whole number
   // than fp32 rounding can move it.
@@ -1188,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 : "memory");
         }
         __syncwarp();
-        ++segs;
+        issued = ++segs;
         continue;
       }
       if (segs > 0) {
@@ -1332,18 +1343,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && j == 0 && n_seg == 1) ok = announce(next = w.next(p));
       }
     }
-    if (!ok) {  // let the copies in flight land before the CTA's memory goes
-      const uint32_t n = ring < NS ? ring : NS;
-      for (uint32_t r = ring - n; r < ring; ++r) {
-        const unsigned long long t0 = gtimer();
-        while (!mbar_try(smem_u32(&kv_full[r % NS]), (r / NS) & 1))
-          if (gtimer() - t0 > kWaitNs) break;
-      }
-    }
+    issued = ring;
   }
   fence_before();
   __syncthreads();
   fence_after();
+  if (*(volatile int *)abort_flag) {  // (of the whole CTA: every warp has stopped)
+    const unsigned long long until = gtimer() + kWaitNs;
+    if (warp == kLoadWarp) {
+      for (uint32_t r = issued - min(issued, (uint32_t)NS); r < issued; ++r)
+        mbar_drain(smem_u32(&kv_full[r % NS]), (r / NS) & 1, until);
+    } else if (warp == kMmaWarp) {
+      if (elect_one()) mma_commit(smem_u32(drained));
+      __syncwarp();
+      mbar_drain(smem_u32(drained), 0, until);
+    } else if (issued > 0) {
+      mbar_drain(smem_u32(q_full), (issued - 1) & 1, until);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+  }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                  : "memory");
