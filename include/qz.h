@@ -446,7 +446,7 @@ typedef struct {
 /* The sequences of a step (device arrays, read when the call runs).  Sequence
  * i brings the new tokens cu_q[i] .. cu_q[i+1]-1 of the n_tokens packed rows
  * (cu_q non-decreasing, within 0..n_tokens; rows outside every sequence are
- * neither read nor written) and holds kv_len[i] tokens, the new ones
+ * not written and do not matter) and holds kv_len[i] tokens, the new ones
  * last: its new token j has position kv_len[i] - (cu_q[i+1] - cu_q[i]) + j.
  * Token position p lies in slot p % page_size of page
  * page_table[i * ld_table + p / page_size]. */

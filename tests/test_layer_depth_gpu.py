@@ -238,3 +238,25 @@ def test_attention_caps_of_logits_of_zero(cap):
     got = qz().attention_paged(q, cache, batch([1], [200], table), softcap=cap)
     want = v.to(F64).mean(0)[None]
     within(got, want, C.U16 * want.abs() + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(4, 4, 64), (8, 2, 128), (6, 2, 128), (2, 1, 256)])
+@pytest.mark.parametrize("scale", [None, -0.1])
+def test_attention_rows_of_others_do_not_matter(hq, hkv, D, scale):
+    """Rows before, behind and of another sequence that are not finite."""
+    qs, kvs, before, behind = [5, 140, 1], [40, 300, 77], 3, 4
+    g = gen(98)
+    ks, vs = ([randn(g, n, hkv, D) for n in kvs] for _ in range(2))
+    q = randn(g, sum(qs), hq, D)
+    cache, table = paged(ks, vs, 32, D, hkv)
+    want = qz().attention_paged(q, cache, batch(qs, kvs, table), scale=scale)
+    bad = torch.full((before + q.shape[0] + behind, hq, D), float("nan"), dtype=F16, device=DEV)
+    bad[before:before + q.shape[0]] = q
+    bad[before + 5:before + 145] = float("inf")  # the second sequence
+    seqs = batch([before] + qs, kvs, table)
+    seqs = qz().SeqBatch(seqs.cu_q[1:].contiguous(), seqs.kv_len, table)
+    out = torch.full_like(bad, 7.0)
+    qz().attention_paged(bad, cache, seqs, scale=scale, out=out)
+    assert bool((out[:before] == 7).all()) and bool((out[-behind:] == 7).all())
+    out = out[before:-behind]
+    assert torch.equal(out[:5], want[:5]) and torch.equal(out[145:], want[145:])

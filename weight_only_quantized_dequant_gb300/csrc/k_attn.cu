@@ -16,8 +16,8 @@
 //    NQ = 1: 128 rows, S double-buffered over the key blocks; the two
 //    warpgroups take 64 key columns of every row each and exchange row maxima
 //    through shared memory.  NQ = 1 serves head size 256 (whose O fills half of
-//    tensor memory) and calls whose sequences bring at most 128 rows (decode,
-//    HBM-bound: the padded MMA rows cost nothing there).
+//    tensor memory) and calls that bring at most 128 rows a
+//    sequence on average (decode, HBM-bound: the padded MMA rows cost nothing there).
 //  * m moves only when it would grow by more than 2^8: O is rescaled a few times per
 //    row, not per block.  Weights (and with them l and O, whose quotient does not change)
 //    are 2^7 e^{x - m}: below 2^15, within fp16, and down to 2^-32 of the largest in the
@@ -1494,7 +1494,8 @@ qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t
   // prompts of up to 4096 326 and 381; 8 x 16 tokens over 4000 36.2 with one, 39.7
   // with two, 64 single tokens, 32 heads, 97 and 125.  Short prompts, whose tiles
   // are few, would gain with one (6 of up to 300: 26.8 -> 24.8), but the lengths
-  // held are known on the device only.
+  // are known on the device only.  So the rows are the average: a prompt beside many
+  // single tokens (one of 4096 and 63 of 1, a KV head a head) has one stage.
   const bool two = c.D < 256 && sv.n_tokens * p.G > (int64_t)128 * sv.n_seqs;
   p.q_boxes = scale > 0.0f && query_map(&p.qmap, q, sv.n_tokens, hq, c.D, q_token, q_head, p.G,
                                         two ? 128 : 64);
