@@ -260,3 +260,20 @@ def test_attention_rows_of_others_do_not_matter(hq, hkv, D, scale):
     assert bool((out[:before] == 7).all()) and bool((out[-behind:] == 7).all())
     out = out[before:-behind]
     assert torch.equal(out[:5], want[:5]) and torch.equal(out[145:], want[145:])
+
+
+def test_a_single_token_of_a_wider_row():
+    """One token's heads out of a row whose length is no multiple of 8."""
+    g = gen(99)
+    wide = randn(g, 1, 8 * 64 + 3)[:, :8 * 64]
+    assert wide.stride(0) % 8
+    q, k, v = wide.view(1, 8, 64).split([4, 2, 2], dim=1)
+    ks, vs = [randn(g, 50, 2, 64)], [randn(g, 50, 2, 64)]
+    rope = qz().rope_table(60, 64)
+    outs = []
+    for a, b, c in ((q, k, v), (q.contiguous(), k.contiguous(), v.contiguous())):
+        cache, table = paged(ks, vs, 16, 64, 2)
+        seqs = batch([1], [50], table)
+        r = qz().rope_append(a, b, c, cache, seqs, rope)
+        outs += [r, cache.k.nan_to_num(), qz().attention_paged(r, cache, seqs)]
+    assert all(torch.equal(a, b) for a, b in zip(outs[:3], outs[3:]))

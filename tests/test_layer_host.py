@@ -219,3 +219,37 @@ def test_workspaces(lib, f, make):
         with pytest.raises(ValueError):
             f(**make(workspace=bad))
     assert len(lib.calls) == 1
+
+
+# ---------------------------------------------------------------- strides ---
+def strided(shape, stride, dtype=F16):
+    n = 1 + sum((a - 1) * b for a, b in zip(shape, stride))
+    return OnGpu(torch.zeros(n, dtype=dtype).as_strided(shape, stride))
+
+
+def test_a_dimension_of_one_has_no_stride_of_its_own(lib):
+    """torch reports any number there (a token's row out of a wider one); the kernels'
+    rule of multiples of 8 is for strides that are used."""
+    cache, seqs = handles(S=1)
+    q, k = strided((1, 4, 64), (259, 64, 1)), strided((1, 2, 64), (131, 64, 1))
+    layer.rope_append(q, k, k, cache, seqs, None, q_out=q, stream=Stream)
+    layer.attention_paged(q, cache, seqs, out=q, workspace=gpu(64, dtype=torch.uint8),
+                          stream=Stream)
+    one = layer.PagedKV(*(strided((1, 1, 16, 64), (3, 5, 64, 1)) for _ in range(2)))
+    q = strided((3, 1, 64), (64, 5, 1))
+    layer.rope_append(q, q, q, one, seqs, None, q_out=q, stream=Stream)
+    layer.attention_paged(q, one, seqs, out=q, workspace=gpu(64, dtype=torch.uint8),
+                          stream=Stream)
+    for name, a in lib.calls:
+        a = [x for x in a if x is not Stream.cuda_stream]
+        strides = [a[i] for i in ((2, 3, 5, 6, 8, 9, 15, 16) if name == "qz_rope_append"
+                                  else (2, 3, 10, 11))]
+        assert all(s % 8 == 0 and s >= 64 for s in strides), (name, strides)
+        c = next(x._obj for x in a if isinstance(getattr(x, "_obj", None), _lib.KvCache))
+        assert all(getattr(c, f"{t}_{n}") % 8 == 0 for t in "kv" for n in ("page", "head", "token"))
+    # strides that are used are handed on as they are
+    big = strided((3, 2, 64), (640, 320, 1))
+    lib.calls.clear()
+    layer.attention_paged(big, handles()[0], seqs, out=big, workspace=gpu(64, dtype=torch.uint8),
+                          stream=Stream)
+    assert lib.calls[0][1][2:4] == (640, 320)

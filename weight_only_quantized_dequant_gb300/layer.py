@@ -199,9 +199,9 @@ class PagedKV:
         _need(k.dtype == _F16 and v.dtype == _F16 and k.dim() == 4 and k.shape == v.shape,
               "k and v: fp16 [n_pages, n_kv_heads, page_size, head_dim]")
         _need(k.stride(3) == 1 and v.stride(3) == 1, "k and v: contiguous head_dim")
-        arg = _lib.KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], k.shape[1],
-                           k.shape[3], k.stride(0), k.stride(1), k.stride(2), v.stride(0),
-                           v.stride(1), v.stride(2))
+        pages, heads, size, D = k.shape  # a single page, head or token has no stride of its own
+        k_st, v_st = ([s if n > 1 else D for s, n in zip(t.stride(), k.shape)] for t in (k, v))
+        arg = _lib.KvCache(k.data_ptr(), v.data_ptr(), pages, size, heads, D, *k_st[:3], *v_st[:3])
         _set(self, _arg=arg, _ref=ctypes.byref(arg), shape=tuple(k.shape), device_index=dev)
 
     @classmethod
@@ -255,11 +255,12 @@ class SeqBatch:
 
 
 def _heads(t: torch.Tensor, what: str, dev: int, T: int, heads: int, D: int):
-    """Token and head strides of an fp16 [T, heads, D] with contiguous rows on GPU dev."""
+    """Token and head strides of an fp16 [T, heads, D] with contiguous rows on GPU dev (a
+    single token or head has none of its own: torch may report anything)."""
     if t.get_device() == dev and t.dtype is _F16 and t.shape == (T, heads, D):
         st, sh, sd = t.stride()
         if sd == 1:
-            return st, sh
+            return st if T > 1 else heads * D, sh if heads > 1 else D
     _place_or_raise(t, what, dev)
     raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} with strides {t.stride()}; fp16 "
                      f"{(T, heads, D)} with contiguous rows is needed")
