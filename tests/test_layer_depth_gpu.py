@@ -253,8 +253,8 @@ def test_attention_rows_of_others_do_not_matter(hq, hkv, D, scale):
     bad = torch.full((before + q.shape[0] + behind, hq, D), float("nan"), dtype=F16, device=DEV)
     bad[before:before + q.shape[0]] = q
     bad[before + 5:before + 145] = float("inf")  # the second sequence
-    seqs = batch([before] + qs, kvs, table)
-    seqs = qz().SeqBatch(seqs.cu_q[1:].contiguous(), seqs.kv_len, table)
+    seqs = batch(qs, kvs, table)
+    seqs = qz().SeqBatch(seqs.cu_q + before, seqs.kv_len, table)
     out = torch.full_like(bad, 7.0)
     qz().attention_paged(bad, cache, seqs, scale=scale, out=out)
     assert bool((out[:before] == 7).all()) and bool((out[-behind:] == 7).all())
