@@ -58,7 +58,7 @@ constexpr int kSoftmaxWarps = 8;       // two warpgroups
 // With few rows only softmax warps 0 and 4 have any, both on the SM's first
 // scheduler: the MMA and load warps sit on others.
 constexpr int kQWarp = 8, kMmaWarp = 10, kLoadWarp = 11;  // 8 and 9: queries
-constexpr int kThreads = 384;          // the third warpgroup: MMA, key and value loads, query loads (2)
+constexpr int kThreads = 384;          // the third warpgroup: queries (2), MMA, keys and values
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
 static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "register split");
 constexpr int kMaxCtas = 160;          // grid cap (partial slots in the workspace)
@@ -312,17 +312,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ uint32_t f2h(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
 // Shared-memory operand of 128-byte-swizzled rows of 64 fp16 (8-row groups
 // 1024 bytes apart): low word of its descriptor; mn: bytes between 64-column
 // groups of an N-major operand (unused when K-major).
 __device__ __forceinline__ uint32_t sdesc_lo(uint32_t addr, uint32_t mn) {
   return addr >> 4 | (mn >> 4) << 16;
 }
-constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;  // stride, version, 128-byte swizzle
+// stride, version, 128-byte swizzle
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 // A value that every lane holds, as one the compiler knows to be uniform.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 // kind::f16, A = B = f16, D = f32; A K-major, B K-major or N-major.
@@ -765,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nb = g.b1 - g.b0;
       const bool active = nb > 0 && (NQ == 1 || wg == 0 || g.rows > 128);
       // whole blocks of this range need no mask in this warp
-      const int see_lo = __reduce_max_sync(0xffffffffu, lo), see_hi = __reduce_min_sync(0xffffffffu, hi);
+      const int see_lo = __reduce_max_sync(0xffffffffu, lo);
+      const int see_hi = __reduce_min_sync(0xffffffffu, hi);
       // NQ = 1: the previous block's product is complete.  Every live warp sees
       // each of them before it lets the next one start: a wait tells a
       // barrier's phases apart by parity alone.
@@ -914,7 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            v[e] = active ? f2h(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
+            v[e] = active ? f2h(__uint_as_float(o[2 * e]) * inv,
+                                __uint_as_float(o[2 * e + 1]) * inv)
                           : 0u;
           store_rows(v, dst, k * 2);
         }

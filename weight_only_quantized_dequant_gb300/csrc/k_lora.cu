@@ -630,7 +630,8 @@ qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t 
   p.rows_up = plan.rows_up;
   const int n = plan.along_n;
   const bool va = rows16(p.a, p.a_row) && p.a_adapter % 8 == 0 && rows16(x, ldx) && p.K % 8 == 0;
-  const bool vb = rows16(p.b, p.b_row) && p.b_adapter % 8 == 0 && rows16(y, ldy) && rows16(out, ldo);
+  const bool vb =
+      rows16(p.b, p.b_row) && p.b_adapter % 8 == 0 && rows16(y, ldy) && rows16(out, ldo);
 
   cudaError_t e;
   if (p.order) {

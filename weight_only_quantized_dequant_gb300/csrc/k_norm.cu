@@ -31,14 +31,6 @@ struct NormParams {
   int64_t lds;
 };
 
-__device__ __forceinline__ float2 h2f(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-}
-__device__ __forceinline__ uint32_t f2h(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // 1 / sqrt(mean + eps); a row of zeros with eps = 0 stays zeros where it becomes codes.
 template <bool INT8>
 __device__ __forceinline__ float inv_rms(float ss, int K, float eps) {
@@ -76,8 +68,8 @@ __device__ __forceinline__ float row_reduce(float v, float *part) {
 // q = clamp(rint(y / s)): the IEEE division of the quantizers, so that codes
 // follow the same rule; 0 beside a scale of 0, infinity or NaN.
 __device__ __forceinline__ uint32_t code(float y, float s) {
-  const float c = s > 0.0f && s < INFINITY ? fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f) : 0.0f;
-  return (uint32_t)(int)c & 0xFFu;
+  if (!(s > 0.0f && s < INFINITY)) return 0u;
+  return (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f) & 0xFFu;
 }
 
 // TPR threads hold one row, kMaxVec vectors of 8 each at most.
@@ -238,7 +230,8 @@ qz_status launch_rmsnorm(const __half *x, int64_t ldx, const __half *r, int64_t 
                          const __half *w, float bias, float eps, int64_t T, int64_t K, __half *y,
                          int64_t ldy, int8_t *q, int64_t ldq, float *scale, __half *sum,
                          int64_t lds, cudaStream_t s) {
-  const NormParams p = {x, r, w, ldx, r ? ldr : 0, bias, eps, T, K, y, ldy, q, ldq, scale, sum, lds};
+  const NormParams p = {x, r, w, ldx, r ? ldr : 0, bias, eps, T, K,
+                        y, ldy, q, ldq, scale, sum, lds};
   const bool vec = K % 8 == 0 && K <= 8 * kMaxVec * 512 && fits16(x, ldx) &&
                    (!r || fits16(r, ldr)) && fits16(w, 0) && (!sum || fits16(sum, lds)) &&
                    (q ? ((uintptr_t)q & 7u) == 0 && ldq % 8 == 0 : fits16(y, ldy));

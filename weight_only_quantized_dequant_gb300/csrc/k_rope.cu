@@ -28,14 +28,6 @@ struct RopeParams {
   SeqView s;
 };
 
-__device__ __forceinline__ float2 h2f(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-}
-__device__ __forceinline__ uint32_t f2h(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // Items of a token: (head, 8-column group of the first half), query heads
 // first, then key heads, then value heads.  A thread takes U of them with the
 // same columns, so it reads their cosines and sines once.
@@ -93,8 +85,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
     const float4 *cs = reinterpret_cast<const float4 *>(p.rope + pos * p.c.D + j);
     const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
     const float4 s0 = __ldg(cs + half / 4), s1 = __ldg(cs + half / 4 + 1);
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w;
+    c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w;
+    s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -119,8 +113,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
 template <int U>
 qz_status launch(const RopeParams &p, int items, cudaStream_t s) {
   const int per = kThreads * U;
-  rope_append_kernel<U><<<dim3((unsigned)p.s.n_tokens, (unsigned)((items + per - 1) / per)), kThreads,
-                          0, s>>>(p);
+  const dim3 grid((unsigned)p.s.n_tokens, (unsigned)((items + per - 1) / per));
+  rope_append_kernel<U><<<grid, kThreads, 0, s>>>(p);
   return launch_status();
 }
 

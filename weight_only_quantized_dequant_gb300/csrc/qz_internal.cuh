@@ -142,6 +142,15 @@ inline qz_status read_error_word(Word &word, int *code, int clear) {
 }
 
 // ------------------------------------------------------------ layer glue ---
+// Two fp16 values and their fp32 ones.
+__device__ __forceinline__ float2 h2f(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+__device__ __forceinline__ uint32_t f2h(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 struct PagedView;  // seq_batch.cuh
 struct SeqView;
 qz_status launch_rmsnorm(const __half *x, int64_t ldx, const __half *r, int64_t ldr,
