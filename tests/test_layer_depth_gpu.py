@@ -277,3 +277,52 @@ def test_a_single_token_of_a_wider_row():
         r = qz().rope_append(a, b, c, cache, seqs, rope)
         outs += [r, cache.k.nan_to_num(), qz().attention_paged(r, cache, seqs)]
     assert all(torch.equal(a, b) for a, b in zip(outs[:3], outs[3:]))
+
+
+# ---------------------------------------------------------- 64-bit offsets ---
+def far_apart(n, inner):
+    """fp16 [n, *inner] whose parts lie 2^31 + 64 halves apart or more."""
+    size = 1
+    for d in inner:
+        size *= d
+    step = 2**31 // (n - 1) // 8 * 8 + 64 + size
+    buf = torch.empty(((n - 1) * step + size,), dtype=F16, device=DEV)
+    strides, s = [], size
+    for d in inner:
+        s //= d
+        strides.append(s)
+    return buf.as_strided((n, *inner), (step, *strides))
+
+
+def test_cache_and_adapters_past_32_bits():
+    """Pages, adapters and rows more than 2^32 bytes behind the first."""
+    g = gen(100)
+    kc, vc = far_apart(3, (2, 16, 64)), far_apart(3, (2, 16, 64))
+    assert kc.stride(0) * 2 * kc.element_size() > 2**32
+    near = [torch.empty((3, 2, 16, 64), dtype=F16, device=DEV) for _ in range(2)]
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    q, k, v = randn(g, 40, 4, 64), randn(g, 40, 2, 64), randn(g, 40, 2, 64)
+    outs = []
+    for a, b in ((kc, vc), near):
+        cache, seqs = qz().PagedKV(a, b), batch([40], [40], table)
+        r = qz().rope_append(q, k, v, cache, seqs, qz().rope_table(40, 64))
+        outs.append([r, a[:, :, :8], b[:, :, :8], qz().attention_paged(r, cache, seqs)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    del kc, vc
+    a, b = far_apart(3, (16, 128)), far_apart(3, (96, 16))
+    a.copy_(randn(g, 3, 16, 128, scale=0.1))
+    b.copy_(randn(g, 3, 96, 16))
+    x, y = randn(g, 200, 128), randn(g, 200, 96)
+    scale = torch.ones(3, device=DEV)
+    index = (torch.arange(200, device=DEV) % 4 - 1).to(torch.int32)
+    for rows in (200, 20):
+        got = qz().lora(x[:rows], y[:rows], qz().LoraAdapters(a, b, scale), index[:rows])
+        near = qz().LoraAdapters(a.contiguous(), b.contiguous(), scale)
+        want = qz().lora(x[:rows], y[:rows], near, index[:rows])
+        assert torch.equal(got, want)
+    del a, b
+    rows = far_apart(3, (512,))
+    rows.copy_(randn(g, 3, 512))
+    w, out = randn(g, 512), far_apart(3, (512,))
+    qz().rmsnorm(rows, w, out=out)
+    assert torch.equal(out, qz().rmsnorm(rows.contiguous(), w)[0])
