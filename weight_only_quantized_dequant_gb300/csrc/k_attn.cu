@@ -631,6 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *drained = q_empty + 1;  // the products of a CTA that gave up
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+  // Copies that the load warp has issued, tiles that the query warps have
+  uint32_t *issued = reinterpret_cast<uint32_t *>(abort_flag + 1);  // [kLoadWarp - kQWarp + 1]
   Seg *seg_sm = reinterpret_cast<Seg *>(base + 512);         // [kSegs]
   float *xch = reinterpret_cast<float *>(base + 1024);       // [2][8 warps][32]
   uint8_t *q_sm = base + kHead, *kv_sm = q_sm + C::kQ;
@@ -693,8 +695,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n % kSegs]));
   };
-
-  uint32_t issued = 0;  // copies of a load warp, tiles of a query warp
 
   // n / G for n < G + 256: (n + 1/2) / G stays further from every whole number
   // than fp32 rounding can move it.
@@ -1198,7 +1198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 : "memory");
         }
         __syncwarp();
-        issued = ++segs;
+        ++segs;
         continue;
       }
       if (segs > 0) {
@@ -1234,6 +1234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(q_full));
       ++segs;
     }
+    if (lane == 0) issued[warp - kQWarp] = p.q_boxes ? segs : 0;
   } else {
     // --------------------------------------------------------------- load --
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -1342,7 +1343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && j == 0 && n_seg == 1) ok = announce(next = w.next(p));
       }
     }
-    issued = ring;
+    if (lane == 0) issued[kLoadWarp - kQWarp] = ring;
   }
   fence_before();
   __syncthreads();
@@ -1350,14 +1351,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*(volatile int *)abort_flag) {  // (of the whole CTA: every warp has stopped)
     const unsigned long long until = gtimer() + kWaitNs;
     if (warp == kLoadWarp) {
-      for (uint32_t r = issued - min(issued, (uint32_t)NS); r < issued; ++r)
+      const uint32_t n = issued[kLoadWarp - kQWarp];
+      for (uint32_t r = n - min(n, (uint32_t)NS); r < n; ++r)
         mbar_drain(smem_u32(&kv_full[r % NS]), (r / NS) & 1, until);
     } else if (warp == kMmaWarp) {
       if (elect_one()) mma_commit(smem_u32(drained));
       __syncwarp();
       mbar_drain(smem_u32(drained), 0, until);
-    } else if (issued > 0) {
-      mbar_drain(smem_u32(q_full), (issued - 1) & 1, until);
+    } else if (warp >= kQWarp && issued[warp - kQWarp] > 0) {
+      mbar_drain(smem_u32(q_full), (issued[warp - kQWarp] - 1) & 1, until);
     }
     fence_before();
     __syncthreads();
