@@ -29,10 +29,10 @@
 //    in the workspace; the last warp to arrive for its 32 rows merges them in
 //    CTA order (results repeat).
 //
-// Measured (GB300).  32 single tokens over contexts up to 16384, 64 heads, 8 KV
-// heads of 128: 208 us, 6.56 TB/s of keys and values, the rate of a plain copy.
-// Four packed prompts up to 4096, 32 heads: 317-340 us, 1005-1077 TFLOP/s; four
-// chunks of 64 tokens over 24000, 64 heads on 8: 112 us, 921 TFLOP/s.  A block of
+// Measured (GB300, by box).  32 single tokens over contexts up to 16384, 64 heads, 8
+// KV heads of 128: 205-208 us, 6.6 TB/s of keys and values, the rate of a plain copy.
+// Four packed prompts up to 4096, 32 heads: 323-345 us, 990-1058 TFLOP/s; four
+// chunks of 64 tokens over 24000, 64 heads on 8: 112 us, 925 TFLOP/s.  A block of
 // a 256-row tile takes about 3200 SM clocks: 2048 are the MMAs (64 each), the
 // rest is the chain of one stage (softmax 1550, its two products 1024 + 500 to
 // completion and back) that the other stage's turn does not cover.  A tile's end
@@ -80,9 +80,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Units per CTA at least.  One token over 199 keys takes 11.3 us with 1, 10.2 with 3
 // and 13.6 with 6; over 1000 keys 13.2, 15.0 and 19.5.
 constexpr int kMinUnits = 3;
-// Time to merge one partial, in key blocks: 8 rows over 30000 keys of one KV head
-// take 52 us when all SMs share the tile, 38 with this, 33 with 0.5, which costs
-// one token over 4096 keys 15.3 -> 17.7 us.
+// Time to merge one partial, in key blocks: 8 tokens (64 rows) over 30000 keys of one KV
+// head take 51 us when all SMs share the tile, 34 with this, 31 with 0.5, which costs
+// one token over 4096 keys 15.1 -> 17.0 us.
 constexpr float kMergeUnits = 0.2f;
 // A tile's fixed time, in key blocks.  256 rows: four prompts of up to 4096 take 343
 // us with none, 326 with 1, 317 with 2; 128 rows: one token over 199 keys takes 15.1

@@ -25,10 +25,10 @@
 // the others overlap), so that an adapter is read for up to 32 of its rows at once
 // however they come.
 //
-// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 11.3 us, of
-// which down 5, up 3.5 after it; the chain index, adapter, products, cluster, u,
-// products is latency.  1500 rows of 8 adapters of ranks up to 64 in runs of 300,
-// 4096 x 11008: 52.8 us, 2 of them the sort, down 19 (one wave of CTAs with fewer
+// Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 11.3 us with the
+// adapters in the L2 (down 5, up 3.5 after it), 13 without; the chain index, adapter,
+// products, cluster, u, products is latency.  1500 rows of 8 adapters of ranks up to 64 in runs of 300,
+// 4096 x 11008: 52.5-55.8 us by box, 2 of them the sort, down 19 (one wave of CTAs with fewer
 // slices takes as long), up the rest: each step of 64 outputs waits for its own loads
 // (about half of its 4 us; a product is 8 clocks of a scheduler, so the matrix
 // instructions are a fifth of the time), twice in the few row tiles that two runs
@@ -44,10 +44,10 @@ __device__ int g_lora_error = 0;
 constexpr int kWarps = kLoraWarps, kUpWarps = kLoraUpWarps, kSub = kLoraSub, kSlice = kLoraSlice;
 constexpr int kMaxRows = kLoraMaxRows, kOut = kLoraOut, kMaxSlices = kLoraMaxSlices;
 constexpr int kThreads = 32 * kWarps;       // down
-// Rows from which they are sorted first.  1500 rows of 48 adapters in turn, rank
-// 16, 4096 x 11008: 265 -> 48.5 us; 128 of 16, rank 64: 48 -> 29; 64 of 4, rank 16,
-// 4096 x 4096: 13.8 -> 16.7.  Rows that come grouped
-// pay 2 us for it (1500 in runs of 300: 48.7 -> 50.5).
+// Rows from which they are sorted first.  Unsorted and sorted, rows in turn: 1500 of 48
+// adapters, rank 16, 4096 x 11008: 275 and 50.2 us; 128 of 16, rank 64: 50.1 and 21.0;
+// 128 of 128, rank 16, 4096 x 4096: 19.7 and 21.5; 64 of 4: 13.0 and 12.0.  Rows that come
+// grouped pay 1.6 us for it (1500 in runs of 300: 50.9 and 52.5).
 constexpr int64_t kOrderRows = 128;
 constexpr int kBins = 1024;                 // of the sort by adapter
 constexpr int kSegment = 2048;              // rows sorted together

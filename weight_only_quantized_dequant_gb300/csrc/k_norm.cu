@@ -8,8 +8,9 @@
 // (x, r in; y or q, h out) and HBM bounds long calls, launch latency short ones.
 // The threads of a row are the fewest that hold it in kMaxVec 16-byte vectors each,
 // all loaded before the first use.  Measured (GB300): 2048 x 8192 with residual
-// 21.7 us, 6.2 TB/s (93% of a plain copy's rate); 16 x 8192 2.6 us; 1021 x 3584
-// to INT8 rows 7.7 us.
+// 21.3 us, 6.3 TB/s (94% of a plain copy's rate); 16 x 8192 2.4 us; 1021 x 3584
+// to INT8 rows 8.4 us, 3.1 TB/s: its CTAs are little more than the GPU holds at once, so
+// it is a row's own chain, the maximum and a division a value included.
 #include "qz_internal.cuh"
 
 namespace qz {

@@ -6,7 +6,7 @@
 // copies 16 of a value row.  A token's position and page come from one warp-wide
 // search of the sequence boundaries (seq_of_token).  HBM bounds long steps, launch
 // latency a decode step.  Measured (GB300): 1854 packed tokens, 64 heads, 8 KV
-// heads of 128 14.4 us, 5.3 TB/s (80% of a plain copy's rate; the fp32 cosines are
+// heads of 128 14.8 us, 5.2 TB/s (78% of a plain copy's rate; the fp32 cosines are
 // as many loads as the values, read from L2); 64 single tokens, 32 heads 2.9 us.
 #include "seq_batch.cuh"
 
