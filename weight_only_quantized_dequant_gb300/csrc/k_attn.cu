@@ -29,7 +29,7 @@
 //    in the workspace; the last warp to arrive for its 32 rows merges them in
 //    CTA order (results repeat).
 //
-// Measured (GB300, by box).  32 single tokens over contexts up to 16384, 64 heads, 8
+// Measured (by GPU).  32 single tokens over contexts up to 16384, 64 heads, 8
 // KV heads of 128: 205-208 us, 6.6 TB/s of keys and values, the rate of a plain copy.
 // Four packed prompts up to 4096, 32 heads: 323-345 us, 990-1058 TFLOP/s; four
 // chunks of 64 tokens over 24000, 64 heads on 8: 112 us, 925 TFLOP/s.  A block of

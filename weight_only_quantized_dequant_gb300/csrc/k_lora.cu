@@ -28,7 +28,7 @@
 // Measured (GB300): 32 rows of 32 adapters of rank 16, 8192 x 8192: 11.3 us with the
 // adapters in the L2 (down 5, up 3.5 after it), 13 without; the chain index, adapter,
 // products, cluster, u, products is latency.  1500 rows of 8 adapters of ranks up to 64 in runs of 300,
-// 4096 x 11008: 52.5-55.8 us by box, 2 of them the sort, down 19 (one wave of CTAs with fewer
+// 4096 x 11008: 52.5-55.8 us by GPU, 2 of them the sort, down 19 (one wave of CTAs with fewer
 // slices takes as long), up the rest: each step of 64 outputs waits for its own loads
 // (about half of its 4 us; a product is 8 clocks of a scheduler, so the matrix
 // instructions are a fifth of the time), twice in the few row tiles that two runs
