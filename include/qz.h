@@ -81,7 +81,8 @@ int qz_get_overlap(void);
  * bounded wait (its output is then incomplete); 2 if qz_embed_int8 met a
  * token outside its table (that row was written as zeros); 4 if a page, a
  * position or an adapter index lay outside its table (qz_rope_append,
- * qz_attention_paged, qz_lora; each says what it did then).  0 if none
+ * qz_attention_paged, their _int8 forms, qz_cache_read_int8, qz_lora; each
+ * says what it did then).  0 if none
  * happened since the last clear.  Synchronous (reads device memory);
  * clear = 1 resets it.  Not for use during stream capture. */
 qz_status qz_device_error(int *code, int clear);
@@ -514,6 +515,60 @@ qz_status qz_attention_paged(const qz_half *q, int64_t n_heads, int64_t q_token,
 size_t qz_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t n_heads,
                                     int64_t n_kv_heads, int64_t head_dim);
 
+/* A paged key/value cache of INT8 rows: every row (a token slot of a KV head) is
+ * head_dim codes and one fp32 scale, and stands for code * scale.  The codes lie
+ * as the rows of qz_kv_cache do (strides in bytes, multiples of 16; k and v
+ * 16-byte aligned), the scale of token slot t of page p and head h at
+ * k_scale + p * ks_page + h * ks_head + t * ks_token (strides in floats; v
+ * likewise).  Same page sizes and head sizes. */
+typedef struct {
+  int8_t *k, *v;
+  float *k_scale, *v_scale;
+  int64_t n_pages, page_size, n_kv_heads, head_dim;
+  int64_t k_page, k_head, k_token;
+  int64_t v_page, v_head, v_token;
+  int64_t ks_page, ks_head, ks_token;
+  int64_t vs_page, vs_head, vs_token;
+} qz_kv_cache_int8;
+
+/* qz_rope_append into a cache of INT8 rows.  With y the value, or the rotated key
+ * rounded to fp32 (from its exact products), by the rule of qz_quantize_int8:
+ *   scale = fp32(max_j |y[j]|) / 127;  code[j] = clamp(rint(y[j] / scale), -127, 127)
+ * (IEEE fp32 divisions, ties to even); a row of zeros gives scale 0 and codes 0, a
+ * row with a NaN or an infinity a scale that is not finite and codes 0.  q_out,
+ * positions, what is not stored, and errors are those of qz_rope_append. */
+qz_status qz_rope_append_int8(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                              const qz_half *k, int64_t k_token, int64_t k_head,
+                              const qz_half *v, int64_t v_token, int64_t v_head,
+                              const float *rope, int64_t rope_len,
+                              const qz_kv_cache_int8 *cache, const qz_seq_batch *seqs,
+                              qz_half *q_out, int64_t qo_token, int64_t qo_head, qz_stream s);
+
+/* Rows of such a cache as fp16: row t of k and v [n_tokens][n_kv_heads][head_dim]
+ * (strides k_token, k_head, ...) is the cache's row of the token that seqs gives
+ * row t, fp16(code * scale), the product rounded to fp32 before.  So the sequences
+ * of a step give its new tokens, and cu_q with the running sums of kv_len all
+ * that is held.  Rows outside every sequence, and tokens of a negative position
+ * (which read as zeros), are as in qz_rope_append; a page outside the pool or
+ * beyond ld_table reads as zeros and sets bit 4 of the device error word.  k and
+ * v 16-byte aligned, strides multiples of 8. */
+qz_status qz_cache_read_int8(const qz_kv_cache_int8 *cache, const qz_seq_batch *seqs, qz_half *k,
+                             int64_t k_token, int64_t k_head, qz_half *v, int64_t v_token,
+                             int64_t v_head, qz_stream s);
+
+/* qz_attention_paged over a cache of INT8 rows: k_j and v_j are the rows' codes
+ * times their scales, which multiply logits and weights in fp32, so that the codes
+ * enter the products exactly; the weights times the values' scales are rounded to
+ * fp16 where they enter the tensor cores (to 2^-11 of each, or 2^-30 of the largest).  Everything
+ * else is as in qz_attention_paged, with the same workspace (which calls of both
+ * may share one after the other); codes of slots that no query sees may hold
+ * anything, and so may their scales. */
+qz_status qz_attention_paged_int8(const qz_half *q, int64_t n_heads, int64_t q_token,
+                                  int64_t q_head, const qz_kv_cache_int8 *cache,
+                                  const qz_seq_batch *seqs, float scale, float softcap,
+                                  int64_t window, qz_half *out, int64_t o_token, int64_t o_head,
+                                  void *workspace, size_t workspace_bytes, qz_stream s);
+
 /* Low-rank adapters of many requests beside a shared projection:
  *   out[t][i] = fp16( y[t][i] + scale[a] * sum_{r < rank[a]} B_a[i][r] * u_r ),
  *   u_r = sum_j A_a[r][j] x[t][j],  a = index[t];
@@ -541,6 +596,40 @@ qz_status qz_lora(const qz_lora_adapters *ad, const int32_t *index, int64_t T,
                   const qz_half *x, int64_t ldx, const qz_half *y, int64_t ldy, qz_half *out,
                   int64_t ldo, void *workspace, size_t workspace_bytes, qz_stream s);
 size_t qz_lora_workspace_bytes(int64_t T, int64_t K, int64_t R);
+
+/* The next tokens of B requests from their logits.  With x = row b of the logits
+ * (NaN counts as -inf) and m its largest:
+ *   w_i = e^{(x_i - m) / temperature};
+ *   top_k: the k tokens of largest logit are kept (1 <= k < V; others keep all);
+ *   top_p: of those, the fewest, largest first, whose weights sum to top_p of all
+ *     of theirs, one at least (top_p < 1; others keep all);
+ *   min_p: of those, the ones with w_i >= min_p (0 < min_p; 1 and above keep the
+ *     largest only).
+ * Equal logits are taken lowest index first.  token[b] is the first kept i whose
+ * running sum of kept weights, by index, exceeds u[b] times their total, and
+ * logprob[b] = ln(w_i / total) (logprob may be NULL).  temperature <= 0 takes the
+ * largest logit (probability 1).  u outside [0, 1) is taken as the nearest value
+ * in it.  A row without any logit above -inf gives token -1 and logprob -inf;
+ * logits of +inf share all the weight.
+ * Weights are held as integers, 2^44 for the largest (to 2^-30 of each; below
+ * 2^-45 of the largest they are 0), and summed exactly: results repeat bit for
+ * bit and a row's do not depend on the others.
+ * logits [B][ld] of the given type, aligned to its size (16-byte aligned rows are
+ * read faster), ld >= V.  Options: a device array of B values, or NULL and one
+ * value for all rows.  1 <= V <= QZ_MAX_VOCAB, B <= 2^24. */
+typedef enum { QZ_FP16 = 0, QZ_BF16 = 1, QZ_FP32 = 2 } qz_dtype;
+#define QZ_MAX_VOCAB (1 << 18)
+typedef struct {
+  const float *temperature;
+  const int32_t *top_k;
+  const float *top_p, *min_p;
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all, min_p_all;
+} qz_sampling;
+qz_status qz_sample(const void *logits, int dtype, int64_t B, int64_t V, int64_t ld,
+                    const float *u, const qz_sampling *options, int32_t *token, float *logprob,
+                    qz_stream s);
 
 #ifdef __cplusplus
 }

@@ -49,10 +49,27 @@ class KvCache(ctypes.Structure):
                 ("v_page", c_int64), ("v_head", c_int64), ("v_token", c_int64)]
 
 
+class KvCacheInt8(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("n_pages", c_int64), ("page_size", c_int64), ("n_kv_heads", c_int64),
+                ("head_dim", c_int64),
+                ("k_page", c_int64), ("k_head", c_int64), ("k_token", c_int64),
+                ("v_page", c_int64), ("v_head", c_int64), ("v_token", c_int64),
+                ("ks_page", c_int64), ("ks_head", c_int64), ("ks_token", c_int64),
+                ("vs_page", c_int64), ("vs_head", c_int64), ("vs_token", c_int64)]
+
+
 class SeqBatchArg(ctypes.Structure):
     _fields_ = [("n_seqs", c_int64), ("n_tokens", c_int64),
                 ("cu_q", c_void_p), ("kv_len", c_void_p), ("page_table", c_void_p),
                 ("ld_table", c_int64)]
+
+
+class Sampling(ctypes.Structure):
+    _fields_ = [("temperature", c_void_p), ("top_k", c_void_p), ("top_p", c_void_p),
+                ("min_p", c_void_p),
+                ("temperature_all", c_float), ("top_k_all", c_int),
+                ("top_p_all", c_float), ("min_p_all", c_float)]
 
 
 class LoraArg(ctypes.Structure):
@@ -119,6 +136,17 @@ _SIGS = {
     "qz_attention_paged": (_S, [c_void_p, c_int64, c_int64, c_int64, POINTER(KvCache),
                                 POINTER(SeqBatchArg), c_float, c_float, c_int64, c_void_p,
                                 c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
+    "qz_rope_append_int8": (_S, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_int64,
+                                 c_void_p, c_int64, c_int64, c_void_p, c_int64,
+                                 POINTER(KvCacheInt8), POINTER(SeqBatchArg), c_void_p, c_int64,
+                                 c_int64, c_void_p]),
+    "qz_cache_read_int8": (_S, [POINTER(KvCacheInt8), POINTER(SeqBatchArg), c_void_p, c_int64,
+                                c_int64, c_void_p, c_int64, c_int64, c_void_p]),
+    "qz_attention_paged_int8": (_S, [c_void_p, c_int64, c_int64, c_int64, POINTER(KvCacheInt8),
+                                     POINTER(SeqBatchArg), c_float, c_float, c_int64, c_void_p,
+                                     c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
+    "qz_sample": (_S, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, POINTER(Sampling),
+                       c_void_p, c_void_p, c_void_p]),
     "qz_attention_workspace_bytes": (c_size_t, [c_int64] * 5),
     "qz_lora": (_S, [POINTER(LoraArg), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
                      c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),

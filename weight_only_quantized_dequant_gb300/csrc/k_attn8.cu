@@ -1,0 +1,700 @@
+// Attention of a step's new tokens over the paged cache of INT8 rows, for steps
+// that bring few rows to a KV head (decode and drafts).
+//
+// For one KV head the queries of a sequence are packed row r = token * G +
+// head-in-group; a tile has 16 of them, one operand of the warp's matrix
+// instruction, and
+//   x_j = scale ks_j (q . kc_j),  out = sum_j e^{x_j} vs_j vc_j / sum_j e^{x_j}
+// over the codes kc, vc and the scales ks, vs of the keys.  Codes are exact in fp16
+// (a byte under the bits of 1024, less 1152, is the code), so they enter the
+// products as they are: ks_j multiplies the logit, vs_j the weight, both in fp32.
+//
+//  * HBM bounds a decode step: a token and head is 2 (D + 4) bytes, 11 clocks of an
+//    SM's share at D 128, and its codes are converted once, by the warp that multiplies
+//    them.  A block of 128 keys comes by TMA, page by page, with the swizzle under
+//    which the fragments' 16-byte reads do not conflict; each of eight warps has 16
+//    of the keys to itself, with a running maximum, sum and output of its own, so
+//    nothing is exchanged before the tile's end.
+//  * The order of D in a product is free as long as both operands have it: a thread's
+//    16 bytes of a key are four steps of the first product, and of a value four
+//    columns of the second, so that both come as whole 16-byte reads.
+//  * Weights are rounded to fp16 once, with vs_j in them: 2^6 e^{x - m} vs_j 2^-E,
+//    where m lags the maximum by up to 2^8 and 2^E the largest vs by up to 2.
+//  * The split of (tile, key block) units between CTAs is that of the fp16 kernel.
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+
+#include "attn_plan.cuh"
+
+namespace qz {
+namespace {
+
+constexpr int kM = 16;                // rows of a tile
+constexpr int kWarps = 8;             // each has 16 of a block's keys
+constexpr int kLoadWarp = kWarps;     // the third warpgroup: one warp loads, three do nothing
+constexpr int kThreads = 384;
+constexpr int kMathRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
+static_assert(8 * kMathRegs + 4 * kOtherRegs <= 12 * 168, "register split");
+constexpr float kLift8 = 6.0f;        // log2 of the weight at m
+static_assert(kLift8 + kLag + 1.0f < 16.0f, "weights are fp16");
+constexpr int kHead8 = 4096;          // barriers, announced tiles, row maxima and sums
+
+template <int D>
+struct Cfg8 {
+  static constexpr int kRow = D < 128 ? D : 128;    // bytes of a swizzled row
+  static constexpr int kStage = kN * D;             // bytes of a K or V block
+  static constexpr int kNS = 131072 / kStage;       // K and V slots: 16, 8, 4
+  static constexpr int kSteps = D / 16;             // of the first product
+  static constexpr int kBuf = kWarps * kM * kRow * 4;  // outputs of the warps, 128 columns at a time
+  static constexpr int kQ = D == 256 ? kSteps * 512 : 0;
+  static constexpr int kSmem = 1024 + kHead8 + kNS * kN * 4 + kNS * kStage + kBuf + kQ;
+  static constexpr int kPart = kM * (D + 2);        // floats of a partial
+};
+
+struct Attn8Params : PlanParams, CapParams {
+  CUtensorMap kmap, vmap;  // [page][head][slot][D] bytes, box 128 (64) x min(page, 128)
+  const float *ks, *vs;
+  int64_t ks_page, ks_head, ks_token, vs_page, vs_head, vs_token;
+  const __half *q;
+  __half *out;
+  int64_t q_token, q_head, o_token, o_head;
+  int n_pages, page_size, page_shift;
+  float c;       // logit units to log2 of what the product and ks give
+  float sign;    // of the scale (0: no logits)
+  unsigned *cnt; // [kMaxCtas] arrivals per cut tile, by its first CTA
+  float *part;   // [kMaxCtas][2] partials
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds64f(uint32_t a) {
+  const uint2 v = lds64(a);
+  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+}
+// Two bytes of codes + 128 (chosen by sel, under the bits of 1024) as fp16 codes.
+__device__ __forceinline__ uint32_t code_pair(uint32_t biased, uint32_t sel) {
+  const uint32_t v = __byte_perm(biased, 0x64646464u, sel);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&v),
+                            __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+// D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int CAP>
+__global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
+  using C = Cfg8<D>;
+  constexpr int NS = C::kNS, KS = C::kSteps, NT = D / 8;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *kv_sm = base;
+  uint8_t *buf_sm = kv_sm + NS * C::kStage;
+  uint8_t *q_sm = buf_sm + C::kBuf;
+  float *scale_sm = reinterpret_cast<float *>(q_sm + C::kQ);  // [NS][kN]
+  uint8_t *head = reinterpret_cast<uint8_t *>(scale_sm + NS * kN);
+  uint64_t *kv_full = reinterpret_cast<uint64_t *>(head), *kv_empty = kv_full + 16;
+  uint64_t *seg_full = kv_empty + 16, *seg_empty = seg_full + kSegs;
+  uint64_t *met = seg_empty + kSegs;  // the eight warps of a tile
+  int *abort_flag = reinterpret_cast<int *>(met + 1);
+  uint32_t *issued = reinterpret_cast<uint32_t *>(abort_flag + 1);
+  unsigned *arrived_sm = issued + 1;
+  Seg *seg_sm = reinterpret_cast<Seg *>(head + 512);           // [kSegs]
+  float2 *ml_sm = reinterpret_cast<float2 *>(head + 1024);     // [2][kWarps][kM] maximum and sum
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&kv_full[i]), 33);
+      mbar_init(smem_u32(&kv_empty[i]), kWarps);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(smem_u32(&seg_full[i]), 1);
+      mbar_init(smem_u32(&seg_empty[i]), kWarps);
+    }
+    mbar_init(smem_u32(met), kWarps);
+    *abort_flag = 0;
+    *issued = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  Walker<kM> w;
+  w.u = w.u_end = 0;
+  if (warp == kLoadWarp) {
+    if (p.s.n_seqs <= 32)
+      w.template start<1>(p);
+    else
+      w.template start<8>(p);
+  }
+  __syncthreads();
+
+  if (warp < kWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegs));
+    const int g = lane >> 2, t = lane & 3;
+    // n / G for n < G + 256 (see the fp16 kernel)
+    auto row_token = [&](int n) { return (int)(((float)n + 0.5f) * p.inv_g); };
+    const uint32_t kv0 = smem_u32(kv_sm), sc0 = smem_u32(scale_sm) + warp * 64;
+    // this thread's 16 bytes of a key: rows 8 nt + g of the warp's 16, chunks 2 t and 2 t + 1
+    // (of 8; D 64: t of 4); of a value: rows 2 t + {0, 1, 8, 9}, chunk g (D 64: half of g / 2)
+    const int krow = warp * 16 + g;
+    const uint32_t k_at = krow * C::kRow;
+    const uint32_t k_sw = D == 64 ? (t ^ ((krow >> 1) & 3)) << 4 : ((2 * t) ^ (krow & 7)) << 4;
+    uint32_t v_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = warp * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+      v_at[i] = r * C::kRow + (D == 64 ? (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8
+                                       : (g ^ (r & 7)) << 4);
+    }
+    uint32_t n_seg = 0, ring = 0, n_met = 0;
+    bool ok = true;
+    // All eight warps have come here; false if one gave up.
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(met));
+      return ok = mbar_wait(smem_u32(met), n_met++ & 1, abort_flag);
+    };
+    while (ok) {
+      Seg s;
+      if (!(ok = mbar_wait(smem_u32(&seg_full[n_seg % kSegs]), (n_seg / kSegs) & 1, abort_flag)))
+        break;
+      {
+        const uint4 *src = reinterpret_cast<const uint4 *>(&seg_sm[n_seg % kSegs]);
+        uint4 *dst = reinterpret_cast<uint4 *>(&s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = src[i];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n_seg % kSegs]));
+      const int par = n_seg++ & 1;
+      if (s.rows == 0) break;
+      // ---- rows g and g + 8 (past the tile's end: its last row's limits)
+      int hi[2], lo[2];
+      const __half *qrow[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int n = s.rem + min(g + 8 * i, s.rows - 1), k = row_token(n);
+        hi[i] = s.pos + k + 1;
+        lo[i] = first_key(p, s.pos + k);
+        qrow[i] = p.q + (int64_t)(s.tok + k) * p.q_token +
+                  (int64_t)(s.head * p.G + n - k * p.G) * p.q_head;
+      }
+      const int see_lo = __reduce_max_sync(0xffffffffu, max(lo[0], lo[1]));
+      const int see_hi = __reduce_min_sync(0xffffffffu, min(hi[0], hi[1]));
+      // the first product's operand: step i has columns 4 i .. 4 i + 3 of this thread's D / 4
+      // (of each 128: D 256)
+      uint32_t qa[D == 256 ? 1 : KS][4];
+      if (D == 256) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = warp * 2 + k, d = (i >> 3) * 128 + 32 * t + 4 * (i & 7);
+          const uint2 a = *reinterpret_cast<const uint2 *>(qrow[0] + d);
+          const uint2 b = *reinterpret_cast<const uint2 *>(qrow[1] + d);
+          *reinterpret_cast<uint4 *>(q_sm + i * 512 + lane * 16) = make_uint4(a.x, b.x, a.y, b.y);
+        }
+        if (!meet()) break;
+      } else {
+#pragma unroll
+        for (int i = 0; i < KS; i += 2) {
+          const uint4 a = *reinterpret_cast<const uint4 *>(qrow[0] + t * (D / 4) + 4 * i);
+          const uint4 b = *reinterpret_cast<const uint4 *>(qrow[1] + t * (D / 4) + 4 * i);
+          qa[i][0] = a.x, qa[i][1] = b.x, qa[i][2] = a.y, qa[i][3] = b.y;
+          qa[i + 1][0] = a.z, qa[i + 1][1] = b.z, qa[i + 1][2] = a.w, qa[i + 1][3] = b.w;
+        }
+      }
+      float o[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      float e_pos = exp2f(-40.0f), e_neg = exp2f(40.0f);  // 2^E and 2^-E
+      for (int b = s.b0; b < s.b1; ++b, ring += 2) {
+        const uint32_t ks = ring % NS, vs = (ring + 1) % NS;
+        if (!(ok = mbar_wait(smem_u32(&kv_full[ks]), (ring / NS) & 1, abort_flag))) break;
+        const int key0 = warp * 16;  // of the block
+        // (the block's end may pass 32 bits)
+        const bool none = s.hi - b * kN <= key0 || (int64_t)b * kN + key0 + 16 <= s.lo;
+        float x[2][4];
+        if (!none) {
+          float sa[2][4], sb[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sa[i][j] = sb[i][j] = 0.0f;
+          const uint32_t kb = kv0 + ks * C::kStage + k_at;
+#pragma unroll
+          for (int h = 0; h < KS / 4; ++h) {  // 16 bytes of a key, four steps
+            const uint32_t at = kb + (h >> 1) * (kN * 128) + (k_sw ^ ((h & 1) << 4));
+            const uint4 k0 = lds128(at), k1 = lds128(at + 8 * C::kRow);
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t a[4];
+              if (D == 256) {
+                const uint4 v = lds128(smem_u32(q_sm) + (4 * h + i) * 512 + lane * 16);
+                a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[j] = qa[D == 256 ? 0 : 4 * h + i][j];
+              }
+              const uint32_t u0 = w0[i] ^ 0x80808080u, u1 = w1[i] ^ 0x80808080u;
+              mma16816(i & 1 ? sb[0] : sa[0], a, code_pair(u0, 0x4140), code_pair(u0, 0x4342));
+              mma16816(i & 1 ? sb[1] : sa[1], a, code_pair(u1, 0x4140), code_pair(u1, 0x4342));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 f = lds64f(sc0 + ks * (kN * 4) + i * 32 + t * 8);
+            const float fx = f.x * p.sign, fy = f.y * p.sign;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float v = (sa[i][j] + sb[i][j]) * (j & 1 ? fy : fx);
+              x[i][j] = (CAP == 0 ? v : CAP == 1 ? cap_far(p, v) : cap_any(p, v)) * p.c;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&kv_empty[ks]));
+        if (!(ok = mbar_wait(smem_u32(&kv_full[vs]), ((ring + 1) / NS) & 1, abort_flag))) break;
+        if (!none) {
+          const int k0 = key0 + 2 * t;  // keys k0 + {0, 1, 8, 9} of the block
+          if (see_hi - b * kN < key0 + 16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (k0 + 8 * i + (j & 1) >= hi[j >> 1] - b * kN) x[i][j] = -INFINITY;
+          }
+          if (key0 < see_lo - b * kN) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (k0 + 8 * i + (j & 1) < lo[j >> 1] - b * kN) x[i][j] = -INFINITY;
+          }
+          const float2 va = lds64f(sc0 + vs * (kN * 4) + t * 8);
+          const float2 vb = lds64f(sc0 + vs * (kN * 4) + 32 + t * 8);
+          float x0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+          float x1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+          float sv = fmaxf(fmaxf(va.x, va.y), fmaxf(vb.x, vb.y));
+          if (__any_sync(0xffffffffu, x0 > m[0] + kLag || x1 > m[1] + kLag || sv * e_neg > 2.0f)) {
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+              sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, d));
+            }
+            // (the scales are those of the warp's 16 keys: the same E in every lane)
+            const float e = fmaxf(e_pos, __uint_as_float(__float_as_uint(sv) & 0x7f800000u));
+            const float fe = e_pos * (1.0f / e);
+            e_pos = e;
+            e_neg = 1.0f / e;
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float mn = fmaxf(m[i], i ? x1 : x0);
+              f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - mn);
+              m[i] = mn;
+              l[i] *= f[i];
+              f[i] *= fe;
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              o[i][0] *= f[0], o[i][1] *= f[0];
+              o[i][2] *= f[1], o[i][3] *= f[1];
+            }
+          }
+          const float z0 = m[0] == -INFINITY ? 0.0f : kLift8 - m[0];
+          const float z1 = m[1] == -INFINITY ? 0.0f : kLift8 - m[1];
+          const float sn[4] = {va.x * e_neg, va.y * e_neg, vb.x * e_neg, vb.y * e_neg};
+          uint32_t pa[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float a0 = ex2(x[i][0] + z0), a1 = ex2(x[i][1] + z0);
+            const float b0 = ex2(x[i][2] + z1), b1 = ex2(x[i][3] + z1);
+            l[0] += a0 + a1;
+            l[1] += b0 + b1;
+            pa[2 * i] = f2h(a0 * sn[2 * i], a1 * sn[2 * i + 1]);
+            pa[2 * i + 1] = f2h(b0 * sn[2 * i], b1 * sn[2 * i + 1]);
+          }
+          const uint32_t vbase = kv0 + vs * C::kStage;
+#pragma unroll
+          for (int h = 0; h < (D + 127) / 128; ++h) {
+            uint32_t r[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (D == 64) {
+                const uint2 v = lds64(vbase + v_at[i]);
+                r[i][0] = v.x, r[i][1] = v.y;
+              } else {
+                const uint4 v = lds128(vbase + h * (kN * 128) + v_at[i]);
+                r[i][0] = v.x, r[i][1] = v.y, r[i][2] = v.z, r[i][3] = v.w;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < (D == 64 ? 2 : 4); ++c) {
+              uint32_t u[4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {  // two keys' codes side by side, column by column
+                const uint32_t ka = r[2 * i][c] ^ 0x80808080u, kb = r[2 * i + 1][c] ^ 0x80808080u;
+                u[i] = __byte_perm(ka, kb, 0x5140);
+                u[2 + i] = __byte_perm(ka, kb, 0x7362);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma16816(o[h * 16 + 4 * c + j], pa, code_pair(u[(j >> 1) * 2], j & 1 ? 0x4342 : 0x4140),
+                         code_pair(u[(j >> 1) * 2 + 1], j & 1 ? 0x4342 : 0x4140));
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&kv_empty[vs]));
+      }
+      if (!ok) break;
+      // ---- the warps' parts of the tile together
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if (t == 0) ml_sm[(par * kWarps + warp) * kM + g + 8 * i] = make_float2(m[i], l[i]);
+      }
+      if (!meet()) break;
+      // (a warp's own factor, for its rows g and g + 8)
+      float f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k)
+          M = fmaxf(M, ml_sm[(par * kWarps + k) * kM + g + 8 * i].x);
+        f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - M) * e_pos;
+      }
+      float *mine = p.part + (int64_t)(blockIdx.x * 2 + max(s.slot, 0)) * C::kPart;
+      auto out_at = [&](int r) {
+        const int n = s.rem + r, k = row_token(n);
+        return (int64_t)(s.tok + k) * p.o_token + (int64_t)(s.head * p.G + n - k * p.G) * p.o_head;
+      };
+      float *buf = reinterpret_cast<float *>(buf_sm);
+      constexpr int F4 = C::kRow / 4;  // float4 pieces of a row of the buffer
+#pragma unroll
+      for (int h = 0; ok && h < (D + 127) / 128; ++h) {
+        if (h > 0 && !meet()) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < F4 / 4; ++k) {
+            // this thread's D / 4 columns are contiguous: piece k has tiles n..n+3 of one half
+            constexpr int H = F4 / 8;  // pieces of a half
+            const int n = h * 16 + 4 * (k % H), c = 2 * i + k / H;
+            const int at = (F4 / 4) * t + (D == 64 ? k ^ ((t >> 1) * 2 + (g & 1))
+                                                   : k ^ (2 * t + (g & 1)));
+            *reinterpret_cast<float4 *>(buf + ((warp * kM + g + 8 * i) * F4 + at) * 4) =
+                make_float4(o[n][c] * f[i], o[n + 1][c] * f[i], o[n + 2][c] * f[i],
+                            o[n + 3][c] * f[i]);
+          }
+        if (!meet()) break;
+        for (int it = tid; it < s.rows * F4; it += kWarps * 32) {
+          const int r = it / F4, q4 = it % F4, tt = q4 / (F4 / 4), k = q4 % (F4 / 4);
+          const int at = (F4 / 4) * tt + (D == 64 ? k ^ ((tt >> 1) * 2 + (r & 1))
+                                                  : k ^ (2 * tt + (r & 1)));
+          float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float M = -INFINITY, L = 0.0f;
+#pragma unroll
+          for (int k2 = 0; k2 < kWarps; ++k2) {
+            const float4 v =
+                *reinterpret_cast<const float4 *>(buf + ((k2 * kM + r) * F4 + at) * 4);
+            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+            M = fmaxf(M, ml_sm[(par * kWarps + k2) * kM + r].x);
+          }
+#pragma unroll
+          for (int k2 = 0; k2 < kWarps; ++k2) {
+            const float2 v = ml_sm[(par * kWarps + k2) * kM + r];
+            if (v.x > -INFINITY) L = fmaf(v.y, ex2(v.x - M), L);
+          }
+          if (s.slot < 0) {
+            const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            *reinterpret_cast<uint2 *>(p.out + out_at(r) + h * 128 + q4 * 4) =
+                make_uint2(f2h(a.x * inv, a.y * inv), f2h(a.z * inv, a.w * inv));
+          } else {
+            *reinterpret_cast<float4 *>(mine + 2 * kM + r * D + h * 128 + q4 * 4) = a;
+            if (q4 == 0 && h == 0) {
+              mine[r] = M;
+              mine[kM + r] = L;
+            }
+          }
+        }
+      }
+      if (!ok) break;
+      if (s.slot < 0) continue;
+      // ---- cut between CTAs: the last to arrive merges, in CTA order
+      __threadfence();
+      if (!meet()) break;
+      if (tid == 0) *arrived_sm = atomicAdd(&p.cnt[s.c_lo], 1u);
+      if (!meet()) break;
+      const bool last = (int)*arrived_sm == s.parts - 1;
+      if (last) {
+        __threadfence();
+        auto part_at = [&](int k) {
+          return p.part + (int64_t)((s.c_lo + k) * 2 + (k == 0 ? s.first_slot : 0)) * C::kPart;
+        };
+        for (int it = tid; it < s.rows * (D / 4); it += kWarps * 32) {
+          const int r = it / (D / 4), q4 = it % (D / 4);
+          float M = -INFINITY, L = 0.0f;
+          float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          constexpr int U = 8;
+          for (int k0 = 0; k0 < s.parts; k0 += U) {
+            float mk[U], lk[U];
+            float4 v[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const float *pp = part_at(min(k0 + k, s.parts - 1));
+              mk[k] = k0 + k < s.parts ? __ldcg(pp + r) : -INFINITY;
+              lk[k] = __ldcg(pp + kM + r);
+              v[k] = __ldcg(reinterpret_cast<const float4 *>(pp + 2 * kM + r * D) + q4);
+            }
+            float mn = M;
+#pragma unroll
+            for (int k = 0; k < U; ++k) mn = fmaxf(mn, mk[k]);
+            if (mn == -INFINITY) continue;
+            const float f0 = ex2(M - mn);
+            L *= f0;
+            a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const float fk = ex2(mk[k] - mn);
+              L = fmaf(lk[k], fk, L);
+              a.x = fmaf(v[k].x, fk, a.x), a.y = fmaf(v[k].y, fk, a.y);
+              a.z = fmaf(v[k].z, fk, a.z), a.w = fmaf(v[k].w, fk, a.w);
+            }
+            M = mn;
+          }
+          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+          *reinterpret_cast<uint2 *>(p.out + out_at(r) + q4 * 4) =
+              make_uint2(f2h(a.x * inv, a.y * inv), f2h(a.z * inv, a.w * inv));
+        }
+        if (tid == 0) p.cnt[s.c_lo] = 0;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  }
+  if (warp == kLoadWarp) {
+    // --------------------------------------------------------------- load --
+    uint32_t ring = 0;
+    bool ok = true;
+    const int ppb = p.page_size >= kN ? 1 : kN >> p.page_shift;  // pages per block
+    const int box_rows = min(p.page_size, kN);
+    const int box_shift = min(p.page_shift, 7);
+    int batch = 0, ids = -1, ids_ahead = -1;  // as in the fp16 kernel
+    auto fetch = [&](const Seg &g, int first) -> int {
+      const int pi = first + lane;
+      const int64_t key = (int64_t)pi << p.page_shift;
+      if (key >= g.hi || key + p.page_size <= g.lo) return -1;
+      const int id = pi < p.s.ld_table ? __ldg(p.s.table + (int64_t)g.seq * p.s.ld_table + pi) : -2;
+      return id == -1 ? -2 : id;
+    };
+    auto page_of = [&](const Seg &g, int b) -> int {
+      const int pi = (int)(((int64_t)b * kN + lane * box_rows) >> p.page_shift);
+      if (__shfl_sync(0xffffffffu, pi, ppb - 1) >= batch + 32) {
+        batch += 32;
+        ids = ids_ahead;
+        ids_ahead = fetch(g, batch + 32);
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, pi - batch);
+      if (lane >= ppb || id == -1) return -1;
+      if (id < 0 || id >= p.n_pages) {
+        atomicOr(&g_attn_error, 4);
+        return INT32_MAX;
+      }
+      return id;
+    };
+    auto issue = [&](const CUtensorMap *map, const float *sc, int64_t sc_page, int64_t sc_head,
+                     int64_t sc_token, const Seg &g, int b, int page) -> bool {
+      const int slot = ring % NS;
+      if (ring >= NS && !mbar_wait(smem_u32(&kv_empty[slot]), (ring / NS - 1) & 1, abort_flag))
+        return false;
+      const uint32_t bar = smem_u32(&kv_full[slot]);
+      const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0)
+        asm volatile(
+            "{\n\t.reg .b64 t;\n\t"
+            "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(bar),
+            "r"((uint32_t)(__popc(live) * box_rows * D))
+            : "memory");
+      __syncwarp();
+      if (page >= 0) {
+        const int at = p.page_size > kN ? (b * kN) & (p.page_size - 1) : 0;
+        const uint32_t dst = smem_u32(kv_sm) + slot * C::kStage + lane * box_rows * C::kRow;
+#pragma unroll
+        for (int d = 0; d < (D + 127) / 128; ++d)
+          asm volatile(
+              "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+              "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + d * (kN * 128)),
+              "l"(reinterpret_cast<uint64_t>(map)), "r"(d * 128), "r"(at), "r"(g.head), "r"(page),
+              "r"(bar)
+              : "memory");
+      }
+      // scales, four a lane; of keys that no row sees, and of missing pages, zeros
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = lane + 32 * i;
+        const int64_t key = (int64_t)b * kN + k;
+        const int pg = __shfl_sync(0xffffffffu, page, k >> box_shift);
+        const bool use = pg >= 0 && pg < p.n_pages && key >= g.lo && key < g.hi;
+        const float *src = use ? sc + pg * sc_page + g.head * sc_head +
+                                     (key & (p.page_size - 1)) * sc_token
+                               : sc;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                         smem_u32(scale_sm + slot * kN + k)),
+                     "l"(src), "r"(use ? 4 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+      __syncwarp();
+      ++ring;
+      return true;
+    };
+    uint32_t n_seg = 0;
+    auto announce = [&](const Seg &g) -> bool {
+      const uint32_t at = n_seg % kSegs;
+      if (n_seg >= kSegs &&
+          !mbar_wait(smem_u32(&seg_empty[at]), (n_seg / kSegs - 1) & 1, abort_flag))
+        return false;
+      if (lane == 0) {
+        seg_sm[at] = g;
+        mbar_arrive(smem_u32(&seg_full[at]));
+      }
+      __syncwarp();
+      ++n_seg;
+      return true;
+    };
+    while (ok) {
+      const Seg g = w.next(p);
+      ok = announce(g);
+      if (!ok || g.rows == 0) break;
+      const int nb = g.b1 - g.b0;
+      if (nb > 0) {
+        batch = (int)(((int64_t)g.b0 * kN) >> p.page_shift);
+        ids = fetch(g, batch);
+        ids_ahead = fetch(g, batch + 32);
+      }
+      for (int b = g.b0; ok && b < g.b1; ++b) {
+        const int page = page_of(g, b);
+        ok = issue(&p.kmap, p.ks, p.ks_page, p.ks_head, p.ks_token, g, b, page) &&
+             issue(&p.vmap, p.vs, p.vs_page, p.vs_head, p.vs_token, g, b, page);
+      }
+    }
+    if (lane == 0) *issued = ring;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __syncthreads();
+  if (*(volatile int *)abort_flag && warp == kLoadWarp) {  // copies in flight end before the CTA
+    const unsigned long long until = gtimer() + kWaitNs;
+    const uint32_t n = *issued;
+    for (uint32_t r = n - min(n, (uint32_t)NS); r < n; ++r)
+      mbar_drain(smem_u32(&kv_full[r % NS]), (r / NS) & 1, until);
+  }
+}
+
+// The pool's codes as [page][head][slot][D], boxes of one page's (at most 128) slots by
+// 128 bytes (64).
+qz_status code_map(CUtensorMap *map, const int8_t *base, const PagedInt8View &c, int64_t token,
+                   int64_t head, int64_t page) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return QZ_ERR_CUDA;
+  // a dimension of one element has no stride of its own
+  if (c.hkv == 1) head = token;
+  if (c.n_pages == 1) page = token;
+  const cuuint64_t dim[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.hkv,
+                             (cuuint64_t)c.n_pages};
+  const cuuint64_t stride[3] = {(cuuint64_t)token, (cuuint64_t)head, (cuuint64_t)page};
+  const cuuint32_t box[4] = {(cuuint32_t)(c.D < 128 ? c.D : 128),
+                             (cuuint32_t)(c.page_size < kN ? c.page_size : kN), 1, 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<int8_t *>(base), dim, stride, box,
+         estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         c.D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? QZ_OK : QZ_ERR_UNSUPPORTED;
+}
+
+template <int D, int CAP>
+qz_status launch(const Attn8Params &p, int sms, cudaStream_t s) {
+  using C = Cfg8<D>;
+  const cudaError_t e = allow_smem<attn8_kernel<D, CAP>>(C::kSmem);
+  if (e != cudaSuccess) return cuda_status(e);
+  attn8_kernel<D, CAP><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, C::kSmem, s>>>(p);
+  return launch_status();
+}
+
+template <int D>
+qz_status launch_cap(const Attn8Params &p, int sms, cudaStream_t s) {
+  if (p.cap == 0.0f) return launch<D, 0>(p, sms, s);
+  return p.cap <= kShortCap ? launch<D, 1>(p, sms, s) : launch<D, 2>(p, sms, s);
+}
+
+}  // namespace
+
+qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
+                                const PagedInt8View &c, const SeqView &sv, float scale,
+                                float softcap, int64_t window, __half *out, int64_t o_token,
+                                int64_t o_head, void *workspace, cudaStream_t s) {
+  DeviceInfo di;
+  qz_status st = device_info(&di);
+  if (st != QZ_OK) return st;
+  Attn8Params p;
+  memset(&p, 0, sizeof(p));
+  st = code_map(&p.kmap, c.k, c, c.k_token, c.k_head, c.k_page);
+  if (st == QZ_OK) st = code_map(&p.vmap, c.v, c, c.v_token, c.v_head, c.v_page);
+  if (st != QZ_OK) return st;
+  p.ks = c.ks;
+  p.vs = c.vs;
+  p.ks_page = c.ks_page, p.ks_head = c.ks_head, p.ks_token = c.ks_token;
+  p.vs_page = c.vs_page, p.vs_head = c.vs_head, p.vs_token = c.vs_token;
+  p.q = q;
+  p.out = out;
+  p.q_token = q_token;
+  p.q_head = q_head;
+  p.o_token = o_token;
+  p.o_head = o_head;
+  set_heads(&p, hq, c.hkv);
+  p.n_pages = c.n_pages;
+  p.page_size = c.page_size;
+  p.page_shift = c.page_shift;
+  const float mag = scale == 0.0f ? 1.0f : fabsf(scale);
+  p.sign = scale == 0.0f ? 0.0f : scale < 0.0f ? -1.0f : 1.0f;
+  p.c = (softcap > 0.0f ? 1.0f : mag) * kLog2e;
+  p.cap = softcap;
+  p.mag = mag;
+  p.cap_t = softcap > 0.0f ? fminf(mag / softcap, FLT_MAX) : 0.0f;
+  p.cap_in = fminf(p.cap_t * 2.0f * kLog2e, FLT_MAX);
+  p.window = window > INT32_MAX ? 0 : (int)window;  // longer than any cache: none
+  p.s = sv;
+  p.cnt = static_cast<unsigned *>(workspace);
+  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + QZ_ATTENTION_SYNC_BYTES);
+  if (c.D == 256) return launch_cap<256>(p, di.sms, s);
+  return c.D == 128 ? launch_cap<128>(p, di.sms, s) : launch_cap<64>(p, di.sms, s);
+}
+
+qz_status read_attn8_error(int *code, int clear) {
+  return read_error_word(g_attn_error, code, clear);
+}
+
+}  // namespace qz

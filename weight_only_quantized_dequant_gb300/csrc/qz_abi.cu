@@ -273,6 +273,30 @@ qz_status paged_view(const qz_kv_cache *c, PagedView *v) {
   return QZ_OK;
 }
 
+qz_status paged_int8_view(const qz_kv_cache_int8 *c, PagedInt8View *v) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->n_pages < 1 || c->n_kv_heads < 1)
+    return QZ_ERR_INVALID_ARG;
+  if (c->head_dim < 1 || c->page_size < 1) return QZ_ERR_INVALID_ARG;
+  for (const int64_t s : {c->k_page, c->k_head, c->k_token, c->v_page, c->v_head, c->v_token}) {
+    if (s < 0) return QZ_ERR_INVALID_ARG;
+    if (s % 16) return QZ_ERR_ALIGNMENT;
+  }
+  for (const int64_t s :
+       {c->ks_page, c->ks_head, c->ks_token, c->vs_page, c->vs_head, c->vs_token})
+    if (s < 0) return QZ_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return QZ_ERR_ALIGNMENT;
+  if (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3u) return QZ_ERR_ALIGNMENT;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QZ_ERR_UNSUPPORTED;
+  const int64_t ps = c->page_size;
+  if (ps < 8 || ps > 256 || (ps & (ps - 1))) return QZ_ERR_UNSUPPORTED;
+  if (c->n_pages > INT32_MAX || c->n_kv_heads > 4096) return QZ_ERR_UNSUPPORTED;
+  *v = {c->k,       c->v,       c->k_scale,  c->v_scale, (int)c->n_pages, (int)ps,
+        __builtin_ctz((unsigned)ps), (int)c->n_kv_heads, (int)c->head_dim,
+        c->k_page,  c->k_head,  c->k_token,  c->v_page,  c->v_head,       c->v_token,
+        c->ks_page, c->ks_head, c->ks_token, c->vs_page, c->vs_head,      c->vs_token};
+  return QZ_OK;
+}
+
 qz_status seq_view(const qz_seq_batch *b, SeqView *v) {
   if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->ld_table < 0) return QZ_ERR_INVALID_ARG;
   if (b->n_tokens > 0 && b->n_seqs > 0) {
@@ -283,6 +307,50 @@ qz_status seq_view(const qz_seq_batch *b, SeqView *v) {
   if (b->n_seqs > kMaxSeqs || b->n_tokens > kMaxTokens || b->ld_table > INT32_MAX)
     return QZ_ERR_UNSUPPORTED;
   *v = {(int)b->n_seqs, b->n_tokens, b->cu_q, b->kv_len, b->page_table, b->ld_table};
+  return QZ_OK;
+}
+
+// Shared checks of the two appends; *run: whether there is anything to do.
+qz_status check_append(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                       const qz_half *k, int64_t k_token, int64_t k_head, const qz_half *v,
+                       int64_t v_token, int64_t v_head, const float *rope, int64_t rope_len,
+                       const SeqView &b, const qz_half *q_out, int64_t qo_token, int64_t qo_head,
+                       bool *run) {
+  *run = false;
+  if (rope && rope_len < 0) return QZ_ERR_INVALID_ARG;
+  if (rope && !aligned16(rope)) return QZ_ERR_ALIGNMENT;
+  if (q_out && !q) return QZ_ERR_INVALID_ARG;
+  if (rope && q && !q_out) return QZ_ERR_INVALID_ARG;
+  if (q_out && (n_heads < 1 || n_heads > 65536)) return QZ_ERR_INVALID_ARG;
+  if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
+  QZ_TRY(check_rows16(k, k_token, k_head));
+  QZ_TRY(check_rows16(v, v_token, v_head));
+  if (q_out) {
+    QZ_TRY(check_rows16(q, q_token, q_head));
+    QZ_TRY(check_rows16(q_out, qo_token, qo_head));
+  }
+  *run = true;
+  return QZ_OK;
+}
+
+// Shared checks of the two attentions.
+qz_status check_attention(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                          int hkv, int D, const SeqView &b, float scale, float softcap,
+                          int64_t window, const qz_half *out, int64_t o_token, int64_t o_head,
+                          const void *workspace, size_t workspace_bytes, bool *run) {
+  *run = false;
+  if (n_heads < 1 || n_heads % hkv || window < 0 || !(softcap >= 0.0f) ||
+      !(scale - scale == 0.0f) || !(softcap - softcap == 0.0f))
+    return QZ_ERR_INVALID_ARG;
+  if (n_heads > 65536 || b.n_tokens * n_heads > INT32_MAX) return QZ_ERR_UNSUPPORTED;
+  if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
+  QZ_TRY(check_rows16(q, q_token, q_head));
+  QZ_TRY(check_rows16(out, o_token, o_head));
+  if (!workspace ||
+      workspace_bytes < attention_workspace_bytes(b.n_tokens, b.n_seqs, n_heads, hkv, D))
+    return QZ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return QZ_ERR_ALIGNMENT;
+  *run = true;
   return QZ_OK;
 }
 
@@ -357,7 +425,10 @@ qz_status qz_device_error(int *code, int clear) {
   QZ_TRY(read_rope_error(&e, clear));
   QZ_TRY(read_attn_error(&f, clear));
   QZ_TRY(read_lora_error(&g, clear));
-  *code = a | b | c | d | e | f | g;
+  int h = 0, i = 0;
+  QZ_TRY(read_cache8_error(&h, clear));
+  QZ_TRY(read_attn8_error(&i, clear));
+  *code = a | b | c | d | e | f | g | h | i;
   return QZ_OK;
 }
 
@@ -658,18 +729,10 @@ qz_status qz_rope_append(const qz_half *q, int64_t n_heads, int64_t q_token, int
   SeqView b;
   QZ_TRY(paged_view(cache, &c));
   QZ_TRY(seq_view(seqs, &b));
-  if (rope && rope_len < 0) return QZ_ERR_INVALID_ARG;
-  if (rope && !aligned16(rope)) return QZ_ERR_ALIGNMENT;
-  if (q_out && !q) return QZ_ERR_INVALID_ARG;
-  if (rope && q && !q_out) return QZ_ERR_INVALID_ARG;
-  if (q_out && (n_heads < 1 || n_heads > 65536)) return QZ_ERR_INVALID_ARG;
-  if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
-  QZ_TRY(check_rows16(k, k_token, k_head));
-  QZ_TRY(check_rows16(v, v_token, v_head));
-  if (q_out) {
-    QZ_TRY(check_rows16(q, q_token, q_head));
-    QZ_TRY(check_rows16(q_out, qo_token, qo_head));
-  }
+  bool run;
+  QZ_TRY(check_append(q, n_heads, q_token, q_head, k, k_token, k_head, v, v_token, v_head, rope,
+                      rope_len, b, q_out, qo_token, qo_head, &run));
+  if (!run) return QZ_OK;
   return launch_rope_append(
       reinterpret_cast<const __half *>(q), n_heads, q_token, q_head,
       reinterpret_cast<const __half *>(k), k_token, k_head, reinterpret_cast<const __half *>(v),
@@ -695,20 +758,66 @@ qz_status qz_attention_paged(const qz_half *q, int64_t n_heads, int64_t q_token,
   SeqView b;
   QZ_TRY(paged_view(cache, &c));
   QZ_TRY(seq_view(seqs, &b));
-  if (n_heads < 1 || n_heads % c.hkv || window < 0 || !(softcap >= 0.0f) ||
-      !(scale - scale == 0.0f) || !(softcap - softcap == 0.0f))
-    return QZ_ERR_INVALID_ARG;
-  if (n_heads > 65536 || b.n_tokens * n_heads > INT32_MAX) return QZ_ERR_UNSUPPORTED;
-  if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
-  QZ_TRY(check_rows16(q, q_token, q_head));
-  QZ_TRY(check_rows16(out, o_token, o_head));
-  if (!workspace ||
-      workspace_bytes < attention_workspace_bytes(b.n_tokens, b.n_seqs, n_heads, c.hkv, c.D))
-    return QZ_ERR_INVALID_ARG;
-  if (!aligned16(workspace)) return QZ_ERR_ALIGNMENT;
+  bool run;
+  QZ_TRY(check_attention(q, n_heads, q_token, q_head, c.hkv, c.D, b, scale, softcap, window, out,
+                         o_token, o_head, workspace, workspace_bytes, &run));
+  if (!run) return QZ_OK;
   return launch_attention(reinterpret_cast<const __half *>(q), n_heads, q_token, q_head, c, b,
                           scale, softcap, window, reinterpret_cast<__half *>(out), o_token, o_head,
                           workspace, (cudaStream_t)s);
+}
+
+qz_status qz_rope_append_int8(const qz_half *q, int64_t n_heads, int64_t q_token, int64_t q_head,
+                              const qz_half *k, int64_t k_token, int64_t k_head,
+                              const qz_half *v, int64_t v_token, int64_t v_head,
+                              const float *rope, int64_t rope_len,
+                              const qz_kv_cache_int8 *cache, const qz_seq_batch *seqs,
+                              qz_half *q_out, int64_t qo_token, int64_t qo_head, qz_stream s) {
+  PagedInt8View c;
+  SeqView b;
+  QZ_TRY(paged_int8_view(cache, &c));
+  QZ_TRY(seq_view(seqs, &b));
+  bool run;
+  QZ_TRY(check_append(q, n_heads, q_token, q_head, k, k_token, k_head, v, v_token, v_head, rope,
+                      rope_len, b, q_out, qo_token, qo_head, &run));
+  if (!run) return QZ_OK;
+  return launch_rope_append_int8(
+      reinterpret_cast<const __half *>(q), n_heads, q_token, q_head,
+      reinterpret_cast<const __half *>(k), k_token, k_head, reinterpret_cast<const __half *>(v),
+      v_token, v_head, rope, rope_len, c, b, reinterpret_cast<__half *>(q_out), qo_token, qo_head,
+      (cudaStream_t)s);
+}
+
+qz_status qz_cache_read_int8(const qz_kv_cache_int8 *cache, const qz_seq_batch *seqs, qz_half *k,
+                             int64_t k_token, int64_t k_head, qz_half *v, int64_t v_token,
+                             int64_t v_head, qz_stream s) {
+  PagedInt8View c;
+  SeqView b;
+  QZ_TRY(paged_int8_view(cache, &c));
+  QZ_TRY(seq_view(seqs, &b));
+  if (b.n_tokens == 0 || b.n_seqs == 0) return QZ_OK;
+  QZ_TRY(check_rows16(k, k_token, k_head));
+  QZ_TRY(check_rows16(v, v_token, v_head));
+  return launch_cache_read_int8(c, b, reinterpret_cast<__half *>(k), k_token, k_head,
+                                reinterpret_cast<__half *>(v), v_token, v_head, (cudaStream_t)s);
+}
+
+qz_status qz_attention_paged_int8(const qz_half *q, int64_t n_heads, int64_t q_token,
+                                  int64_t q_head, const qz_kv_cache_int8 *cache,
+                                  const qz_seq_batch *seqs, float scale, float softcap,
+                                  int64_t window, qz_half *out, int64_t o_token, int64_t o_head,
+                                  void *workspace, size_t workspace_bytes, qz_stream s) {
+  PagedInt8View c;
+  SeqView b;
+  QZ_TRY(paged_int8_view(cache, &c));
+  QZ_TRY(seq_view(seqs, &b));
+  bool run;
+  QZ_TRY(check_attention(q, n_heads, q_token, q_head, c.hkv, c.D, b, scale, softcap, window, out,
+                         o_token, o_head, workspace, workspace_bytes, &run));
+  if (!run) return QZ_OK;
+  return launch_attention_int8(reinterpret_cast<const __half *>(q), n_heads, q_token, q_head, c, b,
+                               scale, softcap, window, reinterpret_cast<__half *>(out), o_token,
+                               o_head, workspace, (cudaStream_t)s);
 }
 
 size_t qz_lora_workspace_bytes(int64_t T, int64_t K, int64_t R) {
@@ -743,6 +852,22 @@ qz_status qz_lora(const qz_lora_adapters *ad, const int32_t *index, int64_t T, c
   return launch_lora(*ad, index, T, reinterpret_cast<const __half *>(x), T > 1 ? ldx : 0,
                      reinterpret_cast<const __half *>(y), T > 1 ? ldy : 0,
                      reinterpret_cast<__half *>(out), T > 1 ? ldo : 0, workspace, (cudaStream_t)s);
+}
+
+qz_status qz_sample(const void *logits, int dtype, int64_t B, int64_t V, int64_t ld,
+                    const float *u, const qz_sampling *options, int32_t *token, float *logprob,
+                    qz_stream s) {
+  if (B < 0 || V < 1 || !options || dtype < QZ_FP16 || dtype > QZ_FP32) return QZ_ERR_INVALID_ARG;
+  if (V > QZ_MAX_VOCAB || B > kMaxTokens) return QZ_ERR_UNSUPPORTED;
+  if (B == 0) return QZ_OK;
+  if (!logits || !u || !token || (B > 1 && ld < V)) return QZ_ERR_INVALID_ARG;
+  const qz_sampling &o = *options;
+  if ((uintptr_t)logits & (dtype == QZ_FP32 ? 3u : 1u)) return QZ_ERR_ALIGNMENT;
+  for (const void *p : {(const void *)u, (const void *)o.temperature, (const void *)o.top_k,
+                        (const void *)o.top_p, (const void *)o.min_p, (const void *)token,
+                        (const void *)logprob})
+    if ((uintptr_t)p & 3u) return QZ_ERR_ALIGNMENT;
+  return launch_sample(logits, dtype, B > 1 ? ld : 0, B, V, u, o, token, logprob, (cudaStream_t)s);
 }
 
 }  // extern "C"

@@ -152,6 +152,7 @@ __device__ __forceinline__ uint32_t f2h(float a, float b) {
 }
 
 struct PagedView;  // seq_batch.cuh
+struct PagedInt8View;
 struct SeqView;
 qz_status launch_rmsnorm(const __half *x, int64_t ldx, const __half *r, int64_t ldr,
                          const __half *w, float bias, float eps, int64_t T, int64_t K, __half *y,
@@ -172,6 +173,24 @@ size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t R);
 qz_status launch_lora(const qz_lora_adapters &ad, const int32_t *index, int64_t T, const __half *x,
                       int64_t ldx, const __half *y, int64_t ldy, __half *out, int64_t ldo,
                       void *workspace, cudaStream_t s);
+qz_status launch_rope_append_int8(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
+                                  const __half *k, int64_t k_token, int64_t k_head,
+                                  const __half *v, int64_t v_token, int64_t v_head,
+                                  const float *rope, int64_t rope_len, const PagedInt8View &c,
+                                  const SeqView &sv, __half *qo, int64_t qo_token,
+                                  int64_t qo_head, cudaStream_t s);
+qz_status launch_cache_read_int8(const PagedInt8View &c, const SeqView &sv, __half *k,
+                                 int64_t k_token, int64_t k_head, __half *v, int64_t v_token,
+                                 int64_t v_head, cudaStream_t s);
+qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
+                                const PagedInt8View &c, const SeqView &sv, float scale,
+                                float softcap, int64_t window, __half *out, int64_t o_token,
+                                int64_t o_head, void *workspace, cudaStream_t s);
+qz_status launch_sample(const void *logits, int dtype, int64_t ld, int64_t B, int64_t V,
+                        const float *u, const qz_sampling &o, int32_t *token, float *logprob,
+                        cudaStream_t s);
+qz_status read_cache8_error(int *code, int clear);
+qz_status read_attn8_error(int *code, int clear);
 qz_status read_rope_error(int *code, int clear);
 qz_status read_attn_error(int *code, int clear);
 qz_status read_lora_error(int *code, int clear);

@@ -12,6 +12,15 @@ struct PagedView {
   int64_t k_page, k_head, k_token, v_page, v_head, v_token;
 };
 
+// The same with rows of INT8 codes and one fp32 scale a row.
+struct PagedInt8View {
+  int8_t *k, *v;
+  float *ks, *vs;
+  int n_pages, page_size, page_shift, hkv, D;
+  int64_t k_page, k_head, k_token, v_page, v_head, v_token;          // codes
+  int64_t ks_page, ks_head, ks_token, vs_page, vs_head, vs_token;    // scales
+};
+
 struct SeqView {
   int n_seqs;
   int64_t n_tokens;

@@ -1,7 +1,9 @@
 """The steps of a decoder layer around its quantized products, as thin calls
 of the library (include/qz.h, "Layer glue for serving"): ``rmsnorm`` and
 ``rmsnorm_int8``, ``rope_append`` and ``attention_paged`` over a ``PagedKV``
-cache, and ``lora`` for the low-rank adapters beside a shared projection.
+(fp16) or ``PagedKVInt8`` cache, ``cache_read`` of the latter, ``lora`` for the
+low-rank adapters beside a shared projection, and ``sample`` for the choice of
+the next tokens from their logits.
 
 Every function takes ``stream`` (default: the current one); outputs and
 workspaces that a call allocates belong to that stream.  All tensors of a call
@@ -221,6 +223,53 @@ class PagedKV:
 
 
 @dataclass(frozen=True)
+class PagedKVInt8:
+    """A paged key/value cache of INT8 rows: k and v int8 codes [n_pages, n_kv_heads,
+    page_size, head_dim] with contiguous head_dim and other strides that are
+    multiples of 16, k_scale and v_scale fp32 [n_pages, n_kv_heads, page_size] with
+    any strides; a row stands for its codes times its scale."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    _arg: object = field(default=None, repr=False, compare=False)
+
+    def __post_init__(self):
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        _cuda_or_raise(k)
+        dev = k.get_device()
+        for t, what in ((v, "v"), (ks, "k_scale"), (vs, "v_scale")):
+            _place_or_raise(t, what, dev)
+        _need(k.dtype == torch.int8 and v.dtype == torch.int8 and k.dim() == 4
+              and k.shape == v.shape, "k and v: int8 [n_pages, n_kv_heads, page_size, head_dim]")
+        _need(k.stride(3) == 1 and v.stride(3) == 1, "k and v: contiguous head_dim")
+        _need(ks.dtype == _F32 and vs.dtype == _F32 and ks.shape == k.shape[:3]
+              and vs.shape == k.shape[:3],
+              "k_scale and v_scale: fp32 [n_pages, n_kv_heads, page_size]")
+        pages, heads, size, D = k.shape  # a single page, head or token has no stride of its own
+        st = [[s if n > 1 else least for s, n in zip(t.stride(), k.shape[:3])]
+              for t, least in ((k, D), (v, D), (ks, 1), (vs, 1))]
+        arg = _lib.KvCacheInt8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages,
+                               size, heads, D, *st[0], *st[1], *st[2], *st[3])
+        _set(self, _arg=arg, _ref=ctypes.byref(arg), shape=tuple(k.shape), device_index=dev)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
+              device="cuda") -> "PagedKVInt8":
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        return cls(*(torch.empty(shape, dtype=torch.int8, device=device) for _ in range(2)),
+                   *(torch.empty(shape[:3], dtype=_F32, device=device) for _ in range(2)))
+
+    @property
+    def n_kv_heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3]
+
+
+@dataclass(frozen=True)
 class SeqBatch:
     """The sequences of a step: cu_q int32 [S+1] (rows cu_q[i]..cu_q[i+1]-1 are
     the new tokens of sequence i), kv_len int32 [S] (tokens held, the new ones
@@ -266,12 +315,13 @@ def _heads(t: torch.Tensor, what: str, dev: int, T: int, heads: int, D: int):
                      f"{(T, heads, D)} with contiguous rows is needed")
 
 
-def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKV,
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKV | PagedKVInt8,
                 seqs: SeqBatch, rope: torch.Tensor | None, q_out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """Rotate the new queries q [T, heads, D] (returned, in q_out; may be q) and
     keys k [T, kv_heads, D] by their positions, and store keys and values v
-    into their slots of the cache.  rope: fp32 [positions, D], cosines then
+    into their slots of the cache (as INT8 rows in a PagedKVInt8: scale = max|x| /
+    127, code = round(x / scale)).  rope: fp32 [positions, D], cosines then
     sines (``rope_table``), or None for no rotation."""
     _need(q.dim() == 3, "q: three dimensions are needed")
     T, H, _ = q.shape
@@ -295,12 +345,39 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedK
         q_out, ot, oh = _empty((T, H, D), _F16, q.device, stream), H * D, D
     else:
         ot, oh = _heads(q_out, "q_out", dev, T, H, D)
-    st = _lib.load().qz_rope_append(q.data_ptr(), H, qt, qh, k.data_ptr(), kt, kh, v.data_ptr(),
-                                    vt, vh, rp, n, cache._ref, seqs._ref(T), q_out.data_ptr(), ot,
-                                    oh, _stream_of(dev, stream))
+    lib = _lib.load()
+    name = "qz_rope_append" if type(cache) is PagedKV else "qz_rope_append_int8"
+    st = getattr(lib, name)(q.data_ptr(), H, qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                            rp, n, cache._ref, seqs._ref(T), q_out.data_ptr(), ot, oh,
+                            _stream_of(dev, stream))
     if st:
-        _lib.fail("qz_rope_append", st)
+        _lib.fail(name, st)
     return q_out
+
+
+def cache_read(cache: PagedKVInt8, seqs: SeqBatch, n_tokens: int, k: torch.Tensor | None = None,
+               v: torch.Tensor | None = None, stream=None):
+    """(k, v): the cache's rows of the n_tokens tokens that seqs describes, as fp16
+    [n_tokens, kv_heads, D] (codes times scales).  The sequences of a step give its
+    new tokens; with cu_q the running sums of kv_len, all that is held."""
+    _need(isinstance(cache, PagedKVInt8), "cache: a PagedKVInt8 is needed")
+    _, hkv, _, D = cache.shape
+    dev = _device(cache.k, "cache")
+    if seqs.device_index != dev:
+        _far(seqs, "seqs", dev)
+    _need(n_tokens >= 0, "n_tokens: negative")
+    shape = (n_tokens, hkv, D)
+    if k is None:
+        k = _empty(shape, _F16, cache.k.device, stream)
+    if v is None:
+        v = _empty(shape, _F16, cache.k.device, stream)
+    kt, kh = _heads(k, "k", dev, *shape)
+    vt, vh = _heads(v, "v", dev, *shape)
+    st = _lib.load().qz_cache_read_int8(cache._ref, seqs._ref(n_tokens), k.data_ptr(), kt, kh,
+                                        v.data_ptr(), vt, vh, _stream_of(dev, stream))
+    if st:
+        _lib.fail("qz_cache_read_int8", st)
+    return k, v
 
 
 def rope_table(positions: int, head_dim: int, theta: float = 10000.0,
@@ -326,9 +403,10 @@ def attention_workspace(n_tokens: int, n_seqs: int, n_heads: int, n_kv_heads: in
     return ws
 
 
-def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: float | None = None,
-                    softcap: float = 0.0, window: int = 0, out: torch.Tensor | None = None,
-                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+def attention_paged(q: torch.Tensor, cache: PagedKV | PagedKVInt8, seqs: SeqBatch,
+                    scale: float | None = None, softcap: float = 0.0, window: int = 0,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
     """Causal attention of the new tokens q [T, heads, D] over the cache, which
     already holds their keys and values (``rope_append``).  scale defaults to
     D^-0.5; softcap > 0 caps logits as softcap * tanh(x / softcap); window > 0
@@ -352,12 +430,13 @@ def attention_paged(q: torch.Tensor, cache: PagedKV, seqs: SeqBatch, scale: floa
     if workspace is None:
         workspace = attention_workspace(T, seqs.n_seqs, H, hkv, D, q.device, stream)
     nbytes = _space(workspace, dev)
-    st = _lib.load().qz_attention_paged(q.data_ptr(), H, qt, qh, cache._ref, seqs._ref(T),
-                                        D ** -0.5 if scale is None else scale, softcap, window,
-                                        out.data_ptr(), ot, oh, workspace.data_ptr(),
-                                        nbytes, _stream_of(dev, stream))
+    lib = _lib.load()
+    name = "qz_attention_paged" if type(cache) is PagedKV else "qz_attention_paged_int8"
+    st = getattr(lib, name)(q.data_ptr(), H, qt, qh, cache._ref, seqs._ref(T),
+                            D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
+                            ot, oh, workspace.data_ptr(), nbytes, _stream_of(dev, stream))
     if st:
-        _lib.fail("qz_attention_paged", st)
+        _lib.fail(name, st)
     return out
 
 
@@ -438,3 +517,49 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters, index: torch.
     if st:
         _lib.fail("qz_lora", st)
     return out
+
+
+# ---------------------------------------------------------------- sample ---
+_LOGITS = {_F16: 0, torch.bfloat16: 1, _F32: 2}
+
+
+def _option(v, what: str, dev: int, B: int, dtype):
+    """(address, value) of an option of every row, or of all."""
+    if isinstance(v, torch.Tensor):
+        return _vec(v, what, dev, B, dtype), 0
+    return None, v
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           out: torch.Tensor | None = None, logprob: torch.Tensor | None = None, stream=None):
+    """(tokens, logprob): a token int32 [B] for every row of logits [B, V] (fp16, bf16
+    or fp32), the first whose running probability, by index, exceeds u (fp32 [B], in
+    [0, 1)), and the logarithm of its probability.  Probabilities are those of
+    softmax(logits / temperature) with the top_k largest kept (0: all), of those the
+    fewest of probability top_p together, of those the ones with at least min_p of the
+    largest.  temperature 0 takes the largest logit.  Every option is a number or a
+    tensor [B] (fp32; top_k int32).  A row without a logit above -inf gives token -1."""
+    _need(logits.dim() == 2, "logits: two dimensions are needed")
+    B, V = logits.shape
+    dev = _device(logits, "logits")
+    kind = _LOGITS.get(logits.dtype)
+    _need(kind is not None, "logits: fp16, bf16 or fp32 is needed")
+    _need(V >= 1, "logits: a vocabulary is needed")
+    ld = _rows(logits, "logits", dev, (B, V), logits.dtype)
+    up = _vec(u, "u", dev, B, _F32)
+    t, t_all = _option(temperature, "temperature", dev, B, _F32)
+    k, k_all = _option(top_k, "top_k", dev, B, _I32)
+    p, p_all = _option(top_p, "top_p", dev, B, _F32)
+    m, m_all = _option(min_p, "min_p", dev, B, _F32)
+    _need(-2 ** 31 <= k_all < 2 ** 31, "top_k: 32 bits")
+    if out is None:
+        out = _empty((B,), _I32, logits.device, stream)
+    if logprob is None:
+        logprob = _empty((B,), _F32, logits.device, stream)
+    op, lp = _vec(out, "out", dev, B, _I32), _vec(logprob, "logprob", dev, B, _F32)
+    opts = _lib.Sampling(t, k, p, m, t_all, k_all, p_all, m_all)
+    st = _lib.load().qz_sample(logits.data_ptr(), kind, B, V, ld, up, ctypes.byref(opts), op, lp,
+                               _stream_of(dev, stream))
+    if st:
+        _lib.fail("qz_sample", st)
+    return out, logprob
