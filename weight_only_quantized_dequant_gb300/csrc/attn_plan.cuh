@@ -5,6 +5,8 @@
 
 #include <cuda.h>
 
+#include <cfloat>
+#include <cmath>
 #include <mutex>
 
 #include "seq_batch.cuh"
@@ -59,6 +61,17 @@ struct CapParams {
   float cap, cap_in;  // softcap, and |scale| / softcap * 2 log2(e)
   float mag, cap_t;   // |scale|, and |scale| / softcap
 };
+// Sets them; returns what turns logits into powers of two: |scale| log2(e) of a product,
+// log2(e) of a capped logit.
+inline float set_logits(CapParams *p, float scale, float softcap) {
+  const float mag = scale == 0.0f ? 1.0f : fabsf(scale);
+  p->cap = softcap;
+  // (finite for the smallest caps: a logit of 0 stays 0, the others reach the cap all the same)
+  p->mag = mag;
+  p->cap_t = softcap > 0.0f ? fminf(mag / softcap, FLT_MAX) : 0.0f;
+  p->cap_in = fminf(p->cap_t * 2.0f * kLog2e, FLT_MAX);
+  return (softcap > 0.0f ? 1.0f : mag) * kLog2e;
+}
 
 // ------------------------------------------------------------ PTX pieces --
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -138,6 +151,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
@@ -145,6 +166,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+// Two bytes of codes + 128 (chosen by sel, under the bits of 1024) as fp16 codes.
+__device__ __forceinline__ uint32_t code_pair(uint32_t biased, uint32_t sel) {
+  const uint32_t v = __byte_perm(biased, 0x64646464u, sel);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&v),
+                            __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 // c ? a : b, both formed: a branch for each of a thread's 128 logits costs more.
 __device__ __forceinline__ float pick(bool c, float a, float b) {
@@ -448,6 +476,29 @@ EncodeTiledFn encode_tiled() {
       fn = reinterpret_cast<EncodeTiledFn>(f);
   });
   return fn;
+}
+
+// The pool's codes as [page][head][slot][D], boxes of one page's (at most 128) slots by
+// 128 bytes (64).
+qz_status code_map(CUtensorMap *map, const int8_t *base, const PagedInt8View &c, int64_t token,
+                   int64_t head, int64_t page) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return QZ_ERR_CUDA;
+  // a dimension of one element has no stride of its own
+  if (c.hkv == 1) head = token;
+  if (c.n_pages == 1) page = token;
+  const cuuint64_t dim[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.hkv,
+                             (cuuint64_t)c.n_pages};
+  const cuuint64_t stride[3] = {(cuuint64_t)token, (cuuint64_t)head, (cuuint64_t)page};
+  const cuuint32_t box[4] = {(cuuint32_t)(c.D < 128 ? c.D : 128),
+                             (cuuint32_t)(c.page_size < kN ? c.page_size : kN), 1, 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<int8_t *>(base), dim, stride, box,
+         estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         c.D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? QZ_OK : QZ_ERR_UNSUPPORTED;
 }
 
 }  // namespace

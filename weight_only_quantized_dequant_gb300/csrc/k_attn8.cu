@@ -21,8 +21,6 @@
 //  * Weights are rounded to fp16 once, with vs_j in them: 2^6 e^{x - m} vs_j 2^-E,
 //    where m lags the maximum by up to 2^8 and 2^E the largest vs by up to 2.
 //  * The split of (tile, key block) units between CTAs is that of the fp16 kernel.
-#include <cfloat>
-#include <cmath>
 #include <cstring>
 
 #include "attn_plan.cuh"
@@ -81,13 +79,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ float2 lds64f(uint32_t a) {
   const uint2 v = lds64(a);
   return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-}
-// Two bytes of codes + 128 (chosen by sel, under the bits of 1024) as fp16 codes.
-__device__ __forceinline__ uint32_t code_pair(uint32_t biased, uint32_t sel) {
-  const uint32_t v = __byte_perm(biased, 0x64646464u, sel);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&v),
-                            __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t *>(&r);
 }
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -612,29 +603,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
   }
 }
 
-// The pool's codes as [page][head][slot][D], boxes of one page's (at most 128) slots by
-// 128 bytes (64).
-qz_status code_map(CUtensorMap *map, const int8_t *base, const PagedInt8View &c, int64_t token,
-                   int64_t head, int64_t page) {
-  EncodeTiledFn fn = encode_tiled();
-  if (!fn) return QZ_ERR_CUDA;
-  // a dimension of one element has no stride of its own
-  if (c.hkv == 1) head = token;
-  if (c.n_pages == 1) page = token;
-  const cuuint64_t dim[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.hkv,
-                             (cuuint64_t)c.n_pages};
-  const cuuint64_t stride[3] = {(cuuint64_t)token, (cuuint64_t)head, (cuuint64_t)page};
-  const cuuint32_t box[4] = {(cuuint32_t)(c.D < 128 ? c.D : 128),
-                             (cuuint32_t)(c.page_size < kN ? c.page_size : kN), 1, 1};
-  const cuuint32_t estride[4] = {1, 1, 1, 1};
-  const CUresult r =
-      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<int8_t *>(base), dim, stride, box,
-         estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         c.D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? QZ_OK : QZ_ERR_UNSUPPORTED;
-}
-
 template <int D, int CAP>
 qz_status launch(const Attn8Params &p, int sms, cudaStream_t s) {
   using C = Cfg8<D>;
@@ -656,6 +624,9 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
                                 const PagedInt8View &c, const SeqView &sv, float scale,
                                 float softcap, int64_t window, __half *out, int64_t o_token,
                                 int64_t o_head, void *workspace, cudaStream_t s) {
+  if (sv.n_tokens * (hq / c.hkv) > (int64_t)kM * sv.n_seqs)
+    return launch_attention_int8_tc(q, hq, q_token, q_head, c, sv, scale, softcap, window, out,
+                                    o_token, o_head, workspace, s);
   DeviceInfo di;
   qz_status st = device_info(&di);
   if (st != QZ_OK) return st;
@@ -678,13 +649,8 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
   p.n_pages = c.n_pages;
   p.page_size = c.page_size;
   p.page_shift = c.page_shift;
-  const float mag = scale == 0.0f ? 1.0f : fabsf(scale);
   p.sign = scale == 0.0f ? 0.0f : scale < 0.0f ? -1.0f : 1.0f;
-  p.c = (softcap > 0.0f ? 1.0f : mag) * kLog2e;
-  p.cap = softcap;
-  p.mag = mag;
-  p.cap_t = softcap > 0.0f ? fminf(mag / softcap, FLT_MAX) : 0.0f;
-  p.cap_in = fminf(p.cap_t * 2.0f * kLog2e, FLT_MAX);
+  p.c = set_logits(&p, scale, softcap);
   p.window = window > INT32_MAX ? 0 : (int)window;  // longer than any cache: none
   p.s = sv;
   p.cnt = static_cast<unsigned *>(workspace);

@@ -1,0 +1,48 @@
+// Attention over the paged cache of INT8 rows on the 5th-generation tensor cores: the
+// kernel of k_attn.cu for steps that bring more rows to a KV head than one warp's
+// operand (chunks and prompts).
+//
+// Codes arrive by TMA in half of a slot; four warps turn them into fp16 where they lie,
+// so that the products, their order and the softmax are the fp16 kernel's.  Keys' scales
+// multiply the logits and values' scales the weights, in fp32: scaled rows in fp16 would
+// save the softmax a multiplication or two and cost a rounding of every key and value.
+// A weight enters the product as 2^6 e^{x - m} vs_j 2^-E: 32 keys at a time have their
+// scales in units of 2^e, E lags their largest as m lags the largest logit, and O is
+// rescaled for both at once.
+#include "attn_tc.cuh"
+
+namespace qz {
+
+qz_status launch_attention_int8_tc(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
+                                   const PagedInt8View &c, const SeqView &sv, float scale,
+                                   float softcap, int64_t window, __half *out, int64_t o_token,
+                                   int64_t o_head, void *workspace, cudaStream_t s) {
+  DeviceInfo di;
+  qz_status st = device_info(&di);
+  if (st != QZ_OK) return st;
+  AttnParams p;
+  memset(&p, 0, sizeof(p));
+  st = code_map(&p.kmap, c.k, c, c.k_token, c.k_head, c.k_page);
+  if (st == QZ_OK) st = code_map(&p.vmap, c.v, c, c.v_token, c.v_head, c.v_page);
+  if (st != QZ_OK) return st;
+  set_call(&p, q, hq, q_token, q_head, c.hkv, c.n_pages, c.page_size, c.page_shift, sv, scale,
+           softcap, window, out, o_token, o_head, workspace);
+  p.ks = c.ks;
+  p.vs = c.vs;
+  p.ks_page = c.ks_page, p.ks_head = c.ks_head, p.ks_token = c.ks_token;
+  p.vs_page = c.vs_page, p.vs_head = c.vs_head, p.vs_token = c.vs_token;
+  // (as over fp16 rows)
+  const bool two = c.D < 256 && sv.n_tokens * p.G > (int64_t)128 * sv.n_seqs;
+  p.q_boxes = scale > 0.0f && query_map(&p.qmap, q, sv.n_tokens, hq, c.D, q_token, q_head, p.G,
+                                        two ? 128 : 64);
+  if (c.D == 256) return launch_cap<256, 1, true>(p, di.sms, s);
+  if (c.D == 128)
+    return two ? launch_cap<128, 2, true>(p, di.sms, s) : launch_cap<128, 1, true>(p, di.sms, s);
+  return two ? launch_cap<64, 2, true>(p, di.sms, s) : launch_cap<64, 1, true>(p, di.sms, s);
+}
+
+qz_status read_attn8_tc_error(int *code, int clear) {
+  return read_error_word(g_attn_error, code, clear);
+}
+
+}  // namespace qz

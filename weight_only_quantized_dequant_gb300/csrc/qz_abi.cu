@@ -425,10 +425,11 @@ qz_status qz_device_error(int *code, int clear) {
   QZ_TRY(read_rope_error(&e, clear));
   QZ_TRY(read_attn_error(&f, clear));
   QZ_TRY(read_lora_error(&g, clear));
-  int h = 0, i = 0;
+  int h = 0, i = 0, j = 0;
   QZ_TRY(read_cache8_error(&h, clear));
   QZ_TRY(read_attn8_error(&i, clear));
-  *code = a | b | c | d | e | f | g | h | i;
+  QZ_TRY(read_attn8_tc_error(&j, clear));
+  *code = a | b | c | d | e | f | g | h | i | j;
   return QZ_OK;
 }
 

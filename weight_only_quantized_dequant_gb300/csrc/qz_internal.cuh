@@ -186,11 +186,16 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
                                 const PagedInt8View &c, const SeqView &sv, float scale,
                                 float softcap, int64_t window, __half *out, int64_t o_token,
                                 int64_t o_head, void *workspace, cudaStream_t s);
+qz_status launch_attention_int8_tc(const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
+                                   const PagedInt8View &c, const SeqView &sv, float scale,
+                                   float softcap, int64_t window, __half *out, int64_t o_token,
+                                   int64_t o_head, void *workspace, cudaStream_t s);
 qz_status launch_sample(const void *logits, int dtype, int64_t ld, int64_t B, int64_t V,
                         const float *u, const qz_sampling &o, int32_t *token, float *logprob,
                         cudaStream_t s);
 qz_status read_cache8_error(int *code, int clear);
 qz_status read_attn8_error(int *code, int clear);
+qz_status read_attn8_tc_error(int *code, int clear);
 qz_status read_rope_error(int *code, int clear);
 qz_status read_attn_error(int *code, int clear);
 qz_status read_lora_error(int *code, int clear);
