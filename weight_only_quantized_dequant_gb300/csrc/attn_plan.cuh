@@ -73,6 +73,14 @@ inline float set_logits(CapParams *p, float scale, float softcap) {
   return (softcap > 0.0f ? 1.0f : mag) * kLog2e;
 }
 
+// The pages of a cache, and the scales of an INT8 cache (strides in floats).
+struct ScaleParams {
+  int n_pages, page_size, page_shift;
+  int runs;  // a page's scales are contiguous, and its and its heads' places 16-byte aligned
+  const float *ks, *vs;
+  int64_t ks_page, ks_head, ks_token, vs_page, vs_head, vs_token;
+};
+
 // ------------------------------------------------------------ PTX pieces --
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -363,6 +371,53 @@ struct Walker {
   }
 };
 
+// The scales of a block's 128 rows of an INT8 cache to dst (whole warp; lane i has the
+// block's i-th page, INT32_MAX where the pool has no such page, negative where no row is
+// needed).  Where a page's scales are whole 16-byte pieces (p.runs) each page is one bulk
+// copy, `scale_runs` bytes in all for the barrier, and `scale_zeros` comes before the
+// barrier's arrival; else four a lane by copies that the caller lets arrive there, zeros
+// where no row of the tile sees the key or it has no page.
+__device__ __forceinline__ bool in_pool(const ScaleParams &p, int page) {
+  return page >= 0 && page < p.n_pages;
+}
+__device__ __forceinline__ uint32_t scale_runs(const ScaleParams &p, int page) {
+  return p.runs ? __popc(__ballot_sync(0xffffffffu, in_pool(p, page))) * min(p.page_size, kN) * 4
+                : 0;
+}
+__device__ __forceinline__ void scale_zeros(const ScaleParams &p, float *dst, int page) {
+  const int n = min(p.page_size, kN), lane = threadIdx.x & 31;
+  if (p.runs && page >= p.n_pages)
+    for (int i = 0; i < n; ++i) dst[lane * n + i] = 0.0f;
+}
+__device__ __forceinline__ void scale_copy(const ScaleParams &p, const float *sc, int64_t sc_page,
+                                           int64_t sc_head, int64_t sc_token, float *dst,
+                                           const Seg &g, int b, int page, uint32_t bar) {
+  const int lane = threadIdx.x & 31;
+  if (p.runs) {
+    const int n = min(p.page_size, kN);
+    if (in_pool(p, page)) {
+      const float *src = sc + page * sc_page + g.head * sc_head + ((b * kN) & (p.page_size - 1));
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+          ::"r"(smem_u32(dst + lane * n)), "l"(src), "r"(n * 4), "r"(bar)
+          : "memory");
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = lane + 32 * i;
+    const int64_t key = (int64_t)b * kN + k;
+    const int pg = __shfl_sync(0xffffffffu, page, k >> min(p.page_shift, 7));
+    const bool use = in_pool(p, pg) && key >= g.lo && key < g.hi;
+    const float *src =
+        use ? sc + pg * sc_page + g.head * sc_head + (key & (p.page_size - 1)) * sc_token : sc;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst + k)), "l"(src),
+                 "r"(use ? 4 : 0)
+                 : "memory");
+  }
+}
+
 // Inclusive sum over the lanes.
 __device__ __forceinline__ int64_t warp_scan(int64_t v) {
 #pragma unroll
@@ -499,6 +554,22 @@ qz_status code_map(CUtensorMap *map, const int8_t *base, const PagedInt8View &c,
          c.D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? QZ_OK : QZ_ERR_UNSUPPORTED;
+}
+
+// The pages and scales of a call.
+void set_scales(ScaleParams *p, const PagedInt8View &c) {
+  p->ks = c.ks;
+  p->vs = c.vs;
+  p->ks_page = c.ks_page, p->ks_head = c.ks_head, p->ks_token = c.ks_token;
+  p->vs_page = c.vs_page, p->vs_head = c.vs_head, p->vs_token = c.vs_token;
+  p->n_pages = c.n_pages;
+  p->page_size = c.page_size;
+  p->page_shift = c.page_shift;
+  // (head and page strides count where there are several)
+  p->runs = c.ks_token == 1 && c.vs_token == 1 &&
+            (((uintptr_t)c.ks | (uintptr_t)c.vs) & 15u) == 0 &&
+            (c.hkv == 1 || (c.ks_head | c.vs_head) % 4 == 0) &&
+            (c.n_pages == 1 || (c.ks_page | c.vs_page) % 4 == 0);
 }
 
 }  // namespace

@@ -15,27 +15,24 @@ constexpr int kSoftmaxWarps = 8;       // two warpgroups
 // With few rows only softmax warps 0 and 4 have any, both on the SM's first
 // scheduler: the MMA and load warps sit on others.
 constexpr int kQWarp = 8, kMmaWarp = 10, kLoadWarp = 11;  // 8 and 9: queries
-constexpr int kCodeWarp = 12;          // 12 to 15, INT8 rows: codes to fp16
+constexpr int kThreads = 384;          // the third warpgroup: queries (2), MMA, keys and values
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
+static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "register split");
 constexpr int kBars = 4096;             // barriers and exchange rows at the start of shared memory
 constexpr int kOutBytes = 32 * 64;     // per softmax warp: 32 rows x 32 outputs on their way out
 constexpr int kHead = kBars + 8 * kOutBytes;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kScaleBlocks = 8;        // INT8 rows: key blocks whose scales are kept
-constexpr int kScaleBytes = 9216;      // [kScaleBlocks][2][kN] scales, [kScaleBlocks][4] exponents
+// What is kept of them: factors of the logits and weights [2][kN], units [4], and the
+// fp16 parts of the values' [kN].
+constexpr int kScaleSet = 2 * kN * 4 + 16 + kN * 2;
+constexpr int kScaleBytes = (kScaleBlocks * kScaleSet + 1023) / 1024 * 1024;
+constexpr float kLift = 7.0f;          // log2 of the weight at m
+static_assert(kLag + kLift < 16.0f - 0.1f, "weights are fp16 (INT8 rows: times at most 17/16)");
 
 template <int D, int NQ, bool Q8>
 struct Cfg {
-  // the third warpgroup: queries (2), MMA, keys and values; the fourth: codes
-  static constexpr int kThreads = Q8 ? 512 : 384;
-  // of 168 (128) a thread at launch
-  static constexpr int kSoftmaxRegs = Q8 ? 200 : 216, kOtherRegs = Q8 ? 56 : 72, kCodeRegs = 56;
-  static_assert(Q8 ? 8 * kSoftmaxRegs + 4 * kOtherRegs + 4 * kCodeRegs <= 16 * 128
-                   : 8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168,
-                "register split");
-  // log2 of the weight at m (INT8 rows: times a scale below 2)
-  static constexpr float kLift = Q8 ? 6.0f : 7.0f;
-  static_assert(kLag + kLift + (Q8 ? 1.0f : 0.0f) < 16.0f, "weights are fp16");
   // A slot's codes arrive in its upper half, where a thread turns a row into fp16 in place:
   // the row's last 128 bytes are its own codes' (D 64: behind the slot's fp16 rows).
   static constexpr int kCodes = D == 64 ? kN * D * 2 : kN * D;
@@ -53,12 +50,6 @@ struct Cfg {
   static constexpr int kPart = 32 * (kDC + 2);         // floats of one warp's partial
 };
 
-// The scales of an INT8 cache (strides in floats).
-struct ScaleParams {
-  const float *ks, *vs;
-  int64_t ks_page, ks_head, ks_token, vs_page, vs_head, vs_token;
-};
-
 struct AttnParams : PlanParams, CapParams, ScaleParams {
   CUtensorMap kmap, vmap;  // [page][head][slot][D], box 64 (128 codes) x min(page, 128) rows
   CUtensorMap qmap;        // [token][head][D], box 64 x G heads x tokens of half a tile
@@ -66,7 +57,6 @@ struct AttnParams : PlanParams, CapParams, ScaleParams {
   const __half *q;
   __half *out;
   int64_t q_token, q_head, o_token, o_head;
-  int n_pages, page_size, page_shift;
   float c;              // logit units to log2: |scale| log2(e), or log2(e) with a cap
   uint32_t keep, flip;  // queries are read as (bits & keep) ^ flip: signs turned when scale < 0,
                         // zeros when scale = 0 (c stays positive: masked logits are -inf)
@@ -193,11 +183,10 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_n_major) {
 }
 
 // ---------------------------------------------------------------- kernel --
-// CAP: 0 none, 1 of up to kShortCap, 2 of any size.  Q8: a cache of INT8 rows, whose
-// codes four more warps turn into fp16 before they are multiplied, and whose scales
-// multiply logits and weights.
+// CAP: 0 none, 1 of up to kShortCap, 2 of any size.  Q8: a cache of INT8 rows, which the
+// query warps turn into fp16 before they are multiplied (see turn_rows).
 template <int D, int NQ, int CAP, bool Q8>
-__global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ AttnParams p) {
   using C = Cfg<D, NQ, Q8>;
   constexpr int kM = C::kM, NS = C::kNS, NC = C::kNC, DC = C::kDC;
@@ -219,15 +208,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
   Seg *seg_sm = reinterpret_cast<Seg *>(base + 512);         // [kSegs]
   float *xch = reinterpret_cast<float *>(base + 1024);       // [2][8 warps][32]
   float *scale_sm = reinterpret_cast<float *>(base + kHead);  // [kScaleBlocks][K, V][kN]
-  float *exp_sm = scale_sm + kScaleBlocks * 2 * kN;  // [kScaleBlocks][4], of 32 values' scales
+  float *unit_sm = scale_sm + kScaleBlocks * 2 * kN;          // [kScaleBlocks][4]
+  __half *part_sm = reinterpret_cast<__half *>(unit_sm + kScaleBlocks * 4);  // [kScaleBlocks][kN]
   uint8_t *q_sm = base + C::kFirst, *kv_sm = q_sm + C::kQ;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(smem_u32(&kv_full[i]), Q8 ? 33 : 1);
-      mbar_init(smem_u32(&kv_ready[i]), 4);
+      mbar_init(smem_u32(&kv_full[i]), Q8 && !p.runs ? 33 : 1);
+      mbar_init(smem_u32(&kv_ready[i]), 2);
       mbar_init(smem_u32(&kv_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -242,7 +232,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&xbar[i]), 2);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(smem_u32(&seg_full[i]), 1);
-      mbar_init(smem_u32(&seg_empty[i]), kSoftmaxWarps + (Q8 ? 7 : 3));
+      mbar_init(smem_u32(&seg_empty[i]), kSoftmaxWarps + 3);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -286,9 +276,27 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
   // than fp32 rounding can move it.
   auto row_token = [&](int n) { return (int)(((float)n + 0.5f) * p.inv_g); };
 
+  // Half of a tile's queries, from token tok on, by TMA (one lane).
+  auto copy_queries = [&](const Seg &g, int half, int tok) {
+    asm volatile(
+        "{\n\t.reg .b64 t;\n\t"
+        "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(smem_u32(q_full)),
+        "r"((uint32_t)(kM / 2 * D * 2))
+        : "memory");
+    const uint32_t dst = smem_u32(q_sm) + (NQ == 2 ? half * (128 * D * 2) : half * 64 * 128);
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+          "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst + d * 16384),
+          "l"(reinterpret_cast<uint64_t>(&p.qmap)), "r"(d * 64), "r"(g.head * p.G), "r"(tok),
+          "r"(smem_u32(q_full))
+          : "memory");
+  };
+
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax --
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int wg = warp >> 2, quarter = warp & 3;
     const int my_row = (NQ == 2 ? wg * 128 : 0) + quarter * 32 + lane;  // of the tile
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -299,6 +307,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
     uint32_t ends = 0;     // segments finished (NQ = 2: of this stage)
     uint32_t swaps = 0;    // exchanges with the other warpgroup
     uint32_t scales = 0;   // Q8: key blocks of the tiles so far
+    // Q8: logits get their keys' factors (and c with them) where they become weights, and
+    // the running maximum is held against a bound of theirs
+    constexpr bool kBound = Q8 && CAP == 0;
+    const float c = kBound ? 1.0f : p.c;  // of m and the logits
     bool ok = true;
     // The other warpgroup's value of this row (NQ = 1).
     auto exchange = [&](float v, float *other) -> bool {
@@ -346,7 +358,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
       const int pos = g.pos + row_token(g.rem + min(my_row, g.rows - 1));
       const int hi = pos + 1, lo = first_key(p, pos);
       float m = -INFINITY, l = 0.0f;
-      float unit = -60.0f;  // Q8: O has the values' scales in units of 2^unit
       const int nb = g.b1 - g.b0;
       const uint32_t scale0 = scales;
       scales += nb;
@@ -377,16 +388,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < NC / 32; ++k)
           tmem_ld32(s_tm + col0 + 32 * k, reinterpret_cast<uint32_t *>(s) + 32 * k);
-        const float *ks = scale_sm + ((scale0 + b - g.b0) % kScaleBlocks) * (2 * kN) + col0;
-        const float *ev = exp_sm + ((scale0 + b - g.b0) % kScaleBlocks) * 4;
+        const uint32_t set = (scale0 + b - g.b0) % kScaleBlocks;
+        const float *kf = scale_sm + set * (2 * kN) + col0, *vf = kf + kN;
+        const float *uf = unit_sm + set * 4 + col0 / 32;
         tmem_ld_wait();
-        if (Q8) {
+        if (Q8 && CAP) {
 #pragma unroll
-          for (int k = 0; k < NC / 4; ++k) {
-            const float4 f = *reinterpret_cast<const float4 *>(ks + 4 * k);
-            const float2 a = mul2(make_float2(s[4 * k], s[4 * k + 1]), make_float2(f.x, f.y));
-            const float2 c = mul2(make_float2(s[4 * k + 2], s[4 * k + 3]), make_float2(f.z, f.w));
-            s[4 * k] = a.x, s[4 * k + 1] = a.y, s[4 * k + 2] = c.x, s[4 * k + 3] = c.y;
+          for (int k = 0; k < NC; k += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(kf + k);
+            s[k] *= f.x, s[k + 1] *= f.y, s[k + 2] *= f.z, s[k + 3] *= f.w;
           }
         }
         if (CAP) {
@@ -404,40 +414,60 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < NC; ++k) s[k] = k >= k_lo ? s[k] : -INFINITY;
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        float mb;
+        if (kBound) {
+          // No logit is above this: factors are within 1/16 of their unit.
+          mb = -INFINITY;
 #pragma unroll
-        for (int k = 4; k < NC - 4; k += 8)
+          for (int h = 0; h < NC / 32; ++h) {
+            float a = s[32 * h], c = s[32 * h + 1];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
+            for (int k = 2; k < 30; k += 4) {
+              a = max3(a, s[32 * h + k], s[32 * h + k + 1]);
+              c = max3(c, s[32 * h + k + 2], s[32 * h + k + 3]);
+            }
+            a = max3(a, s[32 * h + 30], s[32 * h + 31]);
+            a = fmaxf(a, c);
+            mb = fmaxf(mb, a * (a > 0.0f ? 1.0625f : 0.9375f) * uf[h]);
+          }
+        } else {
+          float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[NC - 4 + e]);
-        float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int k = 4; k < NC - 4; k += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[NC - 4 + e]);
+          mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        }
         if (NQ == 1) {
           float other;
           if (!(ok = exchange(mb, &other))) break;
           mb = fmaxf(mb, other);
         }
         // move the maximum where it lags too far, and rescale what was summed
-        float e_top = 0.0f, e_off = 0.0f;  // Q8: exponent of the block's values, less unit
-        if (Q8) {
-          const float4 e = *reinterpret_cast<const float4 *>(ev);
-          e_top = fmaxf(fmaxf(e.x, e.y), fmaxf(e.z, e.w));
-          e_off = e_top - unit;
-        }
-        const bool move = (Q8 ? fmaf(mb - m, p.c, e_off) : (mb - m) * p.c) > kLag || (m == -INFINITY && mb > -INFINITY);
+        const bool move = (mb - m) * c > kLag || (m == -INFINITY && mb > -INFINITY);
         if (__any_sync(0xffffffffu, move)) {
-          const float mn = move ? (Q8 ? fmaxf(m, mb) : mb) : m;
-          float f = m == -INFINITY ? (move ? 0.0f : 1.0f) : ex2((m - mn) * p.c);
-          l *= f;
-          if (Q8) {
-            // what was summed counts for the unit by how far m moves
-            const float next = !move ? unit
-                               : m == -INFINITY ? e_top : fmaxf(e_top, unit - (mn - m) * p.c);
-            f *= ex2(unit - next);
-            unit = next;
+          if (kBound) {  // the largest logit itself
+            mb = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(kf + k);
+              mb = max3(mb, s[k] * f.x, s[k + 1] * f.y);
+              mb = max3(mb, s[k + 2] * f.z, s[k + 3] * f.w);
+            }
+            if (NQ == 1) {
+              float other;
+              if (!(ok = exchange(mb, &other))) break;
+              mb = fmaxf(mb, other);
+            }
           }
+          // (kBound: every row of the warp moves, so that the next one comes later)
+          const float mn = kBound ? fmaxf(m, mb) : move ? mb : m;
+          const float f = m == -INFINITY ? (mn > -INFINITY ? 0.0f : 1.0f) : ex2((m - mn) * c);
           m = mn;
-          if (b > g.b0) {
+          l *= f;
+          if (b > g.b0 && (!kBound || __any_sync(0xffffffffu, f != 1.0f))) {
             // NQ = 2: this stage's earlier products precede the S just read
             if (NQ == 1 && !(ok = last_product(b))) break;
             fence_after();
@@ -452,29 +482,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
             }
           }
         }
-        const float mc = m == -INFINITY ? 0.0f : m * p.c - C::kLift;
-        const float2 c2 = make_float2(p.c, p.c);
-        float2 mc2 = make_float2(-mc, -mc);
+        const float mc = m == -INFINITY ? 0.0f : m * c - kLift;
+        const float2 mc2 = make_float2(-mc, -mc);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int h = 0; h < NC / 32; ++h) {
           uint32_t pk[16];
-          float eh = 0.0f;
-          if (Q8) {  // weights in the unit of these 32 values' scales
-            eh = ev[col0 / 32 + h] - unit;
-            mc2 = make_float2(eh - mc, eh - mc);
-            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-          }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float2 e = fma2(make_float2(s[32 * h + 2 * k], s[32 * h + 2 * k + 1]), c2, mc2);
-            e.x = ex2(e.x);
-            e.y = ex2(e.y);
-            sum[k & 1] = add2(sum[k & 1], e);
-            if (Q8) e = mul2(e, *reinterpret_cast<const float2 *>(ks + kN + 32 * h + 2 * k));
-            pk[k] = f2h(e.x, e.y);
+          for (int k = 0; k < 16; k += 2) {
+            const int at = 32 * h + 2 * k;
+            float4 kc = make_float4(c, c, c, c), vc;
+            if (kBound) kc = *reinterpret_cast<const float4 *>(kf + at);
+            if (Q8) vc = *reinterpret_cast<const float4 *>(vf + at);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float2 e = fma2(make_float2(s[at + 2 * j], s[at + 2 * j + 1]),
+                              j ? make_float2(kc.z, kc.w) : make_float2(kc.x, kc.y), mc2);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum[j] = add2(sum[j], e);
+              if (Q8) e = mul2(e, j ? make_float2(vc.z, vc.w) : make_float2(vc.x, vc.y));
+              pk[k + j] = f2h(e.x, e.y);
+            }
           }
-          if (Q8) l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), ex2(-eh), l);
           tmem_st16(s_tm + col0 / 2 + 16 * h, pk);
           if (NQ == 2 && h == 1) {  // the product starts on these
             tmem_st_wait();
@@ -483,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&p_half[buf]));
           }
         }
-        if (!Q8) l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (NQ == 1 && !(ok = last_product(b))) break;
         tmem_st_wait();
         fence_before();
@@ -525,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
         }
       }
       if (g.slot < 0) {
-        const float inv = l > 0.0f ? (Q8 ? ex2(unit) : 1.0f) / l : 0.0f;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int k = 0; k < DC; k += 32) {
           uint32_t o[32], v[16];
@@ -543,9 +573,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
         continue;
       }
       // ---- cut between CTAs: leave the partial, merge if last
-      mine_part[lane] = l > 0.0f ? (m == -INFINITY ? 0.0f : m * p.c) : -INFINITY;
+      mine_part[lane] = l > 0.0f ? (m == -INFINITY ? 0.0f : m * c) : -INFINITY;
       mine_part[32 + lane] = l;
-      const float of_o = Q8 ? ex2(unit) : 1.0f;
 #pragma unroll 1
       for (int k = 0; k < DC; k += 32) {
         uint32_t o[32];
@@ -555,8 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            v[e] = Q8 ? __float_as_uint(__uint_as_float(o[16 * h + e]) * of_o) : o[16 * h + e];
+          for (int e = 0; e < 16; ++e) v[e] = o[16 * h + e];
           store_rows(v, dst, (k + 16 * h) * 4);
         }
       }
@@ -638,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA --
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     constexpr uint32_t id_qk = idesc(128, kN, false), id_pv = idesc(128, D, true);
     uint32_t ring = 0, blocks = 0, segs = 0, n_stage[2] = {0, 0};
     bool ok = true;
@@ -752,7 +780,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
     }
   } else if (warp < kQWarp + 2) {
     // ------------------------------------------------------------ queries --
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // A tile's queries, half of the rows a warp.  Where a group of heads divides
     // them they are a box of the query tensor; else (and for a negative or zero
     // scale, which the copy cannot apply) they are laid row by row as TMA with the
@@ -785,6 +813,104 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
         }
       }
     };
+    // Q8: a tile's blocks of keys and values, half of the rows a warp and a row a lane.  A
+    // scale is s r with s of 4 bits, so that s times a code is exact in fp16, and r within
+    // 1/16 of 1, which stays in fp32: r (and c, without a cap) multiplies the logit, or the
+    // weight.  Keys' s are in units of the largest of 32 keys (2^e: their r has it back; a
+    // key below 2^-21 of it has r = 1, off by less than fp32 logits of the largest are).
+    // Values' s are fp16 as they are, from 2^-21 to 512; r is below 15/16 for smaller ones.
+    // A byte under the bits of 1024 is 1024 + code + 128 once its sign is turned.
+    constexpr int kChunks = D == 64 ? 4 : 8;
+    uint32_t ring = 0, scales = 0, values = 0;
+    auto four_bits = [](float x) {
+      return __uint_as_float((__float_as_uint(x) + 0x00080000u) & 0xfff00000u);
+    };
+    auto turn_rows = [&](const Seg &g) -> bool {
+      const int n = 2 * (g.b1 - g.b0);
+      for (int i = 0; i < n; ++i, ++ring) {
+        const int slot = ring % NS;
+        if (!mbar_wait(smem_u32(&kv_full[slot]), (ring / NS) & 1, abort_flag)) return false;
+        // keys and values in the order of the load warp
+        const bool keys = NQ == 2 ? !(i & 1) : i == 0 || ((i & 1) && i < n - 1);
+        const uint32_t set = (keys ? scales++ : values++) % kScaleBlocks;
+        const uint32_t at = smem_u32(kv_sm) + slot * C::kStage;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int group = (warp - kQWarp) * 2 + half, row = group * 32 + lane;
+          __half s;
+          bool large = false;  // 1152 s is beyond fp16
+          if (keys) {
+            float *k = scale_sm + set * (2 * kN) + row, *v = k + kN;
+            // (of keys that no row sees, and of missing pages, zeros)
+            const int at_key = (g.b0 + (NQ == 2 ? i / 2 : (i + 1) / 2)) * kN;
+            const bool seen = row < g.hi - at_key && row >= g.lo - at_key;
+            const float ks = seen ? *k : 0.0f, y = seen ? *v : 0.0f;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(ks));
+            const int e = min(max((int)(top >> 23) - 127, -100), 126);
+            const float x = ks * __uint_as_float((uint32_t)(127 - e) << 23);
+            const float unit = __uint_as_float((uint32_t)(127 + e) << 23) * (CAP ? 1.0f : p.c);
+            const bool tiny = x < 0x1p-21f;
+            s = __float2half_rn(tiny ? x : four_bits(x));
+            *k = (tiny ? 1.0f : x / four_bits(x)) * unit;
+            if (lane == 0) unit_sm[set * 4 + group] = unit;
+            const float w = fminf(fmaxf(four_bits(y), 0x1p-21f), 512.0f);
+            part_sm[set * kN + row] = __float2half_rn(w);
+            *v = y / w;
+          } else {
+            s = part_sm[set * kN + row];
+            large = __any_sync(0xffffffffu, __half2float(s) > 32.0f);
+          }
+          const __half2 s2 = __half2half2(s), off = __hmul2(s2, __float2half2_rn(-1152.0f));
+          const uint32_t raw = at + C::kCodes + row * (D == 64 ? 64 : 128);
+          const uint32_t turn = D == 64 ? (row >> 1) & 3 : row & 7;
+          auto scaled = [&](uint32_t biased, uint32_t sel) -> uint32_t {
+            const uint32_t b = __byte_perm(biased, 0x64646464u, sel);
+            const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&b), s2, off);
+            return *reinterpret_cast<const uint32_t *>(&r);
+          };
+          auto scaled_large = [&](uint32_t biased, uint32_t sel) -> uint32_t {
+            const uint32_t b = code_pair(biased, sel);
+            const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&b), s2);
+            return *reinterpret_cast<const uint32_t *>(&r);
+          };
+#pragma unroll
+          for (int h = 0; h < (D + 127) / 128; ++h) {
+            uint4 codes[kChunks];
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k)
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(codes[k].x), "=r"(codes[k].y), "=r"(codes[k].z),
+                             "=r"(codes[k].w)
+                           : "r"(raw + h * (kN * 128) + ((k ^ turn) << 4))
+                           : "memory");
+            auto store = [&](auto f) {
+#pragma unroll
+              for (int k = 0; k < kChunks; ++k) {
+                const uint32_t w[4] = {codes[k].x, codes[k].y, codes[k].z, codes[k].w};
+                const uint32_t dst = at + (2 * h + (k >> 2)) * (kN * 128) + row * 128;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const uint32_t a = w[2 * j] ^ 0x80808080u, b = w[2 * j + 1] ^ 0x80808080u;
+                  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                   dst + (((2 * (k & 3) + j) ^ (row & 7)) << 4)),
+                               "r"(f(a, 0x4140)), "r"(f(a, 0x4342)), "r"(f(b, 0x4140)),
+                               "r"(f(b, 0x4342))
+                               : "memory");
+                }
+              }
+            };
+            if (large)
+              store(scaled_large);
+            else
+              store(scaled);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&kv_ready[slot]));
+      }
+      return true;
+    };
     uint32_t n_seg = 0, segs = 0;
     for (;;) {
       Seg g;
@@ -792,6 +918,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
       free_seg(n_seg++);
       if (g.rows == 0) break;
       if (g.b1 <= g.b0) continue;
+      if (Q8 && p.q_boxes) {  // queries come by the load warp
+        if (!turn_rows(g)) break;
+        continue;
+      }
       if (p.q_boxes) {
         // Rows past the tile are whatever follows (or zeros past the last token):
         // they are computed and not stored.
@@ -807,22 +937,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
           __syncwarp();
           if (!mbar_wait(smem_u32(q_empty), (segs - 1) & 1, abort_flag)) break;
         }
-        if (lane == 0) {
-          asm volatile(
-              "{\n\t.reg .b64 t;\n\t"
-              "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(smem_u32(q_full)),
-              "r"((uint32_t)(kM / 2 * D * 2))
-              : "memory");
-          const uint32_t dst = smem_u32(q_sm) + (NQ == 2 ? half * (128 * D * 2) : half * 64 * 128);
-#pragma unroll
-          for (int d = 0; d < D / 64; ++d)
-            asm volatile(
-                "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst + d * 16384),
-                "l"(reinterpret_cast<uint64_t>(&p.qmap)), "r"(d * 64), "r"(g.head * p.G), "r"(tok),
-                "r"(smem_u32(q_full))
-                : "memory");
-        }
+        if (lane == 0) copy_queries(g, half, tok);
         __syncwarp();
         ++segs;
         continue;
@@ -859,11 +974,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(q_full));
       ++segs;
+      if (Q8 && !turn_rows(g)) break;
     }
-    if (lane == 0) issued[warp - kQWarp] = p.q_boxes ? segs : 0;
-  } else if (warp == kLoadWarp) {
+    if (!Q8 && lane == 0) issued[warp - kQWarp] = p.q_boxes ? segs : 0;
+  } else {
     // --------------------------------------------------------------- load --
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     uint32_t ring = 0;
     bool ok = true;
     const int ppb = p.page_size >= kN ? 1 : kN >> p.page_shift;  // pages per block
@@ -895,25 +1011,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
       }
       return id;
     };
-    // (KEYS, Q8: the scales of the block's keys and values come with its keys)
+    // (Q8: the scales of the block's keys and values come with its keys)
     uint32_t scales = 0;
-    const int box_shift = min(p.page_shift, 7);
-    auto scale_copy = [&](float *dst, const float *sc, int64_t sc_page, int64_t sc_head,
-                          int64_t sc_token, const Seg &g, int b, int page) {
-      // four a lane; of keys that no row sees, and of missing pages, zeros
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = lane + 32 * i;
-        const int64_t key = (int64_t)b * kN + k;
-        const int pg = __shfl_sync(0xffffffffu, page, k >> box_shift);
-        const bool use = pg >= 0 && pg < p.n_pages && key >= g.lo && key < g.hi;
-        const float *src =
-            use ? sc + pg * sc_page + g.head * sc_head + (key & (p.page_size - 1)) * sc_token : sc;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst + k)),
-                     "l"(src), "r"(use ? 4 : 0)
-                     : "memory");
-      }
-    };
     auto issue = [&](bool keys, const Seg &g, int b, int page) -> bool {
       const CUtensorMap *map = keys ? &p.kmap : &p.vmap;
       const int slot = ring % NS;
@@ -922,11 +1021,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
         return false;
       const uint32_t bar = smem_u32(&kv_full[slot]);
       const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+      const uint32_t bytes = __popc(live) * box_rows * D * (Q8 ? 1 : 2);
+      float *sc = scale_sm + (scales % kScaleBlocks) * (2 * kN);
+      uint32_t runs = 0;
+      if (Q8 && keys) {
+        runs = 2 * scale_runs(p, page);
+        scale_zeros(p, sc, page);
+        scale_zeros(p, sc + kN, page);
+        __syncwarp();
+      }
       if (lane == 0)
         asm volatile(
             "{\n\t.reg .b64 t;\n\t"
             "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(bar),
-            "r"((uint32_t)(__popc(live) * box_rows * D * (Q8 ? 1 : 2)))
+            "r"(bytes + runs)
             : "memory");
       __syncwarp();
       if (page >= 0) {
@@ -944,15 +1052,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
               "r"(page), "r"(bar)
               : "memory");
       }
-      if (Q8) {
-        if (keys) {
-          float *dst = scale_sm + (scales++ % kScaleBlocks) * (2 * kN);
-          scale_copy(dst, p.ks, p.ks_page, p.ks_head, p.ks_token, g, b, page);
-          scale_copy(dst + kN, p.vs, p.vs_page, p.vs_head, p.vs_token, g, b, page);
-        }
+      if (Q8 && keys) {
+        ++scales;
+        scale_copy(p, p.ks, p.ks_page, p.ks_head, p.ks_token, sc, g, b, page, bar);
+        scale_copy(p, p.vs, p.vs_page, p.vs_head, p.vs_token, sc + kN, g, b, page, bar);
+      }
+      if (Q8 && !p.runs)
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar)
                      : "memory");
-      }
       __syncwarp();
       ++ring;
       return true;
@@ -975,6 +1082,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
     };
     Seg next = w.next(p);
     ok = announce(next);
+    uint32_t q_tiles = 0;  // Q8: whose queries were issued
     while (ok && next.rows > 0) {
       const Seg g = next;
       const int nb = g.b1 - g.b0;
@@ -990,6 +1098,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
         if (nb > 0) {
           const int page = page_of(g, b);
           ok = issue(true, g, b, page);
+          if (Q8 && p.q_boxes && j == 0 && ok) {
+            // the tile before has read its own about when the next slot is free
+            ok = q_tiles == 0 || mbar_wait(smem_u32(q_empty), (q_tiles - 1) & 1, abort_flag);
+            if (ok && lane == 0) {
+              copy_queries(g, 0, g.tok);
+              copy_queries(g, 1, g.tok + kM / 2 / p.G);
+            }
+            __syncwarp();
+            q_tiles += ok;
+          }
           if (NQ == 1) {  // K0, K1, V0, K2, V1, ..., the order in which they are used
             if (ok && j > 0) ok = issue(false, g, b - 1, prev);
             if (ok && j == nb - 1) ok = issue(false, g, b, page);
@@ -1001,71 +1119,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, Q8>::kThreads, 1)
         if (ok && j == 0 && n_seg == 1) ok = announce(next = w.next(p));
       }
     }
-    if (lane == 0) issued[kLoadWarp - kQWarp] = ring;
-    if (Q8) asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
-    // -------------------------------------------------------------- codes --
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kCodeRegs));
-    // A lane has a row of every block: 128 bytes of codes at a time (D 64: 64) become two
-    // rows of 128 bytes of fp16 (one) where the MMA reads them.  A byte under the bits of 1024
-    // is 1024 + code + 128 once its sign is turned.
-    const int row = (warp - kCodeWarp) * 32 + lane;
-    constexpr int kChunks = D == 64 ? 4 : 8;
-    const uint32_t raw = D == 64 ? C::kCodes + row * 64 : C::kCodes + row * 128;
-    const uint32_t turn = D == 64 ? (row >> 1) & 3 : row & 7;
-    uint32_t n_seg = 0, ring = 0, scales = 0;
-    bool ok = true;
-    while (ok) {
-      Seg g;
-      if (!(ok = read_seg(n_seg, g))) break;
-      free_seg(n_seg++);
-      if (g.rows == 0) break;
-      const int n = 2 * (g.b1 - g.b0);
-      for (int i = 0; i < n; ++i, ++ring) {
-        const int slot = ring % NS;
-        if (!(ok = mbar_wait(smem_u32(&kv_full[slot]), (ring / NS) & 1, abort_flag))) break;
-        // keys and values in the order of the load warp
-        const bool keys = NQ == 2 ? !(i & 1) : i == 0 || ((i & 1) && i < n - 1);
-        if (keys) {
-          // the values' scales of these 32 rows in units of their largest power of two
-          const uint32_t at = scales++ % kScaleBlocks;
-          float *v = scale_sm + at * (2 * kN) + kN + row;
-          const float s = *v;
-          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(s) & 0x7fffffffu);
-          const int e = min(max((int)(top >> 23) - 127, -60), 126);
-          *v = s * __uint_as_float((uint32_t)(127 - e) << 23);
-          if (lane == 0) exp_sm[at * 4 + warp - kCodeWarp] = (float)e;
-        }
-        const uint32_t at = smem_u32(kv_sm) + slot * C::kStage;
-#pragma unroll
-        for (int h = 0; h < (D + 127) / 128; ++h) {
-          uint4 c[kChunks];
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(c[k].x), "=r"(c[k].y), "=r"(c[k].z), "=r"(c[k].w)
-                         : "r"(at + raw + h * (kN * 128) + ((k ^ turn) << 4))
-                         : "memory");
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-            const uint32_t dst = at + (2 * h + (k >> 2)) * (kN * 128) + row * 128;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t a = w[2 * j] ^ 0x80808080u, b = w[2 * j + 1] ^ 0x80808080u;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                               dst + (((2 * (k & 3) + j) ^ (row & 7)) << 4)),
-                           "r"(code_pair(a, 0x4140)), "r"(code_pair(a, 0x4342)),
-                           "r"(code_pair(b, 0x4140)), "r"(code_pair(b, 0x4342))
-                           : "memory");
-            }
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&kv_ready[slot]));
-      }
+    if (lane == 0) {
+      issued[kLoadWarp - kQWarp] = ring;
+      if (Q8) issued[0] = q_tiles, issued[1] = 0;
     }
+    if (Q8) asm volatile("cp.async.wait_all;" ::: "memory");
   }
   fence_before();
   __syncthreads();
@@ -1110,9 +1168,8 @@ bool query_map(CUtensorMap *map, const __half *q, int64_t T, int64_t H, int D, i
 }
 // What the launches over either cache have in common.
 void set_call(AttnParams *p, const __half *q, int64_t hq, int64_t q_token, int64_t q_head,
-              int hkv, int n_pages, int page_size, int page_shift, const SeqView &sv, float scale,
-              float softcap, int64_t window, __half *out, int64_t o_token, int64_t o_head,
-              void *workspace) {
+              int hkv, const SeqView &sv, float scale, float softcap, int64_t window, __half *out,
+              int64_t o_token, int64_t o_head, void *workspace) {
   p->q = q;
   p->out = out;
   p->q_token = q_token;
@@ -1120,9 +1177,6 @@ void set_call(AttnParams *p, const __half *q, int64_t hq, int64_t q_token, int64
   p->o_token = o_token;
   p->o_head = o_head;
   set_heads(p, hq, hkv);
-  p->n_pages = n_pages;
-  p->page_size = page_size;
-  p->page_shift = page_shift;
   p->keep = scale == 0.0f ? 0u : ~0u;
   p->flip = scale < 0.0f ? 0x80008000u : 0u;
   p->c = set_logits(p, scale, softcap);
@@ -1137,7 +1191,7 @@ qz_status launch(const AttnParams &p, int sms, cudaStream_t s) {
   using C = Cfg<D, NQ, Q8>;
   const cudaError_t e = allow_smem<attn_kernel<D, NQ, CAP, Q8>>(C::kSmem);
   if (e != cudaSuccess) return cuda_status(e);
-  attn_kernel<D, NQ, CAP, Q8><<<sms < kMaxCtas ? sms : kMaxCtas, C::kThreads, C::kSmem, s>>>(p);
+  attn_kernel<D, NQ, CAP, Q8><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, C::kSmem, s>>>(p);
   return launch_status();
 }
 

@@ -85,8 +85,11 @@ qz_status launch_attention(const __half *q, int64_t hq, int64_t q_token, int64_t
   st = pool_map(&p.kmap, c.k, c, c.k_token, c.k_head, c.k_page);
   if (st == QZ_OK) st = pool_map(&p.vmap, c.v, c, c.v_token, c.v_head, c.v_page);
   if (st != QZ_OK) return st;
-  set_call(&p, q, hq, q_token, q_head, c.hkv, c.n_pages, c.page_size, c.page_shift, sv, scale,
-           softcap, window, out, o_token, o_head, workspace);
+  p.n_pages = c.n_pages;
+  p.page_size = c.page_size;
+  p.page_shift = c.page_shift;
+  set_call(&p, q, hq, q_token, q_head, c.hkv, sv, scale, softcap, window, out, o_token, o_head,
+           workspace);
   // Two stages of rows pay once a sequence fills the second one: 4 x 64 tokens
   // over 24000 keys, 64 heads on 8, take 111 us with two and 144 with one, four
   // prompts of up to 4096 326 and 381; 8 x 16 tokens over 4000 36.2 with one, 39.7

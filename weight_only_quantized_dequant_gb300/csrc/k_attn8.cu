@@ -50,14 +50,11 @@ struct Cfg8 {
   static constexpr int kPart = kM * (D + 2);        // floats of a partial
 };
 
-struct Attn8Params : PlanParams, CapParams {
+struct Attn8Params : PlanParams, CapParams, ScaleParams {
   CUtensorMap kmap, vmap;  // [page][head][slot][D] bytes, box 128 (64) x min(page, 128)
-  const float *ks, *vs;
-  int64_t ks_page, ks_head, ks_token, vs_page, vs_head, vs_token;
   const __half *q;
   __half *out;
   int64_t q_token, q_head, o_token, o_head;
-  int n_pages, page_size, page_shift;
   float c;       // logit units to log2 of what the product and ks give
   float sign;    // of the scale (0: no logits)
   unsigned *cnt; // [kMaxCtas] arrivals per cut tile, by its first CTA
@@ -114,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(smem_u32(&kv_full[i]), 33);
+      mbar_init(smem_u32(&kv_full[i]), p.runs ? 1 : 33);
       mbar_init(smem_u32(&kv_empty[i]), kWarps);
     }
     for (int i = 0; i < kSegs; ++i) {
@@ -279,8 +276,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
               for (int j = 0; j < 4; ++j)
                 if (k0 + 8 * i + (j & 1) < lo[j >> 1] - b * kN) x[i][j] = -INFINITY;
           }
-          const float2 va = lds64f(sc0 + vs * (kN * 4) + t * 8);
-          const float2 vb = lds64f(sc0 + vs * (kN * 4) + 32 + t * 8);
+          float2 va = lds64f(sc0 + vs * (kN * 4) + t * 8);
+          float2 vb = lds64f(sc0 + vs * (kN * 4) + 32 + t * 8);
+          if (s.hi - b * kN < key0 + 16 || s.lo - b * kN > key0) {
+            // scales of keys that no row sees may be anything
+            auto seen = [&](int k) { return k < s.hi - b * kN && k >= s.lo - b * kN; };
+            va.x = seen(k0) ? va.x : 0.0f, va.y = seen(k0 + 1) ? va.y : 0.0f;
+            vb.x = seen(k0 + 8) ? vb.x : 0.0f, vb.y = seen(k0 + 9) ? vb.y : 0.0f;
+          }
           float x0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
           float x1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
           float sv = fmaxf(fmaxf(va.x, va.y), fmaxf(vb.x, vb.y));
@@ -491,7 +494,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
     bool ok = true;
     const int ppb = p.page_size >= kN ? 1 : kN >> p.page_shift;  // pages per block
     const int box_rows = min(p.page_size, kN);
-    const int box_shift = min(p.page_shift, 7);
     int batch = 0, ids = -1, ids_ahead = -1;  // as in the fp16 kernel
     auto fetch = [&](const Seg &g, int first) -> int {
       const int pi = first + lane;
@@ -515,18 +517,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       }
       return id;
     };
-    auto issue = [&](const CUtensorMap *map, const float *sc, int64_t sc_page, int64_t sc_head,
-                     int64_t sc_token, const Seg &g, int b, int page) -> bool {
+    auto issue = [&](bool keys, const Seg &g, int b, int page) -> bool {
       const int slot = ring % NS;
       if (ring >= NS && !mbar_wait(smem_u32(&kv_empty[slot]), (ring / NS - 1) & 1, abort_flag))
         return false;
       const uint32_t bar = smem_u32(&kv_full[slot]);
       const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+      float *sc = scale_sm + slot * kN;
+      const uint32_t bytes = __popc(live) * box_rows * D + scale_runs(p, page);
+      scale_zeros(p, sc, page);
+      __syncwarp();
       if (lane == 0)
         asm volatile(
             "{\n\t.reg .b64 t;\n\t"
             "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(bar),
-            "r"((uint32_t)(__popc(live) * box_rows * D))
+            "r"(bytes)
             : "memory");
       __syncwarp();
       if (page >= 0) {
@@ -537,26 +542,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
           asm volatile(
               "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
               "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + d * (kN * 128)),
-              "l"(reinterpret_cast<uint64_t>(map)), "r"(d * 128), "r"(at), "r"(g.head), "r"(page),
+              "l"(reinterpret_cast<uint64_t>(keys ? &p.kmap : &p.vmap)), "r"(d * 128), "r"(at), "r"(g.head), "r"(page),
               "r"(bar)
               : "memory");
       }
-      // scales, four a lane; of keys that no row sees, and of missing pages, zeros
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = lane + 32 * i;
-        const int64_t key = (int64_t)b * kN + k;
-        const int pg = __shfl_sync(0xffffffffu, page, k >> box_shift);
-        const bool use = pg >= 0 && pg < p.n_pages && key >= g.lo && key < g.hi;
-        const float *src = use ? sc + pg * sc_page + g.head * sc_head +
-                                     (key & (p.page_size - 1)) * sc_token
-                               : sc;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                         smem_u32(scale_sm + slot * kN + k)),
-                     "l"(src), "r"(use ? 4 : 0)
+      if (keys)
+        scale_copy(p, p.ks, p.ks_page, p.ks_head, p.ks_token, sc, g, b, page, bar);
+      else
+        scale_copy(p, p.vs, p.vs_page, p.vs_head, p.vs_token, sc, g, b, page, bar);
+      if (!p.runs)
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar)
                      : "memory");
-      }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       __syncwarp();
       ++ring;
       return true;
@@ -587,8 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       }
       for (int b = g.b0; ok && b < g.b1; ++b) {
         const int page = page_of(g, b);
-        ok = issue(&p.kmap, p.ks, p.ks_page, p.ks_head, p.ks_token, g, b, page) &&
-             issue(&p.vmap, p.vs, p.vs_page, p.vs_head, p.vs_token, g, b, page);
+        ok = issue(true, g, b, page) && issue(false, g, b, page);
       }
     }
     if (lane == 0) *issued = ring;
@@ -635,10 +630,7 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
   st = code_map(&p.kmap, c.k, c, c.k_token, c.k_head, c.k_page);
   if (st == QZ_OK) st = code_map(&p.vmap, c.v, c, c.v_token, c.v_head, c.v_page);
   if (st != QZ_OK) return st;
-  p.ks = c.ks;
-  p.vs = c.vs;
-  p.ks_page = c.ks_page, p.ks_head = c.ks_head, p.ks_token = c.ks_token;
-  p.vs_page = c.vs_page, p.vs_head = c.vs_head, p.vs_token = c.vs_token;
+  set_scales(&p, c);
   p.q = q;
   p.out = out;
   p.q_token = q_token;
@@ -646,9 +638,6 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
   p.o_token = o_token;
   p.o_head = o_head;
   set_heads(&p, hq, c.hkv);
-  p.n_pages = c.n_pages;
-  p.page_size = c.page_size;
-  p.page_shift = c.page_shift;
   p.sign = scale == 0.0f ? 0.0f : scale < 0.0f ? -1.0f : 1.0f;
   p.c = set_logits(&p, scale, softcap);
   p.window = window > INT32_MAX ? 0 : (int)window;  // longer than any cache: none

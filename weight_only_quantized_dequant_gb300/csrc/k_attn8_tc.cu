@@ -25,12 +25,9 @@ qz_status launch_attention_int8_tc(const __half *q, int64_t hq, int64_t q_token,
   st = code_map(&p.kmap, c.k, c, c.k_token, c.k_head, c.k_page);
   if (st == QZ_OK) st = code_map(&p.vmap, c.v, c, c.v_token, c.v_head, c.v_page);
   if (st != QZ_OK) return st;
-  set_call(&p, q, hq, q_token, q_head, c.hkv, c.n_pages, c.page_size, c.page_shift, sv, scale,
-           softcap, window, out, o_token, o_head, workspace);
-  p.ks = c.ks;
-  p.vs = c.vs;
-  p.ks_page = c.ks_page, p.ks_head = c.ks_head, p.ks_token = c.ks_token;
-  p.vs_page = c.vs_page, p.vs_head = c.vs_head, p.vs_token = c.vs_token;
+  set_scales(&p, c);
+  set_call(&p, q, hq, q_token, q_head, c.hkv, sv, scale, softcap, window, out, o_token, o_head,
+           workspace);
   // (as over fp16 rows)
   const bool two = c.D < 256 && sv.n_tokens * p.G > (int64_t)128 * sv.n_seqs;
   p.q_boxes = scale > 0.0f && query_map(&p.qmap, q, sv.n_tokens, hq, c.D, q_token, q_head, p.G,
