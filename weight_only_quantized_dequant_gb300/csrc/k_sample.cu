@@ -28,10 +28,12 @@
 namespace qz {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kList = 2048;       // tokens that a CTA can list
 constexpr int kMaxCluster = 8;
-constexpr int kUnitBits = 44;  // the largest logit's weight is 2^44
+constexpr int kUnitBits = 44;     // the largest logit's weight is 2^44
+constexpr int kSliceBytes = 64 << 10;  // two CTAs an SM
 using u64 = unsigned long long;
 
 struct SampleParams {
@@ -154,34 +156,36 @@ struct Powers {
 
 // 2^44 e^{(x - m)/T}, to the nearest integer.  With t = (m - x) c as an fp32
 // pair, q = rint(32 t) and f = t - q/32: 2^-t = 2^-(q>>5) 2^-((q&31)/32) 2^-f, the
-// last by its series to f^4 (|f| <= 1/64: the next term is below 2^-39).
+// last by its series to f^4 (|f| <= 1/64: the next term is below 2^-39).  EXACT:
+// m - x loses nothing that matters (16-bit logits).
+template <bool EXACT>
 __device__ __forceinline__ u64 weight(const Scale &s, const Powers &pw, float x) {
   const float d = x == s.m ? 0.0f : s.m - x;
   const float t = d * s.c_hi;
-  if (!(t < 46.0f)) return 0;  // (x = -inf with c = 0 gives NaN)
-  // m - x is exact for 16-bit logits of like size; what fp32 lost else
-  const float xv = s.m - d;
-  const float e = (s.m - (d + xv)) + (xv - x);
-  const float lo = fmaf(d, s.c_lo, fmaf(d, s.c_hi, -t)) + (x == s.m ? 0.0f : e * s.c_hi);
+  float lo = fmaf(d, s.c_lo, fmaf(d, s.c_hi, -t));
+  if (!EXACT) {
+    const float xv = s.m - d;
+    const float e = (s.m - (d + xv)) + (xv - x);
+    lo = x == s.m ? 0.0f : fmaf(e, s.c_hi, lo);
+  }
   const float magic = 12582912.0f;  // 1.5 * 2^23
   const float qf = fmaf(t, 32.0f, magic);
   const int q = (int)(__float_as_uint(qf) & 0x3fffffu);
   const float f = fmaf(qf - magic, -0.03125f, t) + lo;
-  // 2^-f - 1, f = g / ln 2
-  const float g = -f * 0.69314718055994531f;
-  // (the product's own rounding, below 2^-30, aside)
-  float p = fmaf(g, 1.0f / 24.0f, 1.0f / 6.0f);
-  p = fmaf(g, p, 0.5f);
-  p = fmaf(g * g, p, g);
-  const int i = q & 31, n = q >> 5;
-  const int add = __float2int_rn(p * pw.flt[i]);  // below 2^31.6 / 64
+  // 2^-f - 1: powers of ln 2 over factorials
+  float p = fmaf(f, 9.6181291e-3f, -5.5504109e-2f);
+  p = fmaf(f, p, 2.4022651e-1f);
+  p = fmaf(f, p, -6.9314718e-1f) * f;
+  const int i = q & 31, n = min(q >> 5, 63);
+  const int add = __float2int_rn(p * pw.flt[i]);  // below 2^31
   const u64 w = pw.fix[i] + (u64)((long long)add * 128);
-  return n == 0 ? w : ((w >> (n - 1)) + 1) >> 1;
+  // (x = -inf with c = 0 gives NaN)
+  return t < 46.0f ? (w + ((1ull << n) >> 1)) >> n : 0;
 }
 
 __device__ __forceinline__ int bin_of(const Scale &s, float x) {
   const float t = (s.m - x) * s.bins;  // NaN for x = m = inf
-  return x == s.m ? 0 : (int)fminf(t, (float)(kBins - 1));
+  return x == s.m ? 0 : (int)fminf(t, (float)(kBins - 1));  // (fminf drops a NaN)
 }
 
 // v * f for 0 <= f < 1, rounded down (the rest in *more).
@@ -213,22 +217,29 @@ struct Cut {
 struct Shared {
   uint32_t count[kBins];
   u64 mass[kBins];
+  u64 list[kList];
   Powers pw;
-  uint32_t max_key;      // of this CTA's slice
-  u64 warp_mass[kWarps]; // kept weights above the cut, of every warp's tokens
-  u64 warp_ties[kWarps]; // tokens at the cut
+  uint32_t cta_max[kMaxCluster];  // largest key of every CTA's slice
+  uint32_t n_list;
+  u64 warp_mass[kWarps];  // kept weights above the cut, of every warp's tokens
+  u64 warp_ties[kWarps];  // tokens at the cut
+  u64 warp_all[kWarps];   // all weights
   u64 scan[kWarps];
-  u64 found[4];          // what the first CTA found: bin, sum before it, sum, count in it
+  u64 found[5];           // what the first CTA found, in every CTA
 };
 
 template <typename T>
 struct Row {
   Shared *sm;
-  const T *x;  // this CTA's tokens, in shared memory, padded with -inf to whole vectors
+  const T *x;  // this CTA's tokens, in shared memory, whole vectors
   int n, seg;  // how many; tokens of a warp
+  int first;   // the first one's index
   uint32_t rank, ranks;
 
-  // f(value, index in the slice) for this warp's tokens, lane by lane in order.
+  __device__ __forceinline__ void load(int i, float (&v)[Vec<T>::N]) const {
+    Vec<T>::get(*reinterpret_cast<const uint4 *>(x + i), v);
+  }
+  // f(value, index in the slice, place in its vector) for this warp's tokens.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     constexpr int N = Vec<T>::N;
@@ -236,11 +247,27 @@ struct Row {
     const int a = warp * seg, b = min(n, a + seg);
     for (int i = a + lane * N; i < b; i += 32 * N) {
       float v[N];
-      Vec<T>::get(*reinterpret_cast<const uint4 *>(x + i), v);
+      load(i, v);
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (i + j < b) f(clean(v[j]), i + j);
+        if (i + j < b) f(clean(v[j]), i + j, j);
     }
+  }
+  __device__ __forceinline__ void sync() const {
+    if (ranks > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
+  // What the first CTA's thread 0 has in found goes to all.
+  __device__ __forceinline__ void tell() const {
+    if (rank == 0) {
+      __syncthreads();
+      if (ranks > 1 && threadIdx.x < 5 * ranks)
+        st_remote64(remote(&sm->found[threadIdx.x % 5], threadIdx.x / 5),
+                    sm->found[threadIdx.x % 5]);
+    }
+    sync();
   }
 };
 
@@ -267,124 +294,110 @@ __device__ __forceinline__ u64 block_scan(Shared *sm, u64 v, u64 *total) {
   return before + in - v;
 }
 
-// The cut at which the running count (MASS: sum of weights) of the row's tokens
-// first reaches `target`; with MASS, of the tokens inside `in` only, and target
-// is that fraction of all of theirs.
-template <typename T, bool MASS>
-__device__ Cut find_cut(const Row<T> &r, const Scale &s, const Cut &in, u64 target, float fraction) {
+__device__ __forceinline__ u64 fraction_of(u64 total, float f) {  // rounded up, 1 at least
+  bool more;
+  const u64 v = times(total, f, &more);
+  return max(v + more, (u64)1);
+}
+
+__device__ __forceinline__ void add_mass(u64 *m, u64 w) {
+  const uint32_t lo = (uint32_t)w;
+  uint32_t *p = reinterpret_cast<uint32_t *>(m);
+  const uint32_t was = atomicAdd(p, lo);
+  const uint32_t hi = (uint32_t)(w >> 32) + (was + lo < lo ? 1u : 0u);
+  if (hi) atomicAdd(p + 1, hi);
+}
+
+// The cut at which the running count (MASS: sum of weights) of the tokens with keys in
+// [lo, hi] first reaches `target`; with MASS, of those inside `in` only, and with a
+// fraction >= 0 target is that fraction of all their weights.  each(f) calls f(value) for
+// this CTA's tokens, those outside [lo, hi] among them or not.  A histogram of 2048 steps
+// of the key, then of the steps in the one that was found.  False: they do not reach it.
+template <typename T, bool MASS, typename E>
+__device__ bool find_cut(const Row<T> &r, const Scale &s, E each, uint32_t lo, uint32_t hi,
+                         const Cut &in, u64 target, float fraction, Cut *cut) {
+  constexpr bool kExact = sizeof(T) == 2;
+  constexpr int kGrain = sizeof(T) == 4 ? 0 : 13;  // zeros behind a 16-bit value
   Shared *sm = r.sm;
-  constexpr int kLevels = 1 + (sizeof(T) == 4 ? 3 : 2);  // bins, then digits of the key
-  int bin = 0;            // found at level 0
-  uint32_t prefix = 0;    // digits of the key found since
-  int bits = 0;           // how many bits
-  u64 last = 0;           // the weight, or count, of one token at the cut
-  for (int level = 0; level < kLevels; ++level) {
-    const int take = level == 3 ? 10 : 11;
+  for (;;) {
+    const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
       sm->count[i] = 0;
       if (MASS) sm->mass[i] = 0;
     }
+    if (threadIdx.x == 0) sm->found[4] = 0;
     __syncthreads();
-    r.each([&](float x, int) {
+    each([&](float x) {
       const uint32_t key = key_of(x);
-      int b = bin_of(s, x);
-      if (MASS && key < in.key) return;
-      if (level > 0) {
-        if (b != bin || (level > 1 && key >> (32 - bits) != prefix)) return;
-        b = kBins - 1 - (int)((key >> (32 - bits - take)) & ((1u << take) - 1));
-      }
-      if (!MASS || key > in.key) atomicAdd(&sm->count[b], 1u);
-      if (MASS && key > in.key) {
-        const u64 w = weight(s, sm->pw, x);
-        if (w) {
-          const uint32_t lo = (uint32_t)w;
-          uint32_t *m = reinterpret_cast<uint32_t *>(&sm->mass[b]);
-          const uint32_t was = atomicAdd(m, lo);
-          const uint32_t hi = (uint32_t)(w >> 32) + (was + lo < lo ? 1u : 0u);
-          if (hi) atomicAdd(m + 1, hi);
-        }
+      if (key < lo || key > hi || (MASS && key <= in.key)) return;
+      const uint32_t b = (hi - key) >> shift;
+      atomicAdd(&sm->count[b], 1u);
+      if (MASS) {
+        const u64 w = weight<kExact>(s, sm->pw, x);
+        if (w) add_mass(&sm->mass[b], w);
       }
     });
-    // the tokens at the cut of `in`: so many of them, counted by the first CTA
     __syncthreads();
-    if (MASS && r.rank == 0 && threadIdx.x == 0) {
-      const float x = value_of(in.key);
-      int b = bin_of(s, x);
-      bool of = true;
-      if (level > 0) {
-        of = b == bin && (level == 1 || in.key >> (32 - bits) == prefix);
-        b = kBins - 1 - (int)((in.key >> (32 - bits - take)) & ((1u << take) - 1));
-      }
-      if (of) {
-        sm->count[b] += (uint32_t)in.ties;
-        sm->mass[b] += (u64)in.ties * weight(s, sm->pw, x);
-      }
+    // the tokens at the cut of `in`: so many of them, counted by the first CTA
+    if (MASS && r.rank == 0 && threadIdx.x == 0 && in.ties && in.key >= lo && in.key <= hi) {
+      const uint32_t b = (hi - in.key) >> shift;
+      sm->count[b] += (uint32_t)in.ties;
+      sm->mass[b] += (u64)in.ties * weight<kExact>(s, sm->pw, value_of(in.key));
     }
     if (r.ranks > 1) {
       cluster_sync();
-      if (r.rank != 0) {
-        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+      if (r.rank != 0)
+        for (int i = threadIdx.x; i < kBins; i += kThreads)
           if (sm->count[i]) {
             add_remote32(remote(&sm->count[i], 0), sm->count[i]);
             if (MASS) add_remote64(remote(&sm->mass[i], 0), sm->mass[i]);
           }
-        }
-      }
       cluster_sync();
     } else {
       __syncthreads();
     }
     if (r.rank == 0) {
-      constexpr int E = kBins / kThreads;
-      u64 v[E], sum = 0, total;
+      constexpr int P = kBins / kThreads;
+      u64 v[P], sum = 0, total;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = threadIdx.x * E + e;
+      for (int e = 0; e < P; ++e) {
+        const int i = threadIdx.x * P + e;
         v[e] = MASS ? sm->mass[i] : (u64)sm->count[i];
         sum += v[e];
       }
       u64 at = block_scan(sm, sum, &total);
-      if (MASS && level == 0) {
-        bool more;
-        target = times(total, fraction, &more);
-        target = max(target + more, (u64)1);
-      }
+      if (MASS && fraction >= 0.0f) target = fraction_of(total, fraction);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int e = 0; e < P; ++e) {
         if (at < target && target <= at + v[e]) {
-          sm->found[0] = (u64)(threadIdx.x * E + e);
+          sm->found[0] = (u64)(threadIdx.x * P + e);
           sm->found[1] = target - at;
           sm->found[2] = v[e];
-          sm->found[3] = sm->count[threadIdx.x * E + e];
+          sm->found[3] = sm->count[threadIdx.x * P + e];
+          sm->found[4] = 1;
         }
         at += v[e];
       }
-      __syncthreads();
-      if (r.ranks > 1 && threadIdx.x < 4 * r.ranks)
-        st_remote64(remote(&sm->found[threadIdx.x & 3], threadIdx.x >> 2),
-                    sm->found[threadIdx.x & 3]);
     }
-    if (r.ranks > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    r.tell();
     const uint32_t b = (uint32_t)sm->found[0];
+    const u64 in_bin = sm->found[2], n = sm->found[3];
+    const bool ok = sm->found[4] != 0;
     target = sm->found[1];
-    last = sm->found[3] ? sm->found[2] / sm->found[3] : 0;
-    if (level == 0) {
-      bin = (int)b;
-    } else {
-      prefix = (prefix << take) | (uint32_t)(kBins - 1 - b);
-      bits += take;
-    }
+    fraction = -1.0f;
     __syncthreads();
+    if (!ok) return false;
+    hi -= b << shift;
+    lo = max(lo, hi - ((1u << shift) - 1));
+    if (shift <= kGrain) {
+      // one value is left: zeros (or, of a negative one's key, ones) behind it
+      const uint32_t rest = (1u << kGrain) - 1;
+      cut->key = shift == 0 ? hi : hi & 0x80000000u ? hi & ~rest : ((hi + 1) & ~rest) - 1;
+      const u64 one = MASS ? max(in_bin / max(n, (u64)1), (u64)1) : 1;
+      cut->ties = (int)((target + one - 1) / one);
+      return true;
+    }
   }
-  Cut c;
-  // a 16-bit value has zeros in the bits that are left, a negative one's key has ones
-  const int rest = 32 - bits;
-  c.key = rest == 0 ? prefix : prefix << rest | (prefix >> (bits - 1) ? 0u : (1u << rest) - 1);
-  c.ties = MASS ? (int)((target + last - 1) / max(last, (u64)1)) : (int)target;
-  return c;
 }
 
 // The shorter of two prefixes.
@@ -393,9 +406,101 @@ __device__ __forceinline__ Cut shorter(const Cut &a, const Cut &b) {
   return a.ties < b.ties ? a : b;
 }
 
+// Sorts n <= kList numbers in shared memory, padded to a power of two (one CTA).
+__device__ __forceinline__ void sort_list(u64 *v, int n) {
+  int size = 2;
+  while (size < n) size *= 2;
+  for (int i = n + (int)threadIdx.x; i < size; i += kThreads) v[i] = ~0ull;
+  for (int k = 2; k <= size; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+        const int a = 2 * i - (i & (j - 1)), b = a + j;
+        const u64 x = v[a], y = v[b];
+        if ((x > y) == ((a & k) == 0)) v[a] = y, v[b] = x;
+      }
+    }
+  __syncthreads();
+}
+
+// A row's options.
+struct Options {
+  float temp, top_p, min_p;
+  int top_k;
+  bool greedy;
+  uint32_t min_key;  // of min_p, 0: none
+};
+
+__device__ __forceinline__ void answer(const SampleParams &p, int64_t row, int token, float x,
+                                       const Scale &s, const Options &o, u64 total) {
+  p.token[row] = token;
+  if (!p.logprob) return;
+  const double z = x == s.m || o.greedy ? 0.0 : ((double)x - (double)s.m) / (double)o.temp;
+  p.logprob[row] = (float)(z - log((double)total / (double)(1ull << kUnitBits)));
+}
+
+// The whole choice from the list of all tokens that any filter may keep, n in the first
+// CTA's shared memory as (~key, index): in order of value for the filters, then of index.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p) {
+__device__ void solve_list(const SampleParams &p, const Row<T> &r, const Scale &s,
+                           const Options &o, int64_t row, int n) {
+  constexpr bool kExact = sizeof(T) == 2;
+  constexpr int P = kList / kThreads;
+  Shared *sm = r.sm;
+  sort_list(sm->list, n);
+  auto value = [&](int i) { return value_of(~(uint32_t)(sm->list[i] >> 32)); };
+  const int a = threadIdx.x * P;
+  int kept = o.top_k > 0 ? min(n, o.top_k) : n;
+  if (o.top_p < 1.0f) {
+    u64 w[P], sum = 0, total;
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      w[e] = a + e < kept ? weight<kExact>(s, sm->pw, value(a + e)) : 0;
+      sum += w[e];
+    }
+    u64 at = block_scan(sm, sum, &total);
+    const u64 target = fraction_of(total, fmaxf(o.top_p, 0.0f));
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      if (at < target && target <= at + w[e]) sm->found[0] = (u64)(a + e + 1);
+      at += w[e];
+    }
+    __syncthreads();
+    kept = (int)sm->found[0];
+  }
+  if (o.min_key) {
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < P; ++e) mine += a + e < kept && key_of(value(a + e)) >= o.min_key;
+    u64 total;
+    block_scan(sm, (u64)mine, &total);
+    kept = (int)total;
+  }
+  for (int i = threadIdx.x; i < kept; i += kThreads)
+    sm->mass[i] = (sm->list[i] << 32) | (u64)i;
+  sort_list(sm->mass, kept);
+  u64 w[P], sum = 0, total;
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    w[e] = a + e < kept ? weight<kExact>(s, sm->pw, value((int)(uint32_t)sm->mass[a + e])) : 0;
+    sum += w[e];
+  }
+  u64 at = block_scan(sm, sum, &total);
+  bool more;
+  const u64 goal = times(total, fminf(fmaxf(p.u[row], 0.0f), 0.99999994f), &more);
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    if (at <= goal && goal < at + w[e])
+      answer(p, row, (int)(sm->mass[a + e] >> 32), value((int)(uint32_t)sm->mass[a + e]), s, o,
+             total);
+    at += w[e];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   constexpr int N = Vec<T>::N;
+  constexpr bool kExact = sizeof(T) == 2;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared *sm = reinterpret_cast<Shared *>(smem);
   T *slice = reinterpret_cast<T *>(smem + (sizeof(Shared) + 15) / 16 * 16);
@@ -406,201 +511,364 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
   r.rank = cluster_rank();
   r.ranks = cluster_size();
   const int64_t row = blockIdx.x / r.ranks;
-  const int first = (int)r.rank * p.slice;
-  r.n = max(0, min(p.V - first, p.slice));
+  r.first = (int)r.rank * p.slice;
+  r.n = max(0, min(p.V - r.first, p.slice));
   r.seg = (r.n + kWarps * 32 * N - 1) / (kWarps * 32 * N) * (32 * N);
-  if (threadIdx.x < 32) {
-    const double e = exp2(-(double)threadIdx.x / 32.0);
-    sm->pw.fix[threadIdx.x] = (u64)rint(e * (double)(1ull << kUnitBits));
-    sm->pw.flt[threadIdx.x] = (float)(e * (double)(1ull << (kUnitBits - 7)));
-  }
-  if (threadIdx.x == 0) sm->max_key = 0;
-  __syncthreads();
 
-  // ---- the slice, and its largest logit
-  const T *src = static_cast<const T *>(p.logits) + row * p.ld + first;
-  float m = -INFINITY;
+  // ---- the slice, and the largest logit of each of four groups a thread
+  const T *src = static_cast<const T *>(p.logits) + row * p.ld + r.first;
+  float g[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   if (p.vec) {
-    for (int i = threadIdx.x * N; i < r.n; i += kThreads * N) {
-      uint4 w;
-      if (i + N <= r.n) {
-        w = __ldcs(reinterpret_cast<const uint4 *>(src + i));
-        float v[N];
-        Vec<T>::get(w, v);
+    constexpr int U = 4;  // loads ahead of their uses
+    for (int i = threadIdx.x * N; i < r.n; i += kThreads * N * U) {
+      uint4 w[U];
 #pragma unroll
-        for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
-        *reinterpret_cast<uint4 *>(slice + i) = w;
-      } else {
-        for (int j = 0; i + j < r.n; ++j) {
-          slice[i + j] = src[i + j];
-          m = fmaxf(m, (float)src[i + j]);
+      for (int k = 0; k < U; ++k)
+        if (i + k * kThreads * N + N <= r.n)
+          w[k] = __ldcs(reinterpret_cast<const uint4 *>(src + i + k * kThreads * N));
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int at = i + k * kThreads * N;
+        if (at + N <= r.n) {
+          float v[N];
+          Vec<T>::get(w[k], v);
+#pragma unroll
+          for (int j = 0; j < N; ++j) g[j & 3] = fmaxf(g[j & 3], v[j]);
+          *reinterpret_cast<uint4 *>(slice + at) = w[k];
+        } else {
+          for (int j = at; j < r.n; ++j) {
+            slice[j] = src[j];
+            g[0] = fmaxf(g[0], (float)src[j]);
+          }
         }
       }
     }
   } else {
     for (int i = threadIdx.x; i < r.n; i += kThreads) {
       slice[i] = src[i];
-      m = fmaxf(m, (float)src[i]);
+      g[0] = fmaxf(g[0], (float)src[i]);
     }
   }
-  const uint32_t k = __reduce_max_sync(0xffffffffu, key_of(clean(m)));
-  if (lane == 0) atomicMax(&sm->max_key, k);
-  __syncthreads();
-  uint32_t max_key = sm->max_key;
-  if (r.ranks > 1) {
-    cluster_sync();
-    for (uint32_t i = 0; i < r.ranks; ++i)
-      max_key = max(max_key, ld_remote32(remote(&sm->max_key, i)));
+  if (threadIdx.x < 32) {
+    const double e = exp2(-(double)threadIdx.x / 32.0);
+    sm->pw.fix[threadIdx.x] = (u64)rint(e * (double)(1ull << kUnitBits));
+    sm->pw.flt[threadIdx.x] = (float)(e * (double)(1ull << (kUnitBits - 7)));
   }
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm->count[i] = 0, sm->mass[i] = 0;
+  if (threadIdx.x == 0) sm->n_list = 0;
+  const uint32_t top = __reduce_max_sync(
+      0xffffffffu, key_of(clean(fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3])))));
+  if (lane == 0) sm->scan[warp] = top;
+  __syncthreads();
+  if (threadIdx.x < r.ranks) {  // this CTA's to all
+    uint32_t k = 0;
+    for (int w = 0; w < kWarps; ++w) k = max(k, (uint32_t)sm->scan[w]);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                     remote(&sm->cta_max[r.rank], threadIdx.x)),
+                 "r"(k)
+                 : "memory");
+  }
+  r.sync();
+  uint32_t max_key = 0;
+  for (uint32_t i = 0; i < r.ranks; ++i) max_key = max(max_key, sm->cta_max[i]);
   Scale s;
   s.m = value_of(max_key);
 
   // ---- the row's options
-  const float temp = p.temperature ? p.temperature[row] : p.temperature_all;
-  const float top_p = p.top_p ? p.top_p[row] : p.top_p_all;
-  const float min_p = p.min_p ? p.min_p[row] : p.min_p_all;
-  int top_k = p.top_k ? p.top_k[row] : p.top_k_all;
-  const bool greedy = !(temp > 0.0f);
-  if (greedy) top_k = 1;
-  const double c = greedy ? 1.0 : 1.4426950408889634074 / (double)temp;
+  Options o;
+  o.temp = p.temperature ? p.temperature[row] : p.temperature_all;
+  o.top_p = p.top_p ? p.top_p[row] : p.top_p_all;
+  o.min_p = p.min_p ? p.min_p[row] : p.min_p_all;
+  o.top_k = p.top_k ? p.top_k[row] : p.top_k_all;
+  o.greedy = !(o.temp > 0.0f);
+  if (o.top_k >= p.V) o.top_k = 0;
+  const double c = o.greedy ? 1.0 : 1.4426950408889634074 / (double)o.temp;
   s.c_hi = (float)fmin(c, (double)FLT_MAX);
   s.c_lo = c < 1e30 ? (float)(c - (double)s.c_hi) : 0.0f;
   s.bins = fminf(fmaxf(16.0f * s.c_hi, 32.0f), 75.0f);
+  o.min_key = 0;
+  if (o.min_p > 0.0f) {
+    // x >= m + T ln(min_p), compared in 64 bits; the smallest fp32 value that is
+    const double least =
+        o.min_p < 1.0f ? (double)s.m + (double)o.temp * log((double)o.min_p) : (double)s.m;
+    float v = (float)least;
+    if ((double)v < least) v = nextafterf(v, INFINITY);
+    o.min_key = s.m == INFINITY ? max_key : key_of(clean(v));
+  }
 
   if (s.m == -INFINITY) {  // no token may be chosen
     if (r.rank == 0 && threadIdx.x == 0) {
       p.token[row] = -1;
       if (p.logprob) p.logprob[row] = -INFINITY;
     }
-  } else {
-    Cut cut = {0, 0};  // every token
-    if (top_k == 1) {
-      cut = {max_key, 1};
+    if (r.ranks > 1) cluster_sync();
+    return;
+  }
+
+  const bool one = o.greedy || o.top_k == 1;
+  const bool small = p.V <= kList && r.ranks == 1 && !one;
+  bool listed = small;  // the first CTA's list holds all that may be kept
+  int n_listed = p.V;
+  auto entry = [&](float x, int i) {
+    return (u64)(uint32_t)~key_of(x) << 32 | (u64)(uint32_t)(r.first + i);
+  };
+  if (small) r.each([&](float x, int i, int) { sm->list[i] = entry(x, i); });
+  __syncthreads();
+
+  // ---- what the first CTA looks for in a histogram of distances from the maximum: top-k,
+  // a bin up to which that many groups have their largest; else top-p, the bin of its cut
+  const bool by_k = !one && !small && o.top_k > 0;
+  const bool by_p = !one && !small && o.top_k <= 0 && o.top_p < 1.0f;
+  bool found = false;
+  float edge_hi = 0.0f, edge_lo = 0.0f;  // values that bound what was found
+  if (by_k || by_p) {
+    uint32_t *mine = r.rank == 0 ? reinterpret_cast<uint32_t *>(sm->mass) : sm->count;
+    if (by_k) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (g[j] > -INFINITY) atomicAdd(&mine[bin_of(s, clean(g[j]))], 1u);
     } else {
-      if (top_k > 0 && top_k < p.V)
-        cut = find_cut<T, false>(r, s, cut, (u64)top_k, 0.0f);
-      Cut last = cut;
-      if (top_p < 1.0f)
-        last = find_cut<T, true>(r, s, cut, 0, fmaxf(top_p, 0.0f));
-      if (min_p > 0.0f) {
-        // x >= m + T ln(min_p), compared in 64 bits; the smallest fp32 value that is
-        const double least = min_p < 1.0f ? (double)s.m + (double)temp * log((double)min_p)
-                                          : (double)s.m;
-        float v = (float)least;
-        if ((double)v < least) v = nextafterf(v, INFINITY);
-        const Cut b = {s.m == INFINITY ? max_key : key_of(clean(v)), INT32_MAX};
-        last = shorter(last, b);
-      }
-      cut = last;
+      // tokens within six octaves of the maximum, and one in four of the others
+      const float near = 6.0f / s.c_hi * s.bins;
+      r.each([&](float x, int, int j) {
+        const int b = bin_of(s, x);
+        const bool close = (float)b < near;
+        if (close || (j & 3) == 0) atomicAdd(&mine[b], close ? 1u : 4u);
+      });
     }
-    // ---- kept weights and tokens at the cut, warp by warp
+    __syncthreads();
+    if (r.ranks > 1) {
+      if (r.rank != 0)
+        for (int i = threadIdx.x; i < kBins; i += kThreads)
+          if (mine[i]) add_remote32(remote(&sm->count[i], 0), mine[i]);
+      cluster_sync();
+    }
+    if (r.rank == 0) {
+      constexpr int P = kBins / kThreads;
+      u64 v[P], sum = 0, total;
+      const float step = s.c_hi / s.bins;  // octaves of a bin
+      if (threadIdx.x == 0) sm->found[4] = 0;
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const int i = threadIdx.x * P + e;
+        const uint32_t k = mine[i] + sm->count[i];
+        v[e] = by_k ? (u64)k : (u64)((float)k * exp2f(40.0f - ((float)i + 0.5f) * step));
+        sum += v[e];
+      }
+      u64 at = block_scan(sm, sum, &total);
+      const u64 target = by_k ? (u64)o.top_k : fraction_of(total, fmaxf(o.top_p, 0.0f));
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const int i = threadIdx.x * P + e;
+        // (the last bin holds everything further away)
+        if (at < target && target <= at + v[e] && i < kBins - 4) {
+          sm->found[0] = (u64)i;
+          sm->found[4] = 1;
+        }
+        at += v[e];
+      }
+    }
+    r.tell();
+    found = sm->found[4] != 0;
+    const float b = (float)sm->found[0];
+    // one bin further down for what rounding may have moved; for top-p two to each side
+    edge_lo = s.m - (b + (by_k ? 1.1f : 3.0f)) / s.bins;
+    edge_hi = by_k || b < 3.0f ? INFINITY : s.m - (b - 2.0f) / s.bins;
+    found = found && s.m < INFINITY;
+    __syncthreads();
+  }
+
+  // ---- top-k: the tokens that may be among them, to the first CTA's list
+  if (by_k && found) {
+    r.each([&](float x, int i, int) {
+      if (x >= edge_lo) {
+        const uint32_t at = atomicAdd(&sm->n_list, 1u);
+        if (at < kList) sm->list[at] = entry(x, i);
+      }
+    });
+    r.sync();
+    uint32_t n = 0;
+    for (uint32_t i = 0; i < r.ranks; ++i) n += ld_remote32(remote(&sm->n_list, i));
+    listed = n <= kList && n >= (uint32_t)o.top_k;
+    n_listed = (int)n;
+    if (listed && r.rank == 0) {
+      uint32_t at = sm->n_list;
+      for (uint32_t i = 1; i < r.ranks; ++i) {
+        const uint32_t k = ld_remote32(remote(&sm->n_list, i)), from = remote(sm->list, i);
+        for (uint32_t j = threadIdx.x; j < k; j += kThreads)
+          sm->list[at + j] = ld_remote64(from + j * 8);
+        at += k;
+      }
+    }
+    __syncthreads();
+  }
+  if (listed) {
+    if (r.rank == 0) solve_list(p, r, s, o, row, n_listed);
+    if (r.ranks > 1) cluster_sync();  // the first CTA has read the others' lists
+    return;
+  }
+
+  // ---- the cut
+  Cut cut = {0, 0};      // every token
+  bool summed = false;   // the weights above the cut are, warp by warp
+  auto slice_each = [&](auto f) { r.each([&](float x, int, int) { f(x); }); };
+  if (one) {
+    cut = {max_key, 1};
+  } else {
+    if (o.top_k > 0)
+      find_cut<T, false>(r, s, slice_each, 0u, max_key, cut, (u64)o.top_k, -1.0f, &cut);
+    Cut last = cut;
+    if (o.top_p < 1.0f) {
+      bool done = false;
+      if (by_p && found) {
+        // all weights, those above the bins around the cut, and a list of those in them
+        const uint32_t key_hi = edge_hi == INFINITY ? max_key : key_of(clean(edge_hi));
+        const uint32_t key_lo = key_of(clean(edge_lo));
+        const bool none = edge_hi == INFINITY;  // above them
+        u64 all = 0, above = 0;
+        r.each([&](float x, int i, int) {
+          const u64 w = weight<kExact>(s, sm->pw, x);
+          all += w;
+          const bool over = !none && x > edge_hi;
+          above += over ? w : 0;
+          if (!over && x >= edge_lo) {
+            const uint32_t at = atomicAdd(&sm->n_list, 1u);
+            if (at < kList) sm->list[at] = entry(x, i);
+          }
+        });
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          all += __shfl_xor_sync(0xffffffffu, all, d);
+          above += __shfl_xor_sync(0xffffffffu, above, d);
+        }
+        if (lane == 0) {
+          sm->warp_all[warp] = all;
+          sm->warp_mass[warp] = above;
+          sm->warp_ties[warp] = 0;
+        }
+        r.sync();
+        u64 t_all = 0, t_above = 0, total, total_above;
+        bool full = false;
+        if (threadIdx.x < kWarps * r.ranks) {
+          t_all = ld_remote64(remote(&sm->warp_all[threadIdx.x % kWarps], threadIdx.x / kWarps));
+          t_above =
+              ld_remote64(remote(&sm->warp_mass[threadIdx.x % kWarps], threadIdx.x / kWarps));
+          full = ld_remote32(remote(&sm->n_list, threadIdx.x / kWarps)) > kList;
+        }
+        full = __syncthreads_or(full);
+        block_scan(sm, t_all, &total);
+        block_scan(sm, t_above, &total_above);
+        const u64 target = fraction_of(total, fmaxf(o.top_p, 0.0f));
+        if (!full && total_above < target) {
+          const int n = (int)sm->n_list;
+          auto list_each = [&](auto f) {
+            for (int i = threadIdx.x; i < n; i += kThreads)
+              f(value_of(~(uint32_t)(sm->list[i] >> 32)));
+          };
+          done = find_cut<T, true>(r, s, list_each, key_lo, key_hi, Cut{0, 0},
+                                   target - total_above, -1.0f, &last);
+          if (done && (o.min_key == 0 || o.min_key <= last.key)) {
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+              const uint32_t key = ~(uint32_t)(sm->list[i] >> 32);
+              const int w = ((int)(uint32_t)sm->list[i] - r.first) / r.seg;
+              if (key > last.key)
+                add_mass(&sm->warp_mass[w], weight<kExact>(s, sm->pw, value_of(key)));
+              else if (key == last.key)
+                add_mass(&sm->warp_ties[w], 1);
+            }
+            summed = true;
+          }
+        }
+      }
+      if (!done)
+        find_cut<T, true>(r, s, slice_each, 0u, max_key, cut, 0, fmaxf(o.top_p, 0.0f), &last);
+    }
+    if (o.min_key) last = shorter(last, Cut{o.min_key, INT32_MAX});
+    cut = last;
+  }
+
+  // ---- kept weights and tokens at the cut, warp by warp
+  if (!summed) {
     u64 mass = 0;
     uint32_t ties = 0;
-    r.each([&](float x, int) {
+    r.each([&](float x, int, int) {
       const uint32_t key = key_of(x);
       if (key > cut.key)
-        mass += weight(s, sm->pw, x);
+        mass += weight<kExact>(s, sm->pw, x);
       else
         ties += key == cut.key;
     });
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    for (int d = 16; d > 0; d >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, d);
     ties = __reduce_add_sync(0xffffffffu, ties);
     if (lane == 0) {
       sm->warp_mass[warp] = mass;
       sm->warp_ties[warp] = ties;
     }
-    if (r.ranks > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-    // Every CTA sums all of them; thread i has warp i of the row.
-    const u64 cut_weight = weight(s, sm->pw, value_of(cut.key));
-    const bool live = threadIdx.x < kWarps * r.ranks;
-    u64 w_mass = 0, w_ties = 0, all;
-    if (live) {
-      w_mass = ld_remote64(remote(&sm->warp_mass[threadIdx.x % kWarps], threadIdx.x / kWarps));
-      w_ties = ld_remote64(remote(&sm->warp_ties[threadIdx.x % kWarps], threadIdx.x / kWarps));
-    }
-    const u64 t_before = block_scan(sm, w_ties, &all);
-    const u64 left = (u64)cut.ties > t_before ? (u64)cut.ties - t_before : 0;
-    const u64 mine = w_mass + min(w_ties, left) * cut_weight;
-    u64 total;
-    const u64 before = block_scan(sm, mine, &total);
-    const float u = fminf(fmaxf(p.u[row], 0.0f), 0.99999994f);
-    bool more;
-    const u64 goal = times(total, u, &more);  // the first running sum above it
-    if (live && before <= goal && goal < before + mine) {
-      sm->found[0] = threadIdx.x;
-      sm->found[1] = goal - before;
-      sm->found[2] = left;
-    }
-    __syncthreads();
-    const int at = (int)sm->found[0];
-    if (at / kWarps == (int)r.rank && at % kWarps == warp) {
-      // this warp's tokens again, 32 lanes of N at a time
-      u64 want = sm->found[1], rest = sm->found[2];
-      const int a = warp * r.seg, b = min(r.n, a + r.seg);
-      for (int i = a + lane * N; i - lane * N < b; i += 32 * N) {
-        float v[N];
-        Vec<T>::get(*reinterpret_cast<const uint4 *>(slice + min(i, p.slice - N)), v);
-        uint32_t t = 0;
-        u64 w[N], sum = 0;
+  }
+  r.sync();
+  // Every CTA sums all of them; thread i has warp i of the row.
+  const u64 cut_weight = cut.key ? weight<kExact>(s, sm->pw, value_of(cut.key)) : 0;
+  const bool live = threadIdx.x < kWarps * r.ranks;
+  u64 w_mass = 0, w_ties = 0, total;
+  if (live) {
+    w_mass = ld_remote64(remote(&sm->warp_mass[threadIdx.x % kWarps], threadIdx.x / kWarps));
+    w_ties = ld_remote64(remote(&sm->warp_ties[threadIdx.x % kWarps], threadIdx.x / kWarps));
+  }
+  const u64 t_before = block_scan(sm, w_ties, &total);
+  const u64 left = (u64)cut.ties > t_before ? (u64)cut.ties - t_before : 0;
+  const u64 mine = w_mass + min(w_ties, left) * cut_weight;
+  const u64 before = block_scan(sm, mine, &total);
+  bool more;
+  const u64 goal = times(total, fminf(fmaxf(p.u[row], 0.0f), 0.99999994f), &more);
+  if (live && before <= goal && goal < before + mine) {
+    sm->found[0] = threadIdx.x;
+    sm->found[1] = goal - before;
+    sm->found[2] = left;
+  }
+  __syncthreads();
+  const int at = (int)sm->found[0];
+  if (at / kWarps == (int)r.rank) {
+    // that warp's tokens again, by all threads
+    u64 want = sm->found[1], rest = sm->found[2];
+    const int a = at % kWarps * r.seg, b = min(r.n, a + r.seg);
+    for (int i0 = a; i0 < b; i0 += kThreads * N) {
+      const int i = i0 + (int)threadIdx.x * N;
+      float v[N];
+      r.load(min(i, p.slice - N), v);
+      u64 w[N], sum = 0, t = 0, all_t, all_w;
 #pragma unroll
-        for (int j = 0; j < N; ++j) t += i + j < b && key_of(clean(v[j])) == cut.key;
-        uint32_t t_in = t;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t z = __shfl_up_sync(0xffffffffu, t_in, o);
-          if (lane >= o) t_in += z;
+      for (int j = 0; j < N; ++j) {
+        v[j] = clean(v[j]);
+        t += i + j < b && key_of(v[j]) == cut.key;
+      }
+      u64 t_at = block_scan(sm, t, &all_t);  // tokens at the cut before this thread's
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t key = key_of(v[j]);
+        w[j] = 0;
+        if (i + j < b) {
+          if (key > cut.key) {
+            w[j] = weight<kExact>(s, sm->pw, v[j]);
+          } else if (key == cut.key) {
+            if (t_at < rest) w[j] = cut_weight;
+            ++t_at;
+          }
         }
-        u64 t_at = t_in - t;  // tokens at the cut before this lane's
+        sum += w[j];
+      }
+      u64 run = block_scan(sm, sum, &all_w);
+      if (want < all_w) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          const uint32_t key = key_of(clean(v[j]));
-          w[j] = 0;
-          if (i + j < b) {
-            if (key > cut.key) {
-              w[j] = weight(s, sm->pw, clean(v[j]));
-            } else if (key == cut.key) {
-              if (t_at < rest) w[j] = cut_weight;
-              ++t_at;
-            }
-          }
-          sum += w[j];
+          if (run <= want && want < run + w[j])
+            answer(p, row, r.first + i + j, v[j], s, o, total);
+          run += w[j];
         }
-        u64 in = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 z = __shfl_up_sync(0xffffffffu, in, o);
-          if (lane >= o) in += z;
-        }
-        const u64 lane_at = in - sum;
-        const uint32_t hit = __ballot_sync(0xffffffffu, lane_at <= want && want < in);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            u64 run = lane_at;
-            bool done = false;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-              run += w[j];
-              if (!done && run > want) {
-                done = true;
-                const float x = clean(v[j]);
-                p.token[row] = first + i + j;
-                if (p.logprob) {
-                  const double z = x == s.m || greedy ? 0.0 : ((double)x - (double)s.m) / (double)temp;
-                  p.logprob[row] =
-                      (float)(z - log((double)total / (double)(1ull << kUnitBits)));
-                }
-              }
-            }
-          }
-          break;
-        }
-        const u64 all_w = __shfl_sync(0xffffffffu, in, 31);
-        const uint32_t all_t = __shfl_sync(0xffffffffu, t_in, 31);
-        want -= all_w;
-        rest = rest > all_t ? rest - all_t : 0;
+        break;
       }
+      want -= all_w;
+      rest = rest > all_t ? rest - all_t : 0;
     }
   }
   if (r.ranks > 1) cluster_sync();  // others may still read this CTA's shared memory
@@ -613,18 +881,17 @@ qz_status launch(SampleParams p, int64_t B, cudaStream_t s) {
   if (st != QZ_OK) return st;
   constexpr int N = Vec<T>::N;
   const size_t head = (sizeof(Shared) + 15) / 16 * 16;
-  int ranks = 1;
-  // CTAs of a row: while they have 4096 tokens each and the GPU is not full, and as many
-  // as their shared memory asks for
+  // CTAs of a row: as many as let two of them share an SM, and more while they have 2048
+  // tokens each and the GPU is not full
   auto slice_of = [&](int n) { return ((p.V + n - 1) / n + N - 1) / N * N; };
-  auto bytes_of = [&](int n) { return head + (size_t)slice_of(n) * sizeof(T); };
+  auto bytes_of = [&](int n) { return (size_t)slice_of(n) * sizeof(T); };
+  int ranks = 1;
   while (ranks < kMaxCluster &&
-         (bytes_of(ranks) > (size_t)di.max_smem_optin ||
-          (B * ranks < 2 * di.sms && p.V / ranks > 8192)))
+         (bytes_of(ranks) > kSliceBytes || (B * ranks <= di.sms && p.V > 2048 * ranks)))
     ranks *= 2;
-  if (bytes_of(ranks) > (size_t)di.max_smem_optin) return QZ_ERR_UNSUPPORTED;
   p.slice = slice_of(ranks);
-  const size_t smem = bytes_of(ranks);
+  const size_t smem = head + bytes_of(ranks);
+  if (smem > (size_t)di.max_smem_optin) return QZ_ERR_UNSUPPORTED;
   const cudaError_t e = allow_smem<sample_kernel<T>>(smem);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
