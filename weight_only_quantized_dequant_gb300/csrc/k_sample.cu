@@ -28,7 +28,7 @@
 namespace qz {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 2048;       // tokens that a CTA can list
 constexpr int kMaxCluster = 8;
@@ -143,16 +143,57 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 
 // What a row's tokens are weighed and binned by.
 struct Scale {
-  float m;          // largest logit
-  float c_hi, c_lo; // log2(e) / T
-  float bins;       // bins per unit of the logits
+  float m;           // largest logit
+  float c_hi, c_lo;  // log2(e) / T
+  float bins;        // bins per unit of the logits
 };
 
-// 2^(i/32), i < 32, in units of 2^-44 and as 2^37 times the value (shared memory).
-struct Powers {
+// 2^(-i/32), i < 32, in units of 2^-44 (and, as fp32, of 2^-37).
+__constant__ u64 kPower[32] = {
+    17592186044416ull, 17215221774115ull, 16846335070792ull, 16485352848846ull, 16132105731538ull,
+    15786427971528ull, 15448157373097ull, 15117135216047ull, 14793206181226ull, 14476218277651ull,
+    14166022771192ull, 13862474114787ull, 13565429880144ull, 13274750690919ull, 12990300157313ull,
+    12711944812080ull, 12439554047902ull, 12173000056107ull, 11912157766698ull, 11656904789672ull,
+    11407121357589ull, 11162690269381ull, 10923496835354ull, 10689428823381ull, 10460376406236ull,
+    10236232110063ull, 10016890763953ull, 9802249450589ull, 9592207457961ull, 9386666232110ull,
+    9185529330885ull, 8988702378691ull,
+};
+struct Powers {  // in shared memory
   u64 fix[32];
   float flt[32];
 };
+
+// A number near 1 / (1 + (i + 1/2) / 32), and minus its logarithm.
+__constant__ double kLog[32][2] = {
+    {0.9846153846153847, 0.015504186535965199}, {0.9552238805970149, 0.04580953603129422},
+    {0.927536231884058, 0.07522342123758752}, {0.9014084507042254, 0.10379679368164355},
+    {0.8767123287671232, 0.13157635778871932}, {0.8533333333333334, 0.15860503017663852},
+    {0.8311688311688312, 0.18492233849401193}, {0.810126582278481, 0.21056476910734964},
+    {0.7901234567901234, 0.23556607131276697}, {0.7710843373493976, 0.259957524436926},
+    {0.7529411764705882, 0.2837681731306446}, {0.735632183908046, 0.3070250352949119},
+    {0.7191011235955056, 0.32975328637246804}, {0.7032967032967034, 0.3519764231571781},
+    {0.6881720430107527, 0.373716409793584}, {0.6736842105263158, 0.394993808240869},
+    {0.6597938144329897, 0.415827895143711}, {0.6464646464646465, 0.43623676677491796},
+    {0.6336633663366337, 0.4562374334815876}, {0.6213592233009708, 0.475845904869964},
+    {0.6095238095238096, 0.4950772667978514}, {0.5981308411214953, 0.5139457511022344},
+    {0.5871559633027523, 0.5324647988694717}, {0.5765765765765766, 0.5506471179526623},
+    {0.5663716814159292, 0.5685047353526688}, {0.5565217391304348, 0.5860490450035782},
+    {0.5470085470085471, 0.6032908514380841}, {0.5378151260504201, 0.6202404097518576},
+    {0.5289256198347108, 0.6369074622370692}, {0.5203252032520326, 0.6533012720127456},
+    {0.512, 0.6694306539426292}, {0.5039370078740157, 0.6853040030989195},
+};
+// ln(total / 2^44) to 2^-38: total = 2^e z, r = z kLog - 1 (|r| < 1/60) by its series.
+__device__ __forceinline__ double log_total(u64 total) {
+  const int e = 63 - __clzll(total);
+  const double z = (double)total * __hiloint2double((1023 - e) << 20, 0);
+  const int i = (__double2hiint(z) >> 15) & 31;
+  const double r = fma(z, kLog[i][0], -1.0);
+  double s = fma(r, 0.2, -0.25);
+  s = fma(r, s, 1.0 / 3.0);
+  s = fma(r, s, -0.5);
+  s = fma(r * r, s, r);
+  return fma((double)(e - kUnitBits), 0.69314718055994530942, kLog[i][1] + s);
+}
 
 // 2^44 e^{(x - m)/T}, to the nearest integer.  With t = (m - x) c as an fp32
 // pair, q = rint(32 t) and f = t - q/32: 2^-t = 2^-(q>>5) 2^-((q&31)/32) 2^-f, the
@@ -214,11 +255,49 @@ struct Cut {
   int ties;
 };
 
+// A row's options, and what follows from them alone.
+struct Options {
+  float temp, top_p, min_p;
+  int top_k;
+  float c_hi, c_lo;  // log2(e) / T, 1 where the largest logit is taken
+  float l_hi, l_lo;  // T ln(min_p), for 0 < min_p < 1
+};
+__device__ __forceinline__ Options read_options(const SampleParams &p, int64_t row) {
+  Options o;
+  o.temp = p.temperature ? p.temperature[row] : p.temperature_all;
+  o.top_p = p.top_p ? p.top_p[row] : p.top_p_all;
+  o.min_p = p.min_p ? p.min_p[row] : p.min_p_all;
+  o.top_k = p.top_k ? p.top_k[row] : p.top_k_all;
+  if (!(o.temp > 0.0f)) o.temp = 0.0f;
+  // the quotient's fp32 remainder is exact: (c_hi + c_lo) T = log2(e) to 2^-46
+  o.c_hi = 1.0f, o.c_lo = 0.0f;
+  if (o.temp > 0.0f) {
+    o.c_hi = fminf(__fdiv_rn(1.44269502e+00f, o.temp), FLT_MAX);
+    const float left = fmaf(-o.c_hi, o.temp, 1.44269502e+00f) + 1.92596303e-08f;
+    o.c_lo = o.c_hi < 1e30f && o.c_hi > 1e-30f ? __fdiv_rn(left, o.temp) : 0.0f;
+  }
+  o.l_hi = o.l_lo = 0.0f;
+  if (o.temp > 0.0f && o.min_p > 0.0f && o.min_p < 1.0f) {
+    const double l = (double)o.temp * log((double)o.min_p);
+    o.l_hi = (float)l;
+    o.l_lo = isfinite(o.l_hi) ? (float)(l - (double)o.l_hi) : 0.0f;
+  }
+  return o;
+}
+// The key of the smallest value with x >= m + T ln(min_p) (m itself for min_p >= 1).
+__device__ __forceinline__ uint32_t key_of_min_p(const Options &o, float m) {
+  if (!(o.min_p < 1.0f) || m == INFINITY || o.temp == 0.0f) return key_of(m);
+  const float h = m + o.l_hi, v = h - m;  // the sum's error, exactly
+  const float e = ((m - (h - v)) + (o.l_hi - v)) + o.l_lo;
+  return key_of(clean(e > 0.0f ? nextafterf(h, INFINITY) : h));
+}
+
 struct Shared {
   uint32_t count[kBins];
   u64 mass[kBins];
   u64 list[kList];
   Powers pw;
+  Options opt;
   uint32_t cta_max[kMaxCluster];  // largest key of every CTA's slice
   uint32_t n_list;
   u64 warp_mass[kWarps];  // kept weights above the cut, of every warp's tokens
@@ -423,27 +502,43 @@ __device__ __forceinline__ void sort_list(u64 *v, int n) {
   __syncthreads();
 }
 
-// A row's options.
-struct Options {
-  float temp, top_p, min_p;
-  int top_k;
-  bool greedy;
-  uint32_t min_key;  // of min_p, 0: none
-};
-
 __device__ __forceinline__ void answer(const SampleParams &p, int64_t row, int token, float x,
                                        const Scale &s, const Options &o, u64 total) {
   p.token[row] = token;
   if (!p.logprob) return;
-  const double z = x == s.m || o.greedy ? 0.0 : ((double)x - (double)s.m) / (double)o.temp;
-  p.logprob[row] = (float)(z - log((double)total / (double)(1ull << kUnitBits)));
+  double t = 0.0;  // (m - x) / T in powers of two
+  if (x != s.m && o.temp > 0.0f) {
+    const double d = (double)s.m - (double)x;
+    t = fma(d, (double)s.c_hi, d * (double)s.c_lo);
+  }
+  p.logprob[row] = (float)-fma(t, 0.69314718055994530942, log_total(total));
+}
+
+// The CTAs' lists (complete) to the first one's, if it can hold them; how many there are.
+template <typename T>
+__device__ int gather(const Row<T> &r) {
+  Shared *sm = r.sm;
+  int n = 0;
+  for (uint32_t i = 0; i < r.ranks; ++i) n += (int)ld_remote32(remote(&sm->n_list, i));
+  if (n <= kList && r.rank == 0) {
+    uint32_t at = sm->n_list;
+    for (uint32_t i = 1; i < r.ranks; ++i) {
+      const uint32_t k = ld_remote32(remote(&sm->n_list, i)), from = remote(sm->list, i);
+      for (uint32_t j = threadIdx.x; j < k; j += kThreads)
+        sm->list[at + j] = ld_remote64(from + j * 8);
+      at += k;
+    }
+  }
+  __syncthreads();
+  return n;
 }
 
 // The whole choice from the list of all tokens that any filter may keep, n in the first
 // CTA's shared memory as (~key, index): in order of value for the filters, then of index.
+// target: the sum of weights that top-p asks for, 0 for that share of the list's.
 template <typename T>
 __device__ void solve_list(const SampleParams &p, const Row<T> &r, const Scale &s,
-                           const Options &o, int64_t row, int n) {
+                           const Options &o, uint32_t min_key, int64_t row, int n, u64 target) {
   constexpr bool kExact = sizeof(T) == 2;
   constexpr int P = kList / kThreads;
   Shared *sm = r.sm;
@@ -459,7 +554,7 @@ __device__ void solve_list(const SampleParams &p, const Row<T> &r, const Scale &
       sum += w[e];
     }
     u64 at = block_scan(sm, sum, &total);
-    const u64 target = fraction_of(total, fmaxf(o.top_p, 0.0f));
+    if (target == 0) target = fraction_of(total, fmaxf(o.top_p, 0.0f));
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       if (at < target && target <= at + w[e]) sm->found[0] = (u64)(a + e + 1);
@@ -468,10 +563,10 @@ __device__ void solve_list(const SampleParams &p, const Row<T> &r, const Scale &
     __syncthreads();
     kept = (int)sm->found[0];
   }
-  if (o.min_key) {
+  if (min_key) {
     int mine = 0;
 #pragma unroll
-    for (int e = 0; e < P; ++e) mine += a + e < kept && key_of(value(a + e)) >= o.min_key;
+    for (int e = 0; e < P; ++e) mine += a + e < kept && key_of(value(a + e)) >= min_key;
     u64 total;
     block_scan(sm, (u64)mine, &total);
     kept = (int)total;
@@ -518,44 +613,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // ---- the slice, and the largest logit of each of four groups a thread
   const T *src = static_cast<const T *>(p.logits) + row * p.ld + r.first;
   float g[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  if (p.vec) {
-    constexpr int U = 4;  // loads ahead of their uses
-    for (int i = threadIdx.x * N; i < r.n; i += kThreads * N * U) {
-      uint4 w[U];
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (i + k * kThreads * N + N <= r.n)
-          w[k] = __ldcs(reinterpret_cast<const uint4 *>(src + i + k * kThreads * N));
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int at = i + k * kThreads * N;
-        if (at + N <= r.n) {
-          float v[N];
-          Vec<T>::get(w[k], v);
-#pragma unroll
-          for (int j = 0; j < N; ++j) g[j & 3] = fmaxf(g[j & 3], v[j]);
-          *reinterpret_cast<uint4 *>(slice + at) = w[k];
-        } else {
-          for (int j = at; j < r.n; ++j) {
-            slice[j] = src[j];
-            g[0] = fmaxf(g[0], (float)src[j]);
-          }
-        }
-      }
-    }
-  } else {
-    for (int i = threadIdx.x; i < r.n; i += kThreads) {
-      slice[i] = src[i];
-      g[0] = fmaxf(g[0], (float)src[i]);
-    }
+  const int whole = p.vec ? r.n / N * N : 0;  // tokens that come 16 bytes at a time
+  for (int i = threadIdx.x * N; i < whole; i += kThreads * N)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(slice + i)),
+                 "l"(src + i)
+                 : "memory");
+  for (int i = whole + (int)threadIdx.x; i < r.n; i += kThreads) {
+    slice[i] = src[i];
+    g[0] = fmaxf(g[0], (float)src[i]);
   }
   if (threadIdx.x < 32) {
-    const double e = exp2(-(double)threadIdx.x / 32.0);
-    sm->pw.fix[threadIdx.x] = (u64)rint(e * (double)(1ull << kUnitBits));
-    sm->pw.flt[threadIdx.x] = (float)(e * (double)(1ull << (kUnitBits - 7)));
+    sm->pw.fix[threadIdx.x] = kPower[threadIdx.x];
+    sm->pw.flt[threadIdx.x] = (float)kPower[threadIdx.x] * 0.0078125f;
   }
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm->count[i] = 0, sm->mass[i] = 0;
-  if (threadIdx.x == 0) sm->n_list = 0;
+  if (threadIdx.x == 0) {
+    sm->n_list = 0;
+    sm->opt = read_options(p, row);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  for (int i = threadIdx.x * N; i < whole; i += kThreads * N) {  // (its own)
+    float v[N];
+    r.load(i, v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) g[j & 3] = fmaxf(g[j & 3], v[j]);
+  }
   const uint32_t top = __reduce_max_sync(
       0xffffffffu, key_of(clean(fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3])))));
   if (lane == 0) sm->scan[warp] = top;
@@ -574,27 +657,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   Scale s;
   s.m = value_of(max_key);
 
-  // ---- the row's options
-  Options o;
-  o.temp = p.temperature ? p.temperature[row] : p.temperature_all;
-  o.top_p = p.top_p ? p.top_p[row] : p.top_p_all;
-  o.min_p = p.min_p ? p.min_p[row] : p.min_p_all;
-  o.top_k = p.top_k ? p.top_k[row] : p.top_k_all;
-  o.greedy = !(o.temp > 0.0f);
+  Options o = sm->opt;
   if (o.top_k >= p.V) o.top_k = 0;
-  const double c = o.greedy ? 1.0 : 1.4426950408889634074 / (double)o.temp;
-  s.c_hi = (float)fmin(c, (double)FLT_MAX);
-  s.c_lo = c < 1e30 ? (float)(c - (double)s.c_hi) : 0.0f;
+  s.c_hi = o.c_hi;
+  s.c_lo = o.c_lo;
   s.bins = fminf(fmaxf(16.0f * s.c_hi, 32.0f), 75.0f);
-  o.min_key = 0;
-  if (o.min_p > 0.0f) {
-    // x >= m + T ln(min_p), compared in 64 bits; the smallest fp32 value that is
-    const double least =
-        o.min_p < 1.0f ? (double)s.m + (double)o.temp * log((double)o.min_p) : (double)s.m;
-    float v = (float)least;
-    if ((double)v < least) v = nextafterf(v, INFINITY);
-    o.min_key = s.m == INFINITY ? max_key : key_of(clean(v));
-  }
+  const uint32_t min_key = o.min_p > 0.0f ? key_of_min_p(o, s.m) : 0;
 
   if (s.m == -INFINITY) {  // no token may be chosen
     if (r.rank == 0 && threadIdx.x == 0) {
@@ -605,10 +673,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     return;
   }
 
-  const bool one = o.greedy || o.top_k == 1;
+  const bool one = o.temp == 0.0f || o.top_k == 1;
   const bool small = p.V <= kList && r.ranks == 1 && !one;
   bool listed = small;  // the first CTA's list holds all that may be kept
   int n_listed = p.V;
+  u64 p_target = 0;
   auto entry = [&](float x, int i) {
     return (u64)(uint32_t)~key_of(x) << 32 | (u64)(uint32_t)(r.first + i);
   };
@@ -645,36 +714,46 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     if (r.rank == 0) {
       constexpr int P = kBins / kThreads;
-      u64 v[P], sum = 0, total;
+      u64 v[P], k[P], sum = 0, n = 0, total, total_n;
       const float step = s.c_hi / s.bins;  // octaves of a bin
-      if (threadIdx.x == 0) sm->found[4] = 0;
+      if (threadIdx.x == 0) sm->found[3] = sm->found[4] = 0;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const int i = threadIdx.x * P + e;
-        const uint32_t k = mine[i] + sm->count[i];
-        v[e] = by_k ? (u64)k : (u64)((float)k * exp2f(40.0f - ((float)i + 0.5f) * step));
+        k[e] = mine[i] + sm->count[i];
+        v[e] = by_k ? k[e]
+                    : (u64)((float)k[e] * exp2f(40.0f - ((float)i + 0.5f) * step));
         sum += v[e];
+        n += k[e];
       }
-      u64 at = block_scan(sm, sum, &total);
-      const u64 target = by_k ? (u64)o.top_k : fraction_of(total, fmaxf(o.top_p, 0.0f));
+      u64 at = block_scan(sm, sum, &total), at_n = block_scan(sm, n, &total_n);
+      // top-p: the share above a bin is off by what its weights' places in their bins and
+      // the tokens that were not counted leave open: a tenth of share times rest
+      const float q = fminf(fmaxf(o.top_p, 0.0f), 1.0f), off = 0.1f * q * (1.0f - q);
+      const u64 deep = by_k ? (u64)o.top_k : fraction_of(total, fminf(q + off, 0.99999994f));
+      const u64 near = by_k ? (u64)1 : fraction_of(total, q - off);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const int i = threadIdx.x * P + e;
+        at_n += k[e];
+        if (at < near && near <= at + v[e]) sm->found[1] = (u64)i;
         // (the last bin holds everything further away)
-        if (at < target && target <= at + v[e] && i < kBins - 4) {
+        if (at < deep && deep <= at + v[e] && i < kBins - 4) {
           sm->found[0] = (u64)i;
+          sm->found[2] = at_n;
           sm->found[4] = 1;
         }
         at += v[e];
       }
     }
     r.tell();
-    found = sm->found[4] != 0;
-    const float b = (float)sm->found[0];
-    // one bin further down for what rounding may have moved; for top-p two to each side
-    edge_lo = s.m - (b + (by_k ? 1.1f : 3.0f)) / s.bins;
-    edge_hi = by_k || b < 3.0f ? INFINITY : s.m - (b - 2.0f) / s.bins;
-    found = found && s.m < INFINITY;
+    found = sm->found[4] != 0 && s.m < INFINITY;
+    // a bin more to each side for what rounding may have moved; few tokens are all listed
+    const float b = (float)sm->found[0], b1 = (float)sm->found[1];
+    edge_lo = s.m - (b + 2.1f) / s.bins;
+    edge_hi = by_k || b1 < 1.0f || sm->found[2] <= kList / 2 ? INFINITY
+                                                             : s.m - (b1 - 1.0f) / s.bins;
+    if (by_k) edge_lo = s.m - (b + 1.1f) / s.bins;
     __syncthreads();
   }
 
@@ -689,21 +768,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     r.sync();
     uint32_t n = 0;
     for (uint32_t i = 0; i < r.ranks; ++i) n += ld_remote32(remote(&sm->n_list, i));
-    listed = n <= kList && n >= (uint32_t)o.top_k;
+    listed = n >= (uint32_t)o.top_k && gather(r) <= kList;
     n_listed = (int)n;
-    if (listed && r.rank == 0) {
-      uint32_t at = sm->n_list;
-      for (uint32_t i = 1; i < r.ranks; ++i) {
-        const uint32_t k = ld_remote32(remote(&sm->n_list, i)), from = remote(sm->list, i);
-        for (uint32_t j = threadIdx.x; j < k; j += kThreads)
-          sm->list[at + j] = ld_remote64(from + j * 8);
-        at += k;
-      }
-    }
-    __syncthreads();
   }
   if (listed) {
-    if (r.rank == 0) solve_list(p, r, s, o, row, n_listed);
+    if (r.rank == 0) solve_list(p, r, s, o, min_key, row, n_listed, p_target);
     if (r.ranks > 1) cluster_sync();  // the first CTA has read the others' lists
     return;
   }
@@ -759,7 +828,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         block_scan(sm, t_all, &total);
         block_scan(sm, t_above, &total_above);
         const u64 target = fraction_of(total, fmaxf(o.top_p, 0.0f));
-        if (!full && total_above < target) {
+        const int n_all = none && !full ? gather(r) : kList + 1;
+        if (n_all <= kList) {
+          // all that may be kept, unless they fall short
+          if (r.rank == 0) {
+            u64 sum = 0;
+            for (int i = threadIdx.x; i < n_all; i += kThreads)
+              sum += weight<kExact>(s, sm->pw, value_of(~(uint32_t)(sm->list[i] >> 32)));
+            block_scan(sm, sum, &sum);
+            if (threadIdx.x == 0) sm->found[4] = sum >= target;
+            __syncthreads();
+            if (sm->found[4]) solve_list(p, r, s, o, min_key, row, n_all, target);
+            if (threadIdx.x == 0) sm->found[4] = sum >= target;
+          }
+          r.tell();
+          if (sm->found[4]) return;
+          __syncthreads();
+        } else if (!full && total_above < target) {
           const int n = (int)sm->n_list;
           auto list_each = [&](auto f) {
             for (int i = threadIdx.x; i < n; i += kThreads)
@@ -767,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           };
           done = find_cut<T, true>(r, s, list_each, key_lo, key_hi, Cut{0, 0},
                                    target - total_above, -1.0f, &last);
-          if (done && (o.min_key == 0 || o.min_key <= last.key)) {
+          if (done && (min_key == 0 || min_key <= last.key)) {
             for (int i = threadIdx.x; i < n; i += kThreads) {
               const uint32_t key = ~(uint32_t)(sm->list[i] >> 32);
               const int w = ((int)(uint32_t)sm->list[i] - r.first) / r.seg;
@@ -783,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (!done)
         find_cut<T, true>(r, s, slice_each, 0u, max_key, cut, 0, fmaxf(o.top_p, 0.0f), &last);
     }
-    if (o.min_key) last = shorter(last, Cut{o.min_key, INT32_MAX});
+    if (min_key) last = shorter(last, Cut{min_key, INT32_MAX});
     cut = last;
   }
 
