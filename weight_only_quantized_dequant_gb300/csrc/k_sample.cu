@@ -32,7 +32,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 2048;       // tokens that a CTA can list
 constexpr int kMaxCluster = 8;
-constexpr int kUnitBits = 44;     // the largest logit's weight is 2^44
+constexpr int kUnitBits = 45;     // the largest logit's weight is 2^45
 constexpr int kSliceBytes = 64 << 10;  // two CTAs an SM
 using u64 = unsigned long long;
 
@@ -145,23 +145,28 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 struct Scale {
   float m;           // largest logit
   float c_hi, c_lo;  // log2(e) / T
+  float far;         // 46 octaves
   float bins;        // bins per unit of the logits
 };
 
-// 2^(-i/32), i < 32, in units of 2^-44 (and, as fp32, of 2^-37).
+// 2^(-i/32), i < 32, in units of 2^-45.
 __constant__ u64 kPower[32] = {
-    17592186044416ull, 17215221774115ull, 16846335070792ull, 16485352848846ull, 16132105731538ull,
-    15786427971528ull, 15448157373097ull, 15117135216047ull, 14793206181226ull, 14476218277651ull,
-    14166022771192ull, 13862474114787ull, 13565429880144ull, 13274750690919ull, 12990300157313ull,
-    12711944812080ull, 12439554047902ull, 12173000056107ull, 11912157766698ull, 11656904789672ull,
-    11407121357589ull, 11162690269381ull, 10923496835354ull, 10689428823381ull, 10460376406236ull,
-    10236232110063ull, 10016890763953ull, 9802249450589ull, 9592207457961ull, 9386666232110ull,
-    9185529330885ull, 8988702378691ull,
+    35184372088832ull, 34430443548229ull, 33692670141585ull, 32970705697691ull, 32264211463077ull,
+    31572855943056ull, 30896314746195ull, 30234270432094ull, 29586412362452ull, 28952436555301ull,
+    28332045542385ull, 27724948229574ull, 27130859760289ull, 26549501381838ull, 25980600314626ull,
+    25423889624159ull, 24879108095804ull, 24346000112214ull, 23824315533396ull, 23313809579344ull,
+    22814242715178ull, 22325380538761ull, 21846993670708ull, 21378857646762ull, 20920752812471ull,
+    20472464220127ull, 20033781527906ull, 19604498901178ull, 19184414915921ull, 18773332464219ull,
+    18371058661769ull, 17977404757381ull,
 };
-struct Powers {  // in shared memory
-  u64 fix[32];
+// In shared memory, a bank each: 32-bit halves of it, less what kMagic adds in units of
+// 2^17, and 2^28 times it.
+struct Powers {
+  uint32_t lo[32], hi[32];
   float flt[32];
 };
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: a sum with it has whole numbers as low bits
+constexpr uint32_t kMagicBits = 0x4b400000u;
 
 // A number near 1 / (1 + (i + 1/2) / 32), and minus its logarithm.
 __constant__ double kLog[32][2] = {
@@ -182,7 +187,7 @@ __constant__ double kLog[32][2] = {
     {0.5289256198347108, 0.6369074622370692}, {0.5203252032520326, 0.6533012720127456},
     {0.512, 0.6694306539426292}, {0.5039370078740157, 0.6853040030989195},
 };
-// ln(total / 2^44) to 2^-38: total = 2^e z, r = z kLog - 1 (|r| < 1/60) by its series.
+// ln(total / 2^45) to 2^-38: total = 2^e z, r = z kLog - 1 (|r| < 1/60) by its series.
 __device__ __forceinline__ double log_total(u64 total) {
   const int e = 63 - __clzll(total);
   const double z = (double)total * __hiloint2double((1023 - e) << 20, 0);
@@ -195,38 +200,38 @@ __device__ __forceinline__ double log_total(u64 total) {
   return fma((double)(e - kUnitBits), 0.69314718055994530942, kLog[i][1] + s);
 }
 
-// 2^44 e^{(x - m)/T}, to the nearest integer.  With t = (m - x) c as an fp32
-// pair, q = rint(32 t) and f = t - q/32: 2^-t = 2^-(q>>5) 2^-((q&31)/32) 2^-f, the
-// last by its series to f^4 (|f| <= 1/64: the next term is below 2^-39).  EXACT:
-// m - x loses nothing that matters (16-bit logits).
+// 2^45 e^{(x - m)/T}, x <= m.  With t = (m - x) c as an fp32 pair, q = rint(32 t) and
+// f = t - q/32: 2^-t = 2^-(q>>5) 2^-((q&31)/32) 2^-f, the last by its series to f^4 (|f| <=
+// 1/64: the next term is below 2^-39).  What the shift drops is taken as half a unit (the
+// last bit is set), so that it does not add up; 46 octaves below m nothing is left.
+// EXACT: m - x loses nothing that matters (16-bit logits).
 template <bool EXACT>
 __device__ __forceinline__ u64 weight(const Scale &s, const Powers &pw, float x) {
-  const float d = x == s.m ? 0.0f : s.m - x;
+  const float d = fminf(s.m - x, s.far);
   const float t = d * s.c_hi;
   float lo = fmaf(d, s.c_lo, fmaf(d, s.c_hi, -t));
   if (!EXACT) {
     const float xv = s.m - d;
     const float e = (s.m - (d + xv)) + (xv - x);
-    lo = x == s.m ? 0.0f : fmaf(e, s.c_hi, lo);
+    lo = d < s.far ? fmaf(e, s.c_hi, lo) : 0.0f;
   }
-  const float magic = 12582912.0f;  // 1.5 * 2^23
-  const float qf = fmaf(t, 32.0f, magic);
-  const int q = (int)(__float_as_uint(qf) & 0x3fffffu);
-  const float f = fmaf(qf - magic, -0.03125f, t) + lo;
+  const float qf = fmaf(t, 32.0f, kMagic);
+  const uint32_t qb = __float_as_uint(qf), i = qb & 31;
+  const float f = fmaf(qf - kMagic, -0.03125f, t) + lo;
   // 2^-f - 1: powers of ln 2 over factorials
   float p = fmaf(f, 9.6181291e-3f, -5.5504109e-2f);
   p = fmaf(f, p, 2.4022651e-1f);
   p = fmaf(f, p, -6.9314718e-1f) * f;
-  const int i = q & 31, n = min(q >> 5, 63);
-  const int add = __float2int_rn(p * pw.flt[i]);  // below 2^31
-  const u64 w = pw.fix[i] + (u64)((long long)add * 128);
-  // (x = -inf with c = 0 gives NaN)
-  return t < 46.0f ? (w + ((1ull << n) >> 1)) >> n : 0;
+  const uint32_t z = __float_as_uint(fmaf(p, pw.flt[i], kMagic));
+  const u64 w = ((u64)pw.hi[i] << 32 | pw.lo[i]) + (u64)z * 131072u;
+  const uint32_t some = (qb - (kMagicBits + 46 * 32)) >> 31;  // t < 46
+  return w >> ((qb >> 5) & 63) | some;
 }
 
+// Steps of 1 / s.bins below the maximum, the last for everything further away.
 __device__ __forceinline__ int bin_of(const Scale &s, float x) {
-  const float t = (s.m - x) * s.bins;  // NaN for x = m = inf
-  return x == s.m ? 0 : (int)fminf(t, (float)(kBins - 1));  // (fminf drops a NaN)
+  const float t = fminf((s.m - x) * s.bins, (float)(kBins - 1));
+  return (int)(__float_as_uint(t + kMagic) & (kBins - 1));
 }
 
 // v * f for 0 <= f < 1, rounded down (the rest in *more).
@@ -272,7 +277,7 @@ __device__ __forceinline__ Options read_options(const SampleParams &p, int64_t r
   // the quotient's fp32 remainder is exact: (c_hi + c_lo) T = log2(e) to 2^-46
   o.c_hi = 1.0f, o.c_lo = 0.0f;
   if (o.temp > 0.0f) {
-    o.c_hi = fminf(__fdiv_rn(1.44269502e+00f, o.temp), FLT_MAX);
+    o.c_hi = fmaxf(fminf(__fdiv_rn(1.44269502e+00f, o.temp), FLT_MAX), 0x1p-120f);
     const float left = fmaf(-o.c_hi, o.temp, 1.44269502e+00f) + 1.92596303e-08f;
     o.c_lo = o.c_hi < 1e30f && o.c_hi > 1e-30f ? __fdiv_rn(left, o.temp) : 0.0f;
   }
@@ -286,7 +291,7 @@ __device__ __forceinline__ Options read_options(const SampleParams &p, int64_t r
 }
 // The key of the smallest value with x >= m + T ln(min_p) (m itself for min_p >= 1).
 __device__ __forceinline__ uint32_t key_of_min_p(const Options &o, float m) {
-  if (!(o.min_p < 1.0f) || m == INFINITY || o.temp == 0.0f) return key_of(m);
+  if (!(o.min_p < 1.0f) || o.temp == 0.0f) return key_of(m);
   const float h = m + o.l_hi, v = h - m;  // the sum's error, exactly
   const float e = ((m - (h - v)) + (o.l_hi - v)) + o.l_lo;
   return key_of(clean(e > 0.0f ? nextafterf(h, INFINITY) : h));
@@ -310,7 +315,7 @@ struct Shared {
 template <typename T>
 struct Row {
   Shared *sm;
-  const T *x;  // this CTA's tokens, in shared memory, whole vectors
+  const T *x;  // this CTA's tokens, in shared memory, behind the last -inf for whole warps
   int n, seg;  // how many; tokens of a warp
   int first;   // the first one's index
   uint32_t rank, ranks;
@@ -322,14 +327,12 @@ struct Row {
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     constexpr int N = Vec<T>::N;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int a = warp * seg, b = min(n, a + seg);
-    for (int i = a + lane * N; i < b; i += 32 * N) {
+    const int a = (threadIdx.x >> 5) * seg, b = a + seg;
+    for (int i = a + (threadIdx.x & 31) * N; i < b; i += 32 * N) {
       float v[N];
       load(i, v);
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (i + j < b) f(clean(v[j]), i + j, j);
+      for (int j = 0; j < N; ++j) f(clean(v[j]), i + j, j);
     }
   }
   __device__ __forceinline__ void sync() const {
@@ -485,8 +488,25 @@ __device__ __forceinline__ Cut shorter(const Cut &a, const Cut &b) {
   return a.ties < b.ties ? a : b;
 }
 
-// Sorts n <= kList numbers in shared memory, padded to a power of two (one CTA).
+// Sorts n <= kList different numbers in shared memory (one CTA): few of them by how many are
+// smaller, four threads a number, more as a bitonic network over a power of two.
 __device__ __forceinline__ void sort_list(u64 *v, int n) {
+  if (n <= kThreads / 4) {
+    const int i = threadIdx.x >> 2, part = threadIdx.x & 3;
+    u64 x = 0;
+    int at = 0;
+    __syncthreads();
+    if (i < n) {
+      x = v[i];
+      for (int j = part; j < n; j += 4) at += v[j] < x;
+    }
+    at += __shfl_xor_sync(0xffffffffu, at, 1);
+    at += __shfl_xor_sync(0xffffffffu, at, 2);
+    __syncthreads();
+    if (i < n && part == 0) v[at] = x;
+    __syncthreads();
+    return;
+  }
   int size = 2;
   while (size < n) size *= 2;
   for (int i = n + (int)threadIdx.x; i < size; i += kThreads) v[i] = ~0ull;
@@ -511,7 +531,9 @@ __device__ __forceinline__ void answer(const SampleParams &p, int64_t row, int t
     const double d = (double)s.m - (double)x;
     t = fma(d, (double)s.c_hi, d * (double)s.c_lo);
   }
-  p.logprob[row] = (float)-fma(t, 0.69314718055994530942, log_total(total));
+  // (a token alone has probability 1, not the half unit less)
+  const bool alone = t == 0.0 && total == ((1ull << kUnitBits) | 1);
+  p.logprob[row] = alone ? 0.0f : (float)-fma(t, 0.69314718055994530942, log_total(total));
 }
 
 // The CTAs' lists (complete) to the first one's, if it can hold them; how many there are.
@@ -608,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int64_t row = blockIdx.x / r.ranks;
   r.first = (int)r.rank * p.slice;
   r.n = max(0, min(p.V - r.first, p.slice));
-  r.seg = (r.n + kWarps * 32 * N - 1) / (kWarps * 32 * N) * (32 * N);
+  r.seg = (p.slice + kWarps * 32 * N - 1) / (kWarps * 32 * N) * (32 * N);
 
   // ---- the slice, and the largest logit of each of four groups a thread
   const T *src = static_cast<const T *>(p.logits) + row * p.ld + r.first;
@@ -619,13 +641,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                      (uint32_t)__cvta_generic_to_shared(slice + i)),
                  "l"(src + i)
                  : "memory");
-  for (int i = whole + (int)threadIdx.x; i < r.n; i += kThreads) {
-    slice[i] = src[i];
-    g[0] = fmaxf(g[0], (float)src[i]);
+  for (int i = whole + (int)threadIdx.x; i < r.seg * kWarps; i += kThreads) {
+    const T x = i < r.n ? src[i] : (T)-INFINITY;
+    slice[i] = x;
+    g[0] = fmaxf(g[0], (float)x);
   }
   if (threadIdx.x < 32) {
-    sm->pw.fix[threadIdx.x] = kPower[threadIdx.x];
-    sm->pw.flt[threadIdx.x] = (float)kPower[threadIdx.x] * 0.0078125f;
+    const u64 w = kPower[threadIdx.x], v = w - ((u64)kMagicBits << 17);
+    sm->pw.lo[threadIdx.x] = (uint32_t)v;
+    sm->pw.hi[threadIdx.x] = (uint32_t)(v >> 32);
+    sm->pw.flt[threadIdx.x] = (float)w * 0x1p-17f;
   }
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm->count[i] = 0, sm->mass[i] = 0;
   if (threadIdx.x == 0) {
@@ -657,9 +682,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   Scale s;
   s.m = value_of(max_key);
 
+  if (s.m == INFINITY) {  // they share all the weight: 0, and the others -inf
+    for (int i = threadIdx.x; i < r.seg * kWarps; i += kThreads)
+      slice[i] = (float)slice[i] == INFINITY ? (T)0.0f : (T)-INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g[j] = g[j] == INFINITY ? 0.0f : -INFINITY;
+    s.m = 0.0f;
+    max_key = key_of(0.0f);
+    __syncthreads();
+  }
   Options o = sm->opt;
   if (o.top_k >= p.V) o.top_k = 0;
   s.c_hi = o.c_hi;
+  s.far = 46.0f / o.c_hi;
   s.c_lo = o.c_lo;
   s.bins = fminf(fmaxf(16.0f * s.c_hi, 32.0f), 75.0f);
   const uint32_t min_key = o.min_p > 0.0f ? key_of_min_p(o, s.m) : 0;
@@ -681,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   auto entry = [&](float x, int i) {
     return (u64)(uint32_t)~key_of(x) << 32 | (u64)(uint32_t)(r.first + i);
   };
-  if (small) r.each([&](float x, int i, int) { sm->list[i] = entry(x, i); });
+  if (small)
+    for (int i = threadIdx.x; i < r.n; i += kThreads) sm->list[i] = entry(clean((float)slice[i]), i);
   __syncthreads();
 
   // ---- what the first CTA looks for in a histogram of distances from the maximum: top-k,
@@ -695,14 +731,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (by_k) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (g[j] > -INFINITY) atomicAdd(&mine[bin_of(s, clean(g[j]))], 1u);
+        if (const int b = bin_of(s, g[j]); b < kBins - 1) atomicAdd(&mine[b], 1u);
     } else {
       // tokens within six octaves of the maximum, and one in four of the others
-      const float near = 6.0f / s.c_hi * s.bins;
+      const int near = (int)fminf(6.0f / s.c_hi * s.bins, (float)(kBins - 1));
       r.each([&](float x, int, int j) {
         const int b = bin_of(s, x);
-        const bool close = (float)b < near;
-        if (close || (j & 3) == 0) atomicAdd(&mine[b], close ? 1u : 4u);
+        const bool close = b < near;
+        if (close || ((j & 3) == 0 && b < kBins - 1)) atomicAdd(&mine[b], close ? 1u : 4u);
       });
     }
     __syncthreads();
@@ -722,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const int i = threadIdx.x * P + e;
         k[e] = mine[i] + sm->count[i];
         v[e] = by_k ? k[e]
-                    : (u64)((float)k[e] * exp2f(40.0f - ((float)i + 0.5f) * step));
+                    : (u64)((float)k[e] * exp2f(40.0f - (float)i * step));
         sum += v[e];
         n += k[e];
       }
@@ -747,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       }
     }
     r.tell();
-    found = sm->found[4] != 0 && s.m < INFINITY;
+    found = sm->found[4] != 0;
     // a bin more to each side for what rounding may have moved; few tokens are all listed
     const float b = (float)sm->found[0], b1 = (float)sm->found[1];
     edge_lo = s.m - (b + 2.1f) / s.bins;
@@ -759,21 +795,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
   // ---- top-k: the tokens that may be among them, to the first CTA's list
   if (by_k && found) {
+    const uint32_t n_at = remote(&sm->n_list, 0), list_at = remote(sm->list, 0);
     r.each([&](float x, int i, int) {
       if (x >= edge_lo) {
-        const uint32_t at = atomicAdd(&sm->n_list, 1u);
-        if (at < kList) sm->list[at] = entry(x, i);
+        uint32_t at;
+        asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;"
+                     : "=r"(at)
+                     : "r"(n_at)
+                     : "memory");
+        if (at < kList) st_remote64(list_at + at * 8, entry(x, i));
       }
     });
     r.sync();
-    uint32_t n = 0;
-    for (uint32_t i = 0; i < r.ranks; ++i) n += ld_remote32(remote(&sm->n_list, i));
-    listed = n >= (uint32_t)o.top_k && gather(r) <= kList;
-    n_listed = (int)n;
+    n_listed = (int)ld_remote32(n_at);
+    listed = n_listed <= kList && n_listed >= o.top_k;
   }
   if (listed) {
     if (r.rank == 0) solve_list(p, r, s, o, min_key, row, n_listed, p_target);
-    if (r.ranks > 1) cluster_sync();  // the first CTA has read the others' lists
+    if (r.ranks > 1) cluster_sync();  // the others have read how many there are
     return;
   }
 
@@ -916,29 +955,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (at / kWarps == (int)r.rank) {
     // that warp's tokens again, by all threads
     u64 want = sm->found[1], rest = sm->found[2];
-    const int a = at % kWarps * r.seg, b = min(r.n, a + r.seg);
+    const int a = at % kWarps * r.seg, b = a + r.seg;
     for (int i0 = a; i0 < b; i0 += kThreads * N) {
       const int i = i0 + (int)threadIdx.x * N;
       float v[N];
-      r.load(min(i, p.slice - N), v);
+      r.load(min(i, b - N), v);
       u64 w[N], sum = 0, t = 0, all_t, all_w;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        v[j] = clean(v[j]);
-        t += i + j < b && key_of(v[j]) == cut.key;
+        v[j] = i < b ? clean(v[j]) : -INFINITY;
+        t += i < b && key_of(v[j]) == cut.key;
       }
       u64 t_at = block_scan(sm, t, &all_t);  // tokens at the cut before this thread's
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const uint32_t key = key_of(v[j]);
         w[j] = 0;
-        if (i + j < b) {
-          if (key > cut.key) {
-            w[j] = weight<kExact>(s, sm->pw, v[j]);
-          } else if (key == cut.key) {
-            if (t_at < rest) w[j] = cut_weight;
-            ++t_at;
-          }
+        if (key > cut.key) {
+          w[j] = weight<kExact>(s, sm->pw, v[j]);
+        } else if (key == cut.key) {
+          if (t_at < rest) w[j] = cut_weight;
+          ++t_at;
         }
         sum += w[j];
       }
@@ -968,8 +1005,11 @@ qz_status launch(SampleParams p, int64_t B, cudaStream_t s) {
   const size_t head = (sizeof(Shared) + 15) / 16 * 16;
   // CTAs of a row: as many as let two of them share an SM, and more while they have 2048
   // tokens each and the GPU is not full
+  constexpr int kWhole = kWarps * 32 * N;  // in shared memory every warp has as many
   auto slice_of = [&](int n) { return ((p.V + n - 1) / n + N - 1) / N * N; };
-  auto bytes_of = [&](int n) { return (size_t)slice_of(n) * sizeof(T); };
+  auto bytes_of = [&](int n) {
+    return (size_t)((slice_of(n) + kWhole - 1) / kWhole * kWhole) * sizeof(T);
+  };
   int ranks = 1;
   while (ranks < kMaxCluster &&
          (bytes_of(ranks) > kSliceBytes || (B * ranks <= di.sms && p.V > 2048 * ranks)))
