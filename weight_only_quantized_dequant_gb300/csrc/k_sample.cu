@@ -31,6 +31,7 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 2048;       // tokens that a CTA can list
+constexpr int kFew = 112;         // of a row, that are listed in any case (and sorted at once)
 constexpr int kMaxCluster = 8;
 constexpr int kUnitBits = 45;     // the largest logit's weight is 2^45
 constexpr int kSliceBytes = 64 << 10;  // two CTAs an SM
@@ -146,7 +147,6 @@ struct Scale {
   float m;           // largest logit
   float c_hi, c_lo;  // log2(e) / T
   float far;         // 46 octaves
-  float bins;        // bins per unit of the logits
 };
 
 // 2^(-i/32), i < 32, in units of 2^-45.
@@ -168,36 +168,63 @@ struct Powers {
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: a sum with it has whole numbers as low bits
 constexpr uint32_t kMagicBits = 0x4b400000u;
 
-// A number near 1 / (1 + (i + 1/2) / 32), and minus its logarithm.
-__constant__ double kLog[32][2] = {
-    {0.9846153846153847, 0.015504186535965199}, {0.9552238805970149, 0.04580953603129422},
-    {0.927536231884058, 0.07522342123758752}, {0.9014084507042254, 0.10379679368164355},
-    {0.8767123287671232, 0.13157635778871932}, {0.8533333333333334, 0.15860503017663852},
-    {0.8311688311688312, 0.18492233849401193}, {0.810126582278481, 0.21056476910734964},
-    {0.7901234567901234, 0.23556607131276697}, {0.7710843373493976, 0.259957524436926},
-    {0.7529411764705882, 0.2837681731306446}, {0.735632183908046, 0.3070250352949119},
-    {0.7191011235955056, 0.32975328637246804}, {0.7032967032967034, 0.3519764231571781},
-    {0.6881720430107527, 0.373716409793584}, {0.6736842105263158, 0.394993808240869},
-    {0.6597938144329897, 0.415827895143711}, {0.6464646464646465, 0.43623676677491796},
-    {0.6336633663366337, 0.4562374334815876}, {0.6213592233009708, 0.475845904869964},
-    {0.6095238095238096, 0.4950772667978514}, {0.5981308411214953, 0.5139457511022344},
-    {0.5871559633027523, 0.5324647988694717}, {0.5765765765765766, 0.5506471179526623},
-    {0.5663716814159292, 0.5685047353526688}, {0.5565217391304348, 0.5860490450035782},
-    {0.5470085470085471, 0.6032908514380841}, {0.5378151260504201, 0.6202404097518576},
-    {0.5289256198347108, 0.6369074622370692}, {0.5203252032520326, 0.6533012720127456},
-    {0.512, 0.6694306539426292}, {0.5039370078740157, 0.6853040030989195},
+// A number near 1 / (1 + (i + 1/2) / 32), and minus its logarithm in two parts.
+__constant__ float kLog[32][3] = {
+    {0.984615386f, 0.015504186f, -4.37010483e-10f},
+    {0.955223858f, 0.0458095595f, -2.09700451e-10f},
+    {0.927536249f, 0.0752234012f, 1.42228584e-09f},
+    {0.901408434f, 0.10379681f, 2.39636733e-09f},
+    {0.876712322f, 0.131576359f, 5.96729688e-09f},
+    {0.853333354f, 0.158605009f, -3.35514616e-09f},
+    {0.83116883f, 0.184922338f, 1.89329108e-09f},
+    {0.810126603f, 0.210564747f, -3.49109541e-09f},
+    {0.790123463f, 0.235566065f, -8.53199122e-10f},
+    {0.771084309f, 0.259957552f, 9.73365299e-09f},
+    {0.752941191f, 0.283768147f, 6.34272235e-09f},
+    {0.735632181f, 0.307025045f, -6.13627682e-09f},
+    {0.719101131f, 0.32975328f, -3.55805452e-09f},
+    {0.703296721f, 0.351976395f, 3.35814865e-09f},
+    {0.688172042f, 0.373716414f, -3.24985527e-09f},
+    {0.673684239f, 0.394993752f, 1.31588971e-08f},
+    {0.659793794f, 0.41582793f, -4.09624601e-09f},
+    {0.646464646f, 0.436236769f, -1.25471211e-09f},
+    {0.633663356f, 0.456237435f, 1.39731897e-08f},
+    {0.621359229f, 0.475845903f, -7.60144925e-09f},
+    {0.609523833f, 0.495077223f, 6.02794836e-09f},
+    {0.598130822f, 0.513945758f, 2.44244589e-08f},
+    {0.587155938f, 0.532464862f, -2.01595007e-08f},
+    {0.576576591f, 0.55064708f, 1.37936649e-08f},
+    {0.566371679f, 0.568504751f, -1.16506484e-08f},
+    {0.556521714f, 0.58604908f, 1.07433662e-08f},
+    {0.547008574f, 0.603290796f, 5.79808201e-09f},
+    {0.537815154f, 0.620240331f, 2.78330106e-08f},
+    {0.528925598f, 0.636907518f, -1.3763418e-08f},
+    {0.520325184f, 0.653301299f, 1.06473328e-08f},
+    {0.512000024f, 0.669430614f, -7.07258208e-09f},
+    {0.503937006f, 0.685303986f, 2.07516688e-08f},
 };
-// ln(total / 2^45) to 2^-38: total = 2^e z, r = z kLog - 1 (|r| < 1/60) by its series.
-__device__ __forceinline__ double log_total(u64 total) {
+// minus ln(2^-t total / 2^45), t = t_hi + t_lo, to 2^-29 and rounded once: total = 2^e z,
+// z kLog = 1 + r (|r| < 1/60, its logarithm by the series), and whatever rounding drops is
+// carried along.
+__device__ __forceinline__ float log_share(float t_hi, float t_lo, u64 total) {
   const int e = 63 - __clzll(total);
-  const double z = (double)total * __hiloint2double((1023 - e) << 20, 0);
-  const int i = (__double2hiint(z) >> 15) & 31;
-  const double r = fma(z, kLog[i][0], -1.0);
-  double s = fma(r, 0.2, -0.25);
-  s = fma(r, s, 1.0 / 3.0);
-  s = fma(r, s, -0.5);
-  s = fma(r * r, s, r);
-  return fma((double)(e - kUnitBits), 0.69314718055994530942, kLog[i][1] + s);
+  const u64 m = total << (63 - e);  // z 2^63
+  const float z = (float)(uint32_t)(m >> 40) * 0x1p-23f, y = (float)(uint32_t)(m >> 16 & 0xffffff) * 0x1p-47f;
+  const int i = (int)(m >> 58) & 31;
+  const float r = fmaf(y, kLog[i][0], fmaf(z, kLog[i][0], -1.0f));
+  float s = fmaf(r, 0.2f, -0.25f);
+  s = fmaf(r, s, 1.0f / 3.0f);
+  s = fmaf(r, s, -0.5f);
+  s = fmaf(r * r, s, r) + kLog[i][2];
+  // 0.693145751953125 = 22713 / 2^15 is ln 2 to 15 bits: exact with e
+  const float n = (float)(e - kUnitBits), a = n * 0.693145751953125f, b = kLog[i][1];
+  s = fmaf(n, 1.42860677e-06f, s);
+  const float ab = a + b, abv = ab - a;
+  s += (a - (ab - abv)) + (b - abv);
+  const float x = t_hi * 0.693147182f;
+  s += fmaf(t_hi, 0.693147182f, -x) + fmaf(t_hi, -1.90465421e-09f, t_lo * 0.693147182f);
+  const float sum = ab + x, sv = sum - ab;
+  return -(sum + (((ab - (sum - sv)) + (x - sv)) + s));
 }
 
 // 2^45 e^{(x - m)/T}, x <= m.  With t = (m - x) c as an fp32 pair, q = rint(32 t) and
@@ -228,11 +255,14 @@ __device__ __forceinline__ u64 weight(const Scale &s, const Powers &pw, float x)
   return w >> ((qb >> 5) & 63) | some;
 }
 
-// Steps of 1 / s.bins below the maximum, the last for everything further away.
-__device__ __forceinline__ int bin_of(const Scale &s, float x) {
-  const float t = fminf((s.m - x) * s.bins, (float)(kBins - 1));
+// Logits in sixteenths, from the largest (64) down; the last bin has everything from -64
+// on, and rows with logits of 63 and more are not estimated.
+constexpr float kPerLogit = 16.0f;
+__device__ __forceinline__ int bin_of(float x) {
+  const float t = fminf(fmaxf(x * -kPerLogit, -1023.0f), 1024.0f) + 1023.0f;
   return (int)(__float_as_uint(t + kMagic) & (kBins - 1));
 }
+__device__ __forceinline__ float middle_of(float bin) { return (1023.0f - bin) / kPerLogit; }
 
 // v * f for 0 <= f < 1, rounded down (the rest in *more).
 __device__ __forceinline__ u64 times(u64 v, float f, bool *more) {
@@ -323,7 +353,8 @@ struct Row {
   __device__ __forceinline__ void load(int i, float (&v)[Vec<T>::N]) const {
     Vec<T>::get(*reinterpret_cast<const uint4 *>(x + i), v);
   }
-  // f(value, index in the slice, place in its vector) for this warp's tokens.
+  // f(value, index in the slice, place in its vector) for this warp's tokens (as they are:
+  // a NaN compares with nothing and has no weight).
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     constexpr int N = Vec<T>::N;
@@ -332,7 +363,7 @@ struct Row {
       float v[N];
       load(i, v);
 #pragma unroll
-      for (int j = 0; j < N; ++j) f(clean(v[j]), i + j, j);
+      for (int j = 0; j < N; ++j) f(v[j], i + j, j);
     }
   }
   __device__ __forceinline__ void sync() const {
@@ -390,76 +421,106 @@ __device__ __forceinline__ void add_mass(u64 *m, u64 w) {
   if (hi) atomicAdd(p + 1, hi);
 }
 
+__device__ __forceinline__ void clear_bins(Shared *sm) {
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm->count[i] = 0, sm->mass[i] = 0;
+}
+
+// The bin where the running count (MASS: sum of weights) reaches `target`: found gets it,
+// what is missing where it begins, what it has and how many tokens, and 1 (first CTA).
+template <bool MASS>
+__device__ __forceinline__ void find_bin(Shared *sm, u64 target) {
+  constexpr int P = kBins / kThreads;
+  u64 v[P], sum = 0, total;
+  uint32_t n[P];
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    const int i = threadIdx.x * P + e;
+    n[e] = sm->count[i];
+    v[e] = MASS ? sm->mass[i] : (u64)n[e];
+    sum += v[e];
+  }
+  u64 at = block_scan(sm, sum, &total);
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    if (at < target && target <= at + v[e]) {
+      sm->found[0] = (u64)(threadIdx.x * P + e);
+      sm->found[1] = target - at;
+      sm->found[2] = v[e];
+      sm->found[3] = n[e];
+      sm->found[4] = 1;
+    }
+    at += v[e];
+  }
+}
+
+// The cut in a bin of one value, whose steps end at the key hi.
+template <typename T, bool MASS>
+__device__ __forceinline__ Cut last_cut(uint32_t hi, int shift, u64 target, u64 in_bin, u64 n) {
+  // zeros (or, of a negative value's key, ones) behind a 16-bit value
+  const uint32_t rest = sizeof(T) == 4 ? 0 : (1u << 13) - 1;
+  const u64 one = MASS ? max(in_bin / max(n, (u64)1), (u64)1) : 1;
+  return {shift == 0 ? hi : hi & 0x80000000u ? hi & ~rest : ((hi + 1) & ~rest) - 1,
+          (int)((target + one - 1) / one)};
+}
+
 // The cut at which the running count (MASS: sum of weights) of the tokens with keys in
 // [lo, hi] first reaches `target`; with MASS, of those inside `in` only, and with a
 // fraction >= 0 target is that fraction of all their weights.  each(f) calls f(value) for
 // this CTA's tokens, those outside [lo, hi] among them or not.  A histogram of 2048 steps
-// of the key, then of the steps in the one that was found.  False: they do not reach it.
-template <typename T, bool MASS, typename E>
+// of the key in the first CTA (FEW: straight there; else by way of one in every CTA), then
+// of the steps in the one that was found.  The bins are clear before and after, in every
+// CTA.  False: they do not reach it.
+template <typename T, bool MASS, bool FEW, typename E>
 __device__ bool find_cut(const Row<T> &r, const Scale &s, E each, uint32_t lo, uint32_t hi,
                          const Cut &in, u64 target, float fraction, Cut *cut) {
   constexpr bool kExact = sizeof(T) == 2;
   constexpr int kGrain = sizeof(T) == 4 ? 0 : 13;  // zeros behind a 16-bit value
   Shared *sm = r.sm;
+  const uint32_t count_at = remote(sm->count, 0), mass_at = remote(sm->mass, 0);
+  const bool straight = FEW || r.rank == 0;
   for (;;) {
     const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      sm->count[i] = 0;
-      if (MASS) sm->mass[i] = 0;
-    }
-    if (threadIdx.x == 0) sm->found[4] = 0;
-    __syncthreads();
     each([&](float x) {
-      const uint32_t key = key_of(x);
+      const uint32_t key = key_of(clean(x));
       if (key < lo || key > hi || (MASS && key <= in.key)) return;
       const uint32_t b = (hi - key) >> shift;
-      atomicAdd(&sm->count[b], 1u);
-      if (MASS) {
-        const u64 w = weight<kExact>(s, sm->pw, x);
-        if (w) add_mass(&sm->mass[b], w);
+      const u64 w = MASS ? weight<kExact>(s, sm->pw, x) : 0;
+      if (straight) {
+        add_remote32(count_at + b * 4, 1u);
+        if (MASS && w) add_remote64(mass_at + b * 8, w);
+      } else {
+        atomicAdd(&sm->count[b], 1u);
+        if (MASS && w) add_mass(&sm->mass[b], w);
       }
     });
-    __syncthreads();
     // the tokens at the cut of `in`: so many of them, counted by the first CTA
     if (MASS && r.rank == 0 && threadIdx.x == 0 && in.ties && in.key >= lo && in.key <= hi) {
       const uint32_t b = (hi - in.key) >> shift;
-      sm->count[b] += (uint32_t)in.ties;
-      sm->mass[b] += (u64)in.ties * weight<kExact>(s, sm->pw, value_of(in.key));
+      add_remote32(count_at + b * 4, (uint32_t)in.ties);
+      add_remote64(mass_at + b * 8,
+                   (u64)in.ties * weight<kExact>(s, sm->pw, value_of(in.key)));
     }
-    if (r.ranks > 1) {
-      cluster_sync();
-      if (r.rank != 0)
-        for (int i = threadIdx.x; i < kBins; i += kThreads)
-          if (sm->count[i]) {
-            add_remote32(remote(&sm->count[i], 0), sm->count[i]);
-            if (MASS) add_remote64(remote(&sm->mass[i], 0), sm->mass[i]);
-          }
-      cluster_sync();
-    } else {
+    if (!straight) {
       __syncthreads();
-    }
-    if (r.rank == 0) {
-      constexpr int P = kBins / kThreads;
-      u64 v[P], sum = 0, total;
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const int i = threadIdx.x * P + e;
-        v[e] = MASS ? sm->mass[i] : (u64)sm->count[i];
-        sum += v[e];
-      }
-      u64 at = block_scan(sm, sum, &total);
-      if (MASS && fraction >= 0.0f) target = fraction_of(total, fraction);
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        if (at < target && target <= at + v[e]) {
-          sm->found[0] = (u64)(threadIdx.x * P + e);
-          sm->found[1] = target - at;
-          sm->found[2] = v[e];
-          sm->found[3] = sm->count[threadIdx.x * P + e];
-          sm->found[4] = 1;
+      for (int i = threadIdx.x; i < kBins; i += kThreads)
+        if (sm->count[i]) {
+          add_remote32(count_at + i * 4, sm->count[i]);
+          if (MASS) add_remote64(mass_at + i * 8, sm->mass[i]);
+          sm->count[i] = 0;
+          sm->mass[i] = 0;
         }
-        at += v[e];
+    }
+    if (r.rank == 0 && threadIdx.x == 0) sm->found[4] = 0;
+    r.sync();
+    if (r.rank == 0) {
+      if (MASS && fraction >= 0.0f) {
+        u64 sum = 0, total;
+        for (int i = threadIdx.x; i < kBins; i += kThreads) sum += sm->mass[i];
+        block_scan(sm, sum, &total);
+        target = fraction_of(total, fraction);
       }
+      find_bin<MASS>(sm, target);
+      clear_bins(sm);
     }
     r.tell();
     const uint32_t b = (uint32_t)sm->found[0];
@@ -472,11 +533,7 @@ __device__ bool find_cut(const Row<T> &r, const Scale &s, E each, uint32_t lo, u
     hi -= b << shift;
     lo = max(lo, hi - ((1u << shift) - 1));
     if (shift <= kGrain) {
-      // one value is left: zeros (or, of a negative one's key, ones) behind it
-      const uint32_t rest = (1u << kGrain) - 1;
-      cut->key = shift == 0 ? hi : hi & 0x80000000u ? hi & ~rest : ((hi + 1) & ~rest) - 1;
-      const u64 one = MASS ? max(in_bin / max(n, (u64)1), (u64)1) : 1;
-      cut->ties = (int)((target + one - 1) / one);
+      *cut = last_cut<T, MASS>(hi, shift, target, in_bin, n);
       return true;
     }
   }
@@ -526,33 +583,15 @@ __device__ __forceinline__ void answer(const SampleParams &p, int64_t row, int t
                                        const Scale &s, const Options &o, u64 total) {
   p.token[row] = token;
   if (!p.logprob) return;
-  double t = 0.0;  // (m - x) / T in powers of two
+  float t = 0.0f, lo = 0.0f;  // (m - x) / T in powers of two
   if (x != s.m && o.temp > 0.0f) {
-    const double d = (double)s.m - (double)x;
-    t = fma(d, (double)s.c_hi, d * (double)s.c_lo);
+    const float d = s.m - x, v = s.m - d, e = (s.m - (d + v)) + (v - x);
+    t = d * s.c_hi;
+    lo = fmaf(e, s.c_hi, fmaf(d, s.c_lo, fmaf(d, s.c_hi, -t)));
   }
   // (a token alone has probability 1, not the half unit less)
-  const bool alone = t == 0.0 && total == ((1ull << kUnitBits) | 1);
-  p.logprob[row] = alone ? 0.0f : (float)-fma(t, 0.69314718055994530942, log_total(total));
-}
-
-// The CTAs' lists (complete) to the first one's, if it can hold them; how many there are.
-template <typename T>
-__device__ int gather(const Row<T> &r) {
-  Shared *sm = r.sm;
-  int n = 0;
-  for (uint32_t i = 0; i < r.ranks; ++i) n += (int)ld_remote32(remote(&sm->n_list, i));
-  if (n <= kList && r.rank == 0) {
-    uint32_t at = sm->n_list;
-    for (uint32_t i = 1; i < r.ranks; ++i) {
-      const uint32_t k = ld_remote32(remote(&sm->n_list, i)), from = remote(sm->list, i);
-      for (uint32_t j = threadIdx.x; j < k; j += kThreads)
-        sm->list[at + j] = ld_remote64(from + j * 8);
-      at += k;
-    }
-  }
-  __syncthreads();
-  return n;
+  const bool alone = t == 0.0f && total == ((1ull << kUnitBits) | 1);
+  p.logprob[row] = alone ? 0.0f : log_share(t, lo, total);
 }
 
 // The whole choice from the list of all tokens that any filter may keep, n in the first
@@ -652,11 +691,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     sm->pw.hi[threadIdx.x] = (uint32_t)(v >> 32);
     sm->pw.flt[threadIdx.x] = (float)w * 0x1p-17f;
   }
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sm->count[i] = 0, sm->mass[i] = 0;
+  clear_bins(sm);
   if (threadIdx.x == 0) {
     sm->n_list = 0;
     sm->opt = read_options(p, row);
   }
+  // (others may write to this CTA's shared memory once it has come here)
+  if (r.ranks > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   asm volatile("cp.async.wait_all;" ::: "memory");
   for (int i = threadIdx.x * N; i < whole; i += kThreads * N) {  // (its own)
     float v[N];
@@ -668,7 +709,38 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       0xffffffffu, key_of(clean(fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3])))));
   if (lane == 0) sm->scan[warp] = top;
   __syncthreads();
-  if (threadIdx.x < r.ranks) {  // this CTA's to all
+  Options o = sm->opt;
+  if (o.top_k >= p.V) o.top_k = 0;
+  const bool one = o.temp == 0.0f || o.top_k == 1;
+  const bool small = p.V <= kList && r.ranks == 1 && !one;
+  const bool by_k = !one && !small && o.top_k > 0;
+  const bool by_p = !one && !small && o.top_k <= 0 && o.top_p < 1.0f;
+  if (by_k || by_p) {
+    // top-k: the groups' largest logits; top-p: those (the few tokens with most of the
+    // weight are among them), and for the others those of the first group, four times
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (const int b = bin_of(g[j]); b < kBins - 1) atomicAdd(&sm->count[b], 1u);
+    if (by_p)
+      r.each([&](float x, int, int j) {
+        if ((j & 3) == 0) {
+          const int b = bin_of(x);
+          if (b < kBins - 1 && x < g[0]) atomicAdd(&sm->count[b], 4u);
+        }
+      });
+  }
+  if (r.ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  __syncthreads();
+  if (by_k || by_p) {
+    // (a CTA clears what it passes on; the first one's own are in `mass` meanwhile)
+    const uint32_t mass_at = remote(sm->mass, 0);
+    for (int i = threadIdx.x; i < kBins; i += kThreads)
+      if (sm->count[i]) {
+        add_remote32(mass_at + i * 8, sm->count[i]);
+        sm->count[i] = 0;
+      }
+  }
+  if (threadIdx.x < r.ranks) {  // this CTA's largest to all
     uint32_t k = 0;
     for (int w = 0; w < kWarps; ++w) k = max(k, (uint32_t)sm->scan[w]);
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
@@ -685,18 +757,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (s.m == INFINITY) {  // they share all the weight: 0, and the others -inf
     for (int i = threadIdx.x; i < r.seg * kWarps; i += kThreads)
       slice[i] = (float)slice[i] == INFINITY ? (T)0.0f : (T)-INFINITY;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) g[j] = g[j] == INFINITY ? 0.0f : -INFINITY;
     s.m = 0.0f;
     max_key = key_of(0.0f);
     __syncthreads();
   }
-  Options o = sm->opt;
-  if (o.top_k >= p.V) o.top_k = 0;
   s.c_hi = o.c_hi;
   s.far = 46.0f / o.c_hi;
   s.c_lo = o.c_lo;
-  s.bins = fminf(fmaxf(16.0f * s.c_hi, 32.0f), 75.0f);
   const uint32_t min_key = o.min_p > 0.0f ? key_of_min_p(o, s.m) : 0;
 
   if (s.m == -INFINITY) {  // no token may be chosen
@@ -708,103 +775,81 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     return;
   }
 
-  const bool one = o.temp == 0.0f || o.top_k == 1;
-  const bool small = p.V <= kList && r.ranks == 1 && !one;
   bool listed = small;  // the first CTA's list holds all that may be kept
   int n_listed = p.V;
   u64 p_target = 0;
   auto entry = [&](float x, int i) {
-    return (u64)(uint32_t)~key_of(x) << 32 | (u64)(uint32_t)(r.first + i);
+    return (u64)(uint32_t)~key_of(clean(x)) << 32 | (u64)(uint32_t)(r.first + i);
   };
   if (small)
-    for (int i = threadIdx.x; i < r.n; i += kThreads) sm->list[i] = entry(clean((float)slice[i]), i);
+    for (int i = threadIdx.x; i < r.n; i += kThreads) sm->list[i] = entry((float)slice[i], i);
   __syncthreads();
 
-  // ---- what the first CTA looks for in a histogram of distances from the maximum: top-k,
-  // a bin up to which that many groups have their largest; else top-p, the bin of its cut
-  const bool by_k = !one && !small && o.top_k > 0;
-  const bool by_p = !one && !small && o.top_k <= 0 && o.top_p < 1.0f;
+  // ---- what the first CTA looks for in the histogram: top-k, a bin up to which that many
+  // groups have their largest; top-p, the bins of its cut
   bool found = false;
   float edge_hi = 0.0f, edge_lo = 0.0f;  // values that bound what was found
   if (by_k || by_p) {
-    uint32_t *mine = r.rank == 0 ? reinterpret_cast<uint32_t *>(sm->mass) : sm->count;
-    if (by_k) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (const int b = bin_of(s, g[j]); b < kBins - 1) atomicAdd(&mine[b], 1u);
-    } else {
-      // tokens within six octaves of the maximum, and one in four of the others
-      const int near = (int)fminf(6.0f / s.c_hi * s.bins, (float)(kBins - 1));
-      r.each([&](float x, int, int j) {
-        const int b = bin_of(s, x);
-        const bool close = b < near;
-        if (close || ((j & 3) == 0 && b < kBins - 1)) atomicAdd(&mine[b], close ? 1u : 4u);
-      });
-    }
-    __syncthreads();
-    if (r.ranks > 1) {
-      if (r.rank != 0)
-        for (int i = threadIdx.x; i < kBins; i += kThreads)
-          if (mine[i]) add_remote32(remote(&sm->count[i], 0), mine[i]);
-      cluster_sync();
-    }
     if (r.rank == 0) {
       constexpr int P = kBins / kThreads;
       u64 v[P], k[P], sum = 0, n = 0, total, total_n;
-      const float step = s.c_hi / s.bins;  // octaves of a bin
       if (threadIdx.x == 0) sm->found[3] = sm->found[4] = 0;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const int i = threadIdx.x * P + e;
-        k[e] = mine[i] + sm->count[i];
+        k[e] = sm->mass[i];
         v[e] = by_k ? k[e]
-                    : (u64)((float)k[e] * exp2f(40.0f - (float)i * step));
+                    : (u64)((float)k[e] *
+                            exp2f(40.0f - fmaxf(s.m - middle_of((float)i), 0.0f) * s.c_hi));
         sum += v[e];
         n += k[e];
       }
       u64 at = block_scan(sm, sum, &total), at_n = block_scan(sm, n, &total_n);
       // top-p: the share above a bin is off by what its weights' places in their bins and
-      // the tokens that were not counted leave open: a tenth of share times rest
-      const float q = fminf(fmaxf(o.top_p, 0.0f), 1.0f), off = 0.1f * q * (1.0f - q);
+      // the tokens that were not counted leave open, some hundredths of share times rest
+      const float q = fminf(fmaxf(o.top_p, 0.0f), 1.0f), off = 0.06f * q * (1.0f - q);
       const u64 deep = by_k ? (u64)o.top_k : fraction_of(total, fminf(q + off, 0.99999994f));
       const u64 near = by_k ? (u64)1 : fraction_of(total, q - off);
+      const bool ok = s.m < 63.0f;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const int i = threadIdx.x * P + e;
         at_n += k[e];
         if (at < near && near <= at + v[e]) sm->found[1] = (u64)i;
-        // (the last bin holds everything further away)
-        if (at < deep && deep <= at + v[e] && i < kBins - 4) {
+        if (at < deep && deep <= at + v[e] && i < kBins - 1 && ok) {
           sm->found[0] = (u64)i;
           sm->found[2] = at_n;
           sm->found[4] = 1;
         }
+        // (few tokens are listed whatever weight they have)
+        if (by_p && at_n <= kFew && at_n > 0) atomicMax(&sm->found[3], (u64)i);
         at += v[e];
       }
+      clear_bins(sm);
     }
     r.tell();
     found = sm->found[4] != 0;
-    // a bin more to each side for what rounding may have moved; few tokens are all listed
-    const float b = (float)sm->found[0], b1 = (float)sm->found[1];
-    edge_lo = s.m - (b + 2.1f) / s.bins;
-    edge_hi = by_k || b1 < 1.0f || sm->found[2] <= kList / 2 ? INFINITY
-                                                             : s.m - (b1 - 1.0f) / s.bins;
-    if (by_k) edge_lo = s.m - (b + 1.1f) / s.bins;
+    // half a bin to each side, and what rounding may have moved
+    const float b = (float)max(sm->found[0], sm->found[3]), b1 = (float)sm->found[1];
+    edge_lo = middle_of(b + 0.6f);
+    edge_hi = by_k || sm->found[2] <= kList / 2 ? INFINITY : middle_of(b1 - 0.6f);
+    if (edge_hi > s.m) edge_hi = INFINITY;
     __syncthreads();
   }
 
   // ---- top-k: the tokens that may be among them, to the first CTA's list
+  const uint32_t n_at = remote(&sm->n_list, 0), list_at = remote(sm->list, 0);
+  auto push = [&](float x, int i) {
+    uint32_t at;
+    asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;"
+                 : "=r"(at)
+                 : "r"(n_at)
+                 : "memory");
+    if (at < kList) st_remote64(list_at + at * 8, entry(x, i));
+  };
   if (by_k && found) {
-    const uint32_t n_at = remote(&sm->n_list, 0), list_at = remote(sm->list, 0);
     r.each([&](float x, int i, int) {
-      if (x >= edge_lo) {
-        uint32_t at;
-        asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;"
-                     : "=r"(at)
-                     : "r"(n_at)
-                     : "memory");
-        if (at < kList) st_remote64(list_at + at * 8, entry(x, i));
-      }
+      if (x >= edge_lo) push(x, i);
     });
     r.sync();
     n_listed = (int)ld_remote32(n_at);
@@ -817,6 +862,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
 
   // ---- the cut
+  constexpr int kGrain = sizeof(T) == 4 ? 0 : 13;
+  // This warp's kept weights above the cut, some of them summed already, and tokens at it.
+  auto put_sums = [&](u64 had, u64 mass, uint32_t ties) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, d);
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    if (lane == 0) {
+      sm->warp_mass[warp] = had + mass;
+      sm->warp_ties[warp] = ties;
+    }
+  };
   Cut cut = {0, 0};      // every token
   bool summed = false;   // the weights above the cut are, warp by warp
   auto slice_each = [&](auto f) { r.each([&](float x, int, int) { f(x); }); };
@@ -824,26 +880,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     cut = {max_key, 1};
   } else {
     if (o.top_k > 0)
-      find_cut<T, false>(r, s, slice_each, 0u, max_key, cut, (u64)o.top_k, -1.0f, &cut);
+      find_cut<T, false, false>(r, s, slice_each, 0u, max_key, cut, (u64)o.top_k, -1.0f, &cut);
     Cut last = cut;
     if (o.top_p < 1.0f) {
       bool done = false;
       if (by_p && found) {
-        // all weights, those above the bins around the cut, and a list of those in them
-        const uint32_t key_hi = edge_hi == INFINITY ? max_key : key_of(clean(edge_hi));
-        const uint32_t key_lo = key_of(clean(edge_lo));
-        const bool none = edge_hi == INFINITY;  // above them
+        // Few tokens may be kept: all weights, and those tokens to the first CTA's list.
+        // Else: all weights, those above the bins around the cut, and a histogram of those
+        // in them, by steps of the key.
+        const bool few = edge_hi == INFINITY;
+        uint32_t hi = few ? max_key : key_of(clean(edge_hi)), lo = key_of(clean(edge_lo));
+        const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
+        const uint32_t count_at = remote(sm->count, 0), mass_at = remote(sm->mass, 0);
         u64 all = 0, above = 0;
-        r.each([&](float x, int i, int) {
-          const u64 w = weight<kExact>(s, sm->pw, x);
-          all += w;
-          const bool over = !none && x > edge_hi;
-          above += over ? w : 0;
-          if (!over && x >= edge_lo) {
-            const uint32_t at = atomicAdd(&sm->n_list, 1u);
-            if (at < kList) sm->list[at] = entry(x, i);
-          }
-        });
+        if (few) {
+          r.each([&](float x, int i, int) {
+            all += weight<kExact>(s, sm->pw, x);
+            if (x >= edge_lo) push(x, i);
+          });
+        } else {
+          r.each([&](float x, int, int) {
+            const u64 w = weight<kExact>(s, sm->pw, x);
+            all += w;
+            if (x > edge_hi) {
+              above += w;
+            } else if (x >= edge_lo) {
+              const uint32_t b = (hi - key_of(clean(x))) >> shift;
+              if (r.rank == 0) {
+                add_remote32(count_at + b * 4, 1u);
+                if (w) add_remote64(mass_at + b * 8, w);
+              } else {
+                atomicAdd(&sm->count[b], 1u);
+                if (w) add_mass(&sm->mass[b], w);
+              }
+            }
+          });
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
           all += __shfl_xor_sync(0xffffffffu, all, d);
@@ -852,60 +924,71 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (lane == 0) {
           sm->warp_all[warp] = all;
           sm->warp_mass[warp] = above;
-          sm->warp_ties[warp] = 0;
+        }
+        if (!few && r.rank != 0) {
+          __syncthreads();
+          for (int i = threadIdx.x; i < kBins; i += kThreads)
+            if (sm->count[i]) {
+              add_remote32(count_at + i * 4, sm->count[i]);
+              add_remote64(mass_at + i * 8, sm->mass[i]);
+              sm->count[i] = 0;
+              sm->mass[i] = 0;
+            }
         }
         r.sync();
-        u64 t_all = 0, t_above = 0, total, total_above;
-        bool full = false;
-        if (threadIdx.x < kWarps * r.ranks) {
-          t_all = ld_remote64(remote(&sm->warp_all[threadIdx.x % kWarps], threadIdx.x / kWarps));
-          t_above =
-              ld_remote64(remote(&sm->warp_mass[threadIdx.x % kWarps], threadIdx.x / kWarps));
-          full = ld_remote32(remote(&sm->n_list, threadIdx.x / kWarps)) > kList;
-        }
-        full = __syncthreads_or(full);
-        block_scan(sm, t_all, &total);
-        block_scan(sm, t_above, &total_above);
-        const u64 target = fraction_of(total, fmaxf(o.top_p, 0.0f));
-        const int n_all = none && !full ? gather(r) : kList + 1;
-        if (n_all <= kList) {
-          // all that may be kept, unless they fall short
-          if (r.rank == 0) {
-            u64 sum = 0;
-            for (int i = threadIdx.x; i < n_all; i += kThreads)
-              sum += weight<kExact>(s, sm->pw, value_of(~(uint32_t)(sm->list[i] >> 32)));
-            block_scan(sm, sum, &sum);
-            if (threadIdx.x == 0) sm->found[4] = sum >= target;
-            __syncthreads();
-            if (sm->found[4]) solve_list(p, r, s, o, min_key, row, n_all, target);
-            if (threadIdx.x == 0) sm->found[4] = sum >= target;
+        if (r.rank == 0) {
+          u64 t_all = 0, t_above = 0, total, total_above;
+          if (threadIdx.x < kWarps * r.ranks) {
+            const uint32_t w = threadIdx.x % kWarps, from = threadIdx.x / kWarps;
+            t_all = ld_remote64(remote(&sm->warp_all[w], from));
+            t_above = ld_remote64(remote(&sm->warp_mass[w], from));
           }
-          r.tell();
-          if (sm->found[4]) return;
-          __syncthreads();
-        } else if (!full && total_above < target) {
-          const int n = (int)sm->n_list;
-          auto list_each = [&](auto f) {
-            for (int i = threadIdx.x; i < n; i += kThreads)
-              f(value_of(~(uint32_t)(sm->list[i] >> 32)));
-          };
-          done = find_cut<T, true>(r, s, list_each, key_lo, key_hi, Cut{0, 0},
-                                   target - total_above, -1.0f, &last);
+          if (threadIdx.x == 0) sm->found[4] = 0;
+          block_scan(sm, t_all, &total);
+          block_scan(sm, t_above, &total_above);
+          const u64 target = fraction_of(total, fmaxf(o.top_p, 0.0f));
+          if (few) {
+            const int n = (int)sm->n_list;
+            u64 sum = 0;
+            if (n <= kList)
+              for (int i = threadIdx.x; i < n; i += kThreads)
+                sum += weight<kExact>(s, sm->pw, value_of(~(uint32_t)(sm->list[i] >> 32)));
+            block_scan(sm, sum, &sum);
+            if (sum >= target) solve_list(p, r, s, o, min_key, row, n, target);
+            if (threadIdx.x == 0) sm->found[4] = sum >= target;
+          } else {
+            if (total_above < target) find_bin<true>(sm, target - total_above);
+            clear_bins(sm);
+          }
+        }
+        r.tell();
+        const bool ok = sm->found[4] != 0;
+        if (ok && few) return;
+        const u64 left = sm->found[1], in_bin = sm->found[2], n = sm->found[3];
+        hi -= (uint32_t)sm->found[0] << shift;
+        lo = max(lo, hi - ((1u << shift) - 1));
+        __syncthreads();
+        if (ok) {
+          done = shift <= kGrain
+                     ? (last = last_cut<T, true>(hi, shift, left, in_bin, n), true)
+                     : find_cut<T, true, true>(r, s, slice_each, lo, hi, Cut{0, 0}, left, -1.0f,
+                                               &last);
           if (done && (min_key == 0 || min_key <= last.key)) {
-            for (int i = threadIdx.x; i < n; i += kThreads) {
-              const uint32_t key = ~(uint32_t)(sm->list[i] >> 32);
-              const int w = ((int)(uint32_t)sm->list[i] - r.first) / r.seg;
-              if (key > last.key)
-                add_mass(&sm->warp_mass[w], weight<kExact>(s, sm->pw, value_of(key)));
-              else if (key == last.key)
-                add_mass(&sm->warp_ties[w], 1);
-            }
+            // the kept ones among the tokens of those bins
+            const float at = value_of(last.key);
+            u64 mass = 0;
+            uint32_t ties = 0;
+            r.each([&](float x, int, int) {
+              if (x > at && x <= edge_hi) mass += weight<kExact>(s, sm->pw, x);
+              ties += x == at;
+            });
+            put_sums(above, mass, ties);
             summed = true;
           }
         }
       }
       if (!done)
-        find_cut<T, true>(r, s, slice_each, 0u, max_key, cut, 0, fmaxf(o.top_p, 0.0f), &last);
+        find_cut<T, true, false>(r, s, slice_each, 0u, max_key, cut, 0, fmaxf(o.top_p, 0.0f), &last);
     }
     if (min_key) last = shorter(last, Cut{min_key, INT32_MAX});
     cut = last;
@@ -915,20 +998,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (!summed) {
     u64 mass = 0;
     uint32_t ties = 0;
-    r.each([&](float x, int, int) {
-      const uint32_t key = key_of(x);
-      if (key > cut.key)
-        mass += weight<kExact>(s, sm->pw, x);
-      else
-        ties += key == cut.key;
-    });
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, d);
-    ties = __reduce_add_sync(0xffffffffu, ties);
-    if (lane == 0) {
-      sm->warp_mass[warp] = mass;
-      sm->warp_ties[warp] = ties;
+    if (cut.key == 0) {
+      r.each([&](float x, int, int) { mass += weight<kExact>(s, sm->pw, x); });
+    } else {
+      const float at = value_of(cut.key);
+      r.each([&](float x, int, int) {
+        if (x > at) mass += weight<kExact>(s, sm->pw, x);
+        ties += x == at;
+      });
     }
+    put_sums(0, mass, ties);
   }
   r.sync();
   // Every CTA sums all of them; thread i has warp i of the row.
