@@ -98,11 +98,12 @@ __device__ __forceinline__ void add_remote64(uint32_t a, u64 v) {
 // Logits as fp32, NaN as -inf and -0 as 0 (the order of values is that of keys).
 __device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY) + 0.0f; }
 
+// Four logits at a time (more at once would not leave 64 registers a thread).
 template <typename T>
-struct Vec;  // 16 bytes of logits
+struct Vec;
 template <>
 struct Vec<float> {
-  static constexpr int N = 4;
+  using Word = uint4;
   static __device__ __forceinline__ void get(uint4 v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
     x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
@@ -110,28 +111,21 @@ struct Vec<float> {
 };
 template <>
 struct Vec<__half> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void get(uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = h2f(w[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
+  using Word = uint2;
+  static __device__ __forceinline__ void get(uint2 v, float (&x)[4]) {
+    const float2 a = h2f(v.x), b = h2f(v.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
   }
 };
 template <>
 struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void get(uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  using Word = uint2;
+  static __device__ __forceinline__ void get(uint2 v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
   }
 };
+constexpr int N = 4;
 
 // Larger values have larger keys.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -142,7 +136,7 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// What a row's tokens are weighed and binned by.
+// What a row's tokens are weighed by.
 struct Scale {
   float m;           // largest logit
   float c_hi, c_lo;  // log2(e) / T
@@ -350,14 +344,13 @@ struct Row {
   int first;   // the first one's index
   uint32_t rank, ranks;
 
-  __device__ __forceinline__ void load(int i, float (&v)[Vec<T>::N]) const {
-    Vec<T>::get(*reinterpret_cast<const uint4 *>(x + i), v);
+  __device__ __forceinline__ void load(int i, float (&v)[N]) const {
+    Vec<T>::get(*reinterpret_cast<const typename Vec<T>::Word *>(x + i), v);
   }
   // f(value, index in the slice, place in its vector) for this warp's tokens (as they are:
   // a NaN compares with nothing and has no weight).
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    constexpr int N = Vec<T>::N;
     const int a = (threadIdx.x >> 5) * seg, b = a + seg;
     for (int i = a + (threadIdx.x & 31) * N; i < b; i += 32 * N) {
       float v[N];
@@ -655,7 +648,6 @@ __device__ void solve_list(const SampleParams &p, const Row<T> &r, const Scale &
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
-  constexpr int N = Vec<T>::N;
   constexpr bool kExact = sizeof(T) == 2;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared *sm = reinterpret_cast<Shared *>(smem);
@@ -674,8 +666,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // ---- the slice, and the largest logit of each of four groups a thread
   const T *src = static_cast<const T *>(p.logits) + row * p.ld + r.first;
   float g[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  const int whole = p.vec ? r.n / N * N : 0;  // tokens that come 16 bytes at a time
-  for (int i = threadIdx.x * N; i < whole; i += kThreads * N)
+  constexpr int kCopy = 16 / sizeof(T);
+  const int whole = p.vec ? r.n / kCopy * kCopy : 0;  // tokens that come 16 bytes at a time
+  for (int i = threadIdx.x * kCopy; i < whole; i += kThreads * kCopy)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(slice + i)),
                  "l"(src + i)
@@ -699,12 +692,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // (others may write to this CTA's shared memory once it has come here)
   if (r.ranks > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   asm volatile("cp.async.wait_all;" ::: "memory");
-  for (int i = threadIdx.x * N; i < whole; i += kThreads * N) {  // (its own)
-    float v[N];
-    r.load(i, v);
+  for (int i = threadIdx.x * kCopy; i < whole; i += kThreads * kCopy)  // (its own)
 #pragma unroll
-    for (int j = 0; j < N; ++j) g[j & 3] = fmaxf(g[j & 3], v[j]);
-  }
+    for (int k = 0; k < kCopy; k += N) {
+      float v[N];
+      r.load(i + k, v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) g[j] = fmaxf(g[j], v[j]);
+    }
   const uint32_t top = __reduce_max_sync(
       0xffffffffu, key_of(clean(fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3])))));
   if (lane == 0) sm->scan[warp] = top;
@@ -723,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (const int b = bin_of(g[j]); b < kBins - 1) atomicAdd(&sm->count[b], 1u);
     if (by_p)
       r.each([&](float x, int, int j) {
-        if ((j & 3) == 0) {
+        if (j == 0) {
           const int b = bin_of(x);
           if (b < kBins - 1 && x < g[0]) atomicAdd(&sm->count[b], 4u);
         }
@@ -814,6 +809,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const int i = threadIdx.x * P + e;
+        // (few tokens are listed whatever weight they have)
+        if (by_p && at_n <= kFew && kFew < at_n + k[e] && i > 0) sm->found[3] = (u64)(i - 1);
         at_n += k[e];
         if (at < near && near <= at + v[e]) sm->found[1] = (u64)i;
         if (at < deep && deep <= at + v[e] && i < kBins - 1 && ok) {
@@ -821,8 +818,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           sm->found[2] = at_n;
           sm->found[4] = 1;
         }
-        // (few tokens are listed whatever weight they have)
-        if (by_p && at_n <= kFew && at_n > 0) atomicMax(&sm->found[3], (u64)i);
         at += v[e];
       }
       clear_bins(sm);
@@ -899,19 +894,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             if (x >= edge_lo) push(x, i);
           });
         } else {
-          r.each([&](float x, int, int) {
+          uint32_t in = 0;  // of a vector, those in the bins
+          r.each([&](float x, int i, int j) {
             const u64 w = weight<kExact>(s, sm->pw, x);
             all += w;
-            if (x > edge_hi) {
-              above += w;
-            } else if (x >= edge_lo) {
-              const uint32_t b = (hi - key_of(clean(x))) >> shift;
+            above += x > edge_hi ? w : 0;
+            in |= x >= edge_lo && x <= edge_hi ? 1u << j : 0;
+            if (j < N - 1) return;
+            for (; in; in &= in - 1) {
+              const float y = (float)slice[i - (N - 1) + __ffs(in) - 1];
+              const u64 z = weight<kExact>(s, sm->pw, y);
+              const uint32_t b = (hi - key_of(clean(y))) >> shift;
               if (r.rank == 0) {
                 add_remote32(count_at + b * 4, 1u);
-                if (w) add_remote64(mass_at + b * 8, w);
+                if (z) add_remote64(mass_at + b * 8, z);
               } else {
                 atomicAdd(&sm->count[b], 1u);
-                if (w) add_mass(&sm->mass[b], w);
+                if (z) add_mass(&sm->mass[b], z);
               }
             }
           });
@@ -1080,12 +1079,12 @@ qz_status launch(SampleParams p, int64_t B, cudaStream_t s) {
   DeviceInfo di;
   qz_status st = device_info(&di);
   if (st != QZ_OK) return st;
-  constexpr int N = Vec<T>::N;
   const size_t head = (sizeof(Shared) + 15) / 16 * 16;
   // CTAs of a row: as many as let two of them share an SM, and more while they have 2048
   // tokens each and the GPU is not full
   constexpr int kWhole = kWarps * 32 * N;  // in shared memory every warp has as many
-  auto slice_of = [&](int n) { return ((p.V + n - 1) / n + N - 1) / N * N; };
+  constexpr int kCopy = 16 / sizeof(T);
+  auto slice_of = [&](int n) { return ((p.V + n - 1) / n + kCopy - 1) / kCopy * kCopy; };
   auto bytes_of = [&](int n) {
     return (size_t)((slice_of(n) + kWhole - 1) / kWhole * kWhole) * sizeof(T);
   };
