@@ -2,22 +2,25 @@
 // that bring few rows to a KV head (decode and drafts).
 //
 // For one KV head the queries of a sequence are packed row r = token * G +
-// head-in-group; a tile has 16 of them, one operand of the warp's matrix
-// instruction, and
+// head-in-group; a tile has 8 of them (16: NB = 2), and
 //   x_j = scale ks_j (q . kc_j),  out = sum_j e^{x_j} vs_j vc_j / sum_j e^{x_j}
 // over the codes kc, vc and the scales ks, vs of the keys.  Codes are exact in fp16
 // (a byte under the bits of 1024, less 1152, is the code), so they enter the
 // products as they are: ks_j multiplies the logit, vs_j the weight, both in fp32.
 //
 //  * HBM bounds a decode step: a token and head is 2 (D + 4) bytes, 11 clocks of an
-//    SM's share at D 128, and its codes are converted once, by the warp that multiplies
-//    them.  A block of 128 keys comes by TMA, page by page, with the swizzle under
-//    which the fragments' 16-byte reads do not conflict; each of eight warps has 16
-//    of the keys to itself, with a running maximum, sum and output of its own, so
-//    nothing is exchanged before the tile's end.
+//    SM's share at D 128.  The warp's matrix instruction takes 8 clocks an SM whatever
+//    its operands hold, so the rows are its narrow side (8 columns): S^T = K Q^T and
+//    O^T = V^T P^T, a key 1/8 of two instructions a step of 16 columns, 8 clocks.
+//    With the rows as its 16-row operand a key took 16 (32 tokens over 16384 keys, 64
+//    heads on 8: 212 us).
+//  * A block of 128 keys comes by TMA, page by page, with the swizzle under which the
+//    fragments' 16-byte reads do not conflict; each of eight warps has 16 of the keys to
+//    itself, converts their codes, and has a running maximum, sum and output of its own,
+//    so nothing is exchanged before the tile's end.
 //  * The order of D in a product is free as long as both operands have it: a thread's
-//    16 bytes of a key are four steps of the first product, and of a value four
-//    columns of the second, so that both come as whole 16-byte reads.
+//    16 bytes of a key are four steps of the first product, and of a value eight rows
+//    of the second's tiles, so that both come as whole 16-byte reads.
 //  * Weights are rounded to fp16 once, with vs_j in them: 2^6 e^{x - m} vs_j 2^-E,
 //    where m lags the maximum by up to 2^8 and 2^E the largest vs by up to 2.
 //  * The split of (tile, key block) units between CTAs is that of the fp16 kernel.
@@ -28,7 +31,6 @@
 namespace qz {
 namespace {
 
-constexpr int kM = 16;                // rows of a tile
 constexpr int kWarps = 8;             // each has 16 of a block's keys
 constexpr int kLoadWarp = kWarps;     // the third warpgroup: one warp loads, three do nothing
 constexpr int kThreads = 384;
@@ -38,14 +40,15 @@ constexpr float kLift8 = 6.0f;        // log2 of the weight at m
 static_assert(kLift8 + kLag + 1.0f < 16.0f, "weights are fp16");
 constexpr int kHead8 = 4096;          // barriers, announced tiles, row maxima and sums
 
-template <int D>
+template <int D, int NB>
 struct Cfg8 {
+  static constexpr int kM = 8 * NB;                 // rows of a tile
   static constexpr int kRow = D < 128 ? D : 128;    // bytes of a swizzled row
   static constexpr int kStage = kN * D;             // bytes of a K or V block
   static constexpr int kNS = 131072 / kStage;       // K and V slots: 16, 8, 4
   static constexpr int kSteps = D / 16;             // of the first product
   static constexpr int kBuf = kWarps * kM * kRow * 4;  // outputs of the warps, 128 columns at a time
-  static constexpr int kQ = D == 256 ? kSteps * 512 : 0;
+  static constexpr int kQ = D == 256 && NB == 2 ? kSteps * 512 : 0;  // queries by step
   static constexpr int kSmem = 1024 + kHead8 + kNS * kN * 4 + kNS * kStage + kBuf + kQ;
   static constexpr int kPart = kM * (D + 2);        // floats of a partial
 };
@@ -73,10 +76,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-__device__ __forceinline__ float2 lds64f(uint32_t a) {
-  const uint2 v = lds64(a);
-  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-}
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -86,11 +85,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// An 8 x 8 matrix of fp16, two of a row a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float lds32f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
 
-template <int D, int CAP>
+template <int D, int NB, int CAP>
 __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
-  using C = Cfg8<D>;
-  constexpr int NS = C::kNS, KS = C::kSteps, NT = D / 8;
+  using C = Cfg8<D, NB>;
+  constexpr int kM = C::kM, NS = C::kNS, KS = C::kSteps, MT = D / 16;
+  constexpr bool kQinSm = C::kQ > 0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -139,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
     // n / G for n < G + 256 (see the fp16 kernel)
     auto row_token = [&](int n) { return (int)(((float)n + 0.5f) * p.inv_g); };
     const uint32_t kv0 = smem_u32(kv_sm), sc0 = smem_u32(scale_sm) + warp * 64;
-    // this thread's 16 bytes of a key: rows 8 nt + g of the warp's 16, chunks 2 t and 2 t + 1
+    // this thread's 16 bytes of a key: rows g and g + 8 of the warp's 16, chunks 2 t and 2 t + 1
     // (of 8; D 64: t of 4); of a value: rows 2 t + {0, 1, 8, 9}, chunk g (D 64: half of g / 2)
     const int krow = warp * 16 + g;
     const uint32_t k_at = krow * C::kRow;
@@ -151,6 +162,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       v_at[i] = r * C::kRow + (D == 64 ? (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8
                                        : (g ^ (r & 7)) << 4);
     }
+    // where a row's float4 piece lies in its line of the buffer: 8 lanes with the same piece
+    // of two rows' worth of chunks store to different banks
+    auto place = [](int row, int piece) {
+      const int u = (row >> 1) & 3;
+      return piece ^ (D == 64 ? (u & 1) | (u >> 1) << 2 : u);
+    };
     uint32_t n_seg = 0, ring = 0, n_met = 0;
     bool ok = true;
     // All eight warps have come here; false if one gave up.
@@ -173,58 +190,72 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n_seg % kSegs]));
       const int par = n_seg++ & 1;
       if (s.rows == 0) break;
-      // ---- rows g and g + 8 (past the tile's end: its last row's limits)
-      int hi[2], lo[2];
-      const __half *qrow[2];
+      // ---- queries: row 8 b + g as an operand, rows 8 b + 2 t and 2 t + 1 of the logits
+      // (past the tile's end: its last row's)
+      const __half *qrow[NB];
+      int hi[NB][2], lo[NB][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int n = s.rem + min(g + 8 * i, s.rows - 1), k = row_token(n);
-        hi[i] = s.pos + k + 1;
-        lo[i] = first_key(p, s.pos + k);
-        qrow[i] = p.q + (int64_t)(s.tok + k) * p.q_token +
+      for (int b = 0; b < NB; ++b) {
+        const int n = s.rem + min(8 * b + g, s.rows - 1), k = row_token(n);
+        qrow[b] = p.q + (int64_t)(s.tok + k) * p.q_token +
                   (int64_t)(s.head * p.G + n - k * p.G) * p.q_head;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int pos = s.pos + row_token(s.rem + min(8 * b + 2 * t + e, s.rows - 1));
+          hi[b][e] = pos + 1;
+          lo[b][e] = first_key(p, pos);
+        }
       }
-      const int see_lo = __reduce_max_sync(0xffffffffu, max(lo[0], lo[1]));
-      const int see_hi = __reduce_min_sync(0xffffffffu, min(hi[0], hi[1]));
-      // the first product's operand: step i has columns 4 i .. 4 i + 3 of this thread's D / 4
-      // (of each 128: D 256)
-      uint32_t qa[D == 256 ? 1 : KS][4];
-      if (D == 256) {
+      int see_lo = max(lo[0][0], lo[NB - 1][1]), see_hi = min(hi[0][0], hi[NB - 1][1]);
+      see_lo = __reduce_max_sync(0xffffffffu, see_lo);
+      see_hi = __reduce_min_sync(0xffffffffu, see_hi);
+      // step i of the first product has columns 4 i .. 4 i + 3 of this thread's D / 4 (of each
+      // 128: D 256)
+      uint32_t qb[kQinSm ? 1 : NB][kQinSm ? 1 : KS][2];
+      if (kQinSm) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int i = warp * 2 + k, d = (i >> 3) * 128 + 32 * t + 4 * (i & 7);
           const uint2 a = *reinterpret_cast<const uint2 *>(qrow[0] + d);
-          const uint2 b = *reinterpret_cast<const uint2 *>(qrow[1] + d);
-          *reinterpret_cast<uint4 *>(q_sm + i * 512 + lane * 16) = make_uint4(a.x, b.x, a.y, b.y);
+          const uint2 c = *reinterpret_cast<const uint2 *>(qrow[NB - 1] + d);
+          *reinterpret_cast<uint4 *>(q_sm + i * 512 + lane * 16) = make_uint4(a.x, a.y, c.x, c.y);
         }
         if (!meet()) break;
       } else {
 #pragma unroll
-        for (int i = 0; i < KS; i += 2) {
-          const uint4 a = *reinterpret_cast<const uint4 *>(qrow[0] + t * (D / 4) + 4 * i);
-          const uint4 b = *reinterpret_cast<const uint4 *>(qrow[1] + t * (D / 4) + 4 * i);
-          qa[i][0] = a.x, qa[i][1] = b.x, qa[i][2] = a.y, qa[i][3] = b.y;
-          qa[i + 1][0] = a.z, qa[i + 1][1] = b.z, qa[i + 1][2] = a.w, qa[i + 1][3] = b.w;
-        }
-      }
-      float o[NT][4];
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+          for (int i = 0; i < KS; i += 2) {
+            const int d = D == 256 ? (i >> 3) * 128 + 32 * t + 4 * (i & 7) : t * (D / 4) + 4 * i;
+            const uint4 a = *reinterpret_cast<const uint4 *>(qrow[b] + d);
+            qb[kQinSm ? 0 : b][kQinSm ? 0 : i][0] = a.x, qb[kQinSm ? 0 : b][kQinSm ? 0 : i][1] = a.y;
+            qb[kQinSm ? 0 : b][kQinSm ? 0 : i + 1][0] = a.z;
+            qb[kQinSm ? 0 : b][kQinSm ? 0 : i + 1][1] = a.w;
+          }
+      }
+      float o[MT][NB][4];
+      float m[NB][2], l[NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        m[b][0] = m[b][1] = -INFINITY;
+        l[b][0] = l[b][1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[i][b][0] = o[i][b][1] = o[i][b][2] = o[i][b][3] = 0.0f;
+      }
       float e_pos = exp2f(-40.0f), e_neg = exp2f(40.0f);  // 2^E and 2^-E
-      for (int b = s.b0; b < s.b1; ++b, ring += 2) {
+      for (int blk = s.b0; blk < s.b1; ++blk, ring += 2) {
         const uint32_t ks = ring % NS, vs = (ring + 1) % NS;
         if (!(ok = mbar_wait(smem_u32(&kv_full[ks]), (ring / NS) & 1, abort_flag))) break;
         const int key0 = warp * 16;  // of the block
         // (the block's end may pass 32 bits)
-        const bool none = s.hi - b * kN <= key0 || (int64_t)b * kN + key0 + 16 <= s.lo;
-        float x[2][4];
+        const bool none = s.hi - blk * kN <= key0 || (int64_t)blk * kN + key0 + 16 <= s.lo;
+        float x[NB][4];  // keys g (0, 1) and g + 8 (2, 3) of rows 2 t and 2 t + 1
         if (!none) {
-          float sa[2][4], sb[2][4];
+          float sa[NB][4], sb[NB][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sa[i][j] = sb[i][j] = 0.0f;
+            for (int j = 0; j < 4; ++j) sa[b][j] = sb[b][j] = 0.0f;
           const uint32_t kb = kv0 + ks * C::kStage + k_at;
 #pragma unroll
           for (int h = 0; h < KS / 4; ++h) {  // 16 bytes of a key, four steps
@@ -233,99 +264,102 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t a[4];
-              if (D == 256) {
-                const uint4 v = lds128(smem_u32(q_sm) + (4 * h + i) * 512 + lane * 16);
-                a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) a[j] = qa[D == 256 ? 0 : 4 * h + i][j];
-              }
               const uint32_t u0 = w0[i] ^ 0x80808080u, u1 = w1[i] ^ 0x80808080u;
-              mma16816(i & 1 ? sb[0] : sa[0], a, code_pair(u0, 0x4140), code_pair(u0, 0x4342));
-              mma16816(i & 1 ? sb[1] : sa[1], a, code_pair(u1, 0x4140), code_pair(u1, 0x4342));
+              const uint32_t a[4] = {code_pair(u0, 0x4140), code_pair(u1, 0x4140),
+                                     code_pair(u0, 0x4342), code_pair(u1, 0x4342)};
+              uint32_t q[4];
+              if (kQinSm) {
+                const uint4 v = lds128(smem_u32(q_sm) + (4 * h + i) * 512 + lane * 16);
+                q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
+              }
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                mma16816(i & 1 ? sb[b] : sa[b], a,
+                         kQinSm ? q[2 * b] : qb[kQinSm ? 0 : b][kQinSm ? 0 : 4 * h + i][0],
+                         kQinSm ? q[2 * b + 1] : qb[kQinSm ? 0 : b][kQinSm ? 0 : 4 * h + i][1]);
             }
           }
+          const float f0 = lds32f(sc0 + ks * (kN * 4) + g * 4) * p.sign;
+          const float f1 = lds32f(sc0 + ks * (kN * 4) + 32 + g * 4) * p.sign;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 f = lds64f(sc0 + ks * (kN * 4) + i * 32 + t * 8);
-            const float fx = f.x * p.sign, fy = f.y * p.sign;
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float v = (sa[i][j] + sb[i][j]) * (j & 1 ? fy : fx);
-              x[i][j] = (CAP == 0 ? v : CAP == 1 ? cap_far(p, v) : cap_any(p, v)) * p.c;
+              const float v = (sa[b][j] + sb[b][j]) * (j < 2 ? f0 : f1);
+              x[b][j] = (CAP == 0 ? v : CAP == 1 ? cap_far(p, v) : cap_any(p, v)) * p.c;
             }
-          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&kv_empty[ks]));
         if (!(ok = mbar_wait(smem_u32(&kv_full[vs]), ((ring + 1) / NS) & 1, abort_flag))) break;
         if (!none) {
-          const int k0 = key0 + 2 * t;  // keys k0 + {0, 1, 8, 9} of the block
-          if (see_hi - b * kN < key0 + 16) {
+          const int k0 = key0 + g;  // keys k0 and k0 + 8 of the block
+          if (see_hi - blk * kN < key0 + 16) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (k0 + 8 * i + (j & 1) >= hi[j >> 1] - b * kN) x[i][j] = -INFINITY;
-          }
-          if (key0 < see_lo - b * kN) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (k0 + 8 * i + (j & 1) < lo[j >> 1] - b * kN) x[i][j] = -INFINITY;
+                if (k0 + 4 * (j & 2) >= hi[b][j & 1] - blk * kN) x[b][j] = -INFINITY;
           }
-          float2 va = lds64f(sc0 + vs * (kN * 4) + t * 8);
-          float2 vb = lds64f(sc0 + vs * (kN * 4) + 32 + t * 8);
-          if (s.hi - b * kN < key0 + 16 || s.lo - b * kN > key0) {
+          if (key0 < see_lo - blk * kN) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (k0 + 4 * (j & 2) < lo[b][j & 1] - blk * kN) x[b][j] = -INFINITY;
+          }
+          float v0 = lds32f(sc0 + vs * (kN * 4) + g * 4);
+          float v1 = lds32f(sc0 + vs * (kN * 4) + 32 + g * 4);
+          if (s.hi - blk * kN < key0 + 16 || s.lo - blk * kN > key0) {
             // scales of keys that no row sees may be anything
-            auto seen = [&](int k) { return k < s.hi - b * kN && k >= s.lo - b * kN; };
-            va.x = seen(k0) ? va.x : 0.0f, va.y = seen(k0 + 1) ? va.y : 0.0f;
-            vb.x = seen(k0 + 8) ? vb.x : 0.0f, vb.y = seen(k0 + 9) ? vb.y : 0.0f;
+            auto seen = [&](int k) { return k < s.hi - blk * kN && k >= s.lo - blk * kN; };
+            v0 = seen(k0) ? v0 : 0.0f;
+            v1 = seen(k0 + 8) ? v1 : 0.0f;
           }
-          float x0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-          float x1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
-          float sv = fmaxf(fmaxf(va.x, va.y), fmaxf(vb.x, vb.y));
-          if (__any_sync(0xffffffffu, x0 > m[0] + kLag || x1 > m[1] + kLag || sv * e_neg > 2.0f)) {
+          bool move = fmaxf(v0, v1) * e_neg > 2.0f;
 #pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
-              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-              sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, d));
-            }
-            // (the scales are those of the warp's 16 keys: the same E in every lane)
+          for (int b = 0; b < NB; ++b)
+            move |= fmaxf(x[b][0], x[b][2]) > m[b][0] + kLag ||
+                    fmaxf(x[b][1], x[b][3]) > m[b][1] + kLag;
+          if (__any_sync(0xffffffffu, move)) {
+            float sv = fmaxf(v0, v1);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, d));
             const float e = fmaxf(e_pos, __uint_as_float(__float_as_uint(sv) & 0x7f800000u));
             const float fe = e_pos * (1.0f / e);
             e_pos = e;
             e_neg = 1.0f / e;
-            float f[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float mn = fmaxf(m[i], i ? x1 : x0);
-              f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - mn);
-              m[i] = mn;
-              l[i] *= f[i];
-              f[i] *= fe;
-            }
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              o[i][0] *= f[0], o[i][1] *= f[0];
-              o[i][2] *= f[1], o[i][3] *= f[1];
-            }
+              for (int i = 0; i < 2; ++i) {
+                float mn = fmaxf(x[b][i], x[b][i + 2]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                  mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+                mn = fmaxf(mn, m[b][i]);
+                const float f = m[b][i] == -INFINITY ? 0.0f : ex2(m[b][i] - mn);
+                m[b][i] = mn;
+                l[b][i] *= f;
+#pragma unroll
+                for (int k = 0; k < MT; ++k) {
+                  o[k][b][i] *= f * fe;
+                  o[k][b][i + 2] *= f * fe;
+                }
+              }
           }
-          const float z0 = m[0] == -INFINITY ? 0.0f : kLift8 - m[0];
-          const float z1 = m[1] == -INFINITY ? 0.0f : kLift8 - m[1];
-          const float sn[4] = {va.x * e_neg, va.y * e_neg, vb.x * e_neg, vb.y * e_neg};
-          uint32_t pa[4];
+          const float n0 = v0 * e_neg, n1 = v1 * e_neg;
+          uint32_t pb[NB][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float a0 = ex2(x[i][0] + z0), a1 = ex2(x[i][1] + z0);
-            const float b0 = ex2(x[i][2] + z1), b1 = ex2(x[i][3] + z1);
-            l[0] += a0 + a1;
-            l[1] += b0 + b1;
-            pa[2 * i] = f2h(a0 * sn[2 * i], a1 * sn[2 * i + 1]);
-            pa[2 * i + 1] = f2h(b0 * sn[2 * i], b1 * sn[2 * i + 1]);
+          for (int b = 0; b < NB; ++b) {
+            const float z0 = m[b][0] == -INFINITY ? 0.0f : kLift8 - m[b][0];
+            const float z1 = m[b][1] == -INFINITY ? 0.0f : kLift8 - m[b][1];
+            const float a0 = ex2(x[b][0] + z0), a1 = ex2(x[b][1] + z1);
+            const float b0 = ex2(x[b][2] + z0), b1 = ex2(x[b][3] + z1);
+            l[b][0] += a0 + b0;
+            l[b][1] += a1 + b1;
+            pb[b][0] = transpose8(f2h(a0 * n0, a1 * n0));
+            pb[b][1] = transpose8(f2h(b0 * n1, b1 * n1));
           }
           const uint32_t vbase = kv0 + vs * C::kStage;
 #pragma unroll
@@ -351,9 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
                 u[2 + i] = __byte_perm(ka, kb, 0x7362);
               }
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma16816(o[h * 16 + 4 * c + j], pa, code_pair(u[(j >> 1) * 2], j & 1 ? 0x4342 : 0x4140),
-                         code_pair(u[(j >> 1) * 2 + 1], j & 1 ? 0x4342 : 0x4140));
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t a[4] = {code_pair(u[2 * j], 0x4140), code_pair(u[2 * j], 0x4342),
+                                       code_pair(u[2 * j + 1], 0x4140),
+                                       code_pair(u[2 * j + 1], 0x4342)};
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                  mma16816(o[h * 8 + 2 * c + j][b], a, pb[b][0], pb[b][1]);
+              }
             }
           }
         }
@@ -363,22 +402,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       if (!ok) break;
       // ---- the warps' parts of the tile together
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if (t == 0) ml_sm[(par * kWarps + warp) * kM + g + 8 * i] = make_float2(m[i], l[i]);
-      }
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], d);
+          if (g == 0)
+            ml_sm[(par * kWarps + warp) * kM + 8 * b + 2 * t + i] = make_float2(m[b][i], l[b][i]);
+        }
       if (!meet()) break;
-      // (a warp's own factor, for its rows g and g + 8)
-      float f[2];
+      // (a warp's own factor)
+      float f[NB][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float M = -INFINITY;
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k)
-          M = fmaxf(M, ml_sm[(par * kWarps + k) * kM + g + 8 * i].x);
-        f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - M) * e_pos;
-      }
+        for (int i = 0; i < 2; ++i) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k)
+            M = fmaxf(M, ml_sm[(par * kWarps + k) * kM + 8 * b + 2 * t + i].x);
+          f[b][i] = m[b][i] == -INFINITY ? 0.0f : ex2(m[b][i] - M) * e_pos;
+        }
       float *mine = p.part + (int64_t)(blockIdx.x * 2 + max(s.slot, 0)) * C::kPart;
       auto out_at = [&](int r) {
         const int n = s.rem + r, k = row_token(n);
@@ -387,26 +431,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       float *buf = reinterpret_cast<float *>(buf_sm);
       constexpr int F4 = C::kRow / 4;  // float4 pieces of a row of the buffer
 #pragma unroll
-      for (int h = 0; ok && h < (D + 127) / 128; ++h) {
-        if (h > 0 && !meet()) break;
+      for (int h = 0; h < (D + 127) / 128; ++h) {
+        if (h > 0 && ok) meet();
+        if (!ok) break;
+        // a thread's F4 / 2 columns of a row are contiguous: two of each tile
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int k = 0; k < F4 / 4; ++k) {
-            // this thread's D / 4 columns are contiguous: piece k has tiles n..n+3 of one half
-            constexpr int H = F4 / 8;  // pieces of a half
-            const int n = h * 16 + 4 * (k % H), c = 2 * i + k / H;
-            const int at = (F4 / 4) * t + (D == 64 ? k ^ ((t >> 1) * 2 + (g & 1))
-                                                   : k ^ (2 * t + (g & 1)));
-            *reinterpret_cast<float4 *>(buf + ((warp * kM + g + 8 * i) * F4 + at) * 4) =
-                make_float4(o[n][c] * f[i], o[n + 1][c] * f[i], o[n + 2][c] * f[i],
-                            o[n + 3][c] * f[i]);
-          }
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < F4 / 8; ++k) {
+              const int row = 8 * b + 2 * t + i, n = h * 8 + 2 * k;
+              *reinterpret_cast<float4 *>(
+                  buf + ((warp * kM + row) * F4 + place(row, (F4 / 8) * g + k)) * 4) =
+                  make_float4(o[n][b][i] * f[b][i], o[n][b][i + 2] * f[b][i],
+                              o[n + 1][b][i] * f[b][i], o[n + 1][b][i + 2] * f[b][i]);
+            }
         if (!meet()) break;
         for (int it = tid; it < s.rows * F4; it += kWarps * 32) {
-          const int r = it / F4, q4 = it % F4, tt = q4 / (F4 / 4), k = q4 % (F4 / 4);
-          const int at = (F4 / 4) * tt + (D == 64 ? k ^ ((tt >> 1) * 2 + (r & 1))
-                                                  : k ^ (2 * tt + (r & 1)));
+          const int r = it / F4, q4 = it % F4, at = place(r, q4);
           float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           float M = -INFINITY, L = 0.0f;
 #pragma unroll
@@ -598,19 +641,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
   }
 }
 
-template <int D, int CAP>
+template <int D, int NB, int CAP>
 qz_status launch(const Attn8Params &p, int sms, cudaStream_t s) {
-  using C = Cfg8<D>;
-  const cudaError_t e = allow_smem<attn8_kernel<D, CAP>>(C::kSmem);
+  using C = Cfg8<D, NB>;
+  const cudaError_t e = allow_smem<attn8_kernel<D, NB, CAP>>(C::kSmem);
   if (e != cudaSuccess) return cuda_status(e);
-  attn8_kernel<D, CAP><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, C::kSmem, s>>>(p);
+  attn8_kernel<D, NB, CAP><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, C::kSmem, s>>>(p);
   return launch_status();
 }
 
-template <int D>
+template <int D, int NB>
 qz_status launch_cap(const Attn8Params &p, int sms, cudaStream_t s) {
-  if (p.cap == 0.0f) return launch<D, 0>(p, sms, s);
-  return p.cap <= kShortCap ? launch<D, 1>(p, sms, s) : launch<D, 2>(p, sms, s);
+  if (p.cap == 0.0f) return launch<D, NB, 0>(p, sms, s);
+  return p.cap <= kShortCap ? launch<D, NB, 1>(p, sms, s) : launch<D, NB, 2>(p, sms, s);
+}
+
+template <int D>
+qz_status launch_rows(const Attn8Params &p, bool one, int sms, cudaStream_t s) {
+  return one ? launch_cap<D, 1>(p, sms, s) : launch_cap<D, 2>(p, sms, s);
 }
 
 }  // namespace
@@ -619,7 +667,8 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
                                 const PagedInt8View &c, const SeqView &sv, float scale,
                                 float softcap, int64_t window, __half *out, int64_t o_token,
                                 int64_t o_head, void *workspace, cudaStream_t s) {
-  if (sv.n_tokens * (hq / c.hkv) > (int64_t)kM * sv.n_seqs)
+  const int64_t rows = sv.n_tokens * (hq / c.hkv);  // of a KV head, of all sequences
+  if (rows > (int64_t)16 * sv.n_seqs)
     return launch_attention_int8_tc(q, hq, q_token, q_head, c, sv, scale, softcap, window, out,
                                     o_token, o_head, workspace, s);
   DeviceInfo di;
@@ -644,8 +693,9 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
   p.s = sv;
   p.cnt = static_cast<unsigned *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + QZ_ATTENTION_SYNC_BYTES);
-  if (c.D == 256) return launch_cap<256>(p, di.sms, s);
-  return c.D == 128 ? launch_cap<128>(p, di.sms, s) : launch_cap<64>(p, di.sms, s);
+  const bool one = rows <= (int64_t)8 * sv.n_seqs;
+  if (c.D == 256) return launch_rows<256>(p, one, di.sms, s);
+  return c.D == 128 ? launch_rows<128>(p, one, di.sms, s) : launch_rows<64>(p, one, di.sms, s);
 }
 
 qz_status read_attn8_error(int *code, int clear) {
