@@ -31,11 +31,6 @@
 namespace qz {
 namespace {
 
-constexpr int kWarps = 8;             // each has 16 of a block's keys
-constexpr int kLoadWarp = kWarps;     // the third warpgroup: one warp loads, three do nothing
-constexpr int kThreads = 384;
-constexpr int kMathRegs = 216, kOtherRegs = 72;  // of 168 a thread at launch
-static_assert(8 * kMathRegs + 4 * kOtherRegs <= 12 * 168, "register split");
 constexpr float kLift8 = 6.0f;        // log2 of the weight at m
 static_assert(kLift8 + kLag + 1.0f < 16.0f, "weights are fp16");
 constexpr int kHead8 = 4096;          // barriers, announced tiles, row maxima and sums
@@ -43,6 +38,18 @@ constexpr int kHead8 = 4096;          // barriers, announced tiles, row maxima a
 template <int D, int NB>
 struct Cfg8 {
   static constexpr int kM = 8 * NB;                 // rows of a tile
+  // Warps that multiply: 8, each with 16 of a block's keys, or two such groups that take
+  // blocks in turn.  32 tokens over 16384 keys: D 64, 32 heads on 8, 99 us with one group and
+  // 86 with two (a warp's chain of loads, conversions and products is longer than its bytes
+  // take), D 128, 64 on 8, 124 and 138 (96 registers a thread).
+  static constexpr int kGroups = NB == 1 && D == 64 ? 2 : 1;
+  static constexpr int kWarps = 8 * kGroups;
+  // and a warpgroup that loads
+  static constexpr int kThreads = kWarps * 32 + 128;
+  static constexpr int kLaunchRegs = kGroups == 2 ? 96 : 168;  // a thread
+  static constexpr int kMathRegs = kGroups == 2 ? 104 : 216;
+  static constexpr int kOtherRegs = kGroups == 2 ? 64 : 72;
+  static_assert(kWarps * kMathRegs + 4 * kOtherRegs <= (kWarps + 4) * kLaunchRegs, "registers");
   static constexpr int kRow = D < 128 ? D : 128;    // bytes of a swizzled row
   static constexpr int kStage = kN * D;             // bytes of a K or V block
   static constexpr int kNS = 131072 / kStage;       // K and V slots: 16, 8, 4
@@ -98,8 +105,10 @@ __device__ __forceinline__ float lds32f(uint32_t a) {
 }
 
 template <int D, int NB, int CAP>
-__global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
+__global__ void __launch_bounds__(Cfg8<D, NB>::kThreads, 1)
+    attn8_kernel(const __grid_constant__ Attn8Params p) {
   using C = Cfg8<D, NB>;
+  constexpr int kWarps = C::kWarps, kLoadWarp = kWarps, GR = C::kGroups;
   constexpr int kM = C::kM, NS = C::kNS, KS = C::kSteps, MT = D / 16;
   constexpr bool kQinSm = C::kQ > 0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -114,8 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
   uint64_t *seg_full = kv_empty + 16, *seg_empty = seg_full + kSegs;
   uint64_t *met = seg_empty + kSegs;  // the eight warps of a tile
   int *abort_flag = reinterpret_cast<int *>(met + 1);
-  uint32_t *issued = reinterpret_cast<uint32_t *>(abort_flag + 1);
-  unsigned *arrived_sm = issued + 1;
+  unsigned *arrived_sm = reinterpret_cast<unsigned *>(abort_flag + 1);
   Seg *seg_sm = reinterpret_cast<Seg *>(head + 512);           // [kSegs]
   float2 *ml_sm = reinterpret_cast<float2 *>(head + 1024);     // [2][kWarps][kM] maximum and sum
 
@@ -123,15 +131,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(&kv_full[i]), p.runs ? 1 : 33);
-      mbar_init(smem_u32(&kv_empty[i]), kWarps);
+      mbar_init(smem_u32(&kv_empty[i]), 8);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(smem_u32(&seg_full[i]), 1);
-      mbar_init(smem_u32(&seg_empty[i]), kWarps);
+      mbar_init(smem_u32(&seg_empty[i]), kWarps + 3);
     }
     mbar_init(smem_u32(met), kWarps);
     *abort_flag = 0;
-    *issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   Walker<kM> w;
@@ -143,22 +150,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       w.template start<8>(p);
   }
   __syncthreads();
+  uint32_t issued = 0;  // blocks up to the last that this warp loaded of
+
+  // The n-th announced tile (every warp but the one that announces).
+  auto read_seg = [&](uint32_t n, Seg &s) -> bool {
+    if (!mbar_wait(smem_u32(&seg_full[n % kSegs]), (n / kSegs) & 1, abort_flag)) return false;
+    const uint4 *src = reinterpret_cast<const uint4 *>(&seg_sm[n % kSegs]);
+    uint4 *dst = reinterpret_cast<uint4 *>(&s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = src[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n % kSegs]));
+    return true;
+  };
 
   if (warp < kWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMathRegs));
     const int g = lane >> 2, t = lane & 3;
+    const int own = warp & 7, group = warp >> 3;  // place in the group
     // n / G for n < G + 256 (see the fp16 kernel)
     auto row_token = [&](int n) { return (int)(((float)n + 0.5f) * p.inv_g); };
-    const uint32_t kv0 = smem_u32(kv_sm), sc0 = smem_u32(scale_sm) + warp * 64;
+    const uint32_t kv0 = smem_u32(kv_sm), sc0 = smem_u32(scale_sm) + own * 64;
     // this thread's 16 bytes of a key: rows g and g + 8 of the warp's 16, chunks 2 t and 2 t + 1
     // (of 8; D 64: t of 4); of a value: rows 2 t + {0, 1, 8, 9}, chunk g (D 64: half of g / 2)
-    const int krow = warp * 16 + g;
+    const int krow = own * 16 + g;
     const uint32_t k_at = krow * C::kRow;
     const uint32_t k_sw = D == 64 ? (t ^ ((krow >> 1) & 3)) << 4 : ((2 * t) ^ (krow & 7)) << 4;
     uint32_t v_at[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = warp * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+      const int r = own * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
       v_at[i] = r * C::kRow + (D == 64 ? (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8
                                        : (g ^ (r & 7)) << 4);
     }
@@ -178,16 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
     };
     while (ok) {
       Seg s;
-      if (!(ok = mbar_wait(smem_u32(&seg_full[n_seg % kSegs]), (n_seg / kSegs) & 1, abort_flag)))
-        break;
-      {
-        const uint4 *src = reinterpret_cast<const uint4 *>(&seg_sm[n_seg % kSegs]);
-        uint4 *dst = reinterpret_cast<uint4 *>(&s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = src[i];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&seg_empty[n_seg % kSegs]));
+      if (!(ok = read_seg(n_seg, s))) break;
       const int par = n_seg++ & 1;
       if (s.rows == 0) break;
       // ---- queries: row 8 b + g as an operand, rows 8 b + 2 t and 2 t + 1 of the logits
@@ -243,10 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
         for (int i = 0; i < MT; ++i) o[i][b][0] = o[i][b][1] = o[i][b][2] = o[i][b][3] = 0.0f;
       }
       float e_pos = exp2f(-40.0f), e_neg = exp2f(40.0f);  // 2^E and 2^-E
-      for (int blk = s.b0; blk < s.b1; ++blk, ring += 2) {
-        const uint32_t ks = ring % NS, vs = (ring + 1) % NS;
-        if (!(ok = mbar_wait(smem_u32(&kv_full[ks]), (ring / NS) & 1, abort_flag))) break;
-        const int key0 = warp * 16;  // of the block
+      const uint32_t ring0 = ring;
+      ring += 2 * (s.b1 - s.b0);
+      for (int blk = s.b0 + group; blk < s.b1; blk += GR) {
+        const uint32_t at0 = ring0 + 2 * (blk - s.b0);  // of the K slot; the V slot follows
+        const uint32_t ks = at0 % NS, vs = ks + 1;
+        if (!(ok = mbar_wait(smem_u32(&kv_full[ks]), (at0 / NS) & 1, abort_flag))) break;
+        const int key0 = own * 16;  // of the block
         // (the block's end may pass 32 bits)
         const bool none = s.hi - blk * kN <= key0 || (int64_t)blk * kN + key0 + 16 <= s.lo;
         float x[NB][4];  // keys g (0, 1) and g + 8 (2, 3) of rows 2 t and 2 t + 1
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&kv_empty[ks]));
-        if (!(ok = mbar_wait(smem_u32(&kv_full[vs]), ((ring + 1) / NS) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(smem_u32(&kv_full[vs]), (at0 / NS) & 1, abort_flag))) break;
         if (!none) {
           const int k0 = key0 + g;  // keys k0 and k0 + 8 of the block
           if (see_hi - blk * kN < key0 + 16) {
@@ -529,11 +544,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
   }
-  if (warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
     // --------------------------------------------------------------- load --
-    uint32_t ring = 0;
+    // Four warps: keys and values, of every other block each.  (One warp's chain of waits,
+    // pages and copies takes 2600 clocks a block, twice what HBM leaves it.)
+    const bool keys = ((warp - kLoadWarp) & 1) == 0;
+    const uint32_t turn = (uint32_t)(warp - kLoadWarp) >> 1;
+    const CUtensorMap *map = keys ? &p.kmap : &p.vmap;
+    const float *scales = keys ? p.ks : p.vs;
+    const int64_t sc_page = keys ? p.ks_page : p.vs_page, sc_head = keys ? p.ks_head : p.vs_head;
+    const int64_t sc_token = keys ? p.ks_token : p.vs_token;
     bool ok = true;
     const int ppb = p.page_size >= kN ? 1 : kN >> p.page_shift;  // pages per block
     const int box_rows = min(p.page_size, kN);
@@ -560,9 +582,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
       }
       return id;
     };
-    auto issue = [&](bool keys, const Seg &g, int b, int page) -> bool {
-      const int slot = ring % NS;
-      if (ring >= NS && !mbar_wait(smem_u32(&kv_empty[slot]), (ring / NS - 1) & 1, abort_flag))
+    // Keys or values of block b, the n-th of the CTA.
+    auto issue = [&](const Seg &g, int b, uint32_t n, int page) -> bool {
+      const uint32_t fill = 2 * n + (keys ? 0 : 1);
+      const int slot = fill % NS;
+      if (fill >= NS && !mbar_wait(smem_u32(&kv_empty[slot]), (fill / NS - 1) & 1, abort_flag))
         return false;
       const uint32_t bar = smem_u32(&kv_full[slot]);
       const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
@@ -585,22 +609,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
           asm volatile(
               "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
               "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + d * (kN * 128)),
-              "l"(reinterpret_cast<uint64_t>(keys ? &p.kmap : &p.vmap)), "r"(d * 128), "r"(at), "r"(g.head), "r"(page),
+              "l"(reinterpret_cast<uint64_t>(map)), "r"(d * 128), "r"(at), "r"(g.head), "r"(page),
               "r"(bar)
               : "memory");
       }
-      if (keys)
-        scale_copy(p, p.ks, p.ks_page, p.ks_head, p.ks_token, sc, g, b, page, bar);
-      else
-        scale_copy(p, p.vs, p.vs_page, p.vs_head, p.vs_token, sc, g, b, page, bar);
+      scale_copy(p, scales, sc_page, sc_head, sc_token, sc, g, b, page, bar);
       if (!p.runs)
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar)
                      : "memory");
       __syncwarp();
-      ++ring;
+      issued = n + 1;
       return true;
     };
-    uint32_t n_seg = 0;
+    uint32_t n_seg = 0, first = 0;  // tiles; blocks of those before
     auto announce = [&](const Seg &g) -> bool {
       const uint32_t at = n_seg % kSegs;
       if (n_seg >= kSegs &&
@@ -611,33 +632,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(const __grid_constan
         mbar_arrive(smem_u32(&seg_full[at]));
       }
       __syncwarp();
-      ++n_seg;
       return true;
     };
     while (ok) {
-      const Seg g = w.next(p);
-      ok = announce(g);
+      Seg g;
+      if (warp == kLoadWarp) {
+        g = w.next(p);
+        ok = announce(g);
+      } else {
+        ok = read_seg(n_seg, g);
+      }
+      ++n_seg;
       if (!ok || g.rows == 0) break;
-      const int nb = g.b1 - g.b0;
-      if (nb > 0) {
-        batch = (int)(((int64_t)g.b0 * kN) >> p.page_shift);
+      const int nb = g.b1 - g.b0, skip = (int)((first ^ turn) & 1);
+      if (skip < nb) {
+        batch = (int)(((int64_t)(g.b0 + skip) * kN) >> p.page_shift);
         ids = fetch(g, batch);
         ids_ahead = fetch(g, batch + 32);
       }
-      for (int b = g.b0; ok && b < g.b1; ++b) {
-        const int page = page_of(g, b);
-        ok = issue(true, g, b, page) && issue(false, g, b, page);
-      }
+      for (int j = skip; ok && j < nb; j += 2)
+        ok = issue(g, g.b0 + j, first + j, page_of(g, g.b0 + j));
+      first += nb;
     }
-    if (lane == 0) *issued = ring;
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
   __syncthreads();
-  if (*(volatile int *)abort_flag && warp == kLoadWarp) {  // copies in flight end before the CTA
+  if (*(volatile int *)abort_flag && warp >= kLoadWarp) {  // copies in flight end before the CTA
     const unsigned long long until = gtimer() + kWaitNs;
-    const uint32_t n = *issued;
-    for (uint32_t r = n - min(n, (uint32_t)NS); r < n; ++r)
-      mbar_drain(smem_u32(&kv_full[r % NS]), (r / NS) & 1, until);
+    for (uint32_t k = 0; k < NS / 4 && issued > 2 * k; ++k) {
+      const uint32_t fill = 2 * (issued - 1 - 2 * k) + ((warp - kLoadWarp) & 1);
+      mbar_drain(smem_u32(&kv_full[fill % NS]), (fill / NS) & 1, until);
+    }
   }
 }
 
@@ -646,7 +671,7 @@ qz_status launch(const Attn8Params &p, int sms, cudaStream_t s) {
   using C = Cfg8<D, NB>;
   const cudaError_t e = allow_smem<attn8_kernel<D, NB, CAP>>(C::kSmem);
   if (e != cudaSuccess) return cuda_status(e);
-  attn8_kernel<D, NB, CAP><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, C::kSmem, s>>>(p);
+  attn8_kernel<D, NB, CAP><<<sms < kMaxCtas ? sms : kMaxCtas, C::kThreads, C::kSmem, s>>>(p);
   return launch_status();
 }
 
