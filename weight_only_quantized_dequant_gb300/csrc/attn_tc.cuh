@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *seg_full = xbar + 4, *seg_empty = seg_full + kSegs, *q_empty = seg_empty + kSegs;
   uint64_t *drained = q_empty + 1;  // the products of a CTA that gave up
   uint64_t *kv_ready = drained + 1;  // Q8: a slot's codes are fp16
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(kv_ready + kMaxStages);
+  uint64_t *half_done = kv_ready + kMaxStages;  // Q8: a stage's product of the first 64 keys
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(half_done + 2);
   int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
   // Copies that the load warp has issued, tiles that the query warps have
   uint32_t *issued = reinterpret_cast<uint32_t *>(abort_flag + 1);  // [kLoadWarp - kQWarp + 1]
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&p_full[i]), NQ == 2 ? 4 : 8);
       mbar_init(smem_u32(&o_done[i]), 1);
       mbar_init(smem_u32(&p_half[i]), 4);
+      mbar_init(smem_u32(&half_done[i]), 1);
     }
     mbar_init(smem_u32(q_full), 2);
     mbar_init(smem_u32(q_empty), 1);
@@ -310,6 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Q8: logits get their keys' factors (and c with them) where they become weights, and
     // the running maximum is held against a bound of theirs
     constexpr bool kBound = Q8 && CAP == 0;
+    // Q8: a thread's 128 columns in two passes, each with a maximum of its own, since the
+    // factors that it reads leave no registers for all of them
+    constexpr int kParts = Q8 && NQ == 2 ? 2 : 1, NP = NC / kParts;
     const float c = kBound ? 1.0f : p.c;  // of m and the logits
     bool ok = true;
     // The other warpgroup's value of this row (NQ = 1).
@@ -384,141 +389,148 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_after();
         const uint32_t s_tm = tmem + lane_base + 128 * buf;
-        float s[NC];
-#pragma unroll
-        for (int k = 0; k < NC / 32; ++k)
-          tmem_ld32(s_tm + col0 + 32 * k, reinterpret_cast<uint32_t *>(s) + 32 * k);
         const uint32_t set = (scale0 + b - g.b0) % kScaleBlocks;
-        const float *kf = scale_sm + set * (2 * kN) + col0, *vf = kf + kN;
-        const float *uf = unit_sm + set * 4 + col0 / 32;
-        tmem_ld_wait();
-        if (Q8 && CAP) {
+#pragma unroll 1
+        for (int part = 0; part < kParts; ++part) {
+          const int col = col0 + part * NP;  // first key column of this pass
+          float s[NP];
 #pragma unroll
-          for (int k = 0; k < NC; k += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(kf + k);
-            s[k] *= f.x, s[k + 1] *= f.y, s[k + 2] *= f.z, s[k + 3] *= f.w;
-          }
-        }
-        if (CAP) {
+          for (int k = 0; k < NP / 32; ++k)
+            tmem_ld32(s_tm + col + 32 * k, reinterpret_cast<uint32_t *>(s) + 32 * k);
+          const float *kf = scale_sm + set * (2 * kN) + col, *vf = kf + kN;
+          const float *uf = unit_sm + set * 4 + col / 32;
+          tmem_ld_wait();
+          if (Q8 && CAP) {
 #pragma unroll
-          for (int k = 0; k < NC; ++k) s[k] = CAP == 1 ? cap_far(p, s[k]) : cap_any(p, s[k]);
-        }
-        // keys [k_lo, k_hi) of this row; a block that no bound cuts needs neither
-        if (see_hi - b * kN < col0 + NC) {  // (the block's end may pass 32 bits)
-          const int k_hi = hi - b * kN - col0;
-#pragma unroll
-          for (int k = 0; k < NC; ++k) s[k] = k < k_hi ? s[k] : -INFINITY;
-        }
-        if (b * kN + col0 < see_lo) {
-          const int k_lo = lo - b * kN - col0;
-#pragma unroll
-          for (int k = 0; k < NC; ++k) s[k] = k >= k_lo ? s[k] : -INFINITY;
-        }
-        float mb;
-        if (kBound) {
-          // No logit is above this: factors are within 1/16 of their unit.
-          mb = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < NC / 32; ++h) {
-            float a = s[32 * h], c = s[32 * h + 1];
-#pragma unroll
-            for (int k = 2; k < 30; k += 4) {
-              a = max3(a, s[32 * h + k], s[32 * h + k + 1]);
-              c = max3(c, s[32 * h + k + 2], s[32 * h + k + 3]);
+            for (int k = 0; k < NP; k += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(kf + k);
+              s[k] *= f.x, s[k + 1] *= f.y, s[k + 2] *= f.z, s[k + 3] *= f.w;
             }
-            a = max3(a, s[32 * h + 30], s[32 * h + 31]);
-            a = fmaxf(a, c);
-            mb = fmaxf(mb, a * (a > 0.0f ? 1.0625f : 0.9375f) * uf[h]);
           }
-        } else {
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          if (CAP) {
 #pragma unroll
-          for (int k = 4; k < NC - 4; k += 8)
+            for (int k = 0; k < NP; ++k) s[k] = CAP == 1 ? cap_far(p, s[k]) : cap_any(p, s[k]);
+          }
+          // keys [k_lo, k_hi) of this row; a block that no bound cuts needs neither
+          if (see_hi - b * kN < col + NP) {  // (the block's end may pass 32 bits)
+            const int k_hi = hi - b * kN - col;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
+            for (int k = 0; k < NP; ++k) s[k] = k < k_hi ? s[k] : -INFINITY;
+          }
+          if (b * kN + col < see_lo) {
+            const int k_lo = lo - b * kN - col;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[NC - 4 + e]);
-          mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        }
-        if (NQ == 1) {
-          float other;
-          if (!(ok = exchange(mb, &other))) break;
-          mb = fmaxf(mb, other);
-        }
-        // move the maximum where it lags too far, and rescale what was summed
-        const bool move = (mb - m) * c > kLag || (m == -INFINITY && mb > -INFINITY);
-        if (__any_sync(0xffffffffu, move)) {
-          if (kBound) {  // the largest logit itself
+            for (int k = 0; k < NP; ++k) s[k] = k >= k_lo ? s[k] : -INFINITY;
+          }
+          float mb;
+          if (kBound) {
+            // No logit is above this: factors are within 1/16 of their unit.
             mb = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < NC; k += 4) {
-              const float4 f = *reinterpret_cast<const float4 *>(kf + k);
-              mb = max3(mb, s[k] * f.x, s[k + 1] * f.y);
-              mb = max3(mb, s[k + 2] * f.z, s[k + 3] * f.w);
+            for (int h = 0; h < NP / 32; ++h) {
+              float a = s[32 * h], c = s[32 * h + 1];
+#pragma unroll
+              for (int k = 2; k < 30; k += 4) {
+                a = max3(a, s[32 * h + k], s[32 * h + k + 1]);
+                c = max3(c, s[32 * h + k + 2], s[32 * h + k + 3]);
+              }
+              a = max3(a, s[32 * h + 30], s[32 * h + 31]);
+              a = fmaxf(a, c);
+              mb = fmaxf(mb, a * (a > 0.0f ? 1.0625f : 0.9375f) * uf[h]);
             }
-            if (NQ == 1) {
-              float other;
-              if (!(ok = exchange(mb, &other))) break;
-              mb = fmaxf(mb, other);
-            }
+          } else {
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int k = 4; k < NP - 4; k += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[NP - 4 + e]);
+            mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           }
-          // (kBound: every row of the warp moves, so that the next one comes later)
-          const float mn = kBound ? fmaxf(m, mb) : move ? mb : m;
-          const float f = m == -INFINITY ? (mn > -INFINITY ? 0.0f : 1.0f) : ex2((m - mn) * c);
-          m = mn;
-          l *= f;
-          if (b > g.b0 && (!kBound || __any_sync(0xffffffffu, f != 1.0f))) {
-            // NQ = 2: this stage's earlier products precede the S just read
-            if (NQ == 1 && !(ok = last_product(b))) break;
-            fence_after();
+          if (NQ == 1) {
+            float other;
+            if (!(ok = exchange(mb, &other))) break;
+            mb = fmaxf(mb, other);
+          }
+          // move the maximum where it lags too far, and rescale what was summed
+          const bool move = (mb - m) * c > kLag || (m == -INFINITY && mb > -INFINITY);
+          if (__any_sync(0xffffffffu, move)) {
+            if (kBound) {  // the largest logit itself
+              mb = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < NP; k += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(kf + k);
+                mb = max3(mb, s[k] * f.x, s[k + 1] * f.y);
+                mb = max3(mb, s[k + 2] * f.z, s[k + 3] * f.w);
+              }
+              if (NQ == 1) {
+                float other;
+                if (!(ok = exchange(mb, &other))) break;
+                mb = fmaxf(mb, other);
+              }
+            }
+            // (kBound: every row of the warp moves, so that the next one comes later)
+            const float mn = kBound ? fmaxf(m, mb) : move ? mb : m;
+            const float f = m == -INFINITY ? (mn > -INFINITY ? 0.0f : 1.0f) : ex2((m - mn) * c);
+            m = mn;
+            l *= f;
+            if ((b > g.b0 || part > 0) && (!kBound || __any_sync(0xffffffffu, f != 1.0f))) {
+              // NQ = 2: this stage's earlier products precede the S just read, but for that of
+              // this block's first keys
+              if (NQ == 1 && !(ok = last_product(b))) break;
+              if (part > 0 && !(ok = mbar_wait(smem_u32(&half_done[wg]), ph, abort_flag))) break;
+              fence_after();
 #pragma unroll 1
-            for (int k = 0; k < DC; k += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_tm + k, o);
-              tmem_ld_wait();
+              for (int k = 0; k < DC; k += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_tm + k, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_tm + k, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(o_tm + k, o);
+              }
             }
           }
-        }
-        const float mc = m == -INFINITY ? 0.0f : m * c - kLift;
-        const float2 mc2 = make_float2(-mc, -mc);
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          const float mc = m == -INFINITY ? 0.0f : m * c - kLift;
+          const float2 mc2 = make_float2(-mc, -mc);
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int h = 0; h < NC / 32; ++h) {
-          uint32_t pk[16];
+          for (int h = 0; h < NP / 32; ++h) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const int at = 32 * h + 2 * k;
-            float4 kc = make_float4(c, c, c, c), vc;
-            if (kBound) kc = *reinterpret_cast<const float4 *>(kf + at);
-            if (Q8) vc = *reinterpret_cast<const float4 *>(vf + at);
+            for (int k = 0; k < 16; k += 2) {
+              const int at = 32 * h + 2 * k;
+              float4 kc = make_float4(c, c, c, c), vc;
+              if (kBound) kc = *reinterpret_cast<const float4 *>(kf + at);
+              if (Q8) vc = *reinterpret_cast<const float4 *>(vf + at);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float2 e = fma2(make_float2(s[at + 2 * j], s[at + 2 * j + 1]),
-                              j ? make_float2(kc.z, kc.w) : make_float2(kc.x, kc.y), mc2);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
-              sum[j] = add2(sum[j], e);
-              if (Q8) e = mul2(e, j ? make_float2(vc.z, vc.w) : make_float2(vc.x, vc.y));
-              pk[k + j] = f2h(e.x, e.y);
+              for (int j = 0; j < 2; ++j) {
+                float2 e = fma2(make_float2(s[at + 2 * j], s[at + 2 * j + 1]),
+                                j ? make_float2(kc.z, kc.w) : make_float2(kc.x, kc.y), mc2);
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+                sum[j] = add2(sum[j], e);
+                if (Q8) e = mul2(e, j ? make_float2(vc.z, vc.w) : make_float2(vc.x, vc.y));
+                pk[k + j] = f2h(e.x, e.y);
+              }
+            }
+            tmem_st16(s_tm + col / 2 + 16 * h, pk);
+            if (NQ == 2 && kParts == 1 && h == 1) {  // the product starts on these
+              tmem_st_wait();
+              fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&p_half[buf]));
             }
           }
-          tmem_st16(s_tm + col0 / 2 + 16 * h, pk);
-          if (NQ == 2 && h == 1) {  // the product starts on these
-            tmem_st_wait();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_half[buf]));
-          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (NQ == 1 && !(ok = last_product(b))) break;
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&(part == kParts - 1 ? p_full : p_half)[buf]));
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (NQ == 1 && !(ok = last_product(b))) break;
-        tmem_st_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+        if (!ok) break;
       }
       if (!ok) break;
       // ---- the tile's rows, or this CTA's part of them
@@ -762,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < stages; ++t) {
             if (!(ok = mbar_wait(smem_u32(&p_half[t]), n_stage[t] & 1, abort_flag))) break;
             fence_after();
-            pv(t, 0, 256 + t * D, v, j > 0, false, nullptr);
+            pv(t, 0, 256 + t * D, v, j > 0, false, Q8 ? &half_done[t] : nullptr);
             if (!(ok = mbar_wait(smem_u32(&p_full[t]), n_stage[t] & 1, abort_flag))) break;
             fence_after();
             ++n_stage[t];
@@ -851,11 +863,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float unit = __uint_as_float((uint32_t)(127 + e) << 23) * (CAP ? 1.0f : p.c);
             const bool tiny = x < 0x1p-21f;
             s = __float2half_rn(tiny ? x : four_bits(x));
-            *k = (tiny ? 1.0f : x / four_bits(x)) * unit;
+            *k = (tiny ? 1.0f : x * __frcp_rn(four_bits(x))) * unit;
             if (lane == 0) unit_sm[set * 4 + group] = unit;
             const float w = fminf(fmaxf(four_bits(y), 0x1p-21f), 512.0f);
             part_sm[set * kN + row] = __float2half_rn(w);
-            *v = y / w;
+            *v = y * __frcp_rn(w);
           } else {
             s = part_sm[set * kN + row];
             large = __any_sync(0xffffffffu, __half2float(s) > 32.0f);
