@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Values' s are fp16 as they are, from 2^-21 to 512; r is below 15/16 for smaller ones.
     // A byte under the bits of 1024 is 1024 + code + 128 once its sign is turned.
     constexpr int kChunks = D == 64 ? 4 : 8;
-    uint32_t ring = 0, scales = 0, values = 0;
+    uint32_t ring = 0, scales = 0, values = 0, segs = 0;
     auto four_bits = [](float x) {
       return __uint_as_float((__float_as_uint(x) + 0x00080000u) & 0xfff00000u);
     };
@@ -920,17 +920,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&kv_ready[slot]));
+        if (p.q_boxes && i == 0) {  // the tile before has its last logits about now
+          if (segs > 0 && !mbar_wait(smem_u32(q_empty), (segs - 1) & 1, abort_flag)) return false;
+          const int half = warp - kQWarp;
+          if (lane == 0) copy_queries(g, half, g.tok + half * (kM / 2) / p.G);
+          __syncwarp();
+          ++segs;
+        }
       }
       return true;
     };
-    uint32_t n_seg = 0, segs = 0;
+    uint32_t n_seg = 0;
     for (;;) {
       Seg g;
       if (!read_seg(n_seg, g)) break;
       free_seg(n_seg++);
       if (g.rows == 0) break;
       if (g.b1 <= g.b0) continue;
-      if (Q8 && p.q_boxes) {  // queries come by the load warp
+      if (Q8 && p.q_boxes) {  // queries come behind the first keys
         if (!turn_rows(g)) break;
         continue;
       }
@@ -988,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++segs;
       if (Q8 && !turn_rows(g)) break;
     }
-    if (!Q8 && lane == 0) issued[warp - kQWarp] = p.q_boxes ? segs : 0;
+    if (lane == 0) issued[warp - kQWarp] = p.q_boxes ? segs : 0;
   } else {
     // --------------------------------------------------------------- load --
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -1094,7 +1101,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Seg next = w.next(p);
     ok = announce(next);
-    uint32_t q_tiles = 0;  // Q8: whose queries were issued
     while (ok && next.rows > 0) {
       const Seg g = next;
       const int nb = g.b1 - g.b0;
@@ -1110,16 +1116,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nb > 0) {
           const int page = page_of(g, b);
           ok = issue(true, g, b, page);
-          if (Q8 && p.q_boxes && j == 0 && ok) {
-            // the tile before has read its own about when the next slot is free
-            ok = q_tiles == 0 || mbar_wait(smem_u32(q_empty), (q_tiles - 1) & 1, abort_flag);
-            if (ok && lane == 0) {
-              copy_queries(g, 0, g.tok);
-              copy_queries(g, 1, g.tok + kM / 2 / p.G);
-            }
-            __syncwarp();
-            q_tiles += ok;
-          }
           if (NQ == 1) {  // K0, K1, V0, K2, V1, ..., the order in which they are used
             if (ok && j > 0) ok = issue(false, g, b - 1, prev);
             if (ok && j == nb - 1) ok = issue(false, g, b, page);
@@ -1131,10 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && j == 0 && n_seg == 1) ok = announce(next = w.next(p));
       }
     }
-    if (lane == 0) {
-      issued[kLoadWarp - kQWarp] = ring;
-      if (Q8) issued[0] = q_tiles, issued[1] = 0;
-    }
+    if (lane == 0) issued[kLoadWarp - kQWarp] = ring;
     if (Q8) asm volatile("cp.async.wait_all;" ::: "memory");
   }
   fence_before();
