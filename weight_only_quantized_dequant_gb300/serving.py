@@ -5,6 +5,9 @@ tokens of many requests, each request with its own low-rank adapter.
     norm -> q, k, v (+ adapters) -> rotary, cache -> attention -> o (+ adapter)
     norm -> gate, up (+ adapters) -> silu(gate) * up -> down (+ adapter)
 
+and behind the last layer the head: norm -> vocabulary product -> the next tokens, whose
+embeddings come from the same INT8 table.
+
 The residual stream is one fp16 buffer that the norms update in place.  The
 products take at most QZ_MAX_BATCH rows a call, so longer steps run them in
 slices; everything else takes the whole step at once.
@@ -34,7 +37,8 @@ class Products:
         """[x @ W^T for the matrices `names`, which share the input x [T, K]]."""
         ws = [self.mats[n] for n in names]
         T = x.shape[0]
-        ys = [torch.empty((T, w.N), dtype=torch.float16, device=x.device) for w in ws]
+        ys = [torch.empty((T, -(-w.N // 8) * 8), dtype=torch.float16, device=x.device)[:, :w.N]
+              for w in ws]
         gemm = api.gemm_int8_grouped if self.int8 else api.gemm_int4_outlier_grouped
         for a in range(0, T, _lib.QZ_MAX_BATCH):
             b = min(T, a + _lib.QZ_MAX_BATCH)
@@ -45,11 +49,11 @@ class Products:
 @dataclass
 class ServedLayer:
     """mats: q, k, v, o, gate, up, down as Int8Matrix or Int4oMatrix; norms:
-    the two fp16 weights; adapters: LoraAdapters by matrix name (those that have
-    any).  window and softcap as in layer.attention_paged."""
+    the two fp16 weights; cache: fp16 or INT8 rows; adapters: LoraAdapters by
+    matrix name (those that have any).  window and softcap as in layer.attention_paged."""
     mats: dict
     norms: tuple
-    cache: layer.PagedKV
+    cache: layer.PagedKV | layer.PagedKVInt8
     rope: torch.Tensor
     adapters: dict = field(default_factory=dict)
     eps: float = 1e-5
@@ -92,6 +96,35 @@ class ServedLayer:
         h = torch.nn.functional.silu(gate.float()).mul_(up).half()
         (out,) = self._linear(("down",), h, index)
         return out, residual
+
+
+@dataclass
+class ServedHead:
+    """The end of a step: norm, logits from the INT8 vocabulary table (tied with the
+    embeddings), and the choice of every row's next token."""
+    table: api.Int8Matrix
+    norm: torch.Tensor
+    eps: float = 1e-5
+    w_bias: float = 0.0
+    softcap: float = 0.0
+
+    def __post_init__(self):
+        self.products = Products({"head": self.table}, self.table.q.device)
+
+    def embed(self, tokens: torch.Tensor) -> torch.Tensor:
+        """The first layer's input for int32 tokens [T]."""
+        return api.embed_int8(self.table, tokens)
+
+    def logits(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
+        """fp16 [T, vocabulary] of the last layer's output and residual (or those rows of
+        them that are wanted)."""
+        y, _ = layer.rmsnorm(x, self.norm, self.eps, residual=residual, w_bias=self.w_bias)
+        (z,) = self.products(("head",), y)
+        return z if self.softcap == 0.0 else torch.tanh(z / self.softcap) * self.softcap
+
+    def __call__(self, x: torch.Tensor, residual: torch.Tensor, u: torch.Tensor, **options):
+        """(tokens, log probabilities) with the options of layer.sample."""
+        return layer.sample(self.logits(x, residual), u, **options)
 
 
 class PageTable:
