@@ -89,6 +89,22 @@ def test_handles(lib):  # noqa: F811
             dataclasses.replace(c, **bad)
 
 
+def test_a_cache_decides_by_its_kind(lib):  # noqa: F811
+    """Classes derived from a cache's are that kind of cache."""
+    class Mine(layer.PagedKV):
+        pass
+
+    class Mine8(layer.PagedKVInt8):
+        pass
+
+    a, b = handles()[0], cache8()
+    caches = (Mine(a.k, a.v), Mine8(b.k, b.v, b.k_scale, b.v_scale))
+    for f, make, name in CALLS[:2]:
+        for c in caches:
+            f(**make(cache=c))
+        assert [c[0] for c in lib.calls[-2:]] == [name[:-len("_int8")], name]
+
+
 def test_strides_of_a_cache(lib):  # noqa: F811
     """Strides are handed on as they are, and a dimension of one has none of its own."""
     nhd = layer.PagedKVInt8(

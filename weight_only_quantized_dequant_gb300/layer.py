@@ -346,7 +346,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedK
     else:
         ot, oh = _heads(q_out, "q_out", dev, T, H, D)
     lib = _lib.load()
-    name = "qz_rope_append" if type(cache) is PagedKV else "qz_rope_append_int8"
+    name = "qz_rope_append_int8" if isinstance(cache, PagedKVInt8) else "qz_rope_append"
     st = getattr(lib, name)(q.data_ptr(), H, qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
                             rp, n, cache._ref, seqs._ref(T), q_out.data_ptr(), ot, oh,
                             _stream_of(dev, stream))
@@ -431,7 +431,8 @@ def attention_paged(q: torch.Tensor, cache: PagedKV | PagedKVInt8, seqs: SeqBatc
         workspace = attention_workspace(T, seqs.n_seqs, H, hkv, D, q.device, stream)
     nbytes = _space(workspace, dev)
     lib = _lib.load()
-    name = "qz_attention_paged" if type(cache) is PagedKV else "qz_attention_paged_int8"
+    name = ("qz_attention_paged_int8" if isinstance(cache, PagedKVInt8) else
+            "qz_attention_paged")
     st = getattr(lib, name)(q.data_ptr(), H, qt, qh, cache._ref, seqs._ref(T),
                             D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
                             ot, oh, workspace.data_ptr(), nbytes, _stream_of(dev, stream))
