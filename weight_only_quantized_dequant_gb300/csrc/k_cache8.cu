@@ -9,9 +9,13 @@
 //
 // Append: a thread takes the 8 + 8 values that rotate into one another, as in the
 // fp16 append; the D / 16 threads of a row share its largest value by shuffles.
-// Read: 16 codes a thread, one 16-byte load and two 16-byte stores; a CTA takes
-// several tokens, whose sequences and pages its first warp looks up at once.
-// Both are bound by HBM for long steps and by launch latency for short ones.
+// Longer steps take three items a thread (2700 tokens, 64 heads on 8, D 128: 24.3 us, 3.9
+// TB/s; with two 25.3, with one 27.2), and warps of queries leave before the rows' part
+// (30.3 us when they went through it).  What is left over HBM's 14 us is latency: a thread's
+// loads, divisions and shuffles are one chain.  64 tokens, 32 heads: 5 us, the launch's.
+// Read: 16 codes a thread, one 16-byte load and two 16-byte stores; a CTA takes 8 tokens,
+// whose sequences and pages its first threads look up at once.  8 sequences of up to 16384
+// tokens, 8 heads of 128: 95 us, 5.6 TB/s, HBM's; 199 tokens 4.5 us, the launch's.
 #include "seq_batch.cuh"
 
 namespace qz {
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) append_int8_kernel(const AppendParam
       const float2 u = h2f(av[k]), w = h2f(bv[k]);
       x[2 * k] = u.x, x[2 * k + 1] = u.y, y[2 * k] = w.x, y[2 * k + 1] = w.y;
     }
-    if (rotate && key) {
+    if (rotate && key && head >= hq) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float u = x[k], w = y[k];
@@ -143,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) append_int8_kernel(const AppendParam
         y[k] = rotated(w, c[k], -u, s[k]);
       }
     }
+    if (!__any_sync(0xffffffffu, ok && head >= hq && head < heads)) continue;  // queries
     uint32_t mx = 0;  // magnitudes' bits: a NaN is larger than any value
 #pragma unroll
     for (int k = 0; k < 8; ++k)
