@@ -132,6 +132,15 @@ def test_chunks(hq, hkv, D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("qs", [[4, 4], [5, 4], [8, 8], [9, 8], [57] + [1] * 7, [58] + [1] * 7])
+def test_between_drafts_and_chunks(qs, D):
+    """Rows around the number at which another kernel takes them, evenly and on one
+    sequence."""
+    check(qs, [700 + 57 * i for i in range(len(qs))], 8, 2, D, 32, seed=21)
+    check(qs, [q + 3 * i for i, q in enumerate(qs)], 8, 2, D, 16, seed=22, window=40)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("lens", [[1, 2, 127, 128, 129], [513, 31], [1025]])
 @pytest.mark.parametrize("hq,hkv", [(4, 4), (6, 2)])
 def test_prompts(lens, hq, hkv, D):

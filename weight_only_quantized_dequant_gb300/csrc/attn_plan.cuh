@@ -386,8 +386,11 @@ __device__ __forceinline__ uint32_t scale_runs(const ScaleParams &p, int page) {
 }
 __device__ __forceinline__ void scale_zeros(const ScaleParams &p, float *dst, int page) {
   const int n = min(p.page_size, kN), lane = threadIdx.x & 31;
-  if (p.runs && page >= p.n_pages)
+  if (p.runs && page >= p.n_pages) {
     for (int i = 0; i < n; ++i) dst[lane * n + i] = 0.0f;
+    // (a later block's bulk copy goes over them)
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
 }
 __device__ __forceinline__ void scale_copy(const ScaleParams &p, const float *sc, int64_t sc_page,
                                            int64_t sc_head, int64_t sc_token, float *dst,

@@ -23,6 +23,11 @@
 //    of the second's tiles, so that both come as whole 16-byte reads.
 //  * Weights are rounded to fp16 once, with vs_j in them: 2^6 e^{x - m} vs_j 2^-E,
 //    where m lags the maximum by up to 2^8 and 2^E the largest vs by up to 2.
+//    A pair of tiles of 16 rows a sequence (drafts) is still faster than one tile of the
+//    other kernel.
+//  * Measured: 32 tokens over up to 16384 keys, 64 heads on 8, D 128, 124 us, 5.7 TB/s (the
+//    fp16 kernel 207 over its rows); D 64, 32 on 8, 86; 8 over 8192, D 256, cap and window, 34;
+//    one token over 200 keys 8.2, which is the launch, the plan and one chain of loads.
 //  * The split of (tile, key block) units between CTAs is that of the fp16 kernel.
 #include <cstring>
 
@@ -54,7 +59,7 @@ struct Cfg8 {
   static constexpr int kStage = kN * D;             // bytes of a K or V block
   static constexpr int kNS = 131072 / kStage;       // K and V slots: 16, 8, 4
   static constexpr int kSteps = D / 16;             // of the first product
-  static constexpr int kBuf = kWarps * kM * kRow * 4;  // outputs of the warps, 128 columns at a time
+  static constexpr int kBuf = kWarps * kM * kRow * 4;  // warps' outputs, 128 columns at a time
   static constexpr int kQ = D == 256 && NB == 2 ? kSteps * 512 : 0;  // queries by step
   static constexpr int kSmem = 1024 + kHead8 + kNS * kN * 4 + kNS * kStage + kBuf + kQ;
   static constexpr int kPart = kM * (D + 2);        // floats of a partial
@@ -240,7 +245,8 @@ __global__ void __launch_bounds__(Cfg8<D, NB>::kThreads, 1)
           for (int i = 0; i < KS; i += 2) {
             const int d = D == 256 ? (i >> 3) * 128 + 32 * t + 4 * (i & 7) : t * (D / 4) + 4 * i;
             const uint4 a = *reinterpret_cast<const uint4 *>(qrow[b] + d);
-            qb[kQinSm ? 0 : b][kQinSm ? 0 : i][0] = a.x, qb[kQinSm ? 0 : b][kQinSm ? 0 : i][1] = a.y;
+            qb[kQinSm ? 0 : b][kQinSm ? 0 : i][0] = a.x;
+            qb[kQinSm ? 0 : b][kQinSm ? 0 : i][1] = a.y;
             qb[kQinSm ? 0 : b][kQinSm ? 0 : i + 1][0] = a.z;
             qb[kQinSm ? 0 : b][kQinSm ? 0 : i + 1][1] = a.w;
           }
@@ -693,7 +699,14 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
                                 float softcap, int64_t window, __half *out, int64_t o_token,
                                 int64_t o_head, void *workspace, cudaStream_t s) {
   const int64_t rows = sv.n_tokens * (hq / c.hkv);  // of a KV head, of all sequences
-  if (rows > (int64_t)16 * sv.n_seqs)
+  // Two tiles of 16 rows read a sequence's keys twice, from L2 the second time, and still take
+  // less than one tile of the other kernel: 16 sequences of 32 rows over 8000 keys, 8 heads, D
+  // 64, 128, 256: 89, 129, 220 us here and 127, 152, 231 there; three tiles 127, 184, 319 and
+  // 129, 157, 233 (of prompts of 24 tokens, 64 of them at D 128, two take 55 and 44).  Only
+  // the mean is known here, but however uneven the rows, they are at most three tiles a
+  // sequence.  255 single tokens over 4000 keys beside a chunk of 2048: 1.35 ms and 2.47; over
+  // 500 and 16384 keys 2.16 and 0.92.
+  if (rows > (int64_t)32 * sv.n_seqs)
     return launch_attention_int8_tc(q, hq, q_token, q_head, c, sv, scale, softcap, window, out,
                                     o_token, o_head, workspace, s);
   DeviceInfo di;
