@@ -559,10 +559,13 @@ qz_status qz_cache_read_int8(const qz_kv_cache_int8 *cache, const qz_seq_batch *
 /* qz_attention_paged over a cache of INT8 rows: k_j and v_j are the rows' codes
  * times their scales, which multiply logits and weights in fp32, so that the codes
  * enter the products exactly; the weights times the values' scales are rounded to
- * fp16 where they enter the tensor cores (to 2^-11 of each, or 2^-30 of the largest).  Everything
- * else is as in qz_attention_paged, with the same workspace (which calls of both
- * may share one after the other); codes of slots that no query sees may hold
- * anything, and so may their scales. */
+ * fp16 where they enter the tensor cores (to 2^-11 of each, or 2^-30 of the
+ * largest).  Scales are those of qz_rope_append_int8: not negative, the values' at
+ * most 65504 / 127.  A seen row whose scale is not finite makes outputs of its
+ * sequence in the step that see it NaN, and may those of its other rows.
+ * Everything else is as in qz_attention_paged, with the same workspace (which
+ * calls of both may share one after the other); codes of slots that no query sees
+ * may hold anything, and so may their scales. */
 qz_status qz_attention_paged_int8(const qz_half *q, int64_t n_heads, int64_t q_token,
                                   int64_t q_head, const qz_kv_cache_int8 *cache,
                                   const qz_seq_batch *seqs, float scale, float softcap,
@@ -611,9 +614,9 @@ size_t qz_lora_workspace_bytes(int64_t T, int64_t K, int64_t R);
  * largest logit (probability 1).  u outside [0, 1) is taken as the nearest value
  * in it.  A row without any logit above -inf gives token -1 and logprob -inf;
  * logits of +inf share all the weight.
- * Weights are held as integers, 2^44 for the largest (to 2^-30 of each; below
- * 2^-45 of the largest they are 0), and summed exactly: results repeat bit for
- * bit and a row's do not depend on the others.
+ * Weights are held as integers, 2^45 for the largest (to 2^-28 of each and half a
+ * unit; below 2^-46 of the largest they are 0), and summed exactly: results repeat
+ * bit for bit and a row's do not depend on the others.
  * logits [B][ld] of the given type, aligned to its size (16-byte aligned rows are
  * read faster), ld >= V.  Options: a device array of B values, or NULL and one
  * value for all rows.  1 <= V <= QZ_MAX_VOCAB, B <= 2^24. */

@@ -9,7 +9,7 @@
 //
 // Append: a thread takes the 8 + 8 values that rotate into one another, as in the
 // fp16 append; the D / 16 threads of a row share its largest value by shuffles.
-// Longer steps take three items a thread (2700 tokens, 64 heads on 8, D 128: 24.3 us, 3.9
+// Longer steps take three items a thread (1854 tokens, 64 heads on 8, D 128: 24.3 us, 3.9
 // TB/s; with two 25.3, with one 27.2), and warps of queries leave before the rows' part
 // (30.3 us when they went through it).  What is left over HBM's 14 us is latency: a thread's
 // loads, divisions and shuffles are one chain.  64 tokens, 32 heads: 5 us, the launch's.
