@@ -277,3 +277,16 @@ def test_refusals():
         qz().sample(torch.zeros((1, 2 ** 18 + 1), dtype=F16, device=DEV), u[:1])
     tok, lp = qz().sample(x[:0], u[:0])
     assert tok.shape == (0,) and lp.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("V", [60000, 200000])
+def test_nearly_equal_logits(V, dtype):
+    """Most of a row lies around the cut: more than a warp lists."""
+    g = torch.Generator(device=DEV).manual_seed(31)
+    x = (torch.randn((4, V), generator=g, device=DEV) * 0.02 + 3).to(dtype)
+    x[1, ::3] -= 1.0
+    x[2, : V // 8] += 0.3  # all of them on one part of the row
+    u = torch.tensor([0.1, 0.5, 0.9, 0.999], device=DEV)
+    check(x, u, p=torch.tensor([0.5, 0.95, 0.2, 0.9], device=DEV))
+    check(x, u, T=0.7, p=0.6, min_p=0.98)

@@ -22,9 +22,12 @@
 //    which it sorts and answers from;
 //  * top-p of a whole row: a histogram of a quarter of the tokens (and of all groups'
 //    largest), sixteenths of a logit wide, says about where the cut is; one pass sums
-//    all weights, those above the bins around the cut, and by steps of the key (the
-//    fp32 value's bits in their order) those in them, so the cut is exact whatever the
-//    estimate was; where few tokens may be kept they are listed as for top-k;
+//    all weights and those above the bins around the cut, and lists the places of the
+//    tokens in them, warp by warp; the lists are what the histogram by steps of the key
+//    (the fp32 value's bits in their order), its refinement and the sums below the bins go
+//    through, so the cut is exact whatever the estimate was (64 rows of 256000: 100 us with
+//    a branch for those tokens in each pass, 84 with the lists); where few tokens may be
+//    kept they are listed as for top-k;
 //  * what the estimate misses (logits of 63 and more, lists that overflow, a cut
 //    outside) takes the general way, histograms of 2048 steps of the key, refined
 //    until a step is one value;
@@ -33,10 +36,10 @@
 //
 // What bounds it: the instructions of a weight (about 25) and of its sums, and, with few
 // rows, the chain of cluster barriers (about 1 us each).  Measured: 64 rows of 256000, top-p
-// 0.95, 100 us (307 by the general way alone, before the weights' other form); 16 of 128000 fp32 with options of each row 31.5; one
-// of 32000, top-k 50 and top-p 0.9, 11.1.  Clusters of 8 with 64 KB slices leave some SMs
-// without work (126 thousand instructions a scheduler on the busiest SM, 86 on average);
-// larger slices would leave an SM one CTA.
+// 0.95, 84 us (307 by the general way alone, before the weights' other form); 16 of
+// 128000 fp32 with options of each row 30; one of 32000, top-k 50 and top-p 0.9, 11.5.
+// Clusters of 8 with 64 KB slices leave some SMs without work; slices of 128 KB (one CTA an
+// SM) took 150 us for 64 rows where these took 103, and 1024 threads a CTA 116.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -51,6 +54,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 2048;       // tokens that a CTA can list
 constexpr int kFew = 112;         // of a row, that are listed in any case (and sorted at once)
+constexpr int kMine = kList * 8 / kWarps / 2;  // a warp's share of the list, as 16-bit places
 constexpr int kMaxCluster = 8;
 constexpr int kUnitBits = 45;     // the largest logit's weight is 2^45
 constexpr int kSliceBytes = 64 << 10;  // two CTAs an SM
@@ -908,30 +912,46 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
         const uint32_t count_at = remote(sm->count, 0), mass_at = remote(sm->mass, 0);
         u64 all = 0, above = 0;
+        // this warp's tokens in the bins, as places in the slice (below 2^15: 64 KB of
+        // 16-bit logits, an eighth of QZ_MAX_VOCAB); more than fit are looked for again
+        uint16_t *const in_bins = reinterpret_cast<uint16_t *>(sm->list) + warp * kMine;
+        uint32_t n_in = 0;
+        auto each_in_bins = [&](auto f) {
+          if (n_in <= kMine) {
+            for (uint32_t k = lane; k < n_in; k += 32) f((float)slice[in_bins[k]]);
+          } else {
+            r.each([&](float x, int, int) {
+              if (x >= edge_lo && x <= edge_hi) f(x);
+            });
+          }
+        };
         if (few) {
           r.each([&](float x, int i, int) {
             all += weight<kExact>(s, sm->pw, x);
             if (x >= edge_lo) push(x, i);
           });
         } else {
-          uint32_t in = 0;  // of a vector, those in the bins
-          r.each([&](float x, int i, int j) {
+          r.each([&](float x, int i, int) {
             const u64 w = weight<kExact>(s, sm->pw, x);
             all += w;
             above += x > edge_hi ? w : 0;
-            in |= x >= edge_lo && x <= edge_hi ? 1u << j : 0;
-            if (j < N - 1) return;
-            for (; in; in &= in - 1) {
-              const float y = (float)slice[i - (N - 1) + __ffs(in) - 1];
-              const u64 z = weight<kExact>(s, sm->pw, y);
-              const uint32_t b = (hi - key_of(clean(y))) >> shift;
-              if (r.rank == 0) {
-                add_remote32(count_at + b * 4, 1u);
-                if (z) add_remote64(mass_at + b * 8, z);
-              } else {
-                atomicAdd(&sm->count[b], 1u);
-                if (z) add_mass(&sm->mass[b], z);
-              }
+            const bool in = x >= edge_lo && x <= edge_hi;
+            const uint32_t m = __ballot_sync(0xffffffffu, in);  // (whole warps)
+            if (m == 0) return;
+            const uint32_t at = n_in + __popc(m & ((1u << lane) - 1));
+            if (in && at < kMine) in_bins[at] = (uint16_t)i;
+            n_in += __popc(m);
+          });
+          __syncwarp();
+          each_in_bins([&](float x) {
+            const u64 z = weight<kExact>(s, sm->pw, x);
+            const uint32_t b = (hi - key_of(clean(x))) >> shift;
+            if (r.rank == 0) {
+              add_remote32(count_at + b * 4, 1u);
+              if (z) add_remote64(mass_at + b * 8, z);
+            } else {
+              atomicAdd(&sm->count[b], 1u);
+              if (z) add_mass(&sm->mass[b], z);
             }
           });
         }
@@ -990,15 +1010,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (ok) {
           done = shift <= kGrain
                      ? (last = last_cut<T, true>(hi, shift, left, in_bin, n), true)
-                     : find_cut<T, true, true>(r, s, slice_each, lo, hi, Cut{0, 0}, left, -1.0f,
-                                               &last);
+                     : find_cut<T, true, true>(r, s, each_in_bins, lo, hi, Cut{0, 0}, left,
+                                               -1.0f, &last);
           if (done && (min_key == 0 || min_key <= last.key)) {
             // the kept ones among the tokens of those bins
             const float at = value_of(last.key);
             u64 mass = 0;
             uint32_t ties = 0;
-            r.each([&](float x, int, int) {
-              if (x > at && x <= edge_hi) mass += weight<kExact>(s, sm->pw, x);
+            each_in_bins([&](float x) {
+              if (x > at) mass += weight<kExact>(s, sm->pw, x);
               ties += x == at;
             });
             put_sums(above, mass, ties);
