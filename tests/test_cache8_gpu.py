@@ -278,6 +278,33 @@ def test_strided_queries():
         assert torch.equal(qz().attention_paged(qh, p.cache, p.seqs), want)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,hq", [(4, 2), (8, 8), (100, 8)])
+def test_rows_that_are_not_finite(new, hq, D, which, bad):
+    """A new token's key or value that is not finite (scale so, codes 0): queries that see it
+    get NaN; earlier ones of the step their own answer, or NaN beside such a value."""
+    n, pos = 600, 600 - new // 2
+    p = Paged8([new, 1], [n, 300], 2, 32, D, 60)
+    page = p.rows[0][pos // 32]
+    codes, scale = (p.cache.k, p.cache.k_scale) if which == "k" else (p.cache.v, p.cache.v_scale)
+    codes[page, :, pos % 32] = 0
+    scale[page, :, pos % 32] = bad
+    q = randn(gen(61), p.T, hq, D)
+    out = qz().attention_paged(q, p.cache, p.seqs)
+    want, mag, dot = attention_ref(p, q, hq, D ** -0.5, 0.0, 0)
+    first = new - (n - pos)  # new tokens before it
+    assert bool(out[first:new].isnan().all())
+    tol = tolerance(p, want, mag, dot, n)
+    keep = torch.tensor([i for i in range(p.T) if not first <= i < new], device=DEV)
+    got = out[keep].double()
+    if which == "v":
+        assert not bool(got[-1].isnan().any())  # (another sequence's)
+        got = torch.where(got.isnan(), want[keep], got)
+    within(got, want[keep], tol[keep], "out")
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_bad_pages_read_as_zeros(new):
     p = Paged8([1, new], [40, 40], 2, 16, 64, 20)

@@ -857,13 +857,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int at_key = (g.b0 + (NQ == 2 ? i / 2 : (i + 1) / 2)) * kN;
             const bool seen = row < g.hi - at_key && row >= g.lo - at_key;
             const float ks = seen ? *k : 0.0f, y = seen ? *v : 0.0f;
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(ks));
+            // (a key that is not finite has no part in its neighbours' unit)
+            const uint32_t top =
+                __reduce_max_sync(0xffffffffu, ks < INFINITY ? __float_as_uint(ks) : 0u);
             const int e = min(max((int)(top >> 23) - 127, -100), 126);
             const float x = ks * __uint_as_float((uint32_t)(127 - e) << 23);
             const float unit = __uint_as_float((uint32_t)(127 + e) << 23) * (CAP ? 1.0f : p.c);
-            const bool tiny = x < 0x1p-21f;
-            s = __float2half_rn(tiny ? x : four_bits(x));
-            *k = (tiny ? 1.0f : x * __frcp_rn(four_bits(x))) * unit;
+            // (nor a factor that would make a NaN of a masked logit)
+            const bool whole = x < 0x1p-21f || !(ks < INFINITY);
+            s = __float2half_rn(whole ? x : four_bits(x));
+            *k = (whole ? 1.0f : x * __frcp_rn(four_bits(x))) * unit;
             if (lane == 0) unit_sm[set * 4 + group] = unit;
             const float w = fminf(fmaxf(four_bits(y), 0x1p-21f), 512.0f);
             part_sm[set * kN + row] = __float2half_rn(w);
