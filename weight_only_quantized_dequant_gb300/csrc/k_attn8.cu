@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(Cfg8<D, NB>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < F4 / 8; ++k) {
               const int row = 8 * b + 2 * t + i, n = h * 8 + 2 * k;
+              if (row >= s.rows) continue;
               *reinterpret_cast<float4 *>(
                   buf + ((warp * kM + row) * F4 + place(row, (F4 / 8) * g + k)) * 4) =
                   make_float4(o[n][b][i] * f[b][i], o[n][b][i + 2] * f[b][i],

@@ -368,11 +368,13 @@ def cache_read(cache: PagedKVInt8, seqs: SeqBatch, n_tokens: int, k: torch.Tenso
     _need(n_tokens >= 0, "n_tokens: negative")
     shape = (n_tokens, hkv, D)
     if k is None:
-        k = _empty(shape, _F16, cache.k.device, stream)
+        k, kt, kh = _empty(shape, _F16, cache.k.device, stream), hkv * D, D
+    else:
+        kt, kh = _heads(k, "k", dev, *shape)
     if v is None:
-        v = _empty(shape, _F16, cache.k.device, stream)
-    kt, kh = _heads(k, "k", dev, *shape)
-    vt, vh = _heads(v, "v", dev, *shape)
+        v, vt, vh = _empty(shape, _F16, cache.k.device, stream), hkv * D, D
+    else:
+        vt, vh = _heads(v, "v", dev, *shape)
     st = _lib.load().qz_cache_read_int8(cache._ref, seqs._ref(n_tokens), k.data_ptr(), kt, kh,
                                         v.data_ptr(), vt, vh, _stream_of(dev, stream))
     if st:
@@ -555,12 +557,15 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     _need(-2 ** 31 <= k_all < 2 ** 31, "top_k: 32 bits")
     if out is None:
         out = _empty((B,), _I32, logits.device, stream)
+    else:
+        _vec(out, "out", dev, B, _I32)
     if logprob is None:
         logprob = _empty((B,), _F32, logits.device, stream)
-    op, lp = _vec(out, "out", dev, B, _I32), _vec(logprob, "logprob", dev, B, _F32)
+    else:
+        _vec(logprob, "logprob", dev, B, _F32)
     opts = _lib.Sampling(t, k, p, m, t_all, k_all, p_all, m_all)
-    st = _lib.load().qz_sample(logits.data_ptr(), kind, B, V, ld, up, ctypes.byref(opts), op, lp,
-                               _stream_of(dev, stream))
+    st = _lib.load().qz_sample(logits.data_ptr(), kind, B, V, ld, up, ctypes.byref(opts),
+                               out.data_ptr(), logprob.data_ptr(), _stream_of(dev, stream))
     if st:
         _lib.fail("qz_sample", st)
     return out, logprob
