@@ -8,11 +8,11 @@
 // weights: scaled rows in fp16 would save the softmax a multiplication or two and cost a
 // rounding of every key and value, twice the plain form's error.
 //
-// Measured (64 heads on 8, D 128): 4 x 64 tokens over up to 24576 keys 193 us, 537 TFLOP/s;
-// four prompts of up to 2048 (32 heads) 230 (fp16 rows: 114 and 121).  The difference is the
-// codes' way through registers and, in the softmax, two factors a key from shared memory,
-// which every lane of a row's warp reads: both go through the shared-memory pipe that also
-// feeds the tensor cores.
+// Measured (64 heads on 8, D 128): 4 x 64 tokens over up to 24000 keys 189 us, 548 TFLOP/s;
+// four prompts of up to 2048 (32 heads) 226 (fp16 rows: 114 and 121).  The difference is the
+// codes' way through the registers of two warps (a few instructions more there show in the
+// whole) and, in the softmax, two factors a key from shared memory, which every lane of a
+// row's warp reads.
 #include "attn_tc.cuh"
 
 namespace qz {
