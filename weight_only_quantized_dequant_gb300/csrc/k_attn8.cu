@@ -558,13 +558,14 @@ __global__ void __launch_bounds__(Cfg8<D, NB>::kThreads, 1)
             float mn = M;
 #pragma unroll
             for (int k = 0; k < U; ++k) mn = fmaxf(mn, mk[k]);
-            if (mn == -INFINITY) continue;
-            const float f0 = ex2(M - mn);
+            // (-inf: rows that saw no key, or a NaN in every logit, which goes on as 0 * NaN)
+            const float z = mn == -INFINITY ? 0.0f : mn;
+            const float f0 = ex2(M - z);
             L *= f0;
             a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-              const float fk = ex2(mk[k] - mn);
+              const float fk = ex2(mk[k] - z);
               L = fmaf(lk[k], fk, L);
               a.x = fmaf(v[k].x, fk, a.x), a.y = fmaf(v[k].y, fk, a.y);
               a.z = fmaf(v[k].z, fk, a.z), a.w = fmaf(v[k].w, fk, a.w);
