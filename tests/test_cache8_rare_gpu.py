@@ -1,10 +1,11 @@
 """The INT8 key/value cache where one query, key or value is unlike its neighbours: what is
-not finite stays where it is seen.  Tolerances are those of test_cache8_gpu."""
+not finite stays where it is seen, and what is very large or very small leaves the others
+their own precision.  Tolerances are those of test_cache8_gpu."""
 import pytest
 import torch
 
 from test_cache8_gpu import F32, I8, Paged8, tolerance
-from test_layer_gpu import DEV, F64, attention_ref, gen, randn, within
+from test_layer_gpu import DEV, F16, F64, attention_ref, gen, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -38,6 +39,10 @@ def set_keys(p, i, codes, scale):
         a, b = j * p.page, min(p.kvs[i], (j + 1) * p.page)
         p.cache.k[p.rows[i][j], :, :b - a] = codes[a:b].to(I8).transpose(0, 1)
         p.cache.k_scale[p.rows[i][j], :, :b - a] = scale[a:b].to(F32).transpose(0, 1)
+
+
+def codes_like(p, i, seed):
+    return torch.randint(-127, 128, (p.kvs[i], p.hkv, p.D), generator=gen(seed), device=DEV)
 
 
 # ------------------------------------------------------------- not finite ---
@@ -77,3 +82,46 @@ def test_no_key_is_finite(new, n, D, scale):
     out = qz().attention_paged(q, p.cache, p.seqs)
     assert bool(out[:new].isnan().all())
     assert torch.equal(out[new], good[new])
+
+
+# --------------------------------------------------------- large and small ---
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("softcap", [0.0, 50.0])
+@pytest.mark.parametrize("new,n", [(3, 70), (64, 64), (64, 700), (150, 150)])
+def test_a_key_far_above_its_neighbours(new, n, softcap, D):
+    """The last token's key is 2^25 times the others'.  Queries before it do not see it, and
+    attend over small keys (their own queries are large)."""
+    p = Paged8([new], [n], 2, 32, D, 5, spread=0.0)
+    scale = torch.full((n, 2), 1.5e-5, device=DEV)
+    scale *= 1 + torch.rand((n, 2), generator=gen(6), device=DEV)
+    scale[-1] = 500.0
+    set_keys(p, 0, codes_like(p, 0, 7), scale)
+    q = randn(gen(8), p.T, 8, D, scale=1500.0)
+    out = qz().attention_paged(q, p.cache, p.seqs, softcap=softcap)
+    want, mag, dot = attention_ref(p, q, 8, D ** -0.5, softcap, 0)
+    tol = tolerance(p, want, mag, dot, n)
+    assert float(want[:-1].abs().median()) > 20 * float(tol[:-1].median())
+    within(out, want, tol, "out")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("first", [25.0, 40.0, 60.0])
+@pytest.mark.parametrize("new", [3, 64, 150])
+def test_small_keys_beside_a_large_one_that_repels(new, first, D):
+    """All logits are below zero.  Keys of logits near -first, then blocks with a large key,
+    whose weight is zero, and small keys, whose logits are the largest of all."""
+    n = 400
+    p = Paged8([new], [n], 1, 32, D, 9, spread=0.0)
+    codes = torch.randint(40, 128, (n, 1, D), generator=gen(10), device=DEV)
+    q = (torch.rand((p.T, 4, D), generator=gen(11), device=DEV) * 256 + 256).to(F16)
+    one = float(q[0, 0].double().sum()) * 84 * D ** -0.5  # the logit of a key of scale 1
+    scale = torch.full((n, 1), first / one, device=DEV)
+    scale[200:] = 2.0 / one
+    scale[[210, 300, 350]] = 500.0
+    set_keys(p, 0, codes, scale)
+    out = qz().attention_paged(-q, p.cache, p.seqs)
+    want, mag, _ = attention_ref(p, -q, 4, D ** -0.5, 0.0, 0)
+    # (a large key's weight is 0, and its products enter no other logit: the small ones' bound)
+    p.kc[0] = torch.where(scale[..., None] < 1, p.kc[0], 0.0)
+    _, _, dot = attention_ref(p, -q, 4, D ** -0.5, 0.0, 0)
+    within(out, want, tolerance(p, want, mag, dot, n), "out")

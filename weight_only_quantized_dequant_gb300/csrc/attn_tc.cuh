@@ -24,9 +24,9 @@ constexpr int kHead = kBars + 8 * kOutBytes;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kScaleBlocks = 8;        // INT8 rows: key blocks whose scales are kept
-// What is kept of them: factors of the logits and weights [2][kN], units [4], and the
-// fp16 parts of the values' [kN].
-constexpr int kScaleSet = 2 * kN * 4 + 16 + kN * 2;
+// What is kept of them: factors of the logits and weights [2][kN], bounds of the former
+// [4][2], and the fp16 parts of the values' [kN].
+constexpr int kScaleSet = 2 * kN * 4 + 32 + kN * 2;
 constexpr int kScaleBytes = (kScaleBlocks * kScaleSet + 1023) / 1024 * 1024;
 constexpr float kLift = 7.0f;          // log2 of the weight at m
 static_assert(kLag + kLift < 16.0f - 0.1f, "weights are fp16 (INT8 rows: times at most 17/16)");
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Seg *seg_sm = reinterpret_cast<Seg *>(base + 512);         // [kSegs]
   float *xch = reinterpret_cast<float *>(base + 1024);       // [2][8 warps][32]
   float *scale_sm = reinterpret_cast<float *>(base + kHead);  // [kScaleBlocks][K, V][kN]
-  float *unit_sm = scale_sm + kScaleBlocks * 2 * kN;          // [kScaleBlocks][4]
-  __half *part_sm = reinterpret_cast<__half *>(unit_sm + kScaleBlocks * 4);  // [kScaleBlocks][kN]
+  float2 *bound_sm = reinterpret_cast<float2 *>(scale_sm + kScaleBlocks * 2 * kN);  // [..][4]
+  __half *part_sm = reinterpret_cast<__half *>(bound_sm + kScaleBlocks * 4);  // [kScaleBlocks][kN]
   uint8_t *q_sm = base + C::kFirst, *kv_sm = q_sm + C::kQ;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < NP / 32; ++k)
             tmem_ld32(s_tm + col + 32 * k, reinterpret_cast<uint32_t *>(s) + 32 * k);
           const float *kf = scale_sm + set * (2 * kN) + col, *vf = kf + kN;
-          const float *uf = unit_sm + set * 4 + col / 32;
+          const float2 *bf = bound_sm + set * 4 + col / 32;
           tmem_ld_wait();
           if (Q8 && CAP) {
 #pragma unroll
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float mb;
           if (kBound) {
-            // No logit is above this: factors are within 1/16 of their unit.
+            // No logit is above this.  (A masked group times a bound of 0 is NaN, and not taken.)
             mb = -INFINITY;
 #pragma unroll
             for (int h = 0; h < NP / 32; ++h) {
@@ -436,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               a = max3(a, s[32 * h + 30], s[32 * h + 31]);
               a = fmaxf(a, c);
-              mb = fmaxf(mb, a * (a > 0.0f ? 1.0625f : 0.9375f) * uf[h]);
+              const float2 f = bf[h];
+              mb = fmaxf(mb, a * (a > 0.0f ? f.x : f.y));
             }
           } else {
             float mx[4] = {s[0], s[1], s[2], s[3]};
@@ -828,9 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Q8: a tile's blocks of keys and values, half of the rows a warp and a row a lane.  A
     // scale is s r with s of 4 bits, so that s times a code is exact in fp16, and r within
     // 1/16 of 1, which stays in fp32: r (and c, without a cap) multiplies the logit, or the
-    // weight.  Keys' s are in units of the largest of 32 keys (2^e: their r has it back; a
-    // key below 2^-21 of it has r = 1, off by less than fp32 logits of the largest are).
-    // Values' s are fp16 as they are, from 2^-21 to 512; r is below 15/16 for smaller ones.
+    // weight.  Keys' s are in units of the largest of 32 keys (2^e, which their r has), not
+    // below 2^-21 of it: r is below 15/16 for smaller keys, so that no key's scale depends on
+    // its neighbours, and the bound of a group that has one is 0 where its products are
+    // negative.  Values' s are fp16 as they are, from 2^-21 to 512, and r likewise.
     // A byte under the bits of 1024 is 1024 + code + 128 once its sign is turned.
     constexpr int kChunks = D == 64 ? 4 : 8;
     uint32_t ring = 0, scales = 0, values = 0, segs = 0;
@@ -864,12 +866,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float x = ks * __uint_as_float((uint32_t)(127 - e) << 23);
             const float unit = __uint_as_float((uint32_t)(127 + e) << 23) * (CAP ? 1.0f : p.c);
             // (nor a factor that would make a NaN of a masked logit)
-            const bool whole = !(x >= 0x1p-21f && x < 4.0f);
-            s = __float2half_rn(whole ? x : four_bits(x));
+            const bool whole = !(x > 0.0f && x < 4.0f);
+            const float part = fmaxf(four_bits(x), 0x1p-21f);
+            s = __float2half_rn(whole ? x : part);
             // (approximate reciprocals, 2^-23: these two warps are what a block waits for; 4 x 64
             // tokens over up to 24000 keys 189 us, with correctly rounded ones 198)
-            *k = (whole ? 1.0f : x * rcp(four_bits(x))) * unit;
-            if (lane == 0) unit_sm[set * 4 + group] = unit;
+            *k = (whole ? 1.0f : x * rcp(part)) * unit;
+            const bool small = __any_sync(0xffffffffu, x > 0.0f && x < 0x1p-21f);
+            if (lane == 0)
+              bound_sm[set * 4 + group] =
+                  make_float2(1.0625f * unit, small ? 0.0f : 0.9375f * unit);
             const float w = fminf(fmaxf(four_bits(y), 0x1p-21f), 512.0f);
             part_sm[set * kN + row] = __float2half_rn(w);
             *v = y * rcp(w);
