@@ -125,3 +125,19 @@ def test_small_keys_beside_a_large_one_that_repels(new, first, D):
     p.kc[0] = torch.where(scale[..., None] < 1, p.kc[0], 0.0)
     _, _, dot = attention_ref(p, -q, 4, D ** -0.5, 0.0, 0)
     within(out, want, tolerance(p, want, mag, dot, n), "out")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale", [1e-16, -1e-25, 1e-37, 1e-44])
+@pytest.mark.parametrize("new", [2, 64, 150])
+def test_logits_that_vanish(new, scale, D):
+    """A tiny scale, over keys that are ordinary, zero or tiny: every seen key has the same
+    weight, and the masked ones none."""
+    n = 200
+    p = Paged8([new, new, new], [n, n, n], 2, 32, D, 12)
+    set_keys(p, 1, torch.zeros((n, 2, D), device=DEV), torch.zeros((n, 2), device=DEV))
+    set_keys(p, 2, codes_like(p, 2, 13), torch.full((n, 2), 2.0 ** -60, device=DEV))
+    q = randn(gen(14), p.T, 8, D)
+    out = qz().attention_paged(q, p.cache, p.seqs, scale=scale)
+    want, mag, dot = attention_ref(p, q, 8, scale, 0.0, 0)
+    within(out, want, tolerance(p, want, mag, dot, n), "out")

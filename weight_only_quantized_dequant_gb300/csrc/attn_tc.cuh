@@ -865,13 +865,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = min(max((int)(top >> 23) - 127, -100), 126);
             const float x = ks * __uint_as_float((uint32_t)(127 - e) << 23);
             const float unit = __uint_as_float((uint32_t)(127 + e) << 23) * (CAP ? 1.0f : p.c);
-            // (nor a factor that would make a NaN of a masked logit)
+            // (nor a factor that is not)
             const bool whole = !(x > 0.0f && x < 4.0f);
             const float part = fmaxf(four_bits(x), 0x1p-21f);
             s = __float2half_rn(whole ? x : part);
             // (approximate reciprocals, 2^-23: these two warps are what a block waits for; 4 x 64
             // tokens over up to 24000 keys 189 us, with correctly rounded ones 198)
-            *k = (whole ? 1.0f : x * rcp(part)) * unit;
+            // (a factor of 0, of tiny keys and scales, would make a NaN of a masked logit)
+            *k = fmaxf((whole ? 1.0f : x * rcp(part)) * unit, 0x1p-126f);
             const bool small = __any_sync(0xffffffffu, x > 0.0f && x < 0x1p-21f);
             if (lane == 0)
               bound_sm[set * 4 + group] =
