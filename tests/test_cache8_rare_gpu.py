@@ -4,7 +4,7 @@ their own precision.  Tolerances are those of test_cache8_gpu."""
 import pytest
 import torch
 
-from test_cache8_gpu import F32, I8, Paged8, tolerance
+from test_cache8_gpu import F32, I8, Paged8, new_tokens, quantised, tolerance
 from test_layer_gpu import DEV, F16, F64, attention_ref, gen, randn, within
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +141,32 @@ def test_logits_that_vanish(new, scale, D):
     out = qz().attention_paged(q, p.cache, p.seqs, scale=scale)
     want, mag, dot = attention_ref(p, q, 8, scale, 0.0, 0)
     within(out, want, tolerance(p, want, mag, dot, n), "out")
+
+
+# ------------------------------------------------------------------ append ---
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rotated_keys_are_rounded_once(D):
+    """Rows of two values that rotate into one another, by any two fp32 factors: the larger
+    result decides the scale, to the last bit.  (Products are exact in 64 bits, and so are
+    sums of products of about one size: one rounding to fp32 is left.)"""
+    T, page = 4096, 64
+    p, q, k, v = new_tokens([T], [T], 1, 2, page, D, 40)
+    g = gen(41)
+    half = D // 2
+    rope = torch.rand((T, D), generator=g, device=DEV) + 0.5
+    rope[::2] *= torch.sign(torch.randn((T // 2, D), generator=g, device=DEV))
+    t = torch.arange(T, device=DEV)
+    at = t % half
+    k.zero_()
+    for h in range(2):
+        for j in (at, at + half):
+            k[t, h, j] = (torch.rand((T,), generator=g, device=DEV) + 0.5).to(F16)
+    qz().rope_append(q, k, v, p.cache, p.seqs, rope)
+    x = k.to(F64)
+    c, s = rope[:, None, :half].to(F64), rope[:, None, half:].to(F64)
+    x = torch.cat([x[..., :half] * c - x[..., half:] * s, x[..., half:] * c + x[..., :half] * s], -1)
+    codes, scale = quantised(x.float())
+    pages = p.seqs.page_table[0, :T // page].long()
+    assert torch.equal(p.cache.k_scale[pages].transpose(1, 2).reshape(T, 2).cpu(), scale)
+    got = p.cache.k[pages].transpose(1, 2).reshape(T, 2, D)
+    assert torch.equal(got.cpu(), codes)

@@ -37,9 +37,10 @@ struct AppendParams {
 };
 
 // a c - b s rounded to fp32: the products' errors by FMA, the difference's exactly
-// (Knuth's two-sum); what is left of the error is below 2^-46 of the larger product.
+// (Knuth's two-sum); what is left of the error is below 2^-46 of the larger product.  (The
+// products by intrinsics: joined with a sum, a product's error would be in it twice.)
 __device__ __forceinline__ float rotated(float a, float c, float b, float s) {
-  const float h = a * c, g = -b * s;
+  const float h = __fmul_rn(a, c), g = __fmul_rn(-b, s);
   const float eh = fmaf(a, c, -h), eg = fmaf(-b, s, -g);
   const float sum = h + g, t = sum - h;
   const float e = (h - (sum - t)) + (g - t);
