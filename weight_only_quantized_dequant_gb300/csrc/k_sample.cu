@@ -239,7 +239,7 @@ __device__ __forceinline__ float log_share(float t_hi, float t_lo, u64 total) {
   s = fmaf(n, 1.42860677e-06f, s);
   const float ab = a + b, abv = ab - a;
   s += (a - (ab - abv)) + (b - abv);
-  const float x = t_hi * 0.693147182f;
+  const float x = __fmul_rn(t_hi, 0.693147182f);  // (never joined with the sums)
   s += fmaf(t_hi, 0.693147182f, -x) + fmaf(t_hi, -1.90465421e-09f, t_lo * 0.693147182f);
   const float sum = ab + x, sv = sum - ab;
   return -(sum + (((ab - (sum - sv)) + (x - sv)) + s));
