@@ -116,11 +116,13 @@ class ServedHead:
         return api.embed_int8(self.table, tokens)
 
     def logits(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
-        """fp16 [T, vocabulary] of the last layer's output and residual (or those rows of
-        them that are wanted)."""
+        """[T, vocabulary] of the last layer's output and residual (or those rows of them that
+        are wanted): fp16, and fp32 with a cap, which would make ties of neighbours in fp16."""
         y, _ = layer.rmsnorm(x, self.norm, self.eps, residual=residual, w_bias=self.w_bias)
         (z,) = self.products(("head",), y)
-        return z if self.softcap == 0.0 else torch.tanh(z / self.softcap) * self.softcap
+        if self.softcap == 0.0:
+            return z
+        return z.float().div_(self.softcap).tanh_().mul_(self.softcap)
 
     def __call__(self, x: torch.Tensor, residual: torch.Tensor, u: torch.Tensor, **options):
         """(tokens, log probabilities) with the options of layer.sample."""
