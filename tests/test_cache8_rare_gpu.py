@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from test_cache8_gpu import F32, I8, Paged8, new_tokens, quantised, tolerance
-from test_layer_gpu import DEV, F16, F64, attention_ref, gen, randn, within
+from test_layer_gpu import DEV, F16, F64, Paged, attention_ref, gen, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -143,6 +143,27 @@ def test_logits_that_vanish(new, scale, D):
     within(out, want, tolerance(p, want, mag, dot, n), "out")
 
 
+# -------------------------------------------------------------- workspaces ---
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_both_caches_share_a_workspace(D):
+    """Calls over fp16 and INT8 rows, of single tokens, drafts and chunks, one after the other
+    with one workspace, whose contexts are cut between CTAs."""
+    hq, hkv, page = 8, 2, 64
+    ws = qz().attention_workspace(200, 3, hq, hkv, D)
+    calls = []
+    shapes = [([1], [30000]), ([3, 1], [9000, 20000]), ([70, 1], [9000, 5000])]
+    for i, (qs, kvs) in enumerate(shapes):
+        for kind in (Paged, Paged8):
+            p = kind(qs, kvs, hkv, page, D, 20 + i)
+            q = randn(gen(30 + i), p.T, hq, D)
+            calls.append((p, q, qz().attention_paged(q, p.cache, p.seqs)))
+    for order in (calls, calls[::-1], calls[::2] + calls[1::2]):
+        got = [qz().attention_paged(q, p.cache, p.seqs, workspace=ws) for p, q, _ in order]
+        for o, (_, _, want) in zip(got, order):
+            assert torch.equal(o, want)
+    assert not bool(ws[:8192].any())
+
+
 # ------------------------------------------------------------------ append ---
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_rotated_keys_are_rounded_once(D):
@@ -164,7 +185,8 @@ def test_rotated_keys_are_rounded_once(D):
     qz().rope_append(q, k, v, p.cache, p.seqs, rope)
     x = k.to(F64)
     c, s = rope[:, None, :half].to(F64), rope[:, None, half:].to(F64)
-    x = torch.cat([x[..., :half] * c - x[..., half:] * s, x[..., half:] * c + x[..., :half] * s], -1)
+    a, b = x[..., :half], x[..., half:]
+    x = torch.cat([a * c - b * s, b * c + a * s], -1)
     codes, scale = quantised(x.float())
     pages = p.seqs.page_table[0, :T // page].long()
     assert torch.equal(p.cache.k_scale[pages].transpose(1, 2).reshape(T, 2).cpu(), scale)
