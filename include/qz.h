@@ -557,12 +557,15 @@ qz_status qz_cache_read_int8(const qz_kv_cache_int8 *cache, const qz_seq_batch *
                              int64_t v_head, qz_stream s);
 
 /* qz_attention_paged over a cache of INT8 rows: k_j and v_j are the rows' codes
- * times their scales, which multiply logits and weights in fp32, so that the codes
- * enter the products exactly; the weights times the values' scales are rounded to
- * fp16 where they enter the tensor cores (to 2^-11 of each, or 2^-30 of the
- * largest).  Scales are those of qz_rope_append_int8: not negative, the values' at
+ * times their scales.  Nothing of them is rounded to fewer than 32 bits: codes enter
+ * the products as they are, or times four bits of their scales (exact in fp16), and
+ * the scales, or the rest of them, multiply logits and weights in fp32.  The
+ * weights times that of the values' scales are rounded to fp16 where they enter the
+ * tensor cores (to 2^-11 of each, or 2^-30 of the largest that the sequence's new
+ * tokens see).  Scales are those of qz_rope_append_int8: not negative, the values' at
  * most 65504 / 127.  A seen row whose scale is not finite makes outputs of its
- * sequence in the step that see it NaN, and may those of its other rows.
+ * sequence in the step that see it NaN, and may, if it is a value's, those of its
+ * other rows.
  * Everything else is as in qz_attention_paged, with the same workspace (which
  * calls of both may share one after the other); codes of slots that no query sees
  * may hold anything, and so may their scales. */

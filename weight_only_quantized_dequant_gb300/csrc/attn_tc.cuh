@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float part = fmaxf(four_bits(x), 0x1p-21f);
             s = __float2half_rn(whole ? x : part);
             // (approximate reciprocals, 2^-23: these two warps are what a block waits for; 4 x 64
-            // tokens over up to 24000 keys 189 us, with correctly rounded ones 198)
+            // tokens over up to 24000 keys 190 us, with correctly rounded ones 198)
             // (a factor of 0, of tiny keys and scales, would make a NaN of a masked logit)
             *k = fmaxf((whole ? 1.0f : x * rcp(part)) * unit, 0x1p-126f);
             const bool small = __any_sync(0xffffffffu, x > 0.0f && x < 0x1p-21f);

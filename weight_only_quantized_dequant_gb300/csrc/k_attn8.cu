@@ -733,9 +733,9 @@ qz_status launch_attention_int8(const __half *q, int64_t hq, int64_t q_token, in
   // less than one tile of the other kernel: 16 sequences of 32 rows over 8000 keys, 8 heads, D
   // 64, 128, 256: 89, 129, 220 us here and 127, 152, 231 there; three tiles 127, 184, 319 and
   // 129, 157, 233 (of prompts of 24 tokens, 64 of them at D 128, two take 55 and 44).  Only
-  // the mean is known here, but however uneven the rows, they are at most three tiles a
-  // sequence.  255 single tokens over 4000 keys beside a chunk of 2048: 1.35 ms and 2.47; over
-  // 500 and 16384 keys 2.16 and 0.92.
+  // the mean is known here, of all sequences, those without new tokens too, and a step of
+  // very uneven ones may lose by it: 255 single tokens over 4000 keys beside a chunk of 2048
+  // take 1.35 ms here and 2.47 there, but over 500 beside a chunk over 16384 2.16 and 0.92.
   if (rows > (int64_t)32 * sv.n_seqs)
     return launch_attention_int8_tc(q, hq, q_token, q_head, c, sv, scale, softcap, window, out,
                                     o_token, o_head, workspace, s);

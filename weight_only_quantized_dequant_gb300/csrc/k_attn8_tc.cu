@@ -4,12 +4,13 @@
 //
 // Codes arrive by TMA in half of a slot; the two warps that bring the queries turn them into
 // fp16 where they lie, so that the products, their order and the softmax are the fp16
-// kernel's.  Codes are exact in fp16; keys' scales multiply the logits and values' scales the
-// weights: scaled rows in fp16 would save the softmax a multiplication or two and cost a
-// rounding of every key and value, twice the plain form's error.
+// kernel's.  A scale is split: four bits of it multiply the codes, which is exact in fp16 (7 +
+// 4 bits), and the rest multiplies, in fp32, the logit (keys) or the weight (values).  Whole
+// scales in the fp16 rows would save the softmax a multiplication or two and cost a rounding
+// of every key and value, twice the plain form's error.
 //
-// Measured (64 heads on 8, D 128): 4 x 64 tokens over up to 24000 keys 189 us, 548 TFLOP/s;
-// four prompts of up to 2048 (32 heads) 226 (fp16 rows: 114 and 121).  The difference is the
+// Measured (64 heads on 8, D 128): 4 x 64 tokens over up to 24000 keys 190 us, 545 TFLOP/s;
+// four prompts of up to 2048 (32 heads) 228 (fp16 rows: 114 and 121).  The difference is the
 // codes' way through the registers of two warps (a few instructions more there show in the
 // whole) and, in the softmax, two factors a key from shared memory, which every lane of a
 // row's warp reads.

@@ -9,10 +9,12 @@
 //
 // Append: a thread takes the 8 + 8 values that rotate into one another, as in the
 // fp16 append; the D / 16 threads of a row share its largest value by shuffles.
-// Longer steps take three items a thread (1854 tokens, 64 heads on 8, D 128: 24.3 us, 3.9
-// TB/s; with two 25.3, with one 27.2), and warps of queries leave before the rows' part
-// (30.3 us when they went through it).  What is left over HBM's 14 us is latency: a thread's
-// loads, divisions and shuffles are one chain.  64 tokens, 32 heads: 5 us, the launch's.
+// Longer steps take three items a thread, and warps of queries leave before the rows' part:
+// 1854 tokens, 64 heads on 8, D 128, 18.9 us, 3.9 TB/s (with the 3600 rows that their
+// sequences hold read back 24.3; with two items 25.3, with one 27.2, and 30.3 when queries
+// went through the rows' part).  What is left over HBM's 10.8 us is latency: the place is
+// looked up, then loads, divisions and shuffles, one chain.  64 tokens, 32 heads: 4.3 us, the
+// launch's.
 // Read: 16 codes a thread, one 16-byte load and two 16-byte stores; a CTA takes 8 tokens,
 // whose sequences and pages its first threads look up at once.  8 sequences of up to 16384
 // tokens, 8 heads of 128: 95 us, 5.6 TB/s, HBM's; 199 tokens 4.5 us, the launch's.

@@ -34,10 +34,13 @@
 //  * the kept weights are summed warp by warp, and the warp that the answer is in goes
 //    through its tokens again.
 //
-// What bounds it: the instructions of a weight (about 25) and of its sums, and, with few
-// rows, the chain of cluster barriers (about 1 us each).  Measured: 64 rows of 256000, top-p
-// 0.95, 84 us (307 by the general way alone, before the weights' other form); 16 of
-// 128000 fp32 with options of each row 30; one of 32000, top-k 50 and top-p 0.9, 11.5.
+// What bounds it: with many rows the instructions (83 a logit in all, of which a weight is
+// about 25; at full issue they would take 36 us of 84) and barriers, at which a cluster waits
+// for its first CTA's scans of the bins; with few the chain of cluster barriers (about 1 us
+// each).  Measured: 64 rows of 256000 fp16, top-p 0.95, 84 us, by the general way (a row
+// whose largest logit is 63 or more) 274, equal logits 381; greedy 29, a temperature alone 49,
+// top-k 50 32, top-k 4000 (more than a list holds) 99.  16 of 128000 fp32 with options of each
+// row 30; one of 32000, top-k 50 and top-p 0.9, 12.
 // Clusters of 8 with 64 KB slices leave some SMs without work; slices of 128 KB (one CTA an
 // SM) took 150 us for 64 rows where these took 103, and 1024 threads a CTA 116.
 #include <cuda_bf16.h>
